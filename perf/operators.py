@@ -151,6 +151,10 @@ def _randn(g, *shape, dtype=torch.bfloat16):
     return torch.randn(*shape, generator=g, device=DEV).to(dtype)
 
 
+def _ints(n, dtype=torch.int32):
+    return torch.empty(n, dtype=dtype, device=DEV)
+
+
 def _inv_freq(R, factor, base=10000.0, original=4096, fast=32.0, slow=1.0):
     """Rotary frequencies [R/2] in fp64 and the factor of cos and sin.  With
     factor > 1 the slow ones are divided by it and the fast ones kept, with a
@@ -166,6 +170,7 @@ def _inv_freq(R, factor, base=10000.0, original=4096, fast=32.0, slow=1.0):
 
 
 def prepare(case, seed):
+    """Inputs, and the output buffers that a decode loop keeps from step to step."""
     c, g = dict(case), _gen(seed)
     s = {"c": c}
     if c["op"] == "extend":
@@ -181,7 +186,8 @@ def prepare(case, seed):
         table = torch.full((c["B"], width), -1, dtype=torch.int32, device=DEV)
         table[mine] = pool[:sum(held)]
         s.update(seq_lens=torch.tensor(old, dtype=torch.int32, device=DEV), new_tokens=torch.tensor(new, dtype=torch.int32, device=DEV),
-                 table=table, free=pool[sum(held):].contiguous(), rows=_extend_rows(c))
+                 table=table, free=pool[sum(held):].contiguous(), rows=_extend_rows(c),
+                 out=(_ints(c["B"]), _ints(c["B"] + 1), _ints(_extend_rows(c), torch.int64), _ints(_extend_rows(c), torch.int64), _ints(2)))
         return s
     if c["op"] == "attention":
         lens = _lens(c)
@@ -196,7 +202,9 @@ def prepare(case, seed):
         cache = _randn(g, sum(held) + 4, page, c["DK"])
         cache.mul_(gamma.to(torch.bfloat16))
         s.update(q=_randn(g, c["B"], c["H"], c["DK"]), cache=cache, table=table,
-                 lens=torch.tensor(lens, dtype=torch.int32, device=DEV), scale=(c["DK"] / 3.0) ** -0.5)
+                 lens=torch.tensor(lens, dtype=torch.int32, device=DEV), scale=(c["DK"] / 3.0) ** -0.5,
+                 out=torch.empty(c["B"], c["H"], c["DV"], dtype=torch.bfloat16, device=DEV),
+                 lse=torch.empty(c["B"], c["H"], dtype=torch.float32, device=DEV))
         return s
     f, m = _inv_freq(c["R"], c["factor"])
     first = torch.randint(0, c["maxpos"], (1,), generator=g, device=DEV)
@@ -206,7 +214,7 @@ def prepare(case, seed):
     if c["op"] == "rope":
         H, D = c["H"], c["D"]
         buf = _randn(g, c["M"], H * D + (64 if c["wide"] else 0))
-        s.update(x=buf[:, :H * D].view(c["M"], H, D),
+        s.update(x=buf[:, :H * D].view(c["M"], H, D), out=torch.empty(c["M"], H, D, dtype=torch.bfloat16, device=DEV),
                  gamma=(torch.rand(D, generator=g, device=DEV) + 0.5).to(torch.bfloat16) if c["gamma"] else None)
         return s
     K, P, M, page = c["K"], c["P"], c["M"], c["page"]
@@ -329,15 +337,15 @@ def _own(s):
     import gemm_dsnq_dual_gb300 as dsnq
     c = s["c"]
     if c["op"] == "extend":
-        return *dsnq.extend_block_tables(s["seq_lens"], s["new_tokens"], s["free"], s["table"], c["page"], s["rows"]), s["table"]
+        return *dsnq.extend_block_tables(s["seq_lens"], s["new_tokens"], s["free"], s["table"], c["page"], s["rows"], out=s["out"]), s["table"]
     if c["op"] == "rope":
         return dsnq.head_rmsnorm_rope(s["x"], s["positions"], s["inv_freq"], gamma=s["gamma"], eps=EPS, normalize=bool(c["norm"]),
-                                      rope_offset=c["off"], layout=c["layout"], rope_scale=s["rope_scale"])
+                                      rope_offset=c["off"], layout=c["layout"], rope_scale=s["rope_scale"], out=s["out"])
     if c["op"] == "write":
         return dsnq.latent_cache_write(s["kv"], s["pe"], s["positions"], s["slots"], s["inv_freq"], s["cache"], gamma=s["gamma"],
                                        eps=EPS, normalize=bool(c["norm"]), rope_offset=s["off"], layout=c["layout"],
                                        rope_scale=s["rope_scale"])
-    return dsnq.paged_latent_attention(s["q"], s["cache"], s["table"], s["lens"], c["DV"], s["scale"])
+    return dsnq.paged_latent_attention(s["q"], s["cache"], s["table"], s["lens"], c["DV"], s["scale"], out=s["out"], lse=s["lse"])
 
 
 def run(state):
