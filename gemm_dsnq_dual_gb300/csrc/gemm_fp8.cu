@@ -58,6 +58,8 @@
 #include "debug_check.cuh"
 #include "dsnq_internal.h"
 #include "group_quant.cuh"
+#include "tensor_host.h"
+#include "tensor_ptx.cuh"
 
 namespace dsnq {
 namespace gemm {
@@ -65,7 +67,6 @@ namespace gemm {
 constexpr int kBK = 128;            // K bytes per stage = one scale block
 constexpr int kUmmaK = 32;          // K per tcgen05.mma kind::f8f6f4
 constexpr int kPRows = 128;         // MMA M
-__device__ unsigned int g_status;   // device status word (kStatusTimeout: a wait timed out)
 
 struct Problem {
     int N;
@@ -108,157 +109,9 @@ struct Params {
 
 // ----------------------------------------------------------------- PTX glue
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// try_wait that lets the hardware suspend the thread until the phase
-// completes or `hint_ns` passes, so a waiting warp takes no issue slots.
-__device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(hint_ns)
-        : "memory");
-    return ok != 0;
-}
-
-constexpr uint32_t kSleepHintNs = 100000;   // re-check abort/timeout at least every 100 us
-
-// Bounded wait for the phase of `parity` to complete.  Gives up when another
-// thread of the CTA has raised *abort, or after timeout_ns, in which case it
-// raises *abort and records the timeout in the device status word.  SPIN
-// polls (lowest wake-up latency, for the waits on the MMA <-> promotion
-// ring); otherwise the thread sleeps in hardware between polls.
-template <bool SPIN = false>
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort,
-                                             uint64_t timeout_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = now_ns();
-    uint32_t n = 0;
-    while (true) {
-        if (SPIN ? mbar_try_wait(bar, parity) : mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
-        if (SPIN && (++n & 63)) continue;       // check abort and the clock every 64 polls
-        
-        if (*abort) return false;
-        if (now_ns() - t0 > timeout_ns) {
-            *abort = 1;
-            atomicOr(&g_status, kStatusTimeout);
-            return false;
-        }
-    }
-}
-
-// Drain wait: bounded by time only (used after an abort, to let this CTA's own
-// copies and MMAs land before its shared and tensor memory are released).
-__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
-    const uint64_t t0 = now_ns();
-    while (!mbar_try_wait_sleep(bar, parity, kSleepHintNs)) {
-        if (now_ns() - t0 > timeout_ns) return;
-    }
-}
-
-// Lets `ns` nanoseconds pass (abort path only): long enough for any bulk
-// copy already issued to land, when there is no barrier this thread can
-// watch for it.
-constexpr uint64_t kAbortSettleNs = 200000;
-__device__ __forceinline__ void settle_ns(uint64_t ns) {
-    const uint64_t t0 = now_ns();
-    while (now_ns() - t0 < ns) __nanosleep(1000);
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int32_t x, int32_t y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
-
-// Tiled bulk store shared -> global (rows past the tensor's extent are clipped).
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(src), "r"(x), "r"(y)
-                 : "memory");
-}
-
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void fence_proxy_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// Tiled bulk prefetch of a tensor tile into L2 (no shared memory, no barrier).
-__device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int32_t x, int32_t y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y)
-                 : "memory");
-}
-
 // K blocks of weight tiles a decode CTA prefetches into L2 before waiting
 // for the previous kernel of its stream (16 KB each).
 constexpr int kPrefetchKBlocks = 24;
-
-__device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// The MMA-issuing code runs converged in a whole warp (warp-uniform values,
-// so they can live in uniform registers); one elected lane issues each
-// tcgen05 instruction.  Issuing from a divergent single lane measured about
-// 1.5x slower per K block on GB300.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-        : "memory");
-}
 
 // D[tmem] (+)= A[smem] * B[smem]^T, E4M3 x E4M3 -> fp32 (elected lane).
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -270,159 +123,6 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// 32 lanes x N consecutive 32-bit TMEM columns, returned as N/2 column pairs
-// (64-bit registers, ready for the paired f32x2 instructions); thread i gets
-// lane (base+i).  Includes the wait for the load to complete.
-template <int N>
-__device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, uint64_t (&r)[N / 2]);
-
-template <>
-__device__ __forceinline__ void tmem_ld_pairs<8>(uint32_t taddr, uint64_t (&r)[4]) {
-    asm volatile(
-        "{\n\t.reg .b32 t<8>;\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {t0, t1, t2, t3, t4, t5, t6, t7}, [%4];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n\t"
-        "mov.b64 %0, {t0, t1};\n\t"
-        "mov.b64 %1, {t2, t3};\n\t"
-        "mov.b64 %2, {t4, t5};\n\t"
-        "mov.b64 %3, {t6, t7};\n\t"
-        "}"
-        : "=l"(r[0]), "=l"(r[1]), "=l"(r[2]), "=l"(r[3])
-        : "r"(taddr)
-        : "memory");
-}
-
-template <>
-__device__ __forceinline__ void tmem_ld_pairs<16>(uint32_t taddr, uint64_t (&r)[8]) {
-    asm volatile(
-        "{\n\t.reg .b32 t<16>;\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15}, [%8];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n\t"
-        "mov.b64 %0, {t0, t1};\n\t"
-        "mov.b64 %1, {t2, t3};\n\t"
-        "mov.b64 %2, {t4, t5};\n\t"
-        "mov.b64 %3, {t6, t7};\n\t"
-        "mov.b64 %4, {t8, t9};\n\t"
-        "mov.b64 %5, {t10, t11};\n\t"
-        "mov.b64 %6, {t12, t13};\n\t"
-        "mov.b64 %7, {t14, t15};\n\t"
-        "}"
-        : "=l"(r[0]), "=l"(r[1]), "=l"(r[2]), "=l"(r[3]), "=l"(r[4]), "=l"(r[5]), "=l"(r[6]), "=l"(r[7])
-        : "r"(taddr)
-        : "memory");
-}
-
-// Split form for software pipelining: the load is issued by one statement and
-// completed by another, which takes the destination registers as operands so
-// that no use of them can be scheduled before the wait.
-__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
-
-template <>
-__device__ __forceinline__ void tmem_ld_pairs<32>(uint32_t taddr, uint64_t (&r)[16]) {
-    asm volatile(
-        "{\n\t.reg .b32 t<32>;\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15, t16, t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n\t"
-        "mov.b64 %0, {t0, t1};\n\t"
-        "mov.b64 %1, {t2, t3};\n\t"
-        "mov.b64 %2, {t4, t5};\n\t"
-        "mov.b64 %3, {t6, t7};\n\t"
-        "mov.b64 %4, {t8, t9};\n\t"
-        "mov.b64 %5, {t10, t11};\n\t"
-        "mov.b64 %6, {t12, t13};\n\t"
-        "mov.b64 %7, {t14, t15};\n\t"
-        "mov.b64 %8, {t16, t17};\n\t"
-        "mov.b64 %9, {t18, t19};\n\t"
-        "mov.b64 %10, {t20, t21};\n\t"
-        "mov.b64 %11, {t22, t23};\n\t"
-        "mov.b64 %12, {t24, t25};\n\t"
-        "mov.b64 %13, {t26, t27};\n\t"
-        "mov.b64 %14, {t28, t29};\n\t"
-        "mov.b64 %15, {t30, t31};\n\t"
-        "}"
-        : "=l"(r[0]), "=l"(r[1]), "=l"(r[2]), "=l"(r[3]), "=l"(r[4]), "=l"(r[5]), "=l"(r[6]), "=l"(r[7]), "=l"(r[8]), "=l"(r[9]), "=l"(r[10]), "=l"(r[11]), "=l"(r[12]), "=l"(r[13]), "=l"(r[14]), "=l"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-
-template <>
-__device__ __forceinline__ void tmem_ld_pairs<64>(uint32_t taddr, uint64_t (&r)[32]) {
-    asm volatile(
-        "{\n\t.reg .b32 t<64>;\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15, t16, t17, t18, t19, t20, t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31, t32, t33, t34, t35, t36, t37, t38, t39, t40, t41, t42, t43, t44, t45, t46, t47, t48, t49, t50, t51, t52, t53, t54, t55, t56, t57, t58, t59, t60, t61, t62, t63}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n\t"
-        "mov.b64 %0, {t0, t1};\n\t"
-        "mov.b64 %1, {t2, t3};\n\t"
-        "mov.b64 %2, {t4, t5};\n\t"
-        "mov.b64 %3, {t6, t7};\n\t"
-        "mov.b64 %4, {t8, t9};\n\t"
-        "mov.b64 %5, {t10, t11};\n\t"
-        "mov.b64 %6, {t12, t13};\n\t"
-        "mov.b64 %7, {t14, t15};\n\t"
-        "mov.b64 %8, {t16, t17};\n\t"
-        "mov.b64 %9, {t18, t19};\n\t"
-        "mov.b64 %10, {t20, t21};\n\t"
-        "mov.b64 %11, {t22, t23};\n\t"
-        "mov.b64 %12, {t24, t25};\n\t"
-        "mov.b64 %13, {t26, t27};\n\t"
-        "mov.b64 %14, {t28, t29};\n\t"
-        "mov.b64 %15, {t30, t31};\n\t"
-        "mov.b64 %16, {t32, t33};\n\t"
-        "mov.b64 %17, {t34, t35};\n\t"
-        "mov.b64 %18, {t36, t37};\n\t"
-        "mov.b64 %19, {t38, t39};\n\t"
-        "mov.b64 %20, {t40, t41};\n\t"
-        "mov.b64 %21, {t42, t43};\n\t"
-        "mov.b64 %22, {t44, t45};\n\t"
-        "mov.b64 %23, {t46, t47};\n\t"
-        "mov.b64 %24, {t48, t49};\n\t"
-        "mov.b64 %25, {t50, t51};\n\t"
-        "mov.b64 %26, {t52, t53};\n\t"
-        "mov.b64 %27, {t54, t55};\n\t"
-        "mov.b64 %28, {t56, t57};\n\t"
-        "mov.b64 %29, {t58, t59};\n\t"
-        "mov.b64 %30, {t60, t61};\n\t"
-        "mov.b64 %31, {t62, t63};\n\t"
-        "}"
-        : "=l"(r[0]), "=l"(r[1]), "=l"(r[2]), "=l"(r[3]), "=l"(r[4]), "=l"(r[5]), "=l"(r[6]), "=l"(r[7]), "=l"(r[8]), "=l"(r[9]), "=l"(r[10]), "=l"(r[11]), "=l"(r[12]), "=l"(r[13]), "=l"(r[14]), "=l"(r[15]), "=l"(r[16]), "=l"(r[17]), "=l"(r[18]), "=l"(r[19]), "=l"(r[20]), "=l"(r[21]), "=l"(r[22]), "=l"(r[23]), "=l"(r[24]), "=l"(r[25]), "=l"(r[26]), "=l"(r[27]), "=l"(r[28]), "=l"(r[29]), "=l"(r[30]), "=l"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-
-__device__ __forceinline__ float2 as_float2(uint64_t v) {
-    float2 f;
-    memcpy(&f, &v, sizeof(f));
-    return f;
-}
-
-// Shared-memory matrix descriptor of a K-major tile written by TMA with the
-// 128-byte swizzle: rows of 128 bytes, 8-row swizzle atoms 1024 bytes apart
-// (stride byte offset), leading byte offset unused for this layout,
-// descriptor version 1, layout code 2 = 128-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t addr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFF);
-    d |= static_cast<uint64_t>(1) << 16;                 // LBO (ignored), 16 bytes
-    d |= static_cast<uint64_t>((1024 >> 4) & 0x3FFF) << 32;  // SBO
-    d |= static_cast<uint64_t>(1) << 46;                 // version
-    d |= static_cast<uint64_t>(2) << 61;                 // 128-byte swizzle
-    return d;
 }
 
 // Instruction descriptor of kind::f8f6f4: D fp32, A and B E4M3, both K-major,
@@ -1690,24 +1390,6 @@ pair_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
 
 namespace {
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 // 2-D map over a K-major e4m3 matrix [rows, K] with row stride ld bytes; box
 // = 128 bytes of K x box_rows rows, 128-byte swizzle, zero fill past the end.
 bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int64_t ld, int box_rows) {
@@ -1799,30 +1481,6 @@ bool cached_out_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int6
     map_cache().put(k, *m);
     return true;
 }
-
-// cudaFuncSetAttribute once per (kernel, device, size): it is host work on
-// every call otherwise.
-bool set_smem_attr(const void* kern, size_t smem) {
-    static std::mutex mu;
-    static std::vector<std::tuple<const void*, int, size_t>> done;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    std::lock_guard<std::mutex> lock(mu);
-    for (const auto& d : done)
-        if (std::get<0>(d) == kern && std::get<1>(d) == dev && std::get<2>(d) >= smem) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-        cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    done.emplace_back(kern, dev, smem);
-    return true;
-}
-
-constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
 
 struct Consumer {
     int64_t N;
@@ -2254,13 +1912,13 @@ extern "C" dsnq_status dsnq_fused_norm_quant_gemm_dual(
 extern "C" dsnq_status dsnq_debug_status(void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned int v = 0, w = 0, n = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, gemm::g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+    if (cudaMemcpyFromSymbolAsync(&v, g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess) {
         cudaGetLastError();
         return DSNQ_ERR_CUDA;
     }
     const unsigned int zero = 0;
-    if (cudaMemcpyToSymbolAsync(gemm::g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+    if (cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess) {
         cudaGetLastError();
         return DSNQ_ERR_CUDA;
