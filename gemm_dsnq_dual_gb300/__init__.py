@@ -9,6 +9,10 @@ kernels.  Output tensors are allocated here with torch when not supplied.
   block_scaled_fp8_gemm_dual      -- both wq_b consumers in one launch
   quantize_weight_block128        -- load-time 128x128 weight-block quantization
   dual_rmsnorm_bf16, group_quant_bf16 -- the unfused baseline sequence
+  extend_block_tables             -- block tables, positions and slots of a step
+  head_rmsnorm_rope               -- per-head RMSNorm and rotary positions in one pass
+  latent_cache_write              -- normalized, rotated latent rows into the paged cache
+  paged_latent_attention          -- one new token per request over the paged latent cache
 
 Method: vLLM PR #53540 (fused_qk_rmsnorm_group_quant feeding
 apply_pre_quantized_block_scaled_mm for the attention and indexer wq_b) and
@@ -18,6 +22,7 @@ sglang PR #27289 (transpose_scale: column-major activation scales).
 from __future__ import annotations
 
 import ctypes as C
+import math
 
 import torch
 
@@ -26,6 +31,8 @@ from ._native import DsnqError, check, lib  # noqa: F401
 ROW_MAJOR = 0
 COL_MAJOR = 1
 GROUP = 128
+ROPE_INTERLEAVED = 0
+ROPE_HALF = 1
 
 __all__ = [
     "ROW_MAJOR", "COL_MAJOR", "DsnqError",
@@ -34,6 +41,8 @@ __all__ = [
     "block_scaled_fp8_gemm_dual_bf16a", "block_scaled_fp8_gemm_dual_bf16a_static", "fused_quant_fits",
     "bf16a_workspace_bytes", "gemm_plan",
     "fused_norm_quant_gemm_dual",
+    "ROPE_INTERLEAVED", "ROPE_HALF", "rope_frequencies", "extend_block_tables", "head_rmsnorm_rope",
+    "latent_cache_write", "paged_latent_attention", "paged_latent_attention_workspace_bytes",
     "quant_output_sizes", "debug_status", "debug_set", "set_launch_overlap", "scale_layout_of", "scale_ld_for",
     "empty_scales",
 ]
@@ -342,6 +351,199 @@ def fused_norm_quant_gemm_dual(q, kv, gamma_q, gamma_kv, eps, w1_fp8, w1_scale, 
         0 if q_fp8 is None else q_fp8.data_ptr(), 0 if q_scale is None else q_scale.data_ptr(),
         _stream(stream, q.device)), "dsnq_fused_norm_quant_gemm_dual")
     return out1, out2, kv_out, q_fp8, q_scale
+
+
+def _need(t, name: str, dtype, dim: int, dev=None):
+    """Checks a tensor argument's type, rank and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return t
+
+
+def _flat(t, name: str, dtype, n: int, dev):
+    """A contiguous 1-D tensor of n elements; its address."""
+    _need(t, name, dtype, 1, dev)
+    if t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous with {n} elements, got shape {tuple(t.shape)}, strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _strides3(t, name: str):
+    """Strides of the two outer dimensions of a 3-D tensor with contiguous
+    rows (a dimension of size 1 gets the stride it would have if packed)."""
+    n0, n1, n2 = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and n2 > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if n1 == 1:
+        s1 = n2
+    if n0 == 1:
+        s0 = n1 * s1
+    return s0, s1
+
+
+def _rope_layout(layout) -> int:
+    if layout in (ROPE_INTERLEAVED, "interleaved"):
+        return ROPE_INTERLEAVED
+    if layout in (ROPE_HALF, "half"):
+        return ROPE_HALF
+    raise ValueError(f"unknown rotary layout {layout!r}")
+
+
+def rope_frequencies(rope_dim: int, base: float = 10000.0, factor: float = 1.0, original_length: int = 4096,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq [rope_dim/2] float64, rope_scale) of head_rmsnorm_rope and
+    latent_cache_write.  With factor > 1 (a context `factor` times
+    original_length) the frequencies of fewer than beta_slow turns over the
+    original length are divided by it, those of more than beta_fast kept, the
+    ones between blended (the YaRN scheme), and rope_scale is its attention
+    factor 0.1 ln(factor) + 1.  Any other table serves as well."""
+    if rope_dim <= 0 or rope_dim % 2:
+        raise ValueError(f"rope_dim must be even and positive, got {rope_dim}")
+    i = torch.arange(0, rope_dim, 2, dtype=torch.float64)
+    freq = torch.pow(torch.tensor(float(base), dtype=torch.float64), -i / rope_dim)
+    if factor <= 1.0:
+        return freq.to(device), 1.0
+
+    def pair_of(turns):                  # the (fractional) pair that makes so many turns
+        return rope_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+    low = max(math.floor(pair_of(beta_fast)), 0)
+    high = min(math.ceil(pair_of(beta_slow)), rope_dim - 1)
+    ramp = ((i / 2 - low) / max(high - low, 1e-3)).clamp(0, 1)
+    return (freq / factor * ramp + freq * (1 - ramp)).to(device), 0.1 * math.log(factor) + 1.0
+
+
+def extend_block_tables(seq_lens, new_tokens, free_pages, block_table, page_size: int, rows: int, out=None, stream=None):
+    """Gives each request (int32 lengths seq_lens [B]) new_tokens [B] more
+    tokens (None: one each): takes the pages they need from free_pages in
+    order, enters them in block_table [B, width] (in place; only new entries
+    are written) and lays the tokens out as `rows` rows of the step.
+    Returns (new_lens [B] int32, row_starts [B+1] int32, positions [rows]
+    int64, slots [rows] int64, counts [2] int32 = pages taken and wanted);
+    `out` supplies those five.  Padded rows and tokens without a place have
+    slot -1."""
+    B, dev = seq_lens.shape[0], seq_lens.device
+    _need(block_table, "block_table", torch.int32, 2, dev)
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table has {block_table.shape[0]} rows for {B} requests")
+    if out is None:
+        out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B + 1, dtype=torch.int32, device=dev),
+               torch.empty(rows, dtype=torch.int64, device=dev), torch.empty(rows, dtype=torch.int64, device=dev),
+               torch.empty(2, dtype=torch.int32, device=dev))
+    new_lens, row_starts, positions, slots, counts = out
+    F = free_pages.shape[0]
+    check(lib().dsnq_extend_block_tables(
+        B, rows, page_size, _flat(seq_lens, "seq_lens", torch.int32, B, dev),
+        None if new_tokens is None else _flat(new_tokens, "new_tokens", torch.int32, B, dev),
+        _flat(free_pages, "free_pages", torch.int32, F, dev), F,
+        block_table.data_ptr(), block_table.shape[1], _row_view_ok(block_table, "block_table"),
+        _flat(new_lens, "new_lens", torch.int32, B, dev), _flat(row_starts, "row_starts", torch.int32, B + 1, dev),
+        _flat(positions, "positions", torch.int64, rows, dev), _flat(slots, "slots", torch.int64, rows, dev),
+        _flat(counts, "counts", torch.int32, 2, dev), _stream(stream, dev)), "dsnq_extend_block_tables")
+    return new_lens, row_starts, positions, slots, counts
+
+
+def head_rmsnorm_rope(x, positions, inv_freq, gamma=None, eps: float = 1e-6, normalize: bool = True, rope_offset=None,
+                      layout="interleaved", rope_scale: float = 1.0, inverse: bool = False, out=None, stream=None):
+    """RMSNorm of each head of x [M,H,D] (bf16, token and head strides free)
+    and rotation of its columns [rope_offset, rope_offset + 2 * len(inv_freq))
+    (default: the last ones) by positions [M] int64 times inv_freq float64,
+    one rounding.  `out` may be x.  Returns out [M,H,D]."""
+    M, H, D = _need(x, "x", torch.bfloat16, 3).shape
+    dev = x.device
+    if out is None:
+        out = torch.empty(M, H, D, dtype=torch.bfloat16, device=dev)
+    elif _need(out, "out", torch.bfloat16, 3, dev).shape != x.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
+    pairs = inv_freq.shape[0]
+    sx, so = _strides3(x, "x"), _strides3(out, "out")
+    check(lib().dsnq_head_rmsnorm_rope(
+        M, H, D, x.data_ptr(), sx[0], sx[1], 1 if normalize else 0,
+        None if gamma is None else _flat(gamma, "gamma", torch.bfloat16, D, dev), float(eps),
+        _flat(positions, "positions", torch.int64, M, dev), _flat(inv_freq, "inv_freq", torch.float64, pairs, dev),
+        D - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), float(rope_scale),
+        1 if inverse else 0, out.data_ptr(), so[0], so[1], _stream(stream, dev)), "dsnq_head_rmsnorm_rope")
+    return out
+
+
+def latent_cache_write(kv, pe, positions, slots, inv_freq, cache, gamma=None, eps: float = 1e-6, normalize: bool = False,
+                       rope_offset=None, layout="interleaved", rope_scale: float = 1.0, stream=None):
+    """Stores row m = [kv[m] | pe[m]] (bf16; pe [M,P] or None) at slots[m] of
+    the paged cache [pages, page_size, K+P], kv RMSNormed first when
+    `normalize`, columns [rope_offset, + 2 * len(inv_freq)) of the row
+    (default: the last ones) rotated.  Negative slots are skipped; the slots
+    of a call must be distinct.  Returns cache."""
+    M, K = _need(kv, "kv", torch.bfloat16, 2).shape
+    dev = kv.device
+    P = 0
+    if pe is not None:
+        P = _need(pe, "pe", torch.bfloat16, 2, dev).shape[1]
+        if pe.shape[0] != M:
+            raise ValueError(f"pe has {pe.shape[0]} rows, kv {M}")
+    pages, page_size, W = _need(cache, "cache", torch.bfloat16, 3, dev).shape
+    if W != K + P:
+        raise ValueError(f"cache rows have {W} columns, kv and pe {K + P}")
+    pairs = inv_freq.shape[0]
+    sc = _strides3(cache, "cache")
+    check(lib().dsnq_latent_cache_write(
+        M, K, P, kv.data_ptr(), _row_view_ok(kv, "kv"), pe.data_ptr() if P else None, _row_view_ok(pe, "pe") if P else 0,
+        1 if normalize else 0, None if gamma is None else _flat(gamma, "gamma", torch.bfloat16, K, dev), float(eps),
+        _flat(positions, "positions", torch.int64, M, dev), _flat(inv_freq, "inv_freq", torch.float64, pairs, dev),
+        W - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), float(rope_scale),
+        _flat(slots, "slots", torch.int64, M, dev), cache.data_ptr(), pages, page_size, sc[0], sc[1],
+        _stream(stream, dev)), "dsnq_latent_cache_write")
+    return cache
+
+
+def paged_latent_attention_workspace_bytes(B: int, H: int, v_dim: int, table_width: int, page_size: int) -> int:
+    """Bytes of paged_latent_attention's workspace (host-only query)."""
+    n = C.c_int64()
+    check(lib().dsnq_paged_latent_attention_workspace_bytes(B, H, v_dim, table_width, page_size, C.byref(n)),
+          "dsnq_paged_latent_attention_workspace_bytes")
+    return n.value
+
+
+def paged_latent_attention(q, cache, block_table, seq_lens, v_dim: int, scale: float, out=None, lse=None, workspace=None,
+                           stream=None):
+    """Attention of q [B,H,DK] (bf16, one new token per request) over the
+    first seq_lens[b] (int32) tokens of each request in the paged cache
+    [pages, page_size, DK], whose pages block_table [B, width] (int32) names.
+    The value of a row is its first v_dim columns.  Returns (out [B,H,v_dim]
+    bf16, lse [B,H] fp32).  The uint8 `workspace` is allocated if omitted."""
+    B, H, DK = _need(q, "q", torch.bfloat16, 3).shape
+    dev = q.device
+    pages, page_size, W = _need(cache, "cache", torch.bfloat16, 3, dev).shape
+    if W != DK:
+        raise ValueError(f"cache rows have {W} columns, q {DK}")
+    _need(block_table, "block_table", torch.int32, 2, dev)
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table has {block_table.shape[0]} rows for {B} requests")
+    width = block_table.shape[1]
+    if out is None:
+        out = torch.empty(B, H, v_dim, dtype=torch.bfloat16, device=dev)
+    elif _need(out, "out", torch.bfloat16, 3, dev).shape != (B, H, v_dim):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(B, H, v_dim)}")
+    if lse is None:
+        lse = torch.empty(B, H, dtype=torch.float32, device=dev)
+    elif _need(lse, "lse", torch.float32, 2, dev).shape != (B, H):
+        raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(B, H)}")
+    if workspace is None:
+        workspace = torch.empty(paged_latent_attention_workspace_bytes(B, H, v_dim, width, page_size), dtype=torch.uint8,
+                                device=dev)
+    elif _need(workspace, "workspace", torch.uint8, 1, dev).stride(0) != 1:
+        raise ValueError("workspace must be contiguous")
+    sq, sc, so = _strides3(q, "q"), _strides3(cache, "cache"), _strides3(out, "out")
+    check(lib().dsnq_paged_latent_attention(
+        B, H, DK, v_dim, q.data_ptr(), sq[0], sq[1], cache.data_ptr(), pages, page_size, sc[0], sc[1],
+        block_table.data_ptr(), width, _row_view_ok(block_table, "block_table"), _flat(seq_lens, "seq_lens", torch.int32, B, dev),
+        float(scale), out.data_ptr(), so[0], so[1], lse.data_ptr(), _row_view_ok(lse, "lse"), workspace.data_ptr(),
+        workspace.numel(), _stream(stream, dev)), "dsnq_paged_latent_attention")
+    return out, lse
 
 
 def debug_status(stream=None) -> int:

@@ -62,6 +62,17 @@ SIGNATURES = {
               vp, vp, vp]),
     "dsnq_gemm_plan": (i32, [i64, i64, C.POINTER(C.c_int32), pi64]),
     "dsnq_bf16a_workspace_bytes": (i32, [i64, i64, pi64, pi64]),
+    "dsnq_extend_block_tables": (
+        i32, [i64, i64, i64, vp, vp, vp, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp]),
+    "dsnq_head_rmsnorm_rope": (
+        i32, [i64, i64, i64, vp, i64, i64, i32, vp, f32, vp, vp, i64, i64, i32, f32, i32, vp, i64, i64, vp]),
+    "dsnq_latent_cache_write": (
+        i32, [i64, i64, i64, vp, i64, vp, i64, i32, vp, f32, vp, vp, i64, i64, i32, f32,
+              vp, vp, i64, i64, i64, i64, vp]),
+    "dsnq_paged_latent_attention_workspace_bytes": (i32, [i64, i64, i64, i64, i64, pi64]),
+    "dsnq_paged_latent_attention": (
+        i32, [i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, i64, i64, vp, i64, i64, vp, f32,
+              vp, i64, i64, vp, i64, vp, i64, vp]),
     "dsnq_debug_status": (i32, [vp]),
     "dsnq_debug_build": (i32, []),
     "dsnq_debug_set": (None, [u32, u64]),

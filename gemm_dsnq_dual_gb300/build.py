@@ -25,7 +25,7 @@ LIB_NAME = "libdsnq.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libdsnq_debug.so")   # device index checks (DSNQ_DEBUG)
 
-SOURCES = ["norm_quant.cu", "gemm_fp8.cu", "dsnq_api.cu", "static_scratch.cu"]
+SOURCES = ["norm_quant.cu", "gemm_fp8.cu", "dsnq_api.cu", "static_scratch.cu", "rope_cache.cu", "latent_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

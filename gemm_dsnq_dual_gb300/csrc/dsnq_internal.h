@@ -23,6 +23,10 @@ uint64_t debug_wait_timeout_ns();
 
 // The status word of the norm+quant unit, read and cleared (norm_quant.cu).
 bool take_norm_quant_debug_word(cudaStream_t s, unsigned int* v);
+// The status words of the units around the pre-projection, read and cleared
+// (rope_cache.cu, latent_attention.cu).
+bool take_rope_cache_words(cudaStream_t s, unsigned int* v);
+bool take_attention_words(cudaStream_t s, unsigned int* v);
 
 inline bool aligned(const void* p, uintptr_t a) {
     return (reinterpret_cast<uintptr_t>(p) % a) == 0;

@@ -1911,7 +1911,7 @@ extern "C" dsnq_status dsnq_fused_norm_quant_gemm_dual(
 
 extern "C" dsnq_status dsnq_debug_status(void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    unsigned int v = 0, w = 0, n = 0;
+    unsigned int v = 0, w = 0, n = 0, r = 0, l = 0;
     if (cudaMemcpyFromSymbolAsync(&v, g_status, sizeof(v), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess) {
         cudaGetLastError();
@@ -1923,9 +1923,11 @@ extern "C" dsnq_status dsnq_debug_status(void* stream) {
         cudaGetLastError();
         return DSNQ_ERR_CUDA;
     }
-    // The index-check words of this unit and of the norm+quant unit.
-    if (!take_debug_word(s, &w) || !take_norm_quant_debug_word(s, &n)) return DSNQ_ERR_CUDA;
-    v |= w | n;
+    // The index-check words of this unit and the words of the other units.
+    if (!take_debug_word(s, &w) || !take_norm_quant_debug_word(s, &n) || !take_rope_cache_words(s, &r) ||
+        !take_attention_words(s, &l))
+        return DSNQ_ERR_CUDA;
+    v |= w | n | r | l;
     if (v & kStatusTimeout) return DSNQ_ERR_TIMEOUT;
     return (v & kStatusBounds) ? DSNQ_ERR_BOUNDS : DSNQ_OK;
 }

@@ -1,0 +1,662 @@
+// The steps between the pre-projection and the attention of a decode step:
+// block tables and slots from request lengths, per-head RMSNorm with rotary
+// positions, and the write of normalized, rotated latent rows into the paged
+// cache.
+//
+// Rotary positions: the pair (a, b) of frequency i at position p becomes
+//   (a cos t - b sin t, b cos t + a sin t) * rope_scale,   t = p * inv_freq[i].
+// At position 10^6 an fp32 product p * inv_freq is off by up to 0.06 rad, so
+// the angle is formed in fp64 as a number of turns, its whole turns dropped,
+// and only the fraction (|.| <= 1/2) goes to fp32 (sincospif).  The table of a
+// token's angles is formed once per CTA (or warp) in shared memory and used
+// for all its heads.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "debug_check.cuh"
+#include "dsnq_internal.h"
+#include "group_quant.cuh"
+#include "tensor_host.h"
+
+namespace dsnq {
+namespace {
+
+__device__ unsigned int g_rope_status;   // kStatusBounds: a slot outside the cache was given
+
+constexpr int kChunk = 8;                // bf16 per 16-byte chunk
+constexpr int kMaxRope = 256;            // rotated columns
+constexpr int kMaxWidth = 1024;          // columns of a head or cache row
+
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+    uint4 v;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[i].x, f[i].y);
+    return v;
+}
+
+struct Rope {
+    const int64_t* positions;   // [M]
+    const double* inv_freq;     // [dim / 2]
+    int off, dim;               // rotated columns [off, off + dim)
+    int half;                   // pairs (i, i + dim/2) instead of (2i, 2i + 1)
+    float scale;                // factor of cos and sin
+    float sign;                 // -1 rotates back
+};
+
+// (cos, sin) * scale of frequency i at position pos.
+__device__ __forceinline__ float2 rope_angle(const Rope& r, int64_t pos, int i) {
+    const double turns = static_cast<double>(pos) * r.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+    const float frac = static_cast<float>(turns - rint(turns));
+    float s, c;
+    sincospif(2.0f * frac, &s, &c);
+    return make_float2(c * r.scale, s * (r.scale * r.sign));
+}
+
+// The values of a chunk whose first column is `q` of the rotated range, given
+// its own values x and, for the half layout, its partner chunk's values y.
+__device__ __forceinline__ void rotate_chunk(const Rope& r, const float2* cs, int q, float2 (&x)[4],
+                                             const float2 (&y)[4]) {
+    if (!r.half) {
+        const float2* t = cs + (q >> 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = x[i], w = t[i];
+            x[i] = make_float2(a.x * w.x - a.y * w.y, a.y * w.x + a.x * w.y);
+        }
+        return;
+    }
+    const int hd = r.dim >> 1;
+    const bool low = q < hd;                       // first members of the pairs
+    const float2* t = cs + (low ? q : q - hd);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 w0 = t[2 * i], w1 = t[2 * i + 1];
+        const float s0 = low ? -w0.y : w0.y, s1 = low ? -w1.y : w1.y;
+        x[i] = make_float2(x[i].x * w0.x + y[i].x * s0, x[i].y * w1.x + y[i].y * s1);
+    }
+}
+
+__device__ __forceinline__ float sum_squares(const float2 (&x)[4]) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fma2(x[i], x[i], s);
+    return s.x + s.y;
+}
+
+__device__ __forceinline__ void scale_by(float2 (&x)[4], float r, const uint4& gamma_raw, bool weighted) {
+    const float2 r2 = make_float2(r, r);
+    float2 g[4];
+    if (weighted) unpack8(gamma_raw, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[i] = mul2(x[i], r2);
+        if (weighted) x[i] = mul2(x[i], g[i]);
+    }
+}
+
+// --------------------------------------------------------- head norm + rotary
+struct HeadArgs {
+    const __nv_bfloat16* x;
+    __nv_bfloat16* out;
+    const __nv_bfloat16* gamma;          // NULL: no weight
+    int64_t ldx_tok, ldx_head, ldo_tok, ldo_head;
+    int64_t M;
+    int H, D;
+    int head_blocks, heads_per_block;    // CTAs per token, heads of each
+    int norm;
+    float d_f, eps;
+    Rope rope;
+    uint32_t inject;
+};
+
+constexpr int kHeadWarps = 8;
+
+// LPR lanes hold one head's row (CPL chunks of 16 bytes each, chunk
+// lane + j * LPR), so a warp works on 32 / LPR heads at once.  A CTA takes
+// heads of one token: its first dim/2 threads form the token's angles while
+// the first rows are on their way.
+template <int LPR, int CPL>
+__global__ void __launch_bounds__(kHeadWarps * 32)
+head_norm_rope_kernel(const HeadArgs a) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    bounds_self_test(a.inject);
+    constexpr int kRows = 32 / LPR;      // heads per warp and step
+    __shared__ float2 cs[kMaxRope / 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane % LPR, sub = lane / LPR;
+    const int64_t m = blockIdx.x / a.head_blocks;
+    const int h0 = static_cast<int>(blockIdx.x - m * a.head_blocks) * a.heads_per_block;
+    const int h1 = min(h0 + a.heads_per_block, a.H);
+    const int chunks = a.D / kChunk;
+    const int c_lo = a.rope.off / kChunk, c_n = a.rope.dim / kChunk;
+
+    bool live[CPL], rot[CPL];
+    int col[CPL], pcol[CPL];
+    uint4 graw[CPL], pgraw[CPL];
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) {
+        const int c = l + j * LPR;
+        live[j] = c < chunks;
+        rot[j] = live[j] && c >= c_lo && c < c_lo + c_n;
+        col[j] = c * kChunk;
+        const int q = c - c_lo;
+        pcol[j] = (rot[j] && a.rope.half) ? (q < c_n / 2 ? c + c_n / 2 : c - c_n / 2) * kChunk : col[j];
+        graw[j] = pgraw[j] = make_uint4(0, 0, 0, 0);
+        if (a.gamma && live[j]) {
+            graw[j] = *reinterpret_cast<const uint4*>(a.gamma + col[j]);
+            pgraw[j] = *reinterpret_cast<const uint4*>(a.gamma + pcol[j]);
+        }
+    }
+
+    auto load = [&](int h, uint4 (&raw)[CPL], uint4 (&praw)[CPL]) {
+        const __nv_bfloat16* row = a.x + m * a.ldx_tok + h * a.ldx_head;
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            raw[j] = praw[j] = make_uint4(0, 0, 0, 0);
+            if (h < h1 && live[j] && bounds_ok(m < a.M && h < a.H && col[j] + kChunk <= a.D && pcol[j] + kChunk <= a.D)) {
+                raw[j] = *reinterpret_cast<const uint4*>(row + col[j]);
+                if (rot[j] && a.rope.half) praw[j] = *reinterpret_cast<const uint4*>(row + pcol[j]);
+            }
+        }
+    };
+
+    constexpr int kStep = kHeadWarps * kRows;
+    int h = h0 + warp * kRows + sub;
+    uint4 raw[CPL], praw[CPL];
+    load(h, raw, praw);
+    if (threadIdx.x < static_cast<unsigned>(a.rope.dim / 2))
+        cs[threadIdx.x] = rope_angle(a.rope, a.rope.positions[m], threadIdx.x);
+    __syncthreads();
+
+    for (int base = h0 + warp * kRows; base < h1; base += kStep, h += kStep) {
+        float2 x[CPL][4];
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) unpack8(raw[j], x[j]);
+        float2 y[CPL][4];
+        if (a.rope.half) {
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) unpack8(praw[j], y[j]);
+        }
+        load(h + kStep, raw, praw);      // the next row while this one is worked on
+        if (a.norm) {
+            float ssq = 0.f;
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) ssq += sum_squares(x[j]);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, o);
+            const float r = 1.0f / sqrtf(ssq / a.d_f + a.eps);
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                scale_by(x[j], r, graw[j], a.gamma != nullptr);
+                if (a.rope.half) scale_by(y[j], r, pgraw[j], a.gamma != nullptr);
+            }
+        }
+        // In place, a lane's partner chunk is another lane's output: every
+        // lane has its rows in registers before any lane stores.
+        __syncwarp();
+        if (h < h1) {
+            __nv_bfloat16* row = a.out + m * a.ldo_tok + h * a.ldo_head;
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                if (!live[j] || !bounds_ok(m < a.M && h < a.H && col[j] + kChunk <= a.D)) continue;
+                if (rot[j]) rotate_chunk(a.rope, cs, col[j] - a.rope.off, x[j], y[j]);
+                *reinterpret_cast<uint4*>(row + col[j]) = pack8(x[j]);
+            }
+        }
+    }
+}
+
+template <int LPR, int CPL>
+dsnq_status launch_heads(HeadArgs& a, int sms, cudaStream_t s) {
+    // Heads per CTA: one step of its warps when tokens are few (a decode row
+    // is bound by latency), the whole token once the tokens alone fill the GPU.
+    const int step = kHeadWarps * (32 / LPR);
+    int64_t blocks = (a.H + step - 1) / step;
+    const int64_t want = (8LL * sms + a.M - 1) / a.M;      // CTAs per token that give every SM eight
+    if (blocks > want) blocks = want;
+    const int64_t steps = ((a.H + step - 1) / step + blocks - 1) / blocks;
+    a.heads_per_block = static_cast<int>(steps * step);
+    a.head_blocks = (a.H + a.heads_per_block - 1) / a.heads_per_block;
+    const int64_t grid = a.M * a.head_blocks;
+    if (grid > 0x7fffffffLL) return DSNQ_ERR_UNSUPPORTED;
+    return launch_result(launch_kernel(head_norm_rope_kernel<LPR, CPL>, dim3(static_cast<unsigned>(grid)),
+                                       dim3(kHeadWarps * 32), 0, s, a));
+}
+
+// --------------------------------------------------------- latent cache write
+struct WriteArgs {
+    const __nv_bfloat16* kv;
+    const __nv_bfloat16* pe;
+    const __nv_bfloat16* gamma;
+    int64_t ldkv, ldpe;
+    int64_t M;
+    int K, W;                            // latent columns, row columns (latent + position part)
+    const int64_t* slots;
+    __nv_bfloat16* cache;
+    int64_t ld_page, ld_row, num_slots;
+    int page_size;
+    int norm;
+    float k_f, eps;
+    Rope rope;
+    uint32_t inject;
+};
+
+constexpr int kWriteWarps = 4;
+
+// One warp per row; lane l holds chunks l, l + 32, ... of the concatenated row.
+template <int CPL>
+__global__ void __launch_bounds__(kWriteWarps * 32)
+latent_cache_write_kernel(const WriteArgs a) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    bounds_self_test(a.inject);
+    __shared__ float2 cs_all[kWriteWarps][kMaxRope / 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float2* cs = cs_all[warp];
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * kWriteWarps + warp;
+    if (m >= a.M) return;
+    const int64_t slot = a.slots[m];
+    if (slot < 0) return;                // a padded row
+    if (slot >= a.num_slots) {
+        if (lane == 0) atomicOr(&g_rope_status, kStatusBounds);
+        return;
+    }
+    const int c_lo = a.rope.off / kChunk, c_n = a.rope.dim / kChunk;
+    bool live[CPL], rot[CPL];
+    float2 x[CPL][4], y[CPL][4];
+    uint4 graw[CPL], pgraw[CPL];
+    int pcol[CPL];
+    auto at = [&](int col) {
+        return col < a.K ? a.kv + m * a.ldkv + col : a.pe + m * a.ldpe + (col - a.K);
+    };
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) {
+        const int c = lane + j * 32, col = c * kChunk;
+        live[j] = col < a.W;
+        rot[j] = live[j] && c >= c_lo && c < c_lo + c_n;
+        const int q = c - c_lo;
+        pcol[j] = (rot[j] && a.rope.half) ? (q < c_n / 2 ? c + c_n / 2 : c - c_n / 2) * kChunk : col;
+        uint4 raw = make_uint4(0, 0, 0, 0), praw = raw;
+        graw[j] = pgraw[j] = raw;
+        if (live[j] && bounds_ok(col + kChunk <= a.W && pcol[j] + kChunk <= a.W)) {
+            raw = *reinterpret_cast<const uint4*>(at(col));
+            if (rot[j] && a.rope.half) praw = *reinterpret_cast<const uint4*>(at(pcol[j]));
+            if (a.gamma && col < a.K) graw[j] = *reinterpret_cast<const uint4*>(a.gamma + col);
+            if (a.gamma && pcol[j] < a.K) pgraw[j] = *reinterpret_cast<const uint4*>(a.gamma + pcol[j]);
+        }
+        unpack8(raw, x[j]);
+        unpack8(praw, y[j]);
+    }
+    for (int i = lane; i < a.rope.dim / 2; i += 32) cs[i] = rope_angle(a.rope, a.rope.positions[m], i);
+    __syncwarp();
+    if (a.norm) {
+        float ssq = 0.f;
+#pragma unroll
+        for (int j = 0; j < CPL; ++j)
+            if ((lane + j * 32) * kChunk < a.K) ssq += sum_squares(x[j]);
+        const float r = 1.0f / sqrtf(warp_sum(ssq) / a.k_f + a.eps);
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            if ((lane + j * 32) * kChunk < a.K) scale_by(x[j], r, graw[j], a.gamma != nullptr);
+            if (pcol[j] < a.K) scale_by(y[j], r, pgraw[j], a.gamma != nullptr);
+        }
+    }
+    const int64_t page = slot / a.page_size;
+    __nv_bfloat16* row = a.cache + page * a.ld_page + (slot - page * a.page_size) * a.ld_row;
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) {
+        const int col = (lane + j * 32) * kChunk;
+        if (!live[j] || !bounds_ok(col + kChunk <= a.W)) continue;
+        if (rot[j]) rotate_chunk(a.rope, cs, col - a.rope.off, x[j], y[j]);
+        *reinterpret_cast<uint4*>(row + col) = pack8(x[j]);
+    }
+}
+
+// ------------------------------------------------------- block tables, slots
+struct ExtendArgs {
+    int B, rows, page_size, width;       // requests, token rows, tokens per page, table columns
+    int F;                               // free pages listed
+    const int32_t* seq_lens;
+    const int32_t* new_tokens;           // NULL: one each
+    const int32_t* free_pages;
+    int32_t* table;
+    int64_t ld_table;
+    int32_t* new_lens;
+    int32_t* row_starts;
+    int64_t* positions;
+    int64_t* slots;
+    int32_t* counts;
+    uint32_t inject;
+};
+
+constexpr int kExtendThreads = 512;
+
+// Exclusive sum of one value per thread over the CTA; *total gets the sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t w = lane < kExtendThreads / 32 ? warp_sums[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += u;
+        }
+        if (lane < kExtendThreads / 32) warp_sums[lane] = w;
+    }
+    __syncthreads();
+    const int64_t before = warp ? warp_sums[warp - 1] : 0;
+    *total = warp_sums[kExtendThreads / 32 - 1];
+    __syncthreads();
+    return before + inc - v;
+}
+
+struct Request {
+    int old_len, want, held;             // tokens so far, tokens asked for, pages held
+};
+
+__device__ __forceinline__ Request read_request(const ExtendArgs& a, int b) {
+    Request r;
+    const int64_t cap = static_cast<int64_t>(a.width) * a.page_size;
+    const int32_t len = a.seq_lens[b];
+    r.old_len = static_cast<int>(len < 0 ? 0 : (len > cap ? cap : len));
+    const int32_t n = a.new_tokens ? a.new_tokens[b] : 1;
+    r.want = n < 0 ? 0 : n;
+    r.held = static_cast<int>((static_cast<int64_t>(r.old_len) + a.page_size - 1) / a.page_size);
+    return r;
+}
+
+// Pages request r needs for the tokens that have a row (rows - start) and a
+// place in the table; *fit gets their number.
+__device__ __forceinline__ int pages_needed(const ExtendArgs& a, const Request& r, int64_t start, int* fit) {
+    const int64_t cap = static_cast<int64_t>(a.width) * a.page_size;
+    int64_t f = r.want;
+    const int64_t room = a.rows > start ? a.rows - start : 0;
+    if (f > room) f = room;
+    if (f > cap - r.old_len) f = cap - r.old_len;
+    *fit = static_cast<int>(f);
+    return static_cast<int>((r.old_len + f + a.page_size - 1) / a.page_size) - r.held;
+}
+
+// Every CTA forms the sums over all requests in shared memory (they are few
+// and in L2; a second launch would cost more), then takes its strip of the
+// requests (table, lengths) and of the token rows (positions, slots).  A
+// row's page is read from the entries the request already held, or straight
+// from the free list, never from an entry that another CTA writes.
+__global__ void __launch_bounds__(kExtendThreads)
+extend_tables_kernel(const ExtendArgs a) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    bounds_self_test(a.inject);
+    extern __shared__ int32_t sums[];    // [B] first row (at most rows), [B] first free page (at most F)
+    int32_t* first_row = sums;
+    int32_t* first_page = sums + a.B;
+    __shared__ int64_t warp_sums[kExtendThreads / 32];
+    const int t = threadIdx.x, lane = t & 31;
+    const int per = (a.B + kExtendThreads - 1) / kExtendThreads;
+    const int b0 = min(t * per, a.B), b1 = min(b0 + per, a.B);
+
+    int64_t n = 0, total_rows, total_pages;
+    for (int b = b0; b < b1; ++b) n += read_request(a, b).want;
+    const int64_t start0 = block_scan(n, warp_sums, &total_rows);
+    int64_t start = start0, pages = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = read_request(a, b);
+        int fit;
+        first_row[b] = static_cast<int32_t>(start < a.rows ? start : a.rows);
+        pages += pages_needed(a, r, start, &fit);
+        start += r.want;
+    }
+    int64_t page = block_scan(pages, warp_sums, &total_pages);
+    start = start0;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = read_request(a, b);
+        int fit;
+        first_page[b] = static_cast<int32_t>(page < a.F ? page : a.F);
+        page += pages_needed(a, r, start, &fit);
+        start += r.want;
+    }
+    __syncthreads();
+    const int live_rows = static_cast<int>(total_rows < a.rows ? total_rows : a.rows);
+
+    if (blockIdx.x == 0 && t == 0) {
+        a.row_starts[a.B] = live_rows;
+        a.counts[0] = static_cast<int32_t>(total_pages < a.F ? total_pages : a.F);
+        a.counts[1] = static_cast<int32_t>(total_pages < 0x7fffffff ? total_pages : 0x7fffffff);
+    }
+
+    // Requests: one per thread; a request's new pages are stored by its whole
+    // warp when they are many (a prompt), by its thread otherwise.
+    for (int bw = (blockIdx.x * kExtendThreads + (t & ~31)); bw < a.B; bw += gridDim.x * kExtendThreads) {
+        const int b = bw + lane;
+        int got = 0, held = 0, from = 0;
+        if (b < a.B) {
+            const Request r = read_request(a, b);
+            int fit;
+            const int need = pages_needed(a, r, first_row[b], &fit);
+            from = first_page[b];
+            got = min(need, a.F - from);
+            held = r.held;
+            const int64_t end = static_cast<int64_t>(r.old_len) + fit;
+            const int64_t backed = static_cast<int64_t>(held + got) * a.page_size;
+            a.new_lens[b] = static_cast<int32_t>(end < backed ? end : backed);
+            a.row_starts[b] = first_row[b];
+            if (got <= 2)
+                for (int k = 0; k < got; ++k)
+                    if (bounds_ok(held + k < a.width && from + k < a.F))
+                        a.table[b * a.ld_table + held + k] = a.free_pages[from + k];
+        }
+        unsigned many = __ballot_sync(0xffffffffu, got > 2);
+        while (many) {
+            const int src = __ffs(many) - 1;
+            many &= many - 1;
+            const int g = __shfl_sync(0xffffffffu, got, src), hd = __shfl_sync(0xffffffffu, held, src);
+            const int f = __shfl_sync(0xffffffffu, from, src);
+            for (int k = lane; k < g; k += 32)
+                if (bounds_ok(hd + k < a.width && f + k < a.F))
+                    a.table[(bw + src) * a.ld_table + hd + k] = a.free_pages[f + k];
+        }
+    }
+
+    // Token rows.
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kExtendThreads + t; r0 < a.rows;
+         r0 += static_cast<int64_t>(gridDim.x) * kExtendThreads) {
+        const int row = static_cast<int>(r0);
+        int64_t pos = 0, slot = -1;
+        if (row < live_rows) {
+            // The last request whose first row is at most `row` (requests
+            // without tokens share their successor's first row and lose).
+            int lo = 0, hi = a.B;        // first_row[lo] <= row, first_row[hi] > row
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first_row[mid] <= row) lo = mid;
+                else hi = mid;
+            }
+            const Request r = read_request(a, lo);
+            int fit;
+            const int need = pages_needed(a, r, first_row[lo], &fit);
+            const int from = first_page[lo];
+            const int got = min(need, a.F - from);
+            const int j = row - first_row[lo];
+            pos = static_cast<int64_t>(r.old_len) + j;
+            const int64_t p = pos / a.page_size;
+            if (j < fit && p < r.held + got) {
+                const int k = static_cast<int>(p) - r.held;
+                int32_t id = -1;
+                if (bounds_ok(p < a.width && from + k < a.F))
+                    id = k < 0 ? a.table[lo * a.ld_table + p] : a.free_pages[from + k];
+                if (id >= 0) slot = static_cast<int64_t>(id) * a.page_size + (pos - p * a.page_size);
+            }
+        }
+        a.positions[row] = pos;
+        a.slots[row] = slot;
+    }
+}
+
+dsnq_status check_rope(int64_t width, int64_t off, int64_t dim, int32_t layout, float scale) {
+    if (dim < 0 || off < 0 || dim > width || off > width - dim) return DSNQ_ERR_INVALID_ARG;
+    if (layout != DSNQ_ROPE_INTERLEAVED && layout != DSNQ_ROPE_HALF) return DSNQ_ERR_INVALID_ARG;
+    if (!(scale > -3.0e38f && scale < 3.0e38f)) return DSNQ_ERR_INVALID_ARG;      // also rejects NaN
+    if (dim % 16 || off % kChunk || dim > kMaxRope) return DSNQ_ERR_UNSUPPORTED;
+    return DSNQ_OK;
+}
+
+}  // namespace
+
+bool take_rope_cache_words(cudaStream_t s, unsigned int* v) {
+    unsigned int w = 0, st = 0;
+    const unsigned int zero = 0;
+    if (!take_debug_word(s, &w)) return false;
+    if (cudaMemcpyFromSymbolAsync(&st, g_rope_status, sizeof(st), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_rope_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    *v = w | st;
+    return true;
+}
+
+}  // namespace dsnq
+
+using namespace dsnq;
+
+extern "C" dsnq_status dsnq_head_rmsnorm_rope(
+    int64_t M, int64_t H, int64_t D, const void* x, int64_t ldx_tok, int64_t ldx_head, int32_t normalize,
+    const void* gamma, float eps, const int64_t* positions, const double* inv_freq, int64_t rope_offset,
+    int64_t rope_dim, dsnq_rope_layout layout, float rope_scale, int32_t inverse, void* out, int64_t ldo_tok,
+    int64_t ldo_head, void* stream) {
+    if (M < 0 || H <= 0 || D <= 0) return DSNQ_ERR_INVALID_ARG;
+    if (normalize && (!(eps >= 0.f) || eps > 3.0e38f)) return DSNQ_ERR_INVALID_ARG;   // also rejects NaN
+    if (!normalize && gamma) return DSNQ_ERR_INVALID_ARG;
+    if (D % kChunk || D > kMaxWidth || H > 65535 || M > 0x7fffffffLL) return DSNQ_ERR_UNSUPPORTED;
+    dsnq_status st = check_rope(D, rope_offset, rope_dim, layout, rope_scale);
+    if (st != DSNQ_OK) return st;
+    if (M == 0) return DSNQ_OK;
+    if (!x || !out || (rope_dim && (!positions || !inv_freq))) return DSNQ_ERR_INVALID_ARG;
+    if ((H > 1 && (ldx_head < D || ldo_head < D)) || (M > 1 && (ldx_tok < D || ldo_tok < D))) return DSNQ_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(out, 16) || ldx_tok % kChunk || ldx_head % kChunk || ldo_tok % kChunk ||
+        ldo_head % kChunk || (gamma && !aligned(gamma, 16)) || !aligned(positions, 8) || !aligned(inv_freq, 8))
+        return DSNQ_ERR_MISALIGNED;
+    const int sms = device_sm_count();
+    if (sms <= 0) {
+        cudaGetLastError();
+        return DSNQ_ERR_CUDA;
+    }
+    HeadArgs a{};
+    a.x = static_cast<const __nv_bfloat16*>(x);
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.gamma = static_cast<const __nv_bfloat16*>(gamma);
+    a.ldx_tok = ldx_tok; a.ldx_head = ldx_head; a.ldo_tok = ldo_tok; a.ldo_head = ldo_head;
+    a.M = M; a.H = static_cast<int>(H); a.D = static_cast<int>(D);
+    a.norm = normalize ? 1 : 0;
+    a.d_f = static_cast<float>(D); a.eps = eps;
+    a.rope = Rope{positions, inv_freq, static_cast<int>(rope_offset), static_cast<int>(rope_dim),
+                  layout == DSNQ_ROPE_HALF, rope_scale, inverse ? -1.0f : 1.0f};
+    a.inject = debug_inject_flags();
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (D <= 64) return launch_heads<8, 1>(a, sms, s);
+    if (D <= 128) return launch_heads<16, 1>(a, sms, s);
+    if (D <= 256) return launch_heads<32, 1>(a, sms, s);
+    if (D <= 512) return launch_heads<32, 2>(a, sms, s);
+    return launch_heads<32, 4>(a, sms, s);
+}
+
+extern "C" dsnq_status dsnq_latent_cache_write(
+    int64_t M, int64_t K, int64_t P, const void* kv, int64_t ldkv, const void* pe, int64_t ldpe, int32_t normalize,
+    const void* gamma, float eps, const int64_t* positions, const double* inv_freq, int64_t rope_offset,
+    int64_t rope_dim, dsnq_rope_layout layout, float rope_scale, const int64_t* slots, void* cache, int64_t num_pages,
+    int64_t page_size, int64_t ld_page, int64_t ld_row, void* stream) {
+    if (M < 0 || K <= 0 || P < 0 || num_pages < 0 || page_size <= 0) return DSNQ_ERR_INVALID_ARG;
+    if (normalize && (!(eps >= 0.f) || eps > 3.0e38f)) return DSNQ_ERR_INVALID_ARG;   // also rejects NaN
+    if (!normalize && gamma) return DSNQ_ERR_INVALID_ARG;
+    if (K % kChunk || P % kChunk || K > kMaxWidth || P > kMaxWidth || K + P > kMaxWidth || M > 0x7fffffffLL ||
+        page_size > (1 << 20) || num_pages > 0x7fffffffLL || ld_row > (1LL << 40))
+        return DSNQ_ERR_UNSUPPORTED;
+    const int64_t W = K + P;
+    dsnq_status st = check_rope(W, rope_offset, rope_dim, layout, rope_scale);
+    if (st != DSNQ_OK) return st;
+    if (M == 0) return DSNQ_OK;
+    if (!kv || (P && !pe) || !slots || (num_pages && !cache) || (rope_dim && (!positions || !inv_freq)))
+        return DSNQ_ERR_INVALID_ARG;
+    if ((M > 1 && (ldkv < K || (P && ldpe < P))) || ld_row < W || ld_page < (page_size - 1) * ld_row + W)
+        return DSNQ_ERR_INVALID_ARG;
+    if (!aligned(kv, 16) || ldkv % kChunk || (P && (!aligned(pe, 16) || ldpe % kChunk)) || !aligned(cache, 16) ||
+        ld_page % kChunk || ld_row % kChunk || (gamma && !aligned(gamma, 16)) || !aligned(slots, 8) ||
+        !aligned(positions, 8) || !aligned(inv_freq, 8))
+        return DSNQ_ERR_MISALIGNED;
+    WriteArgs a{};
+    a.kv = static_cast<const __nv_bfloat16*>(kv);
+    a.pe = static_cast<const __nv_bfloat16*>(pe);
+    a.gamma = static_cast<const __nv_bfloat16*>(gamma);
+    a.ldkv = ldkv; a.ldpe = ldpe;
+    a.M = M; a.K = static_cast<int>(K); a.W = static_cast<int>(W);
+    a.slots = slots;
+    a.cache = static_cast<__nv_bfloat16*>(cache);
+    a.ld_page = ld_page; a.ld_row = ld_row;
+    a.num_slots = num_pages * page_size;
+    a.page_size = static_cast<int>(page_size);
+    a.norm = normalize ? 1 : 0;
+    a.k_f = static_cast<float>(K); a.eps = eps;
+    a.rope = Rope{positions, inv_freq, static_cast<int>(rope_offset), static_cast<int>(rope_dim),
+                  layout == DSNQ_ROPE_HALF, rope_scale, 1.0f};
+    a.inject = debug_inject_flags();
+    const dim3 grid(static_cast<unsigned>((M + kWriteWarps - 1) / kWriteWarps)), block(kWriteWarps * 32);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (W <= 256) return launch_result(launch_kernel(latent_cache_write_kernel<1>, grid, block, 0, s, a));
+    if (W <= 512) return launch_result(launch_kernel(latent_cache_write_kernel<2>, grid, block, 0, s, a));
+    if (W <= 768) return launch_result(launch_kernel(latent_cache_write_kernel<3>, grid, block, 0, s, a));
+    return launch_result(launch_kernel(latent_cache_write_kernel<4>, grid, block, 0, s, a));
+}
+
+extern "C" dsnq_status dsnq_extend_block_tables(
+    int64_t B, int64_t rows, int64_t page_size, const int32_t* seq_lens, const int32_t* new_tokens,
+    const int32_t* free_pages, int64_t num_free, int32_t* block_table, int64_t table_width, int64_t ld_table,
+    int32_t* new_lens, int32_t* row_starts, int64_t* positions, int64_t* slots, int32_t* counts, void* stream) {
+    if (B < 0 || rows < 0 || page_size <= 0 || num_free < 0 || table_width < 0) return DSNQ_ERR_INVALID_ARG;
+    if (B > DSNQ_MAX_REQUESTS || rows > 0x7fffffffLL || num_free > 0x7fffffffLL || page_size > (1 << 20) ||
+        table_width > 0x7fffffffLL || table_width * page_size > 0x7fffffffLL)
+        return DSNQ_ERR_UNSUPPORTED;
+    if (!row_starts || !counts || (B && (!seq_lens || !new_lens)) || (B && table_width && !block_table) ||
+        (num_free && !free_pages) || (rows && (!positions || !slots)))
+        return DSNQ_ERR_INVALID_ARG;
+    if (B > 1 && ld_table < table_width) return DSNQ_ERR_INVALID_ARG;
+    // Every CTA reads the lengths, so no output may take their place.
+    if (B && (new_lens == seq_lens || new_lens == new_tokens || row_starts == seq_lens || row_starts == new_tokens))
+        return DSNQ_ERR_INVALID_ARG;
+    if (!aligned(seq_lens, 4) || !aligned(new_tokens, 4) || !aligned(free_pages, 4) || !aligned(block_table, 4) ||
+        !aligned(new_lens, 4) || !aligned(row_starts, 4) || !aligned(positions, 8) || !aligned(slots, 8) ||
+        !aligned(counts, 4))
+        return DSNQ_ERR_MISALIGNED;
+    ExtendArgs a{};
+    a.B = static_cast<int>(B); a.rows = static_cast<int>(rows);
+    a.page_size = static_cast<int>(page_size); a.width = static_cast<int>(table_width);
+    a.F = static_cast<int>(num_free);
+    a.seq_lens = seq_lens; a.new_tokens = new_tokens; a.free_pages = free_pages;
+    a.table = block_table; a.ld_table = ld_table;
+    a.new_lens = new_lens; a.row_starts = row_starts; a.positions = positions; a.slots = slots; a.counts = counts;
+    a.inject = debug_inject_flags();
+    const int sms = device_sm_count();
+    if (sms <= 0) {
+        cudaGetLastError();
+        return DSNQ_ERR_CUDA;
+    }
+    int64_t grid = ((rows > B ? rows : B) + kExtendThreads - 1) / kExtendThreads;
+    grid = grid < 1 ? 1 : (grid > sms ? sms : grid);
+    const size_t smem = static_cast<size_t>(2 * B) * sizeof(int32_t);
+    static_assert(2 * DSNQ_MAX_REQUESTS * sizeof(int32_t) <= 128 * 1024, "two words per request in shared memory");
+    if (smem > 48 * 1024 && !set_smem_attr(reinterpret_cast<const void*>(extend_tables_kernel), smem)) return DSNQ_ERR_CUDA;
+    return launch_result(launch_kernel(extend_tables_kernel, dim3(static_cast<unsigned>(grid)), dim3(kExtendThreads), smem,
+                                       static_cast<cudaStream_t>(stream), a));
+}

@@ -43,16 +43,20 @@ inline bool set_smem_attr(const void* kern, size_t smem) {
         cudaGetLastError();
         return false;
     }
-    std::lock_guard<std::mutex> lock(mu);
-    for (const auto& d : done)
-        if (std::get<0>(d) == kern && std::get<1>(d) == dev && std::get<2>(d) >= smem) return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-        cudaSuccess) {
-        cudaGetLastError();
+    try {
+        std::lock_guard<std::mutex> lock(mu);
+        for (const auto& d : done)
+            if (std::get<0>(d) == kern && std::get<1>(d) == dev && std::get<2>(d) >= smem) return true;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        done.emplace_back(kern, dev, smem);
+        return true;
+    } catch (...) {                                        // no exception leaves a C entry point
         return false;
     }
-    done.emplace_back(kern, dev, smem);
-    return true;
 }
 
 }  // namespace dsnq

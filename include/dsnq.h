@@ -378,11 +378,177 @@ DSNQ_API dsnq_status dsnq_fused_norm_quant_gemm_dual(
     void* stream);
 
 /*
- * Device status words.  Kernels with bounded waits (the GEMM's mbarrier
- * waits) record a timeout there instead of hanging.  In the debug build
+ * ---- Between the pre-projection and the attention of a decode step ----
+ *
+ * The published path hands wq_b's output and the normalized kv latent to a
+ * fused "qnorm + rope + kv insert" op and an attention op whose cache layout
+ * it does not give; the four calls below are this implementation's own.  They
+ * share a paged cache: pages of page_size token rows of bf16, page p's row i
+ * at cache + p * ld_page + i * ld_row (elements), so token slot s is row
+ * s % page_size of page s / page_size.  A request's tokens lie in the pages
+ * that its row of the block table names, in order.
+ */
+
+/* Most requests of one call of dsnq_extend_block_tables and
+ * dsnq_paged_latent_attention. */
+#define DSNQ_MAX_REQUESTS 16384
+
+/* Pairing of the rotated columns x[0 .. R): pair i is (x[2i], x[2i+1]) or
+ * (x[i], x[i + R/2]). */
+typedef enum {
+    DSNQ_ROPE_INTERLEAVED = 0,
+    DSNQ_ROPE_HALF = 1
+} dsnq_rope_layout;
+
+/*
+ * Block tables, positions and slots of a step, from the lengths of its
+ * requests.  Request b holds seq_lens[b] tokens in ceil(seq_lens[b] /
+ * page_size) pages (the first entries of its table row) and gets
+ * new_tokens[b] more; the tokens of all requests are laid end to end as the
+ * step's rows.  New pages are taken from free_pages in the order of the
+ * requests.
+ *   B, rows, page_size : requests (<= DSNQ_MAX_REQUESTS), token rows of the step
+ *                 (at least sum new_tokens; the rest are padded rows), tokens
+ *                 per page (<= 2^20).
+ *   seq_lens    : int32 [B], tokens so far (taken as within [0, table_width *
+ *                 page_size]).
+ *   new_tokens  : int32 [B] (negative counts as 0), or NULL: one each.
+ *   free_pages, num_free : int32 page ids.
+ *   block_table, table_width, ld_table : int32 [B, table_width], updated: only
+ *                 the entries of new pages are written.
+ *   new_lens    : int32 [B] <- tokens after the step.
+ *   row_starts  : int32 [B + 1] <- first row of each request, then the rows in use.
+ *   positions   : int64 [rows] <- the token's position (0 for a padded row).
+ *   slots       : int64 [rows] <- its slot in the cache, -1 for a padded row
+ *                 and for a token that got no place.
+ *   counts      : int32 [2] <- pages taken from the list, pages that were wanted.
+ * A token gets no place when its row would lie past `rows`, its request's
+ * table is full, or the free list is used up (counts[1] > num_free); new_lens
+ * counts the tokens that got one.  table_width * page_size < 2^31.
+ * The outputs must not overlap the inputs or each other (new_lens and
+ * row_starts equal to seq_lens or new_tokens: DSNQ_ERR_INVALID_ARG).
+ */
+DSNQ_API dsnq_status dsnq_extend_block_tables(
+    int64_t B, int64_t rows, int64_t page_size,
+    const int32_t* seq_lens, const int32_t* new_tokens,
+    const int32_t* free_pages, int64_t num_free,
+    int32_t* block_table, int64_t table_width, int64_t ld_table,
+    int32_t* new_lens, int32_t* row_starts, int64_t* positions, int64_t* slots, int32_t* counts,
+    void* stream);
+
+/*
+ * RMSNorm of each head and rotary positions of part of it, in one pass:
+ *   y = x * r * gamma,  r = 1 / sqrt(mean_d x[m,h,d]^2 + eps)   (fp32; y = x without
+ *       normalize; gamma == NULL: no weight)
+ *   pairs (a, b) of columns [rope_offset, rope_offset + rope_dim) of y:
+ *       (a cos t - b sin t, b cos t + a sin t) * rope_scale,
+ *       t = positions[m] * inv_freq[i]   (angle in fp64; -t with inverse)
+ *   out = bf16_rn(y), one rounding.
+ * Scaled rotary positions (long contexts) are a matter of inv_freq and
+ * rope_scale, which the caller prepares once.
+ *   x, ldx_tok, ldx_head : bf16 [M, H, D], e.g. the output of
+ *                 dsnq_block_scaled_fp8_gemm with ldx_head = D; D a multiple
+ *                 of 8, <= 1024; H <= 65535.
+ *   gamma       : bf16 [D] or NULL (must be NULL without normalize).
+ *   positions   : int64 [M]; inv_freq : fp64 [rope_dim / 2].  May be NULL when
+ *                 rope_dim == 0.
+ *   rope_offset : multiple of 8; rope_dim : multiple of 16, <= 256.
+ *   out, ldo_tok, ldo_head : bf16 [M, H, D]; may be x itself with the same
+ *                 strides, otherwise must not overlap it.
+ * Alignment: x, out, gamma 16 bytes, strides multiples of 8; positions and
+ * inv_freq 8 bytes.
+ */
+DSNQ_API dsnq_status dsnq_head_rmsnorm_rope(
+    int64_t M, int64_t H, int64_t D,
+    const void* x, int64_t ldx_tok, int64_t ldx_head,
+    int32_t normalize, const void* gamma, float eps,
+    const int64_t* positions, const double* inv_freq,
+    int64_t rope_offset, int64_t rope_dim, dsnq_rope_layout layout, float rope_scale, int32_t inverse,
+    void* out, int64_t ldo_tok, int64_t ldo_head,
+    void* stream);
+
+/*
+ * Latent rows into the paged cache: row m is [kv[m] (K columns) | pe[m]
+ * (P columns)], kv RMSNormed as above when `normalize` (over K columns, with
+ * gamma [K] or NULL), columns [rope_offset, rope_offset + rope_dim) of the
+ * whole row rotated as above, rounded once to bf16 and stored at slots[m].
+ * Rows with a negative slot are skipped (padded rows); a slot past the cache
+ * is skipped and reported by dsnq_debug_status as DSNQ_ERR_BOUNDS.  The slots
+ * of one call must be distinct: of two rows with the same slot, each column
+ * holds one's or the other's value.
+ *   kv, ldkv : bf16 [M, K], e.g. kv_out of the fused norm+quant (normalize =
+ *              0) or the raw latent; pe, ldpe : bf16 [M, P], e.g. the position
+ *              columns of the projection row; P may be 0 (pe NULL).
+ *   K, P     : multiples of 8, K + P <= 1024.
+ *   cache, num_pages, page_size, ld_page, ld_row : the cache, ld_row >= K + P,
+ *              ld_page >= (page_size - 1) * ld_row + K + P.
+ * Alignment: bf16 pointers 16 bytes, strides multiples of 8; positions, slots
+ * (int64 [M]) and inv_freq 8 bytes.  kv and pe must not overlap the cache.
+ */
+DSNQ_API dsnq_status dsnq_latent_cache_write(
+    int64_t M, int64_t K, int64_t P,
+    const void* kv, int64_t ldkv, const void* pe, int64_t ldpe,
+    int32_t normalize, const void* gamma, float eps,
+    const int64_t* positions, const double* inv_freq,
+    int64_t rope_offset, int64_t rope_dim, dsnq_rope_layout layout, float rope_scale,
+    const int64_t* slots, void* cache, int64_t num_pages, int64_t page_size, int64_t ld_page, int64_t ld_row,
+    void* stream);
+
+/*
+ * Host-only query: bytes of the workspace dsnq_paged_latent_attention needs
+ * (partial results of requests that are split over their length; at most
+ * about 42 MB).  Errors as in that call.  `bytes` may be NULL.
+ */
+DSNQ_API dsnq_status dsnq_paged_latent_attention_workspace_bytes(int64_t B, int64_t H, int64_t DV, int64_t table_width,
+                                                                 int64_t page_size, int64_t* bytes);
+
+/*
+ * Attention of one new token per request over its rows of the paged latent
+ * cache, which all heads share; a row is the key (DK columns) and, by its
+ * first DV columns, the value:
+ *   z_j = scale * q[b,h] . c_j,   j < seq_lens[b]
+ *   out[b,h,:] = sum_j softmax(z)_j c_j[0:DV],   lse[b,h] = log sum_j exp z_j
+ * fp32 scores, sums and accumulation; the probabilities are rounded to bf16
+ * for the second product.  An empty request gets zeros and lse = -infinity.
+ *   B, H, DK, DV : requests (<= DSNQ_MAX_REQUESTS), heads (<= 1024), key and value
+ *                 width: DK a multiple of 64, <= 576; DV a multiple of 128,
+ *                 <= 512 and <= DK.
+ *   q, ldq_tok, ldq_head : bf16 [B, H, DK].
+ *   cache, num_pages, page_size, ld_page, ld_row : as above, num_pages >= 1,
+ *                 page_size a multiple of 8.
+ *   block_table, table_width, ld_table : int32 [B, table_width]; only the
+ *                 entries of tokens below the length are read.  An entry
+ *                 outside [0, num_pages) reads as zero rows and is reported
+ *                 by dsnq_debug_status as DSNQ_ERR_BOUNDS.
+ *   seq_lens    : int32 [B], taken as within [0, table_width * page_size].
+ *   scale       : > 0.
+ *   out, ldo_tok, ldo_head : bf16 [B, H, DV]; lse, ldl_tok : fp32 [B, H] or NULL.
+ *   workspace, workspace_bytes : caller-owned, at least
+ *                 dsnq_paged_latent_attention_workspace_bytes, 16-byte
+ *                 aligned; it needs no initial contents.  Calls that may run
+ *                 at the same time need one each.
+ * Two launches (one when a single worker takes all).  Alignment: q, cache, out
+ * 16 bytes, their strides multiples of 8.  The outputs and the workspace must
+ * not overlap the inputs or each other.
+ */
+DSNQ_API dsnq_status dsnq_paged_latent_attention(
+    int64_t B, int64_t H, int64_t DK, int64_t DV,
+    const void* q, int64_t ldq_tok, int64_t ldq_head,
+    const void* cache, int64_t num_pages, int64_t page_size, int64_t ld_page, int64_t ld_row,
+    const int32_t* block_table, int64_t table_width, int64_t ld_table,
+    const int32_t* seq_lens, float scale,
+    void* out, int64_t ldo_tok, int64_t ldo_head, float* lse, int64_t ldl_tok,
+    void* workspace, int64_t workspace_bytes,
+    void* stream);
+
+/*
+ * Device status words.  Kernels with bounded waits (the mbarrier waits
+ * of the GEMM and the attention) record a timeout there instead of hanging.  In the debug build
  * (libdsnq_debug.so, compiled with DSNQ_DEBUG) every kernel also checks the
  * indices of its memory accesses against the buffer extents its arguments
  * describe; a failed check skips the access and records a bounds error.
+ * In both builds a cache slot or page id that lies outside the cache records
+ * one too (dsnq_latent_cache_write, dsnq_paged_latent_attention).
  * This call synchronizes `stream`, reads the words of the current device,
  * clears them and returns DSNQ_OK, DSNQ_ERR_TIMEOUT, DSNQ_ERR_BOUNDS (a
  * timeout takes precedence when both are recorded), or DSNQ_ERR_CUDA if the
@@ -410,7 +576,7 @@ DSNQ_API void dsnq_set_launch_overlap(int32_t enable);
 /*
  * Test hooks (affect later launches on all devices of this process).
  * wait_timeout_ns bounds every device wait (0 restores the default of 2 s).
- * inject_flags bit 0 makes the GEMM's producer skip the first stage's load,
+ * inject_flags bit 0 makes the producer of the GEMM and of the attention skip the first stage's load,
  * so the consumer's wait on it must run out: the kernel then records
  * DSNQ_ERR_TIMEOUT, releases its tensor memory and returns.  Bit 1 (debug
  * build only; ignored otherwise) makes every launch record one failed index
