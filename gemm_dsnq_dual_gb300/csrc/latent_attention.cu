@@ -56,6 +56,7 @@ constexpr int kTmemCols = 512;
 constexpr int kTmemS = 256;           // first column of the two S buffers
 constexpr float kRaise = 8.0f;        // log2 by which a maximum may grow before O is rescaled
 constexpr int kMiscBytes = 2048;
+constexpr int kRequestUnits = 2;      // what a request costs a worker beside its tiles, in tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -64,7 +65,7 @@ struct Params {
     const int32_t* table;
     int64_t ld_table;
     int B, H, G, W;                   // requests, heads, head groups, workers
-    int width, page_size, box_rows, num_pages;
+    int width, page_size, box_rows, num_pages;   // box_rows: tokens of one copy
     int64_t cap;                      // tokens the table can hold per request
     int ck, nblk;                     // 64-column chunks of a row, 128-column blocks of the value
     int stages;
@@ -73,9 +74,9 @@ struct Params {
     int64_t ldo_b, ldo_h;
     float* lse;                       // NULL: not written
     int64_t ldl_b;
-    int4* meta;                       // [W] (first request, its first tile, tiles of the worker, tiles of the request)
+    int2* meta;                       // [W] first request of the worker and its first tile there
     float2* part_ml;                  // [W * 2][G][64] (max in log2 units, sum)
-    float* part_o;                    // [W * 2][G][64][DV]
+    float* part_o;                    // [W * 2][G][nblk][16][128][4]: value block, four heads, value, head
     uint64_t timeout_ns;
     uint32_t inject;
 };
@@ -87,12 +88,19 @@ __device__ __forceinline__ int request_len(const Params& p, int b) {
 // Tiles of a request; an empty one counts as one (somebody writes its zeros).
 __device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len + kTile - 1) / kTile : 1; }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
-                                            int32_t z) {
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t y, int32_t w) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %3, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(w)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t group,
+                                            int32_t page) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(group), "r"(page)
         : "memory");
 }
 
@@ -108,15 +116,17 @@ __device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
-// Shared-memory descriptor of the cache tile read column-major (M runs along
-// the 64 columns of a 128-byte row, then to the next chunk; K runs down the
-// rows): leading byte offset = the next 64 columns, stride byte offset = the
-// next 8 rows, 128-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr) {
+// Shared-memory descriptors.  A cache tile lies as [8 groups of 8 tokens][ck
+// chunks of 64 columns][8 tokens][128 bytes], 128-byte swizzle: one copy then
+// takes whole groups with all their columns, whatever the page size.  Read
+// K-major (S = Q K^T), the next 8 rows are a group (ck KB) on.  Read
+// column-major (V^T: M runs along the 64 columns of a chunk and on to the
+// next chunk, 1 KB on; K runs down the tokens), likewise.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lead, uint32_t stride) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr >> 4) & 0x3FFF);
-    d |= static_cast<uint64_t>((kChunkBytes >> 4) & 0x3FFF) << 16;
-    d |= static_cast<uint64_t>((1024 >> 4) & 0x3FFF) << 32;
+    d |= static_cast<uint64_t>((lead >> 4) & 0x3FFF) << 16;
+    d |= static_cast<uint64_t>((stride >> 4) & 0x3FFF) << 32;
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(2) << 61;
     return d;
@@ -143,23 +153,67 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// A worker's run of tiles, request by request.
+// 16 lanes x 8 N columns of TMEM in the layout of matrix fragments: of each
+// 8 columns, thread i gets columns 2 (i % 4), + 1 of lane i / 4 (r[0], r[1])
+// and of lane i / 4 + 8 (r[2], r[3]).
+__device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    uint32_t u;
+    memcpy(&u, &h, 4);
+    return u;
+}
+
+// Barrier of the softmax warps; returns whether any thread passed true.  A
+// named barrier has no time limit, so every softmax warp reaches every one of
+// them whether or not its waits succeeded (the counts depend on the run alone).
+__device__ __forceinline__ bool soft_sync_or(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return r != 0;
+}
+
+// A worker's run of tiles, request by request: from tile t0 of request b up
+// to (not including) tile t_end of request b_end.
 struct Run {
-    int b, t0, left;                  // request, its first tile of the run, tiles left in the run
-    bool first;
+    int b, t0, b_end, t_end;
     int len, tiles, n;                // of the current request: tokens, tiles, tiles of this run
     __device__ __forceinline__ bool next(const Params& p) {
-        if (left <= 0) return false;
+        if (b > b_end || (b == b_end && t0 >= t_end)) return false;
         len = request_len(p, b);
         tiles = tiles_of(len);
-        n = min(tiles - t0, left);
+        n = (b == b_end ? t_end : tiles) - t0;
         return true;
     }
     __device__ __forceinline__ void advance() {
-        left -= n;
         ++b;
         t0 = 0;
-        first = false;
     }
 };
 
@@ -171,7 +225,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     const int tile_bytes = p.ck * kChunkBytes;
     uint8_t* q_s = smem;                                   // [ck][64 heads][128 B]
     uint8_t* p_s = q_s + tile_bytes;                       // [64 heads][128 B]
-    uint8_t* kv_s = p_s + kChunkBytes;                     // [stages][ck][64 tokens][128 B]
+    uint8_t* kv_s = p_s + kChunkBytes;                     // [stages][8 groups][ck][8 tokens][128 B]
     uint8_t* misc = kv_s + p.stages * tile_bytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(misc);    // [kMaxStages]
     uint64_t* empty = full + kMaxStages;                   // [kMaxStages]
@@ -181,15 +235,13 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     uint64_t* sempty = sfull + 2;                          // [2]
     uint64_t* pfull = sempty + 2;
     uint64_t* pempty = pfull + 1;
-    uint64_t* xch = pempty + 1;                            // the softmax warps among themselves
-    uint64_t* drain = xch + 1;
+    uint64_t* drain = pempty + 1;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-    int* run_s = reinterpret_cast<int*>(tmem_holder + 2);  // [3] the worker's first request, first tile, tiles
+    int* run_s = reinterpret_cast<int*>(tmem_holder + 2);  // [4] first request and tile, end request and tile
     int64_t* sums = reinterpret_cast<int64_t*>(tmem_holder + 6);   // [kThreads / 32]
     float* alpha_s = reinterpret_cast<float*>(sums + kThreads / 32);   // [2][64]
     float* inv_s = alpha_s + 2 * kHeads;                   // [64]
-    int* raise_s = reinterpret_cast<int*>(inv_s + kHeads); // [2][4]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = blockIdx.x / p.G, g = blockIdx.x - w * p.G;
@@ -207,7 +259,6 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         }
         mbar_init(smem_u32(pfull), kSoftWarps);
         mbar_init(smem_u32(pempty), 1);
-        mbar_init(smem_u32(xch), kSoftWarps);
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -224,13 +275,15 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     allow_dependent_launch();
     bounds_self_test(p.inject);
 
-    // The worker's run: total tiles T, then the request that holds tile
-    // w * T / workers.  Thread t sums requests [t * per, (t + 1) * per).
+    // The worker's run.  Each request counts kRequestUnits units, then one per
+    // tile; worker w takes units [w U / workers, (w + 1) U / workers), and a
+    // cut among a request's leading units is a cut before its first tile.
+    // Thread t sums requests [t * per, (t + 1) * per).
     {
         const int per = (p.B + kThreads - 1) / kThreads;
         const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
         int64_t mine = 0;
-        for (int b = b0; b < b1; ++b) mine += tiles_of(request_len(p, b));
+        for (int b = b0; b < b1; ++b) mine += kRequestUnits + tiles_of(request_len(p, b));
         int64_t inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -245,19 +298,23 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             total += sums[i];
         }
         const int64_t workers = total < p.W ? total : p.W;
-        const int64_t begin = w < workers ? w * total / workers : 0;
-        const int64_t end = w < workers ? (w + 1) * total / workers : 0;
-        if (threadIdx.x == 0 && end == begin) run_s[2] = 0;
-        if (end > begin && begin >= before && begin < before + mine) {
-            int64_t at = before;
-            int b = b0, n = tiles_of(request_len(p, b));
-            while (at + n <= begin) {
-                at += n;
-                n = tiles_of(request_len(p, ++b));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int64_t u = w + e < workers ? (w + e) * total / workers : total;
+            if (threadIdx.x == 0 && u == total) {
+                run_s[2 * e] = p.B;
+                run_s[2 * e + 1] = 0;
             }
-            run_s[0] = b;
-            run_s[1] = static_cast<int>(begin - at);
-            run_s[2] = static_cast<int>(end - begin);
+            if (u >= before && u < before + mine) {
+                int64_t at = before;
+                int b = b0, n = kRequestUnits + tiles_of(request_len(p, b));
+                while (at + n <= u) {
+                    at += n;
+                    n = kRequestUnits + tiles_of(request_len(p, ++b));
+                }
+                run_s[2 * e] = b;
+                run_s[2 * e + 1] = max(static_cast<int>(u - at) - kRequestUnits, 0);
+            }
         }
     }
     tc_fence_before();
@@ -268,32 +325,28 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     Run run;
     run.b = run_s[0];
     run.t0 = run_s[1];
-    run.left = run_s[2];
-    run.first = true;
-    const bool idle = run.left == 0;
-    if (idle) run.b = run.t0 = 0;
-    if (threadIdx.x == 0 && g == 0)
-        p.meta[w] = make_int4(run.b, run.t0, run.left, idle ? 0 : tiles_of(request_len(p, run.b)));
+    run.b_end = run_s[2];
+    run.t_end = run_s[3];
+    const int b_first = run.b;
+    if (threadIdx.x == 0 && g == 0) p.meta[w] = make_int2(run.b, run.t0);
 
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
-        const int pieces = kTile / p.box_rows;             // page pieces of a tile (1, 2, 4 or 8)
-        const uint32_t piece_bytes = p.box_rows * 128;
+        const int pieces = kTile / p.box_rows;             // copies of a tile (1, 2, 4 or 8)
+        const int batch = 32 / pieces;                     // tiles whose table entries the lanes hold
+        const uint32_t piece_bytes = p.box_rows * 128 * p.ck;
         uint32_t n = 0, nq = 0;
         bool ok = true;
         for (; ok && run.next(p); run.advance()) {
             if (run.len == 0) continue;
             const int32_t* row = p.table + run.b * p.ld_table;
-            // Entries of the next 32 / pieces tiles, one per lane.
-            const int batch = 32 / pieces;
             int ids = 0;
             ok = wait_bounded(smem_u32(qempty), (nq & 1) ^ 1, abort_flag, tmo);
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(smem_u32(qfull), tile_bytes);
-            __syncwarp();
-            if (lane < p.ck)
-                tma_load_3d(smem_u32(q_s + lane * kChunkBytes), &map_q, smem_u32(qfull), lane * kChunkCols, g * kHeads,
-                            run.b);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(smem_u32(qfull), tile_bytes);
+                tma_load_4d(smem_u32(q_s), &map_q, smem_u32(qfull), g * kHeads, run.b);
+            }
             ++nq;
             for (int i = 0; i < run.n; ++i, ++n) {
                 const int tile = run.t0 + i;
@@ -316,68 +369,92 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 const int live = min(pieces, (run.len - tok0 + p.box_rows - 1) / p.box_rows);
                 const uint32_t fb = smem_u32(&full[s]);
                 if ((p.inject & kInjectSkipLoad) && n == 0) continue;   // test hook: the waits on it run out
-                if (lane == 0) mbar_arrive_expect_tx(fb, live * piece_bytes * p.ck);
+                if (lane == 0) mbar_arrive_expect_tx(fb, live * piece_bytes);
                 __syncwarp();
-                const uint32_t dst = smem_u32(kv_s) + s * tile_bytes;
-                for (int e = lane; e - lane < live * p.ck; e += 32) {
-                    const bool on = e < live * p.ck;
-                    const int piece = on ? e / p.ck : 0, c = on ? e - piece * p.ck : 0;
-                    const int id = __shfl_sync(0xffffffffu, ids, (i % batch) * pieces + piece);
-                    const int y = (tok0 + piece * p.box_rows) % p.page_size;
-                    if (on) tma_load_3d(dst + c * kChunkBytes + piece * piece_bytes, &map_kv, fb, c * kChunkCols, y, id);
-                }
+                const int id = __shfl_sync(0xffffffffu, ids, (i % batch) * pieces + (lane & (pieces - 1)));
+                if (lane < live)
+                    tma_load_5d(smem_u32(kv_s) + s * tile_bytes + lane * piece_bytes, &map_kv, fb,
+                                (tok0 + lane * p.box_rows) % p.page_size / 8, id);
             }
         }
         if (!ok) settle_ns(kAbortSettleNs);                // copies already issued land before the CTA goes
     } else if (warp == 1) {
         // --------------------------------------------------------- MMA issuer
+        // Two products wait for different things: Q K^T of tile n for its copy,
+        // P V of tile k < n for its softmax.  Whichever is ready is issued: a
+        // P V held back behind the next tile's copy would hold the stage that
+        // the copy after it needs.
         const uint32_t id_s = idesc_bf16(64, kTile, false), id_o = idesc_bf16(128, kHeads, true);
-        uint32_t n = 0, nq = 0;
-        int pend = -1;                                     // stage whose P V product is still to be issued
-        bool pend_first = false, ok = true;
-        const uint64_t q_desc = smem_desc_k_sw128(smem_u32(q_s)), p_desc = smem_desc_k_sw128(smem_u32(p_s));
-        // O^T (+)= V^T P^T of tile n - 1.
-        auto issue_pv = [&]() -> bool {
-            if (!wait_bounded(smem_u32(pfull), (n - 1) & 1, abort_flag, tmo)) return false;
-            tc_fence_after();
-            const uint32_t v0 = smem_u32(kv_s) + pend * tile_bytes;
-            for (int blk = 0; blk < p.nblk; ++blk) {
-#pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    tc_mma_bf16(tmem + blk * kHeads, smem_desc_mn_sw128(v0 + blk * 2 * kChunkBytes + k * 16 * 128),
-                                p_desc + k * 2, id_o, !(pend_first && k == 0));
-            }
-            tc_commit(smem_u32(&empty[pend]));
-            tc_commit(smem_u32(pempty));
-            return true;
+        const uint32_t group = p.ck * 1024;                // bytes of 8 tokens
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(q_s), 16, 1024), p_desc = smem_desc_sw128(smem_u32(p_s), 16, 1024);
+        uint32_t n = 0, k = 0, nq = 0;
+        uint32_t firsts = 0;                               // bit n % 32: tile n is its request's first of the run
+        int i = 0;
+        bool ok = true, q_here = false, more = false;
+        auto next_request = [&]() {
+            while ((more = run.next(p)) && run.len == 0) run.advance();
+            i = 0;
+            q_here = false;
         };
-        for (; ok && run.next(p); run.advance()) {
-            if (run.len == 0) continue;
-            ok = wait_bounded(smem_u32(qfull), nq & 1, abort_flag, tmo);
-            if (!ok) break;
-            ++nq;
-            for (int i = 0; i < run.n; ++i) {
-                const int s = n % p.stages;
-                ok = wait_bounded(smem_u32(&full[s]), (n / p.stages) & 1, abort_flag, tmo) &&
-                     wait_bounded(smem_u32(&sempty[n & 1]), ((n >> 1) & 1) ^ 1, abort_flag, tmo);
-                if (!ok) break;
+        auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity)); };
+        next_request();
+        uint64_t t_wait = now_ns();
+        uint32_t polls = 0;
+        while (more || k < n) {
+            if (k < n && ready(pfull, k & 1)) {
                 tc_fence_after();
-                const uint64_t k_desc = smem_desc_k_sw128(smem_u32(kv_s) + s * tile_bytes);
-                for (int c = 0; c < p.ck; ++c) {
+                const int s = k % p.stages;
+                const uint32_t v0 = smem_u32(kv_s) + s * tile_bytes;
+                const bool first = (firsts >> (k & 31)) & 1;
+                for (int blk = 0; blk < p.nblk; ++blk) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_bf16(tmem + kTmemS + (n & 1) * kTile, q_desc + c * (kChunkBytes >> 4) + k * 2,
-                                    k_desc + c * (kChunkBytes >> 4) + k * 2, id_s, (c | k) != 0);
+                    for (int j = 0; j < kTile / 16; ++j)
+                        tc_mma_bf16(tmem + blk * kHeads, smem_desc_sw128(v0 + blk * 2048 + j * 2 * group, 1024, group),
+                                    p_desc + j * 2, id_o, !(first && j == 0));
                 }
-                tc_commit(smem_u32(&sfull[n & 1]));
-                if (i == run.n - 1) tc_commit(smem_u32(qempty));
-                if (pend >= 0 && !(ok = issue_pv())) break;
-                pend = s;
-                pend_first = i == 0;
-                ++n;
+                tc_commit(smem_u32(&empty[s]));
+                tc_commit(smem_u32(pempty));
+                ++k;
+                polls = 0;
+                continue;
+            }
+            if (more) {
+                if (!q_here) q_here = ready(qfull, nq & 1);
+                const int s = n % p.stages;
+                if (q_here && ready(&full[s], (n / p.stages) & 1) && ready(&sempty[n & 1], ((n >> 1) & 1) ^ 1)) {
+                    tc_fence_after();
+                    const uint64_t k_desc = smem_desc_sw128(smem_u32(kv_s) + s * tile_bytes, 16, group);
+                    for (int c = 0; c < p.ck; ++c) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            tc_mma_bf16(tmem + kTmemS + (n & 1) * kTile, q_desc + c * (kChunkBytes >> 4) + j * 2,
+                                        k_desc + c * (1024 >> 4) + j * 2, id_s, (c | j) != 0);
+                    }
+                    tc_commit(smem_u32(&sfull[n & 1]));
+                    firsts = (firsts & ~(1u << (n & 31))) | (i == 0 ? 1u << (n & 31) : 0u);
+                    ++n;
+                    if (++i == run.n) {
+                        tc_commit(smem_u32(qempty));
+                        ++nq;
+                        run.advance();
+                        next_request();
+                    }
+                    polls = 0;
+                    continue;
+                }
+            }
+            if (polls == 0) t_wait = now_ns();
+            if ((++polls & 63) == 0) {                     // bounded, as every wait
+                if (now_ns() - t_wait > tmo) {
+                    *abort_flag = 1;
+                    if (lane == 0) atomicOr(&g_status, kStatusTimeout);
+                }
+                if (__any_sync(0xffffffffu, *abort_flag)) {
+                    ok = false;
+                    break;
+                }
             }
         }
-        if (ok && pend >= 0) ok = issue_pv();
         if (!ok) {                                         // MMAs already issued end before their memory goes
             tc_commit(smem_u32(drain));
             wait_drain(smem_u32(drain), 0, tmo);
@@ -387,20 +464,19 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         const int quad = warp & 3;                         // TMEM lanes 32 * quad ..
         const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const int st = threadIdx.x - 64;                   // 0..127
-        // S at M = 64: row 16 * quad + i is lane 32 * quad + i, i < 16.
-        const bool on = lane < 16;
-        const int row = quad * 16 + (lane & 15);
+        const float kNegInf = __int_as_float(0xff800000);
+        // S at M = 64: row 16 * quad + i is lane 32 * quad + i, i < 16.  In
+        // the fragment layout a thread holds 16 columns of two rows.
+        const int row0 = quad * 16 + (lane >> 2), col0 = 2 * (lane & 3);   // the other row: row0 + 8
+        // Where this lane's stmatrix row goes: matrices (rows 0-7, 8-15) x two
+        // adjacent 8-column groups of the warp's 16 rows of P.
+        const int p_row = quad * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+        const uint32_t p_addr = smem_u32(p_s) + p_row * 128;
+        const int p_grp = lane >> 4, p_swz = lane & 7;
         const int DV = p.nblk * 128;
-        uint32_t n = 0, nx = 0;
-        bool ok = true;
-        // Barrier of the four warps.  An mbarrier, whose waits are bounded:
-        // after an abort a warp may leave without the others.
-        auto exchange = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(xch));
-            return wait_bounded<true>(smem_u32(xch), nx++ & 1, abort_flag, tmo);
-        };
-        for (; ok && run.next(p); run.advance()) {
+        uint32_t n = 0;
+        bool ok = true;                                    // false: only the barriers are kept up
+        for (; run.next(p); run.advance()) {
             const int b = run.b;
             const bool whole = run.t0 == 0 && run.n == run.tiles;
             if (run.len == 0) {
@@ -410,58 +486,65 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     if (h < p.H && bounds_ok(b < p.B))
                         *reinterpret_cast<uint4*>(p.out + b * p.ldo_b + h * p.ldo_h + c * 8) = make_uint4(0, 0, 0, 0);
                 }
-                if (p.lse && st < kHeads && g * kHeads + st < p.H)
-                    p.lse[b * p.ldl_b + g * kHeads + st] = __int_as_float(0xff800000);
+                if (p.lse && st < kHeads && g * kHeads + st < p.H) p.lse[b * p.ldl_b + g * kHeads + st] = kNegInf;
                 continue;
             }
-            float m = __int_as_float(0xff800000), l = 0.f;  // maximum of the raw scores in use, sum of p
+            // Of the two rows: maximum of the raw scores in use, and this
+            // thread's share of the sum of p.
+            float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
             for (int i = 0; i < run.n; ++i, ++n) {
-                const int tok0 = (run.t0 + i) * kTile;
-                const int valid = min(kTile, run.len - tok0);
-                ok = wait_bounded(smem_u32(&sfull[n & 1]), (n >> 1) & 1, abort_flag, tmo);
-                if (!ok) break;
+                const int valid = min(kTile, run.len - (run.t0 + i) * kTile);
+                ok = ok && wait_bounded<true>(smem_u32(&sfull[n & 1]), (n >> 1) & 1, abort_flag, tmo);
                 tc_fence_after();
-                uint64_t sp[kTile / 2];
-                tmem_ld_pairs<kTile>(tl + kTmemS + (n & 1) * kTile, sp);
+                float s[2][16];                            // [row][8 k + column]
+                {
+                    uint32_t r[2][16];
+                    tmem_ld_frag32(tl + kTmemS + (n & 1) * kTile, r[0]);
+                    tmem_ld_frag32(tl + kTmemS + (n & 1) * kTile + 32, r[1]);
+                    tmem_ld16_wait(r[0]);
+                    tmem_ld16_wait(r[1]);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {         // 8 column groups x 2 columns
+                        s[0][j] = __uint_as_float(r[j >> 3][(j >> 1 & 3) * 4 + (j & 1)]);
+                        s[1][j] = __uint_as_float(r[j >> 3][(j >> 1 & 3) * 4 + 2 + (j & 1)]);
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sempty[n & 1]));
-                float s[kTile];
-#pragma unroll
-                for (int j = 0; j < kTile / 2; ++j) {
-                    const float2 f = as_float2(sp[j]);
-                    s[2 * j] = f.x;
-                    s[2 * j + 1] = f.y;
-                }
                 if (valid < kTile) {
 #pragma unroll
-                    for (int j = 0; j < kTile; ++j)
-                        if (j >= valid) s[j] = __int_as_float(0xff800000);
+                    for (int j = 0; j < 16; ++j)
+                        if ((j >> 1) * 8 + col0 + (j & 1) >= valid) s[0][j] = s[1][j] = kNegInf;
                 }
-                float top = s[0];
-#pragma unroll
-                for (int j = 1; j < kTile; ++j) top = fmaxf(top, s[j]);
-                // Raise the maximum when it grew too far (always on the first tile).
-                float alpha = 1.f;
                 bool raise = false;
-                if (on && (top - m) * p.scale_log2 > kRaise) {
-                    raise = i > 0;
-                    alpha = exp2_fast((m - top) * p.scale_log2);
-                    m = top;
+                float alpha[2];
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = fmaxf(s[a][j], s[a][j + 8]);
+                    float top = fmaxf(fmaxf(fmaxf(x[0], x[4]), fmaxf(x[1], x[5])), fmaxf(fmaxf(x[2], x[6]), fmaxf(x[3], x[7])));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // Raise the maximum when it grew too far (always on the first tile).
+                    alpha[a] = 1.f;
+                    if ((top - m[a]) * p.scale_log2 > kRaise) {
+                        raise |= i > 0;
+                        alpha[a] = exp2_fast((m[a] - top) * p.scale_log2);
+                        m[a] = top;
+                    }
+                    if ((lane & 3) == 0) alpha_s[(n & 1) * kHeads + row0 + 8 * a] = alpha[a];
                 }
-                if (on) alpha_s[(n & 1) * kHeads + row] = alpha;
-                const bool any = __any_sync(0xffffffffu, raise);
-                if (lane == 0) raise_s[(n & 1) * kSoftWarps + quad] = any;
-                ok = exchange();
-                if (!ok) break;
-                const int* rs = raise_s + (n & 1) * kSoftWarps;
-                if (rs[0] | rs[1] | rs[2] | rs[3]) {
-                    ok = wait_bounded(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);   // product n - 1 is in O
-                    if (!ok) break;
+                const bool rescale = soft_sync_or(raise);
+                // P's buffer and O are this tile's once product n - 1 is done.
+                if (rescale) {
+                    ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
                     tc_fence_after();
-                    l *= alpha;
+                    l[0] *= alpha[0];
+                    l[1] *= alpha[1];
                     const float* al = alpha_s + (n & 1) * kHeads;
-                    for (int c = 0; c < p.nblk * kHeads; c += 16) {
+                    for (int c = 0; ok && c < p.nblk * kHeads; c += 16) {
                         uint32_t r[16];
                         tmem_ld16_issue(tl + c, r);
                         tmem_ld16_wait(r);
@@ -472,40 +555,40 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     }
                     tmem_wait_st();
                 }
-                const float off = m == __int_as_float(0xff800000) ? 0.f : m * p.scale_log2;
-                uint32_t pk[kTile / 2];
-                float sum0 = 0.f, sum1 = 0.f;
+                uint32_t pk[2][8];
 #pragma unroll
-                for (int j = 0; j < kTile / 2; ++j) {
-                    const float e0 = exp2_fast(fmaf(s[2 * j], p.scale_log2, -off));
-                    const float e1 = exp2_fast(fmaf(s[2 * j + 1], p.scale_log2, -off));
-                    sum0 += e0;
-                    sum1 += e1;
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
-                    memcpy(&pk[j], &h, 4);
-                }
-                l += sum0 + sum1;
-                // P's buffer is free once product n - 1 is done.
-                ok = n == 0 || wait_bounded(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
-                if (!ok) break;
-                if (on) {
-                    uint8_t* dst = p_s + row * 128;
+                for (int a = 0; a < 2; ++a) {
+                    const float off = m[a] == kNegInf ? 0.f : m[a] * p.scale_log2;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) << 4)) =
-                            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                    for (int j = 0; j < 8; ++j) {
+                        const float e0 = exp2_fast(fmaf(s[a][2 * j], p.scale_log2, -off));
+                        const float e1 = exp2_fast(fmaf(s[a][2 * j + 1], p.scale_log2, -off));
+                        sum[j & 1] += e0;
+                        sum[2 + (j & 1)] += e1;
+                        pk[a][j] = pack_bf16(e0, e1);
+                    }
+                    l[a] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
-                if (valid < kTile) {
-                    // Rows past the length hold whatever the page or the
-                    // buffer held: 0 * NaN would reach O, so they become 0.
-                    const int stage = n % p.stages;
-                    ok = wait_bounded(smem_u32(&full[stage]), (n / p.stages) & 1, abort_flag, tmo);
-                    if (!ok) break;
-                    uint8_t* kv = kv_s + stage * tile_bytes;
-                    const int per = (kTile - valid) * 8;   // 16-byte words of a chunk
-                    for (int e = st; e < per * p.nblk * 2; e += 128) {
-                        const int c = e / per, v = e - c * per;
-                        *reinterpret_cast<uint4*>(kv + c * kChunkBytes + valid * 128 + v * 16) = make_uint4(0, 0, 0, 0);
+                if (n > 0) ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
+                __syncwarp();
+                if (ok) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        stmatrix_x4(p_addr + (((2 * j + p_grp) ^ p_swz) << 4), pk[0][2 * j], pk[1][2 * j], pk[0][2 * j + 1],
+                                    pk[1][2 * j + 1]);
+                    if (valid < kTile) {
+                        // Rows past the length hold whatever the page or the
+                        // buffer held: 0 * NaN would reach O, so they become 0.
+                        const int stage = n % p.stages;
+                        ok = wait_bounded(smem_u32(&full[stage]), (n / p.stages) & 1, abort_flag, tmo);
+                        uint8_t* kv = kv_s + stage * tile_bytes;
+                        const int words = p.nblk * 16;     // 16-byte words of a row's value
+                        for (int e = st; ok && e < (kTile - valid) * words; e += 128) {
+                            const int r = valid + e / words, v = e % words;
+                            *reinterpret_cast<uint4*>(kv + ((r >> 3) * p.ck + (v >> 3)) * 1024 + (r & 7) * 128 + (v & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
                     }
                 }
                 fence_proxy_async_smem();
@@ -513,44 +596,83 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(pfull));
             }
-            if (!ok) break;
             // ---- output of the request (or of this worker's part of it)
-            ok = wait_bounded(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
-            if (!ok) break;
+            ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
             tc_fence_after();
-            const int head = g * kHeads + row;
-            const float m2 = m == __int_as_float(0xff800000) ? m : m * p.scale_log2;
-            const int64_t slot = (static_cast<int64_t>(w) * 2 + (run.first ? 0 : 1)) * p.G + g;
-            if (on) {
-                inv_s[row] = l > 0.f || l != l ? 1.0f / l : 0.f;
-                if (whole) {
-                    if (p.lse && head < p.H)
-                        p.lse[b * p.ldl_b + head] = l == 0.f ? __int_as_float(0xff800000) : (m2 + log2f(l)) * kLn2;
-                } else {
-                    p.part_ml[slot * kHeads + row] = make_float2(m2, l);
+            const int64_t slot = (static_cast<int64_t>(w) * 2 + (b == b_first ? 0 : 1)) * p.G + g;
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                l[a] += __shfl_xor_sync(0xffffffffu, l[a], 1);
+                l[a] += __shfl_xor_sync(0xffffffffu, l[a], 2);
+                const int row = row0 + 8 * a, head = g * kHeads + row;
+                const float m2 = m[a] == kNegInf ? m[a] : m[a] * p.scale_log2;
+                if ((lane & 3) == 0) {
+                    inv_s[row] = l[a] > 0.f || l[a] != l[a] ? 1.0f / l[a] : 0.f;
+                    if (ok && whole) {
+                        if (p.lse && head < p.H) p.lse[b * p.ldl_b + head] = l[a] == 0.f ? kNegInf : (m2 + log2f(l[a])) * kLn2;
+                    } else if (ok) {
+                        p.part_ml[slot * kHeads + row] = make_float2(m2, l[a]);
+                    }
                 }
             }
-            ok = exchange();                               // inv_s is next written after another exchange
-            if (!ok) break;
+            soft_sync_or(false);                           // inv_s is next written after another tile's barrier
+            __syncwarp();
             const int heads = min(kHeads, p.H - g * kHeads);
-            for (int blk = 0; blk < p.nblk; ++blk) {
-                const int dv = blk * 128 + quad * 32 + lane;
-                for (int c = 0; c < heads; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16_issue(tl + blk * kHeads + c, r);
-                    tmem_ld16_wait(r);
-                    if (whole) {
-                        __nv_bfloat16* o = p.out + b * p.ldo_b + static_cast<int64_t>(g * kHeads + c) * p.ldo_h + dv;
+            if (!ok) continue;
+            if (whole) {
+                // 32 values x 32 heads at a time, through the warp's own 2 KB
+                // of P's buffer: stmatrix turns the fragments into rows of 32
+                // values (16-byte chunks, chunk ^ (row / 2) % 4), which leave
+                // as 16-byte stores, 64 bytes of each of eight heads at once.
+                const uint32_t stage = smem_u32(p_s) + quad * 2048;
+                for (int it = 0; it < p.nblk * 2; ++it) {
+                    const int blk = it >> 1, h0 = (it & 1) * 32;
+                    if (h0 >= heads) continue;
+                    uint32_t r[2][16];
+                    const uint32_t src = tl + blk * kHeads + h0;
+                    tmem_ld_frag32(src, r[0]);
+                    tmem_ld_frag32(src + (16u << 16), r[1]);
+                    tmem_ld16_wait(r[0]);
+                    tmem_ld16_wait(r[1]);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c + j < heads && bounds_ok(b < p.B && dv < DV))
-                                o[j * p.ldo_h] = __float2bfloat16_rn(__uint_as_float(r[j]) * inv_s[c + j]);
-                    } else {
-                        float* o = p.part_o + (slot * kHeads + c) * DV + dv;
+                    for (int q = 0; q < 4; ++q) {          // eight heads
+                        const float2 f = *reinterpret_cast<const float2*>(inv_s + h0 + q * 8 + col0);
+                        uint32_t v[4];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c + j < heads && bounds_ok(w < p.W && dv < DV)) o[j * DV] = __uint_as_float(r[j]);
+                        for (int d = 0; d < 4; ++d)        // eight values
+                            v[d] = pack_bf16(__uint_as_float(r[d >> 1][q * 4 + (d & 1) * 2]) * f.x,
+                                             __uint_as_float(r[d >> 1][q * 4 + (d & 1) * 2 + 1]) * f.y);
+                        const int hl = q * 8 + (lane & 7), d = lane >> 3;
+                        stmatrix_x4_trans(stage + hl * 64 + ((d ^ ((hl >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
                     }
+                    __syncwarp();
+                    __nv_bfloat16* o = p.out + b * p.ldo_b + blk * 128 + quad * 32 + (lane & 3) * 8;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int hl = j * 8 + (lane >> 2), head = h0 + hl;
+                        uint4 v;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(stage + hl * 64 + (((lane & 3) ^ ((hl >> 1) & 3)) << 4))
+                                     : "memory");
+                        if (head < heads && bounds_ok(b < p.B))
+                            *reinterpret_cast<uint4*>(o + static_cast<int64_t>(g * kHeads + head) * p.ldo_h) = v;
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // A part, in the order the registers hold it: 512 bytes a store.
+                float4* o = reinterpret_cast<float4*>(p.part_o) + slot * p.nblk * 16 * 128 + quad * 32 + lane;
+                for (int c = 0; c < p.nblk * kHeads; c += 16) {
+                    if ((c & (kHeads - 1)) >= heads) continue;
+                    uint32_t r[16];
+                    tmem_ld16_issue(tl + c, r);
+                    tmem_ld16_wait(r);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (bounds_ok(w < p.W))
+                            o[(c / 4 + j) * 128] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                                               __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
                 }
             }
             tc_fence_before();
@@ -567,12 +689,12 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 
 // ---------------------------------------------------------------------------
 // Joins the parts of requests that more than one worker took.  A request is
-// found at the first worker boundary inside it; its parts are that boundary's
-// left neighbour's and those of the workers from there to its end, in the
-// order of the tokens.
+// found at the first cut inside it; its parts are those of the worker before
+// that cut and of the workers that begin inside it, in the order of the tokens.
 //   out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k,  M = max_k m_k
-// Items: with few parts (<= 8) one warp per (head, 128 columns), eight heads'
-// worth per CTA step; with many, eight warps share the parts of one.
+// An item is 32 values of four heads: one lane holds one value of the four
+// (16 bytes of a part).  With few parts (<= 8) one warp takes an item; with
+// many, the eight warps of a CTA share its parts.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 constexpr int kFewParts = 8;
@@ -582,25 +704,24 @@ latent_attention_join_kernel(const Params p) {
     grid_dependency_wait();
     allow_dependent_launch();
     bounds_self_test(p.inject);
-    __shared__ int first_item[kMaxCtas + 1];               // running item count by boundary
+    __shared__ int first_item[kMaxCtas + 1];               // running item count by cut
     __shared__ int parts_s[kMaxCtas];
-    __shared__ float4 red[kJoinWarps][32];
-    __shared__ float red_l[kJoinWarps], red_m[kJoinWarps];
+    __shared__ float4 red[kJoinWarps][32], red_l[kJoinWarps], red_m[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int DV = p.nblk * 128;
-    const int few_items = (p.H * p.nblk + kJoinWarps - 1) / kJoinWarps, many_items = p.H * p.nblk;
+    const float kNegInf = __int_as_float(0xff800000);
+    const int quads = (p.H + 3) / 4, items = quads * p.nblk * 4;
 
     if (threadIdx.x < static_cast<unsigned>(p.W)) {
         int parts = 0;
         const int w = threadIdx.x;
-        if (w > 0) {
-            const int4 me = p.meta[w], left = p.meta[w - 1];
-            if (me.z > 0 && me.y > 0 && left.z >= me.y) {
-                int covered = me.y, k = w;
-                parts = 1;
-                while (covered < me.w && k < p.W) {
-                    covered += p.meta[k].z;
-                    ++k;
+        const int2 me = p.meta[w];
+        if (w > 0 && me.x < p.B && me.y > 0) {
+            const int2 left = p.meta[w - 1];
+            if (left.x != me.x || left.y == 0) {
+                parts = 2;
+                for (int k = w + 1; k < p.W; ++k) {
+                    const int2 o = p.meta[k];
+                    if (o.x != me.x || o.y == 0) break;
                     ++parts;
                 }
             }
@@ -612,7 +733,7 @@ latent_attention_join_kernel(const Params p) {
         int at = 0;
         for (int w = 0; w < p.W; ++w) {
             first_item[w] = at;
-            at += parts_s[w] == 0 ? 0 : (parts_s[w] <= kFewParts ? few_items : many_items);
+            at += parts_s[w] == 0 ? 0 : (parts_s[w] <= kFewParts ? (items + kJoinWarps - 1) / kJoinWarps : items);
         }
         first_item[p.W] = at;
     }
@@ -624,62 +745,73 @@ latent_attention_join_kernel(const Params p) {
         const bool few = parts <= kFewParts;
         const int sub = few ? (item - first_item[w]) * kJoinWarps + warp : item - first_item[w];
         const int step = few ? 1 : kJoinWarps, k0 = few ? 0 : warp;
-        const bool on = sub < p.H * p.nblk;
-        const int h = on ? sub / p.nblk : 0, blk = on ? sub - h * p.nblk : 0;
-        const int g = h / kHeads, row = h - g * kHeads;
-        const int4 me = p.meta[w];
-        const int left_slot = p.meta[w - 1].z == me.y ? 0 : 1;
+        const bool on = sub < items;
+        // sub = (four heads, value block, 32 values)
+        const int hq = on ? sub / (p.nblk * 4) : 0, rest = on ? sub - hq * (p.nblk * 4) : 0;
+        const int blk = rest >> 2, dv = (rest & 3) * 32 + lane;
+        const int g = hq * 4 / kHeads, hl = hq * 4 - g * kHeads;
+        const int b = p.meta[w].x;
+        const int left_slot = p.meta[w - 1].x == b ? 0 : 1;
         auto slot_of = [&](int k) -> int64_t {             // part k's place in the workspace
-            const int64_t s = k == 0 ? (w - 1) * 2 + left_slot : (w + k - 1) * 2;
-            return (s * p.G + g) * kHeads + row;
+            return static_cast<int64_t>(k == 0 ? (w - 1) * 2 + left_slot : (w + k - 1) * 2) * p.G + g;
         };
-        float M = __int_as_float(0xff800000);
-        for (int k = k0; k < parts; k += step) M = fmaxf(M, p.part_ml[slot_of(k)].x);
-        if (!few) {
-            if (lane == 0) red_m[warp] = M;
-            __syncthreads();
-            M = red_m[0];
-#pragma unroll
-            for (int i = 1; i < kJoinWarps; ++i) M = fmaxf(M, red_m[i]);
+        float M[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+        for (int k = k0; k < parts; k += step) {
+            const float4* ml = reinterpret_cast<const float4*>(p.part_ml + slot_of(k) * kHeads + hl);
+            const float4 x = ml[0], y = ml[1];
+            M[0] = fmaxf(M[0], x.x); M[1] = fmaxf(M[1], x.z);
+            M[2] = fmaxf(M[2], y.x); M[3] = fmaxf(M[3], y.z);
         }
-        const float base = M == __int_as_float(0xff800000) ? 0.f : M;
-        float L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!few) {
+            if (lane == 0) red_m[warp] = make_float4(M[0], M[1], M[2], M[3]);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kJoinWarps; ++i) {
+                const float4 x = red_m[i];
+                M[0] = fmaxf(M[0], x.x); M[1] = fmaxf(M[1], x.y);
+                M[2] = fmaxf(M[2], x.z); M[3] = fmaxf(M[3], x.w);
+            }
+        }
+        float base[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) base[j] = M[j] == kNegInf ? 0.f : M[j];
+        float L[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
         for (int k = k0; k < parts; k += step) {
             const int64_t s = slot_of(k);
-            const float2 ml = p.part_ml[s];
-            const float4 o = *reinterpret_cast<const float4*>(p.part_o + s * DV + blk * 128 + lane * 4);
-            const float f = exp2_fast(ml.x - base);
-            L = fmaf(ml.y, f, L);
-            acc.x = fmaf(o.x, f, acc.x);
-            acc.y = fmaf(o.y, f, acc.y);
-            acc.z = fmaf(o.z, f, acc.z);
-            acc.w = fmaf(o.w, f, acc.w);
+            const float4* ml = reinterpret_cast<const float4*>(p.part_ml + s * kHeads + hl);
+            const float4 x = ml[0], y = ml[1];
+            const float4 o = reinterpret_cast<const float4*>(p.part_o)[((s * p.nblk + blk) * 16 + hl / 4) * 128 + dv];
+            const float f[4] = {exp2_fast(x.x - base[0]), exp2_fast(x.z - base[1]), exp2_fast(y.x - base[2]),
+                                exp2_fast(y.z - base[3])};
+            L[0] = fmaf(x.y, f[0], L[0]); L[1] = fmaf(x.w, f[1], L[1]);
+            L[2] = fmaf(y.y, f[2], L[2]); L[3] = fmaf(y.w, f[3], L[3]);
+            acc[0] = fmaf(o.x, f[0], acc[0]); acc[1] = fmaf(o.y, f[1], acc[1]);
+            acc[2] = fmaf(o.z, f[2], acc[2]); acc[3] = fmaf(o.w, f[3], acc[3]);
         }
         if (!few) {
-            red[warp][lane] = acc;
-            if (lane == 0) red_l[warp] = L;
+            red[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (lane == 0) red_l[warp] = make_float4(L[0], L[1], L[2], L[3]);
             __syncthreads();
             if (warp == 0) {
 #pragma unroll
                 for (int i = 1; i < kJoinWarps; ++i) {
-                    const float4 o = red[i][lane];
-                    acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
-                    L += red_l[i];
+                    const float4 o = red[i][lane], q = red_l[i];
+                    acc[0] += o.x; acc[1] += o.y; acc[2] += o.z; acc[3] += o.w;
+                    L[0] += q.x; L[1] += q.y; L[2] += q.z; L[3] += q.w;
                 }
             }
         }
-        if (on && (few || warp == 0) && bounds_ok(me.x < p.B && h < p.H)) {
-            const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
-            const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-            const __nv_bfloat162 c = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            uint2 v;
-            memcpy(&v.x, &a, 4);
-            memcpy(&v.y, &c, 4);
-            *reinterpret_cast<uint2*>(p.out + me.x * p.ldo_b + h * p.ldo_h + blk * 128 + lane * 4) = v;
-            if (p.lse && blk == 0 && lane == 0)
-                p.lse[me.x * p.ldl_b + h] = L == 0.f ? __int_as_float(0xff800000) : (M + log2f(L)) * kLn2;
+        if (on && (few || warp == 0) && bounds_ok(b < p.B)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int h = hq * 4 + j;
+                if (h >= p.H) continue;
+                const float inv = L[j] > 0.f || L[j] != L[j] ? 1.0f / L[j] : 0.f;
+                p.out[b * p.ldo_b + h * p.ldo_h + blk * 128 + dv] = __float2bfloat16_rn(acc[j] * inv);
+                if (p.lse && rest == 0 && lane == 0)
+                    p.lse[b * p.ldl_b + h] = L[j] == 0.f ? kNegInf : (M[j] + log2f(L[j])) * kLn2;
+            }
         }
         if (!few) __syncthreads();                         // the buffers are free for the next item
     }
@@ -687,18 +819,35 @@ latent_attention_join_kernel(const Params p) {
 
 // --------------------------------------------------------------------- host
 
-// 3-D map of bf16 [n2][n1][n0] with strides ld2, ld1, 1 (elements); box 64
-// columns x rows x 1, 128-byte swizzle, zeros outside.
-bool make_map_3d(CUtensorMap* m, const void* base, int64_t n0, int64_t n1, int64_t n2, int64_t ld1, int64_t ld2, int rows) {
+bool encode_map(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+                const cuuint32_t* box) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(n0), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld1 * 2), static_cast<cuuint64_t>(ld2 * 2)};
-    cuuint32_t box[3] = {kChunkCols, static_cast<cuuint32_t>(rows), 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// q as [request][chunk][head][64 columns]: one copy brings all chunks of 64
+// heads (zeros past the last head).
+bool make_q_map(CUtensorMap* m, const void* q, int64_t B, int64_t H, int64_t ck, int64_t ld_tok, int64_t ld_head) {
+    const cuuint64_t dims[4] = {kChunkCols, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(ck), static_cast<cuuint64_t>(B)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld_head * 2), kChunkCols * 2, static_cast<cuuint64_t>(ld_tok * 2)};
+    const cuuint32_t box[4] = {kChunkCols, kHeads, static_cast<cuuint32_t>(ck), 1};
+    return encode_map(m, 4, q, dims, strides, box);
+}
+
+// The cache as [page][group of 8 tokens][chunk][token][64 columns]: one copy
+// brings `rows` tokens (whole groups) of one page with all their columns.
+bool make_cache_map(CUtensorMap* m, const void* cache, int64_t pages, int64_t page_size, int64_t ck, int64_t ld_page,
+                    int64_t ld_row, int rows) {
+    const cuuint64_t dims[5] = {kChunkCols, 8, static_cast<cuuint64_t>(ck), static_cast<cuuint64_t>(page_size / 8),
+                                static_cast<cuuint64_t>(pages)};
+    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(ld_row * 2), kChunkCols * 2, static_cast<cuuint64_t>(ld_row * 16),
+                                   static_cast<cuuint64_t>(ld_page * 2)};
+    const cuuint32_t box[5] = {kChunkCols, 8, static_cast<cuuint32_t>(ck), static_cast<cuuint32_t>(rows / 8), 1};
+    return encode_map(m, 5, cache, dims, strides, box);
 }
 
 // Workers of a call (CTAs per head group), bounded by the device and by the
@@ -717,7 +866,7 @@ Layout workspace_layout(int64_t W, int64_t G, int64_t DV) {
     Layout L;
     const int64_t slots = W * 2 * G * kHeads;
     L.meta = 0;
-    L.ml = (W * 16 + 255) / 256 * 256;
+    L.ml = (W * 8 + 255) / 256 * 256;
     L.o = (L.ml + slots * 8 + 255) / 256 * 256;
     L.total = L.o + slots * DV * 4;
     return L;
@@ -816,7 +965,7 @@ extern "C" dsnq_status dsnq_paged_latent_attention(
     p.lse = lse; p.ldl_b = ldl_tok;
     const Layout lay = workspace_layout(p.W, G, DV);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.meta = reinterpret_cast<int4*>(ws + lay.meta);
+    p.meta = reinterpret_cast<int2*>(ws + lay.meta);
     p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
     p.part_o = reinterpret_cast<float*>(ws + lay.o);
     const uint64_t t = debug_wait_timeout_ns();
@@ -826,15 +975,15 @@ extern "C" dsnq_status dsnq_paged_latent_attention(
     CUtensorMap mq, mk;
     // A lone token or head has no stride of its own: any valid one will do.
     const int64_t qh = H > 1 ? ldq_head : DK, qt = B > 1 ? ldq_tok : H * qh;
-    if (!make_map_3d(&mq, q, DK, H, B, qh, qt, kHeads) ||
-        !make_map_3d(&mk, cache, DK, page_size, num_pages, ld_row, ld_page, p.box_rows))
+    if (!make_q_map(&mq, q, B, H, p.ck, qt, qh) ||
+        !make_cache_map(&mk, cache, num_pages, page_size, p.ck, ld_page, ld_row, p.box_rows))
         return DSNQ_ERR_CUDA;
     if (!set_smem_attr(reinterpret_cast<const void*>(latent_attention_kernel), smem)) return DSNQ_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = launch_result(launch_kernel(latent_attention_kernel, dim3(static_cast<unsigned>(p.W * G)), dim3(kThreads), smem, s,
                                      mq, mk, p));
     if (st != DSNQ_OK || p.W == 1) return st;
-    const int64_t items = static_cast<int64_t>(p.W - 1) * H * p.nblk / kJoinWarps + 1;
+    const int64_t items = ((H + 3) / 4 * p.nblk * 4 + kJoinWarps - 1) / kJoinWarps * (p.W - 1);
     const int64_t grid = items < 4 * sms ? items : 4 * sms;
     return launch_result(launch_kernel(latent_attention_join_kernel, dim3(static_cast<unsigned>(grid)),
                                        dim3(kJoinWarps * 32), 0, s, p));
