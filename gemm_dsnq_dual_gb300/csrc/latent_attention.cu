@@ -27,8 +27,11 @@
 // two S buffers; heads x DV at M = 64 would take all 512.
 // P is rounded to bf16 (half a step, 2^-9 relative) because the tensor core
 // takes bf16; sums, maxima and O stay in fp32, and the sum is of the unrounded p.
-// Warps: 0 copies tiles (TMA), 1 issues the MMAs, 2..5 the softmax, the
-// rescaling of O and the output.  S(n+1) is computed while softmax(n) runs.
+// Warps: 0 copies tiles (TMA), 1 issues the products Q K^T, 6 the products P V,
+// 2..5 do the softmax, the rescaling of O and the output.  S(n+1) is computed
+// while softmax(n) runs.  Two issuing warps, because the two products wait for
+// different things (a copy, a softmax): one warp that polls both barriers
+// spends more time on the polls than the tensor core on the products.
 // The running maximum is raised (and O rescaled) only when a row's maximum
 // grew by more than 2^8: until then p <= 2^8 is harmless in fp32 and bf16.
 
@@ -47,15 +50,18 @@ namespace attn {
 constexpr int kHeads = 64;            // heads of a CTA
 constexpr int kTile = 64;             // tokens of a tile
 constexpr int kChunkCols = 64;        // columns of a 128-byte swizzled chunk
-constexpr int kChunkBytes = 64 * 128; // 64 rows
-constexpr int kThreads = 192;
+constexpr int kChunkBytes = 64 * 128; // one chunk of a tile
+constexpr int kPairBytes = 2 * kChunkBytes;
+constexpr int kThreads = 224;
 constexpr int kSoftWarps = 4;
-constexpr int kMaxStages = 8;
+constexpr int kMaxPairs = 13;         // slots of the ring of chunk pairs
+constexpr int kMaxOdd = 3;            // slots of the ring of odd chunks
 constexpr int kMaxCtas = 160;         // bound of workers x head groups
 constexpr int kTmemCols = 512;
 constexpr int kTmemS = 256;           // first column of the two S buffers
 constexpr float kRaise = 8.0f;        // log2 by which a maximum may grow before O is rescaled
 constexpr int kMiscBytes = 2048;
+constexpr int kMaxSnap = 3;           // tiles that a cut may move to a request's border
 constexpr int kRequestUnits = 2;      // what a request costs a worker beside its tiles, in tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -68,7 +74,8 @@ struct Params {
     int width, page_size, box_rows, num_pages;   // box_rows: tokens of one copy
     int64_t cap;                      // tokens the table can hold per request
     int ck, nblk;                     // 64-column chunks of a row, 128-column blocks of the value
-    int stages;
+    int q_rows;                       // rows of a chunk of q in shared memory (heads, a multiple of 8)
+    int pair_slots, odd_slots;        // slots of the two rings
     float scale_log2;
     __nv_bfloat16* out;
     int64_t ldo_b, ldo_h;
@@ -95,33 +102,59 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(w)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t group,
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t chunk, int32_t group,
                                             int32_t page) {
     asm volatile(
         "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(group), "r"(page)
+        " [%0], [%1, {%3, %3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(chunk), "r"(group), "r"(page)
         : "memory");
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, bf16 x bf16 -> fp32 (elected lane).
-__device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// A place in a ring of shared-memory slots and the parity of its pass.
+struct Place {
+    int i = 0;
+    uint32_t pass = 0;
+    __device__ __forceinline__ void step(int slots) {
+        if (++i == slots) {
+            i = 0;
+            pass ^= 1;
+        }
+    }
+};
+
+// Four steps of D[tmem] (+)= A[smem] * B[smem]^T, bf16 x bf16 -> fp32, K = 16
+// each; A and B advance by ASTEP and BSTEP (16-byte units) a step, the first
+// overwrites D when !accumulate.  One elected lane issues all four: with an
+// election and 64-bit descriptor arithmetic for each, the issuing warp itself
+// held the products back (61 cycles a step against 39).
+template <int ASTEP, int BSTEP>
+__device__ __forceinline__ void tc_mma4_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.u64 a, %1, %5;\n\tadd.u64 b, %2, %6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, %7;\n\tadd.u64 b, %2, %8;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, %9;\n\tadd.u64 b, %2, %10;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(ASTEP), "n"(BSTEP), "n"(2 * ASTEP), "n"(2 * BSTEP),
+        "n"(3 * ASTEP), "n"(3 * BSTEP)
         : "memory");
 }
 
-// Shared-memory descriptors.  A cache tile lies as [8 groups of 8 tokens][ck
-// chunks of 64 columns][8 tokens][128 bytes], 128-byte swizzle: one copy then
-// takes whole groups with all their columns, whatever the page size.  Read
-// K-major (S = Q K^T), the next 8 rows are a group (ck KB) on.  Read
-// column-major (V^T: M runs along the 64 columns of a chunk and on to the
-// next chunk, 1 KB on; K runs down the tokens), likewise.
+// Shared-memory descriptors.  A tile comes in pairs of 64-column chunks (16 KB)
+// and, when the row has an odd number of chunks, one chunk (8 KB) by itself.  A
+// pair lies as [8 groups of 8 tokens][2 chunks][8 tokens][128 bytes], 128-byte
+// swizzle: one copy then takes whole groups of a page, whatever its size.  Read
+// K-major (S = Q K^T), the next 8 tokens are a group (2 KB; odd chunk: 1 KB)
+// on.  Read column-major (V^T: M runs along the 64 columns of a chunk and on to
+// the next chunk, 1 KB on; K runs down the tokens), likewise.
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lead, uint32_t stride) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr >> 4) & 0x3FFF);
@@ -218,25 +251,30 @@ struct Run {
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kv,
-                        const Params p) {
+latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_pair,
+                        const __grid_constant__ CUtensorMap map_odd, const Params p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int tile_bytes = p.ck * kChunkBytes;
-    uint8_t* q_s = smem;                                   // [ck][64 heads][128 B]
-    uint8_t* p_s = q_s + tile_bytes;                       // [64 heads][128 B]
-    uint8_t* kv_s = p_s + kChunkBytes;                     // [stages][8 groups][ck][8 tokens][128 B]
-    uint8_t* misc = kv_s + p.stages * tile_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(misc);    // [kMaxStages]
-    uint64_t* empty = full + kMaxStages;                   // [kMaxStages]
-    uint64_t* qfull = empty + kMaxStages;
+    const int pairs = p.ck >> 1;
+    const bool odd = p.ck & 1;
+    const int q_bytes = p.ck * p.q_rows * 128;
+    uint8_t* q_s = smem;                                   // [ck][q_rows][128 B]
+    uint8_t* p_s = q_s + q_bytes;                          // [64 heads][128 B]
+    uint8_t* pair_s = p_s + kChunkBytes;                   // [pair_slots][8 groups][2][8 tokens][128 B]
+    uint8_t* odd_s = pair_s + p.pair_slots * kPairBytes;   // [odd_slots][8 groups][8 tokens][128 B]
+    uint8_t* misc = odd_s + p.odd_slots * kChunkBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(misc);    // [kMaxPairs]
+    uint64_t* empty = full + kMaxPairs;                    // [kMaxPairs]
+    uint64_t* ofull = empty + kMaxPairs;                   // [kMaxOdd]
+    uint64_t* oempty = ofull + kMaxOdd;                    // [kMaxOdd]
+    uint64_t* qfull = oempty + kMaxOdd;
     uint64_t* qempty = qfull + 1;
     uint64_t* sfull = qempty + 1;                          // [2]
     uint64_t* sempty = sfull + 2;                          // [2]
     uint64_t* pfull = sempty + 2;
     uint64_t* pempty = pfull + 1;
-    uint64_t* drain = pempty + 1;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* drain = pempty + 1;                          // [2] abort: products already issued
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     int* run_s = reinterpret_cast<int*>(tmem_holder + 2);  // [4] first request and tile, end request and tile
     int64_t* sums = reinterpret_cast<int64_t*>(tmem_holder + 6);   // [kThreads / 32]
@@ -247,9 +285,13 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     const int w = blockIdx.x / p.G, g = blockIdx.x - w * p.G;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
+        for (int s = 0; s < kMaxPairs; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int s = 0; s < kMaxOdd; ++s) {
+            mbar_init(smem_u32(&ofull[s]), 1);
+            mbar_init(smem_u32(&oempty[s]), 1);
         }
         mbar_init(smem_u32(qfull), 1);
         mbar_init(smem_u32(qempty), 1);
@@ -259,11 +301,12 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         }
         mbar_init(smem_u32(pfull), kSoftWarps);
         mbar_init(smem_u32(pempty), 1);
-        mbar_init(smem_u32(drain), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&drain[i]), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tma_prefetch_desc(&map_q);
-        tma_prefetch_desc(&map_kv);
+        tma_prefetch_desc(&map_pair);
+        if (odd) tma_prefetch_desc(&map_odd);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
@@ -298,6 +341,9 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             total += sums[i];
         }
         const int64_t workers = total < p.W ? total : p.W;
+        // A part costs its write and its read in the join, so a cut that would
+        // leave a sliver of a request moves to the request's border.
+        const int snap = static_cast<int>(min(total / workers / 4, static_cast<int64_t>(kMaxSnap)));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int64_t u = w + e < workers ? (w + e) * total / workers : total;
@@ -312,8 +358,14 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     at += n;
                     n = kRequestUnits + tiles_of(request_len(p, ++b));
                 }
+                int tile = max(static_cast<int>(u - at) - kRequestUnits, 0);
+                if (tile < snap) tile = 0;
+                else if (n - kRequestUnits - tile < snap) {
+                    tile = 0;
+                    ++b;
+                }
                 run_s[2 * e] = b;
-                run_s[2 * e + 1] = max(static_cast<int>(u - at) - kRequestUnits, 0);
+                run_s[2 * e + 1] = tile;
             }
         }
     }
@@ -330,13 +382,20 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     const int b_first = run.b;
     if (threadIdx.x == 0 && g == 0) p.meta[w] = make_int2(run.b, run.t0);
 
+    // The issuing warps' wait: the vote makes the result, and so the control
+    // flow after it, uniform to the compiler, which then keeps descriptors in
+    // uniform registers, where tcgen05.mma takes them.
+    auto wait_uniform = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_bounded<true>(bar, parity, abort_flag, tmo));
+    };
+
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
         const int pieces = kTile / p.box_rows;             // copies of a tile (1, 2, 4 or 8)
         const int batch = 32 / pieces;                     // tiles whose table entries the lanes hold
-        const uint32_t piece_bytes = p.box_rows * 128 * p.ck;
-        uint32_t n = 0, nq = 0;
-        bool ok = true;
+        uint32_t nq = 0;
+        Place pp, po;
+        bool ok = true, skip = (p.inject & kInjectSkipLoad) != 0;
         for (; ok && run.next(p); run.advance()) {
             if (run.len == 0) continue;
             const int32_t* row = p.table + run.b * p.ld_table;
@@ -344,11 +403,11 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             ok = wait_bounded(smem_u32(qempty), (nq & 1) ^ 1, abort_flag, tmo);
             if (!ok) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(smem_u32(qfull), tile_bytes);
+                mbar_arrive_expect_tx(smem_u32(qfull), q_bytes);
                 tma_load_4d(smem_u32(q_s), &map_q, smem_u32(qfull), g * kHeads, run.b);
             }
             ++nq;
-            for (int i = 0; i < run.n; ++i, ++n) {
+            for (int i = 0; ok && i < run.n; ++i) {
                 const int tile = run.t0 + i;
                 if (i % batch == 0) {
                     const int64_t tok = static_cast<int64_t>(tile) * kTile + static_cast<int64_t>(lane) * p.box_rows;
@@ -362,102 +421,109 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                         }
                     }
                 }
-                const int s = n % p.stages;
-                ok = wait_bounded(smem_u32(&empty[s]), ((n / p.stages) & 1) ^ 1, abort_flag, tmo);
-                if (!ok) break;
                 const int tok0 = tile * kTile;
                 const int live = min(pieces, (run.len - tok0 + p.box_rows - 1) / p.box_rows);
-                const uint32_t fb = smem_u32(&full[s]);
-                if ((p.inject & kInjectSkipLoad) && n == 0) continue;   // test hook: the waits on it run out
-                if (lane == 0) mbar_arrive_expect_tx(fb, live * piece_bytes);
-                __syncwarp();
                 const int id = __shfl_sync(0xffffffffu, ids, (i % batch) * pieces + (lane & (pieces - 1)));
-                if (lane < live)
-                    tma_load_5d(smem_u32(kv_s) + s * tile_bytes + lane * piece_bytes, &map_kv, fb,
-                                (tok0 + lane * p.box_rows) % p.page_size / 8, id);
+                const int group = (tok0 + lane * p.box_rows) % p.page_size / 8;
+                if (odd) {
+                    ok = wait_bounded(smem_u32(&oempty[po.i]), po.pass ^ 1, abort_flag, tmo);
+                    if (!ok) break;
+                    const uint32_t fb = smem_u32(&ofull[po.i]);
+                    if (lane == 0) mbar_arrive_expect_tx(fb, live * p.box_rows * 128);
+                    __syncwarp();
+                    if (lane < live)
+                        tma_load_5d(smem_u32(odd_s) + po.i * kChunkBytes + lane * p.box_rows * 128, &map_odd, fb, p.ck - 1, group, id);
+                    po.step(p.odd_slots);
+                }
+                for (int j = 0; j < pairs; ++j) {
+                    ok = wait_bounded(smem_u32(&empty[pp.i]), pp.pass ^ 1, abort_flag, tmo);
+                    if (!ok) break;
+                    const uint32_t fb = smem_u32(&full[pp.i]);
+                    if (!skip) {                           // test hook: the first pair never comes, the waits on it run out
+                        if (lane == 0) mbar_arrive_expect_tx(fb, live * p.box_rows * 256);
+                        __syncwarp();
+                        if (lane < live)
+                            tma_load_5d(smem_u32(pair_s) + pp.i * kPairBytes + lane * p.box_rows * 256, &map_pair, fb, 2 * j, group,
+                                        id);
+                    }
+                    skip = false;
+                    pp.step(p.pair_slots);
+                }
             }
         }
         if (!ok) settle_ns(kAbortSettleNs);                // copies already issued land before the CTA goes
     } else if (warp == 1) {
-        // --------------------------------------------------------- MMA issuer
-        // Two products wait for different things: Q K^T of tile n for its copy,
-        // P V of tile k < n for its softmax.  Whichever is ready is issued: a
-        // P V held back behind the next tile's copy would hold the stage that
-        // the copy after it needs.
-        const uint32_t id_s = idesc_bf16(64, kTile, false), id_o = idesc_bf16(128, kHeads, true);
-        const uint32_t group = p.ck * 1024;                // bytes of 8 tokens
-        const uint64_t q_desc = smem_desc_sw128(smem_u32(q_s), 16, 1024), p_desc = smem_desc_sw128(smem_u32(p_s), 16, 1024);
-        uint32_t n = 0, k = 0, nq = 0;
-        uint32_t firsts = 0;                               // bit n % 32: tile n is its request's first of the run
-        int i = 0;
-        bool ok = true, q_here = false, more = false;
-        auto next_request = [&]() {
-            while ((more = run.next(p)) && run.len == 0) run.advance();
-            i = 0;
-            q_here = false;
-        };
-        auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity)); };
-        next_request();
-        uint64_t t_wait = now_ns();
-        uint32_t polls = 0;
-        while (more || k < n) {
-            if (k < n && ready(pfull, k & 1)) {
+        // ------------------------------------------------- products S = Q K^T
+        // Chunk pair by chunk pair as they land.
+        const uint32_t id_s = idesc_bf16(64, kTile, false);
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(q_s), 16, 1024);
+        const uint32_t q_chunk = p.q_rows * 128 >> 4;      // descriptor step of a chunk of q
+        Place po, pp;
+        uint32_t n = 0, nq = 0;
+        bool ok = true;
+        for (; ok && run.next(p); run.advance()) {
+            if (run.len == 0) continue;
+            ok = wait_uniform(smem_u32(qfull), nq & 1);
+            ++nq;
+            for (int i = 0; ok && i < run.n; ++i, ++n) {
+                ok = wait_uniform(smem_u32(&sempty[n & 1]), ((n >> 1) & 1) ^ 1);
                 tc_fence_after();
-                const int s = k % p.stages;
-                const uint32_t v0 = smem_u32(kv_s) + s * tile_bytes;
-                const bool first = (firsts >> (k & 31)) & 1;
-                for (int blk = 0; blk < p.nblk; ++blk) {
-#pragma unroll
-                    for (int j = 0; j < kTile / 16; ++j)
-                        tc_mma_bf16(tmem + blk * kHeads, smem_desc_sw128(v0 + blk * 2048 + j * 2 * group, 1024, group),
-                                    p_desc + j * 2, id_o, !(first && j == 0));
+                const uint32_t d = tmem + kTmemS + (n & 1) * kTile;
+                if (odd && ok) {
+                    ok = wait_uniform(smem_u32(&ofull[po.i]), po.pass);
+                    if (!ok) break;
+                    tc_mma4_bf16<2, 2>(d, q_desc + (p.ck - 1) * q_chunk, smem_desc_sw128(smem_u32(odd_s) + po.i * kChunkBytes, 16, 1024),
+                                       id_s, 0);
+                    tc_commit(smem_u32(&oempty[po.i]));
+                    po.step(p.odd_slots);
                 }
-                tc_commit(smem_u32(&empty[s]));
-                tc_commit(smem_u32(pempty));
-                ++k;
-                polls = 0;
-                continue;
-            }
-            if (more) {
-                if (!q_here) q_here = ready(qfull, nq & 1);
-                const int s = n % p.stages;
-                if (q_here && ready(&full[s], (n / p.stages) & 1) && ready(&sempty[n & 1], ((n >> 1) & 1) ^ 1)) {
-                    tc_fence_after();
-                    const uint64_t k_desc = smem_desc_sw128(smem_u32(kv_s) + s * tile_bytes, 16, group);
-                    for (int c = 0; c < p.ck; ++c) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            tc_mma_bf16(tmem + kTmemS + (n & 1) * kTile, q_desc + c * (kChunkBytes >> 4) + j * 2,
-                                        k_desc + c * (1024 >> 4) + j * 2, id_s, (c | j) != 0);
-                    }
-                    tc_commit(smem_u32(&sfull[n & 1]));
-                    firsts = (firsts & ~(1u << (n & 31))) | (i == 0 ? 1u << (n & 31) : 0u);
-                    ++n;
-                    if (++i == run.n) {
-                        tc_commit(smem_u32(qempty));
-                        ++nq;
-                        run.advance();
-                        next_request();
-                    }
-                    polls = 0;
-                    continue;
+                for (int j = 0; ok && j < pairs; ++j) {
+                    ok = wait_uniform(smem_u32(&full[pp.i]), pp.pass);
+                    if (!ok) break;
+                    const uint64_t kd = smem_desc_sw128(smem_u32(pair_s) + pp.i * kPairBytes, 16, 2048);
+                    const uint64_t qd = q_desc + 2 * j * q_chunk;
+                    tc_mma4_bf16<2, 2>(d, qd, kd, id_s, odd || j > 0);
+                    tc_mma4_bf16<2, 2>(d, qd + q_chunk, kd + 64, id_s, 1);
+                    if (j >= p.nblk) tc_commit(smem_u32(&empty[pp.i]));   // no part of the value
+                    pp.step(p.pair_slots);
                 }
-            }
-            if (polls == 0) t_wait = now_ns();
-            if ((++polls & 63) == 0) {                     // bounded, as every wait
-                if (now_ns() - t_wait > tmo) {
-                    *abort_flag = 1;
-                    if (lane == 0) atomicOr(&g_status, kStatusTimeout);
-                }
-                if (__any_sync(0xffffffffu, *abort_flag)) {
-                    ok = false;
-                    break;
-                }
+                if (!ok) break;
+                tc_commit(smem_u32(&sfull[n & 1]));
+                if (i == run.n - 1) tc_commit(smem_u32(qempty));
             }
         }
-        if (!ok) {                                         // MMAs already issued end before their memory goes
-            tc_commit(smem_u32(drain));
-            wait_drain(smem_u32(drain), 0, tmo);
+        if (!ok) {                                         // products already issued end before their memory goes
+            tc_commit(smem_u32(&drain[0]));
+            wait_drain(smem_u32(&drain[0]), 0, tmo);
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------- products O^T += V^T P^T
+        // They free the chunk pairs one by one.
+        const int heads = min(kHeads, p.H - g * kHeads);
+        const uint32_t id_o = idesc_bf16(128, (heads + 15) & ~15, true);
+        const uint64_t p_desc = smem_desc_sw128(smem_u32(p_s), 16, 1024);
+        Place pv;
+        uint32_t n = 0;
+        bool ok = true;
+        for (; ok && run.next(p); run.advance()) {
+            if (run.len == 0) continue;
+            for (int i = 0; i < run.n; ++i, ++n) {
+                ok = wait_uniform(smem_u32(pfull), n & 1);
+                if (!ok) break;
+                tc_fence_after();
+                for (int blk = 0; blk < p.nblk; ++blk) {
+                    tc_mma4_bf16<4096 / 16, 2>(tmem + blk * kHeads,
+                                               smem_desc_sw128(smem_u32(pair_s) + pv.i * kPairBytes, 1024, 2048), p_desc, id_o, i > 0);
+                    tc_commit(smem_u32(&empty[pv.i]));
+                    pv.step(p.pair_slots);
+                }
+                tc_commit(smem_u32(pempty));
+                for (int j = p.nblk; j < pairs; ++j) pv.step(p.pair_slots);
+            }
+        }
+        if (!ok) {
+            tc_commit(smem_u32(&drain[1]));
+            wait_drain(smem_u32(&drain[1]), 0, tmo);
         }
     } else {
         // ------------------------------------- softmax, rescaling and output
@@ -473,7 +539,9 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         const int p_row = quad * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
         const uint32_t p_addr = smem_u32(p_s) + p_row * 128;
         const int p_grp = lane >> 4, p_swz = lane & 7;
-        const int DV = p.nblk * 128;
+        const int DV = p.nblk * 128, heads = min(kHeads, p.H - g * kHeads);
+        const bool mine = quad * 16 < heads;               // this warp's rows of S hold heads
+        int zslot = 0;                                     // slot of tile n's first pair
         uint32_t n = 0;
         bool ok = true;                                    // false: only the barriers are kept up
         for (; run.next(p); run.advance()) {
@@ -529,7 +597,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     // Raise the maximum when it grew too far (always on the first tile).
                     alpha[a] = 1.f;
-                    if ((top - m[a]) * p.scale_log2 > kRaise) {
+                    if (row0 + 8 * a < heads && (top - m[a]) * p.scale_log2 > kRaise) {
                         raise |= i > 0;
                         alpha[a] = exp2_fast((m[a] - top) * p.scale_log2);
                         m[a] = top;
@@ -556,6 +624,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     tmem_wait_st();
                 }
                 uint32_t pk[2][8];
+                if (mine) {
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
                     const float off = m[a] == kNegInf ? 0.f : m[a] * p.scale_log2;
@@ -570,27 +639,32 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     }
                     l[a] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
+                }
                 if (n > 0) ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
                 __syncwarp();
                 if (ok) {
+                    if (mine) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         stmatrix_x4(p_addr + (((2 * j + p_grp) ^ p_swz) << 4), pk[0][2 * j], pk[1][2 * j], pk[0][2 * j + 1],
                                     pk[1][2 * j + 1]);
+                    }
                     if (valid < kTile) {
                         // Rows past the length hold whatever the page or the
                         // buffer held: 0 * NaN would reach O, so they become 0.
-                        const int stage = n % p.stages;
-                        ok = wait_bounded(smem_u32(&full[stage]), (n / p.stages) & 1, abort_flag, tmo);
-                        uint8_t* kv = kv_s + stage * tile_bytes;
+                        // (S of this tile is done, so its pairs have landed.)
                         const int words = p.nblk * 16;     // 16-byte words of a row's value
-                        for (int e = st; ok && e < (kTile - valid) * words; e += 128) {
+                        for (int e = st; e < (kTile - valid) * words; e += 128) {
                             const int r = valid + e / words, v = e % words;
-                            *reinterpret_cast<uint4*>(kv + ((r >> 3) * p.ck + (v >> 3)) * 1024 + (r & 7) * 128 + (v & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
+                            int slot = zslot + (v >> 4);
+                            if (slot >= p.pair_slots) slot -= p.pair_slots;
+                            *reinterpret_cast<uint4*>(pair_s + slot * kPairBytes + (r >> 3) * 2048 + ((v >> 3) & 1) * 1024 +
+                                                      (r & 7) * 128 + (v & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
                     }
                 }
+                zslot += pairs;
+                while (zslot >= p.pair_slots) zslot -= p.pair_slots;
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
@@ -617,7 +691,6 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             }
             soft_sync_or(false);                           // inv_s is next written after another tile's barrier
             __syncwarp();
-            const int heads = min(kHeads, p.H - g * kHeads);
             if (!ok) continue;
             if (whole) {
                 // 32 values x 32 heads at a time, through the warp's own 2 KB
@@ -692,128 +765,150 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 // found at the first cut inside it; its parts are those of the worker before
 // that cut and of the workers that begin inside it, in the order of the tokens.
 //   out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k,  M = max_k m_k
-// An item is 32 values of four heads: one lane holds one value of the four
-// (16 bytes of a part).  With few parts (<= 8) one warp takes an item; with
-// many, the eight warps of a CTA share its parts.
+// A part's value is read as it lies: 16 bytes are four heads of one value.  An
+// item is one such group of four heads: with few parts all its values (each
+// thread takes two of them), with more one block of 128 values (two threads
+// share a value's parts) or 32 values (eight threads do), so that a thread has
+// a handful of loads, in flight at once, whatever the number of parts.  The
+// parts' factors are formed once per item, in shared memory.
 // ---------------------------------------------------------------------------
-constexpr int kJoinWarps = 8;
-constexpr int kFewParts = 8;
+constexpr int kJoinThreads = 256;
+constexpr int kFewParts = 6, kSomeParts = 16;
 
-__global__ void __launch_bounds__(kJoinWarps * 32)
+__global__ void __launch_bounds__(kJoinThreads)
 latent_attention_join_kernel(const Params p) {
     grid_dependency_wait();
     allow_dependent_launch();
     bounds_self_test(p.inject);
+    __shared__ int2 meta_s[kMaxCtas + 1];
     __shared__ int first_item[kMaxCtas + 1];               // running item count by cut
-    __shared__ int parts_s[kMaxCtas];
-    __shared__ float4 red[kJoinWarps][32], red_l[kJoinWarps], red_m[kJoinWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ int parts_s[kMaxCtas], warp_items[kJoinThreads / 32];
+    __shared__ float2 ml_s[kMaxCtas][4];
+    __shared__ float4 fac_s[kMaxCtas];                     // factor of each part, for the four heads
+    __shared__ float4 red[kJoinThreads];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = threadIdx.x;
     const float kNegInf = __int_as_float(0xff800000);
-    const int quads = (p.H + 3) / 4, items = quads * p.nblk * 4;
+    const int quads = (p.H + 3) / 4;
 
-    if (threadIdx.x < static_cast<unsigned>(p.W)) {
-        int parts = 0;
-        const int w = threadIdx.x;
-        const int2 me = p.meta[w];
-        if (w > 0 && me.x < p.B && me.y > 0) {
-            const int2 left = p.meta[w - 1];
-            if (left.x != me.x || left.y == 0) {
-                parts = 2;
-                for (int k = w + 1; k < p.W; ++k) {
-                    const int2 o = p.meta[k];
-                    if (o.x != me.x || o.y == 0) break;
-                    ++parts;
-                }
-            }
-        }
-        parts_s[w] = parts;
-    }
+    // The cut before each worker: the parts of the request whose first cut it
+    // is (0: none), and the items of all cuts before it.
+    static_assert(kMaxCtas <= kJoinThreads, "one thread per cut");
+    if (t < p.W) meta_s[t] = p.meta[t];
     __syncthreads();
-    if (threadIdx.x == 0) {
-        int at = 0;
-        for (int w = 0; w < p.W; ++w) {
-            first_item[w] = at;
-            at += parts_s[w] == 0 ? 0 : (parts_s[w] <= kFewParts ? (items + kJoinWarps - 1) / kJoinWarps : items);
+    int parts = 0, count = 0;
+    if (t > 0 && t < p.W) {
+        const int2 me = meta_s[t], left = meta_s[t - 1];
+        if (me.x < p.B && me.y > 0 && (left.x != me.x || left.y == 0)) {
+            parts = 2;
+            for (int k = t + 1; k < p.W && meta_s[k].x == me.x && meta_s[k].y > 0; ++k) ++parts;
+            count = quads * (parts <= kFewParts ? 1 : parts <= kSomeParts ? p.nblk : p.nblk * 4);
         }
-        first_item[p.W] = at;
     }
+    int inc = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_items[warp] = inc;
     __syncthreads();
-    int w = 0;
-    for (int item = blockIdx.x; item < first_item[p.W]; item += gridDim.x) {
-        while (item >= first_item[w + 1]) ++w;
-        const int parts = parts_s[w];
-        const bool few = parts <= kFewParts;
-        const int sub = few ? (item - first_item[w]) * kJoinWarps + warp : item - first_item[w];
-        const int step = few ? 1 : kJoinWarps, k0 = few ? 0 : warp;
-        const bool on = sub < items;
-        // sub = (four heads, value block, 32 values)
-        const int hq = on ? sub / (p.nblk * 4) : 0, rest = on ? sub - hq * (p.nblk * 4) : 0;
-        const int blk = rest >> 2, dv = (rest & 3) * 32 + lane;
+    int before = inc - count;
+    for (int i = 0; i < warp; ++i) before += warp_items[i];
+    if (t < p.W) {
+        parts_s[t] = parts;
+        first_item[t] = before;
+    }
+    if (t == p.W - 1) first_item[p.W] = before + count;
+    __syncthreads();
+
+    const int last = first_item[p.W];
+    for (int item = blockIdx.x; item < last; item += gridDim.x) {
+        int w = 0, hi = p.W;                               // first_item[w] <= item < first_item[hi]
+        while (hi - w > 1) {
+            const int mid = (w + hi) >> 1;
+            if (first_item[mid] <= item) w = mid;
+            else hi = mid;
+        }
+        const int np = parts_s[w], b = meta_s[w].x, at = item - first_item[w];
+        const int share = np <= kFewParts ? 1 : np <= kSomeParts ? 2 : 8;       // threads to a value
+        const int split = share == 1 ? 1 : share == 2 ? p.nblk : p.nblk * 4;    // items to four heads
+        const int hq = at / split, sub = at - hq * split;
         const int g = hq * 4 / kHeads, hl = hq * 4 - g * kHeads;
-        const int b = p.meta[w].x;
-        const int left_slot = p.meta[w - 1].x == b ? 0 : 1;
+        const int left_slot = meta_s[w - 1].x == b ? 0 : 1;
         auto slot_of = [&](int k) -> int64_t {             // part k's place in the workspace
             return static_cast<int64_t>(k == 0 ? (w - 1) * 2 + left_slot : (w + k - 1) * 2) * p.G + g;
         };
-        float M[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-        for (int k = k0; k < parts; k += step) {
-            const float4* ml = reinterpret_cast<const float4*>(p.part_ml + slot_of(k) * kHeads + hl);
+        if (t < np) {
+            const float4* ml = reinterpret_cast<const float4*>(p.part_ml + slot_of(t) * kHeads + hl);
             const float4 x = ml[0], y = ml[1];
-            M[0] = fmaxf(M[0], x.x); M[1] = fmaxf(M[1], x.z);
-            M[2] = fmaxf(M[2], y.x); M[3] = fmaxf(M[3], y.z);
+            ml_s[t][0] = make_float2(x.x, x.y);
+            ml_s[t][1] = make_float2(x.z, x.w);
+            ml_s[t][2] = make_float2(y.x, y.y);
+            ml_s[t][3] = make_float2(y.z, y.w);
         }
-        if (!few) {
-            if (lane == 0) red_m[warp] = make_float4(M[0], M[1], M[2], M[3]);
-            __syncthreads();
+        __syncthreads();
+        if (warp < 4) {                                    // warp j: head j of the four
+            float M = kNegInf, L = 0.f;
+            for (int k = lane; k < np; k += 32) M = fmaxf(M, ml_s[k][warp].x);
 #pragma unroll
-            for (int i = 0; i < kJoinWarps; ++i) {
-                const float4 x = red_m[i];
-                M[0] = fmaxf(M[0], x.x); M[1] = fmaxf(M[1], x.y);
-                M[2] = fmaxf(M[2], x.z); M[3] = fmaxf(M[3], x.w);
-            }
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            const float base = M == kNegInf ? 0.f : M;
+            for (int k = lane; k < np; k += 32) L = fmaf(ml_s[k][warp].y, exp2_fast(ml_s[k][warp].x - base), L);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
+            for (int k = lane; k < np; k += 32)
+                reinterpret_cast<float*>(&fac_s[k])[warp] = exp2_fast(ml_s[k][warp].x - base) * inv;
+            const int h = hq * 4 + warp;
+            if (p.lse && sub == 0 && lane == 0 && h < p.H)
+                p.lse[b * p.ldl_b + h] = L == 0.f ? kNegInf : (M + log2f(L)) * kLn2;
         }
-        float base[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) base[j] = M[j] == kNegInf ? 0.f : M[j];
-        float L[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int k = k0; k < parts; k += step) {
-            const int64_t s = slot_of(k);
-            const float4* ml = reinterpret_cast<const float4*>(p.part_ml + s * kHeads + hl);
-            const float4 x = ml[0], y = ml[1];
-            const float4 o = reinterpret_cast<const float4*>(p.part_o)[((s * p.nblk + blk) * 16 + hl / 4) * 128 + dv];
-            const float f[4] = {exp2_fast(x.x - base[0]), exp2_fast(x.z - base[1]), exp2_fast(y.x - base[2]),
-                                exp2_fast(y.z - base[3])};
-            L[0] = fmaf(x.y, f[0], L[0]); L[1] = fmaf(x.w, f[1], L[1]);
-            L[2] = fmaf(y.y, f[2], L[2]); L[3] = fmaf(y.w, f[3], L[3]);
-            acc[0] = fmaf(o.x, f[0], acc[0]); acc[1] = fmaf(o.y, f[1], acc[1]);
-            acc[2] = fmaf(o.z, f[2], acc[2]); acc[3] = fmaf(o.w, f[3], acc[3]);
-        }
-        if (!few) {
-            red[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            if (lane == 0) red_l[warp] = make_float4(L[0], L[1], L[2], L[3]);
-            __syncthreads();
-            if (warp == 0) {
-#pragma unroll
-                for (int i = 1; i < kJoinWarps; ++i) {
-                    const float4 o = red[i][lane], q = red_l[i];
-                    acc[0] += o.x; acc[1] += o.y; acc[2] += o.z; acc[3] += o.w;
-                    L[0] += q.x; L[1] += q.y; L[2] += q.z; L[3] += q.w;
+        __syncthreads();
+        // This thread's values: v0, and with one thread to a value v0 + 256.
+        const int width = kJoinThreads / share;            // values of a pass
+        const int k0 = t / width, v0 = sub * width + (t - k0 * width), all = p.nblk * 128;
+        auto value_at = [&](int64_t s, int v) -> float4 {  // 128 values of a block, 16 groups of heads each
+            return __ldcs(reinterpret_cast<const float4*>(p.part_o) + ((s * p.nblk + (v >> 7)) * 16 + hl / 4) * 128 + (v & 127));
+        };
+        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        auto add = [](float4& a, const float4& o, const float4& f) {
+            a.x = fmaf(o.x, f.x, a.x);
+            a.y = fmaf(o.y, f.y, a.y);
+            a.z = fmaf(o.z, f.z, a.z);
+            a.w = fmaf(o.w, f.w, a.w);
+        };
+        if (share == 1) {
+            const bool two = v0 + width < all;
+            if (v0 < all) {
+#pragma unroll 3
+                for (int k = 0; k < np; ++k) {
+                    const int64_t s = slot_of(k);
+                    const float4 o0 = value_at(s, v0), o1 = two ? value_at(s, v0 + width) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    add(acc[0], o0, fac_s[k]);
+                    add(acc[1], o1, fac_s[k]);
                 }
             }
-        }
-        if (on && (few || warp == 0) && bounds_ok(b < p.B)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int h = hq * 4 + j;
-                if (h >= p.H) continue;
-                const float inv = L[j] > 0.f || L[j] != L[j] ? 1.0f / L[j] : 0.f;
-                p.out[b * p.ldo_b + h * p.ldo_h + blk * 128 + dv] = __float2bfloat16_rn(acc[j] * inv);
-                if (p.lse && rest == 0 && lane == 0)
-                    p.lse[b * p.ldl_b + h] = L[j] == 0.f ? kNegInf : (M[j] + log2f(L[j])) * kLn2;
+        } else {
+#pragma unroll 8
+            for (int k = k0; k < np; k += share) add(acc[0], value_at(slot_of(k), v0), fac_s[k]);
+            red[t] = acc[0];
+            __syncthreads();
+            if (k0 == 0) {
+                for (int i = 1; i < share; ++i) add(acc[0], red[t + i * width], make_float4(1.f, 1.f, 1.f, 1.f));
             }
         }
-        if (!few) __syncthreads();                         // the buffers are free for the next item
+        if (k0 == 0 && bounds_ok(b < p.B)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int v = v0 + i * width;
+                if (v >= all || (i == 1 && share != 1)) continue;
+                const float r[4] = {acc[i].x, acc[i].y, acc[i].z, acc[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (hq * 4 + j < p.H) p.out[b * p.ldo_b + (hq * 4 + j) * p.ldo_h + v] = __float2bfloat16_rn(r[j]);
+            }
+        }
+        __syncthreads();                                   // the buffers are free for the next item
     }
 }
 
@@ -831,22 +926,22 @@ bool encode_map(CUtensorMap* m, int rank, const void* base, const cuuint64_t* di
 
 // q as [request][chunk][head][64 columns]: one copy brings all chunks of 64
 // heads (zeros past the last head).
-bool make_q_map(CUtensorMap* m, const void* q, int64_t B, int64_t H, int64_t ck, int64_t ld_tok, int64_t ld_head) {
+bool make_q_map(CUtensorMap* m, const void* q, int64_t B, int64_t H, int64_t ck, int64_t ld_tok, int64_t ld_head, int rows) {
     const cuuint64_t dims[4] = {kChunkCols, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(ck), static_cast<cuuint64_t>(B)};
     const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld_head * 2), kChunkCols * 2, static_cast<cuuint64_t>(ld_tok * 2)};
-    const cuuint32_t box[4] = {kChunkCols, kHeads, static_cast<cuuint32_t>(ck), 1};
+    const cuuint32_t box[4] = {kChunkCols, static_cast<cuuint32_t>(rows), static_cast<cuuint32_t>(ck), 1};
     return encode_map(m, 4, q, dims, strides, box);
 }
 
 // The cache as [page][group of 8 tokens][chunk][token][64 columns]: one copy
-// brings `rows` tokens (whole groups) of one page with all their columns.
+// brings `chunks` chunks of `rows` tokens (whole groups) of one page.
 bool make_cache_map(CUtensorMap* m, const void* cache, int64_t pages, int64_t page_size, int64_t ck, int64_t ld_page,
-                    int64_t ld_row, int rows) {
+                    int64_t ld_row, int rows, int chunks) {
     const cuuint64_t dims[5] = {kChunkCols, 8, static_cast<cuuint64_t>(ck), static_cast<cuuint64_t>(page_size / 8),
                                 static_cast<cuuint64_t>(pages)};
     const cuuint64_t strides[4] = {static_cast<cuuint64_t>(ld_row * 2), kChunkCols * 2, static_cast<cuuint64_t>(ld_row * 16),
                                    static_cast<cuuint64_t>(ld_page * 2)};
-    const cuuint32_t box[5] = {kChunkCols, 8, static_cast<cuuint32_t>(ck), static_cast<cuuint32_t>(rows / 8), 1};
+    const cuuint32_t box[5] = {kChunkCols, 8, static_cast<cuuint32_t>(chunks), static_cast<cuuint32_t>(rows / 8), 1};
     return encode_map(m, 5, cache, dims, strides, box);
 }
 
@@ -953,12 +1048,17 @@ extern "C" dsnq_status dsnq_paged_latent_attention(
     p.box_rows = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : page_size % 16 == 0 ? 16 : 8;
     p.ck = static_cast<int>(DK / 64);
     p.nblk = static_cast<int>(DV / 128);
-    const int64_t tile_bytes = static_cast<int64_t>(p.ck) * kChunkBytes;
-    const int64_t fixed = 1024 + tile_bytes + kChunkBytes + kMiscBytes;
-    int64_t stages = (227 * 1024 - fixed) / tile_bytes;
-    if (stages > kMaxStages) stages = kMaxStages;
-    p.stages = static_cast<int>(stages);
-    const size_t smem = static_cast<size_t>(fixed + stages * tile_bytes);
+    p.q_rows = static_cast<int>(H < kHeads ? (H + 7) / 8 * 8 : kHeads);
+    // Shared memory: q, P, barriers, and the rest for the rings.  The MMA reads
+    // 64 rows of q whatever H is: past the last chunk's rows it reads P's buffer
+    // (rows of S that no head owns).
+    const int64_t fixed = 1024 + static_cast<int64_t>(p.ck) * p.q_rows * 128 + kChunkBytes + kMiscBytes;
+    int64_t room = 227 * 1024 - fixed;
+    p.odd_slots = p.ck & 1 ? 2 : 0;
+    p.pair_slots = static_cast<int>((room - p.odd_slots * kChunkBytes) / kPairBytes);
+    if (p.pair_slots > kMaxPairs) p.pair_slots = kMaxPairs;
+    if (p.odd_slots && room - p.pair_slots * kPairBytes >= kMaxOdd * kChunkBytes) p.odd_slots = kMaxOdd;
+    const size_t smem = static_cast<size_t>(fixed + p.pair_slots * kPairBytes + p.odd_slots * kChunkBytes);
     p.scale_log2 = scale * kLog2e;
     p.out = static_cast<__nv_bfloat16*>(out);
     p.ldo_b = ldo_tok; p.ldo_h = ldo_head;
@@ -972,19 +1072,20 @@ extern "C" dsnq_status dsnq_paged_latent_attention(
     p.timeout_ns = t ? t : kDefaultTimeoutNs;
     p.inject = debug_inject_flags();
 
-    CUtensorMap mq, mk;
+    CUtensorMap mq, mk, mo;
     // A lone token or head has no stride of its own: any valid one will do.
     const int64_t qh = H > 1 ? ldq_head : DK, qt = B > 1 ? ldq_tok : H * qh;
-    if (!make_q_map(&mq, q, B, H, p.ck, qt, qh) ||
-        !make_cache_map(&mk, cache, num_pages, page_size, p.ck, ld_page, ld_row, p.box_rows))
+    if (!make_q_map(&mq, q, B, H, p.ck, qt, qh, p.q_rows) ||
+        !make_cache_map(&mk, cache, num_pages, page_size, p.ck, ld_page, ld_row, p.box_rows, 2) ||
+        !make_cache_map(&mo, cache, num_pages, page_size, p.ck, ld_page, ld_row, p.box_rows, 1))
         return DSNQ_ERR_CUDA;
     if (!set_smem_attr(reinterpret_cast<const void*>(latent_attention_kernel), smem)) return DSNQ_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = launch_result(launch_kernel(latent_attention_kernel, dim3(static_cast<unsigned>(p.W * G)), dim3(kThreads), smem, s,
-                                     mq, mk, p));
+                                     mq, mk, mo, p));
     if (st != DSNQ_OK || p.W == 1) return st;
-    const int64_t items = ((H + 3) / 4 * p.nblk * 4 + kJoinWarps - 1) / kJoinWarps * (p.W - 1);
+    const int64_t items = (H + 3) / 4 * p.nblk * 4 * (p.W - 1);
     const int64_t grid = items < 4 * sms ? items : 4 * sms;
     return launch_result(launch_kernel(latent_attention_join_kernel, dim3(static_cast<unsigned>(grid)),
-                                       dim3(kJoinWarps * 32), 0, s, p));
+                                       dim3(kJoinThreads), 0, s, p));
 }
