@@ -40,6 +40,7 @@
 #include <cuda_runtime.h>
 
 #include "debug_check.cuh"
+#include "group_quant.cuh"
 #include "dsnq_internal.h"
 #include "tensor_host.h"
 #include "tensor_ptx.cuh"
@@ -61,8 +62,7 @@ constexpr int kTmemCols = 512;
 constexpr int kTmemS = 256;           // first column of the two S buffers
 constexpr float kRaise = 8.0f;        // log2 by which a maximum may grow before O is rescaled
 constexpr int kMiscBytes = 2048;
-constexpr int kMaxSnap = 3;           // tiles that a cut may move to a request's border
-constexpr int kRequestUnits = 2;      // what a request costs a worker beside its tiles, in tiles
+constexpr int kRequestUnits = 3;      // what a request costs a worker beside its tiles, in tiles, at most
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -109,6 +109,20 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%3, %3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(chunk), "r"(group), "r"(page)
         : "memory");
+}
+
+// Whether the phase of `parity` has completed, without waiting (try_wait may
+// suspend the thread for hundreds of cycles).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // A place in a ring of shared-memory slots and the parity of its pass.
@@ -278,8 +292,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     int* run_s = reinterpret_cast<int*>(tmem_holder + 2);  // [4] first request and tile, end request and tile
     int64_t* sums = reinterpret_cast<int64_t*>(tmem_holder + 6);   // [kThreads / 32]
-    float* alpha_s = reinterpret_cast<float*>(sums + kThreads / 32);   // [2][64]
-    float* inv_s = alpha_s + 2 * kHeads;                   // [64]
+    float* alpha_s = reinterpret_cast<float*>(sums + kThreads / 32);   // [64]
+    float* inv_s = alpha_s + kHeads;                       // [64]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = blockIdx.x / p.G, g = blockIdx.x - w * p.G;
@@ -318,15 +332,20 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     allow_dependent_launch();
     bounds_self_test(p.inject);
 
-    // The worker's run.  Each request counts kRequestUnits units, then one per
-    // tile; worker w takes units [w U / workers, (w + 1) U / workers), and a
-    // cut among a request's leading units is a cut before its first tile.
-    // Thread t sums requests [t * per, (t + 1) * per).
+    // The worker's run.  Each request counts `lead` units, then one per tile;
+    // worker w takes units [w U / workers, (w + 1) U / workers), and a cut
+    // among a request's leading units is a cut before its first tile.  Thread
+    // t sums requests [t * per, (t + 1) * per).  The leading units stand for
+    // what a request costs beside its tiles (queries, pipeline fill, output:
+    // ~4 us against ~1.4 us a tile); with less than that many tiles per worker
+    // they would only leave workers idle.  Measured: 96 requests of mixed
+    // lengths 109 us with 3 units, 160 with none; one request of 701 tokens
+    // 14.2 us with 3, 12.8 with none.
     {
         const int per = (p.B + kThreads - 1) / kThreads;
         const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
         int64_t mine = 0;
-        for (int b = b0; b < b1; ++b) mine += kRequestUnits + tiles_of(request_len(p, b));
+        for (int b = b0; b < b1; ++b) mine += tiles_of(request_len(p, b));
         int64_t inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -335,15 +354,16 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         }
         if (lane == 31) sums[warp] = inc;
         __syncthreads();
-        int64_t before = inc - mine, total = 0;
+        int64_t before = inc - mine, tiles = 0;
         for (int i = 0; i < kThreads / 32; ++i) {
             if (i < warp) before += sums[i];
-            total += sums[i];
+            tiles += sums[i];
         }
+        const int lead = tiles / p.W < kRequestUnits ? static_cast<int>(tiles / p.W) : kRequestUnits;
+        const int64_t total = tiles + static_cast<int64_t>(lead) * p.B;
+        before += static_cast<int64_t>(lead) * b0;
+        mine += static_cast<int64_t>(lead) * (b1 - b0);
         const int64_t workers = total < p.W ? total : p.W;
-        // A part costs its write and its read in the join, so a cut that would
-        // leave a sliver of a request moves to the request's border.
-        const int snap = static_cast<int>(min(total / workers / 4, static_cast<int64_t>(kMaxSnap)));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int64_t u = w + e < workers ? (w + e) * total / workers : total;
@@ -353,19 +373,13 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             }
             if (u >= before && u < before + mine) {
                 int64_t at = before;
-                int b = b0, n = kRequestUnits + tiles_of(request_len(p, b));
+                int b = b0, n = lead + tiles_of(request_len(p, b));
                 while (at + n <= u) {
                     at += n;
-                    n = kRequestUnits + tiles_of(request_len(p, ++b));
-                }
-                int tile = max(static_cast<int>(u - at) - kRequestUnits, 0);
-                if (tile < snap) tile = 0;
-                else if (n - kRequestUnits - tile < snap) {
-                    tile = 0;
-                    ++b;
+                    n = lead + tiles_of(request_len(p, ++b));
                 }
                 run_s[2 * e] = b;
-                run_s[2 * e + 1] = tile;
+                run_s[2 * e + 1] = max(static_cast<int>(u - at) - lead, 0);
             }
         }
     }
@@ -585,40 +599,49 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     for (int j = 0; j < 16; ++j)
                         if ((j >> 1) * 8 + col0 + (j & 1) >= valid) s[0][j] = s[1][j] = kNegInf;
                 }
+                // Whether product n - 1 is done (then P's buffer and O are this
+                // tile's) is looked at early: the test takes long, and mostly it is.
+                bool pv_done = n == 0 || mbar_test(smem_u32(pempty), (n & 1) ^ 1);
                 bool raise = false;
-                float alpha[2];
+                float top[2];
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
                     float x[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[j] = fmaxf(s[a][j], s[a][j + 8]);
-                    float top = fmaxf(fmaxf(fmaxf(x[0], x[4]), fmaxf(x[1], x[5])), fmaxf(fmaxf(x[2], x[6]), fmaxf(x[3], x[7])));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // Raise the maximum when it grew too far (always on the first tile).
-                    alpha[a] = 1.f;
-                    if (row0 + 8 * a < heads && (top - m[a]) * p.scale_log2 > kRaise) {
-                        raise |= i > 0;
-                        alpha[a] = exp2_fast((m[a] - top) * p.scale_log2);
-                        m[a] = top;
-                    }
-                    if ((lane & 3) == 0) alpha_s[(n & 1) * kHeads + row0 + 8 * a] = alpha[a];
+                    top[a] = fmaxf(fmaxf(fmaxf(x[0], x[4]), fmaxf(x[1], x[5])), fmaxf(fmaxf(x[2], x[6]), fmaxf(x[3], x[7])));
+                    top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], 1));
+                    top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], 2));
+                    raise |= row0 + 8 * a < heads && (top[a] - m[a]) * p.scale_log2 > kRaise;
                 }
-                const bool rescale = soft_sync_or(raise);
-                // P's buffer and O are this tile's once product n - 1 is done.
-                if (rescale) {
-                    ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
+                if (i == 0) {
+                    m[0] = top[0];
+                    m[1] = top[1];
+                    raise = false;
+                }
+                if (soft_sync_or(raise)) {
+                    // Rare: some maximum grew too far; O and the sums follow.
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        float alpha = 1.f;
+                        if (row0 + 8 * a < heads && (top[a] - m[a]) * p.scale_log2 > kRaise) {
+                            alpha = exp2_fast((m[a] - top[a]) * p.scale_log2);
+                            m[a] = top[a];
+                            l[a] *= alpha;
+                        }
+                        if ((lane & 3) == 0) alpha_s[row0 + 8 * a] = alpha;
+                    }
+                    soft_sync_or(false);
+                    if (!pv_done) ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
+                    pv_done = true;
                     tc_fence_after();
-                    l[0] *= alpha[0];
-                    l[1] *= alpha[1];
-                    const float* al = alpha_s + (n & 1) * kHeads;
                     for (int c = 0; ok && c < p.nblk * kHeads; c += 16) {
                         uint32_t r[16];
                         tmem_ld16_issue(tl + c, r);
                         tmem_ld16_wait(r);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            r[j] = __float_as_uint(__uint_as_float(r[j]) * al[(c & (kHeads - 1)) + j]);
+                            r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha_s[(c & (kHeads - 1)) + j]);
                         tmem_st16(tl + c, r);
                     }
                     tmem_wait_st();
@@ -640,7 +663,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     l[a] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
                 }
-                if (n > 0) ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
+                if (!pv_done) ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
                 __syncwarp();
                 if (ok) {
                     if (mine) {
@@ -678,16 +701,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             for (int a = 0; a < 2; ++a) {
                 l[a] += __shfl_xor_sync(0xffffffffu, l[a], 1);
                 l[a] += __shfl_xor_sync(0xffffffffu, l[a], 2);
-                const int row = row0 + 8 * a, head = g * kHeads + row;
-                const float m2 = m[a] == kNegInf ? m[a] : m[a] * p.scale_log2;
-                if ((lane & 3) == 0) {
-                    inv_s[row] = l[a] > 0.f || l[a] != l[a] ? 1.0f / l[a] : 0.f;
-                    if (ok && whole) {
-                        if (p.lse && head < p.H) p.lse[b * p.ldl_b + head] = l[a] == 0.f ? kNegInf : (m2 + log2f(l[a])) * kLn2;
-                    } else if (ok) {
-                        p.part_ml[slot * kHeads + row] = make_float2(m2, l[a]);
-                    }
-                }
+                if ((lane & 3) == 0) inv_s[row0 + 8 * a] = l[a] > 0.f || l[a] != l[a] ? __fdividef(1.0f, l[a]) : 0.f;
             }
             soft_sync_or(false);                           // inv_s is next written after another tile's barrier
             __syncwarp();
@@ -698,55 +712,90 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 // values (16-byte chunks, chunk ^ (row / 2) % 4), which leave
                 // as 16-byte stores, 64 bytes of each of eight heads at once.
                 const uint32_t stage = smem_u32(p_s) + quad * 2048;
-                for (int it = 0; it < p.nblk * 2; ++it) {
-                    const int blk = it >> 1, h0 = (it & 1) * 32;
-                    if (h0 >= heads) continue;
-                    uint32_t r[2][16];
-                    const uint32_t src = tl + blk * kHeads + h0;
-                    tmem_ld_frag32(src, r[0]);
-                    tmem_ld_frag32(src + (16u << 16), r[1]);
-                    tmem_ld16_wait(r[0]);
-                    tmem_ld16_wait(r[1]);
+                const int halves = heads > 32 ? 2 : 1, its = p.nblk * halves;
+                uint32_t r[2][2][16];
+                auto fetch = [&](int it, uint32_t (&x)[2][16]) {
+                    const uint32_t src = tl + (it / halves) * kHeads + (it % halves) * 32;
+                    tmem_ld_frag32(src, x[0]);
+                    tmem_ld_frag32(src + (16u << 16), x[1]);
+                };
+                auto put = [&](int it, const uint32_t (&x)[2][16]) {
+                    const int blk = it / halves, h0 = (it % halves) * 32;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {          // eight heads
                         const float2 f = *reinterpret_cast<const float2*>(inv_s + h0 + q * 8 + col0);
                         uint32_t v[4];
 #pragma unroll
                         for (int d = 0; d < 4; ++d)        // eight values
-                            v[d] = pack_bf16(__uint_as_float(r[d >> 1][q * 4 + (d & 1) * 2]) * f.x,
-                                             __uint_as_float(r[d >> 1][q * 4 + (d & 1) * 2 + 1]) * f.y);
+                            v[d] = pack_bf16(__uint_as_float(x[d >> 1][q * 4 + (d & 1) * 2]) * f.x,
+                                             __uint_as_float(x[d >> 1][q * 4 + (d & 1) * 2 + 1]) * f.y);
                         const int hl = q * 8 + (lane & 7), d = lane >> 3;
                         stmatrix_x4_trans(stage + hl * 64 + ((d ^ ((hl >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
                     }
                     __syncwarp();
                     __nv_bfloat16* o = p.out + b * p.ldo_b + blk * 128 + quad * 32 + (lane & 3) * 8;
+                    uint4 v[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int hl = j * 8 + (lane >> 2), head = h0 + hl;
-                        uint4 v;
+                        const int hl = j * 8 + (lane >> 2);
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w)
                                      : "r"(stage + hl * 64 + (((lane & 3) ^ ((hl >> 1) & 3)) << 4))
                                      : "memory");
-                        if (head < heads && bounds_ok(b < p.B))
-                            *reinterpret_cast<uint4*>(o + static_cast<int64_t>(g * kHeads + head) * p.ldo_h) = v;
                     }
                     __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int head = h0 + j * 8 + (lane >> 2);
+                        if (head < heads && bounds_ok(b < p.B))
+                            *reinterpret_cast<uint4*>(o + static_cast<int64_t>(g * kHeads + head) * p.ldo_h) = v[j];
+                    }
+                };
+                // The next fragments come from TMEM while these leave.
+                fetch(0, r[0]);
+                for (int it = 0; it < its; it += 2) {
+                    tmem_ld16_wait(r[0][0]);
+                    tmem_ld16_wait(r[0][1]);
+                    if (it + 1 < its) fetch(it + 1, r[1]);
+                    put(it, r[0]);
+                    if (it + 1 >= its) break;
+                    tmem_ld16_wait(r[1][0]);
+                    tmem_ld16_wait(r[1][1]);
+                    if (it + 2 < its) fetch(it + 2, r[0]);
+                    put(it + 1, r[1]);
                 }
             } else {
                 // A part, in the order the registers hold it: 512 bytes a store.
                 float4* o = reinterpret_cast<float4*>(p.part_o) + slot * p.nblk * 16 * 128 + quad * 32 + lane;
-                for (int c = 0; c < p.nblk * kHeads; c += 16) {
-                    if ((c & (kHeads - 1)) >= heads) continue;
-                    uint32_t r[16];
-                    tmem_ld16_issue(tl + c, r);
-                    tmem_ld16_wait(r);
+                const int per = (heads + 15) >> 4, its = p.nblk * per;       // 16 heads a step
+                uint32_t r[2][16];
+                auto fetch = [&](int it, uint32_t (&x)[16]) { tmem_ld16_issue(tl + (it / per) * kHeads + (it % per) * 16, x); };
+                auto put = [&](int it, const uint32_t (&x)[16]) {
+                    const int c = (it / per) * 16 + (it % per) * 4;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (bounds_ok(w < p.W))
-                            o[(c / 4 + j) * 128] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                                                               __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+                        if (bounds_ok(w < p.W && c + j < p.nblk * 16))
+                            o[(c + j) * 128] = make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]),
+                                                           __uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3]));
+                };
+                fetch(0, r[0]);
+                for (int it = 0; it < its; it += 2) {
+                    tmem_ld16_wait(r[0]);
+                    if (it + 1 < its) fetch(it + 1, r[1]);
+                    put(it, r[0]);
+                    if (it + 1 >= its) break;
+                    tmem_ld16_wait(r[1]);
+                    if (it + 2 < its) fetch(it + 2, r[0]);
+                    put(it + 1, r[1]);
                 }
+            }
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const int row = row0 + 8 * a, head = g * kHeads + row;
+                const float m2 = m[a] == kNegInf ? m[a] : m[a] * p.scale_log2;
+                if ((lane & 3) != 0) continue;
+                if (!whole) p.part_ml[slot * kHeads + row] = make_float2(m2, l[a]);
+                else if (p.lse && head < p.H) p.lse[b * p.ldl_b + head] = l[a] == 0.f ? kNegInf : (m2 + log2f(l[a])) * kLn2;
             }
             tc_fence_before();
         }
@@ -766,149 +815,176 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 // that cut and of the workers that begin inside it, in the order of the tokens.
 //   out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k,  M = max_k m_k
 // A part's value is read as it lies: 16 bytes are four heads of one value.  An
-// item is one such group of four heads: with few parts all its values (each
-// thread takes two of them), with more one block of 128 values (two threads
-// share a value's parts) or 32 values (eight threads do), so that a thread has
-// a handful of loads, in flight at once, whatever the number of parts.  The
-// parts' factors are formed once per item, in shared memory.
+// item is four heads of one block of 128 values: SHARE = 1 gives it to one
+// warp, for the few parts of a request in a large batch; SHARE = 8 gives it to
+// the eight warps of a CTA, which take the parts in turn, for long requests
+// that many workers share.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
-constexpr int kFewParts = 6, kSomeParts = 16;
+constexpr int kManyParts = 4;         // workers per request from which a CTA joins an item
 
+template <int SHARE>
 __global__ void __launch_bounds__(kJoinThreads)
-latent_attention_join_kernel(const Params p) {
+latent_attention_join_kernel(const Params p, const int by_cut) {
     grid_dependency_wait();
     allow_dependent_launch();
     bounds_self_test(p.inject);
-    __shared__ int2 meta_s[kMaxCtas + 1];
-    __shared__ int first_item[kMaxCtas + 1];               // running item count by cut
-    __shared__ int parts_s[kMaxCtas], warp_items[kJoinThreads / 32];
-    __shared__ float2 ml_s[kMaxCtas][4];
-    __shared__ float4 fac_s[kMaxCtas];                     // factor of each part, for the four heads
-    __shared__ float4 red[kJoinThreads];
+    constexpr unsigned kAll = 0xffffffffu;
+    __shared__ int first_s, parts_s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = threadIdx.x;
     const float kNegInf = __int_as_float(0xff800000);
-    const int quads = (p.H + 3) / 4;
+    const int quads = (p.H + 3) / 4, items = quads * p.nblk;
+    const int per = (items + 8 / SHARE - 1) / (8 / SHARE); // CTAs of a request
+    const int what = blockIdx.x / per;
 
-    // The cut before each worker: the parts of the request whose first cut it
-    // is (0: none), and the items of all cuts before it.
-    static_assert(kMaxCtas <= kJoinThreads, "one thread per cut");
-    if (t < p.W) meta_s[t] = p.meta[t];
-    __syncthreads();
-    int parts = 0, count = 0;
-    if (t > 0 && t < p.W) {
-        const int2 me = meta_s[t], left = meta_s[t - 1];
-        if (me.x < p.B && me.y > 0 && (left.x != me.x || left.y == 0)) {
-            parts = 2;
-            for (int k = t + 1; k < p.W && meta_s[k].x == me.x && meta_s[k].y > 0; ++k) ++parts;
-            count = quads * (parts <= kFewParts ? 1 : parts <= kSomeParts ? p.nblk : p.nblk * 4);
-        }
+    // The request: `what` itself, or the one whose first cut is the cut before
+    // worker what + 1.  A cut before worker k lies inside request b when
+    // meta[k] = (b, > 0); the cuts of a request are neighbours.
+    static_assert(kMaxCtas <= kJoinThreads, "one thread per worker");
+    const int2 me = t < p.W ? p.meta[t] : make_int2(-1, 0);
+    if (t == 0) {
+        first_s = p.W;
+        parts_s = 0;
     }
-    int inc = count;
+    __syncthreads();
+    const int b = by_cut ? p.meta[what + 1].x : what;
+    const bool cut = me.x == b && me.y > 0 && b < p.B;
+    const unsigned votes = __ballot_sync(kAll, cut);
+    if (lane == 0 && votes) {
+        atomicMin(&first_s, warp * 32 + __ffs(votes) - 1);
+        atomicAdd(&parts_s, __popc(votes));
+    }
+    __syncthreads();
+    const int w = first_s, np = parts_s + 1;               // first cut inside the request, its parts
+    if (np < 2 || (by_cut && w != what + 1)) return;
+    const int sub = static_cast<int>(blockIdx.x) - what * per;
+    const int item = SHARE == 1 ? sub * 8 + warp : sub;
+    if (item >= items) return;                             // SHARE = 8: the whole CTA
+    const int hq = item / p.nblk, blk = item - hq * p.nblk;
+    const int g = hq * 4 / kHeads, hl = hq * 4 - g * kHeads;
+    const int left_slot = p.meta[w - 1].x == b ? 0 : 1;
+    auto slot_of = [&](int k) -> int64_t {                 // part k's place in the workspace
+        return static_cast<int64_t>(k == 0 ? (w - 1) * 2 + left_slot : (w + k - 1) * 2) * p.G + g;
+    };
+    // Values 2 lane, + 1, 2 lane + 64, + 1 of the block.
+    auto load = [&](int k, float4 (&o)[4]) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((slot_of(k) * p.nblk + blk) * 16 + hl / 4) * 128 + 2 * lane;
+        o[0] = src[0];
+        o[1] = src[1];
+        o[2] = src[64];
+        o[3] = src[65];
+    };
+    const int k0 = SHARE == 1 ? 0 : warp, mine = np > k0 ? (np - k0 + SHARE - 1) / SHARE : 0;   // parts of this warp
+    float M[4], L[4] = {0.f, 0.f, 0.f, 0.f}, acc[4][4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
+    for (int j = 0; j < 4; ++j) {
+        M[j] = kNegInf;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i][j] = 0.f;
     }
-    if (lane == 31) warp_items[warp] = inc;
-    __syncthreads();
-    int before = inc - count;
-    for (int i = 0; i < warp; ++i) before += warp_items[i];
-    if (t < p.W) {
-        parts_s[t] = parts;
-        first_item[t] = before;
-    }
-    if (t == p.W - 1) first_item[p.W] = before + count;
-    __syncthreads();
-
-    const int last = first_item[p.W];
-    for (int item = blockIdx.x; item < last; item += gridDim.x) {
-        int w = 0, hi = p.W;                               // first_item[w] <= item < first_item[hi]
-        while (hi - w > 1) {
-            const int mid = (w + hi) >> 1;
-            if (first_item[mid] <= item) w = mid;
-            else hi = mid;
-        }
-        const int np = parts_s[w], b = meta_s[w].x, at = item - first_item[w];
-        const int share = np <= kFewParts ? 1 : np <= kSomeParts ? 2 : 8;       // threads to a value
-        const int split = share == 1 ? 1 : share == 2 ? p.nblk : p.nblk * 4;    // items to four heads
-        const int hq = at / split, sub = at - hq * split;
-        const int g = hq * 4 / kHeads, hl = hq * 4 - g * kHeads;
-        const int left_slot = meta_s[w - 1].x == b ? 0 : 1;
-        auto slot_of = [&](int k) -> int64_t {             // part k's place in the workspace
-            return static_cast<int64_t>(k == 0 ? (w - 1) * 2 + left_slot : (w + k - 1) * 2) * p.G + g;
-        };
-        if (t < np) {
-            const float4* ml = reinterpret_cast<const float4*>(p.part_ml + slot_of(t) * kHeads + hl);
+    for (int c = 0; c < mine; c += 32) {                   // 32 parts at a time, one's (max, sum) per lane
+        const int cnt = min(32, mine - c);
+        float4 o[2][4];
+        load(k0 + c * SHARE, o[0]);                        // on their way while the factors are formed
+        if (cnt > 1) load(k0 + (c + 1) * SHARE, o[1]);
+        float f[4] = {kNegInf, kNegInf, kNegInf, kNegInf}, l[4] = {0.f, 0.f, 0.f, 0.f};
+        if (lane < cnt) {
+            const float4* ml = reinterpret_cast<const float4*>(p.part_ml + slot_of(k0 + (c + lane) * SHARE) * kHeads + hl);
             const float4 x = ml[0], y = ml[1];
-            ml_s[t][0] = make_float2(x.x, x.y);
-            ml_s[t][1] = make_float2(x.z, x.w);
-            ml_s[t][2] = make_float2(y.x, y.y);
-            ml_s[t][3] = make_float2(y.z, y.w);
+            f[0] = x.x; f[1] = x.z; f[2] = y.x; f[3] = y.z;
+            l[0] = x.y; l[1] = x.w; l[2] = y.y; l[3] = y.w;
         }
-        __syncthreads();
-        if (warp < 4) {                                    // warp j: head j of the four
-            float M = kNegInf, L = 0.f;
-            for (int k = lane; k < np; k += 32) M = fmaxf(M, ml_s[k][warp].x);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float base = M == kNegInf ? 0.f : M;
-            for (int k = lane; k < np; k += 32) L = fmaf(ml_s[k][warp].y, exp2_fast(ml_s[k][warp].x - base), L);
+        for (int j = 0; j < 4; ++j) {
+            float top = f[j];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
-            for (int k = lane; k < np; k += 32)
-                reinterpret_cast<float*>(&fac_s[k])[warp] = exp2_fast(ml_s[k][warp].x - base) * inv;
-            const int h = hq * 4 + warp;
-            if (p.lse && sub == 0 && lane == 0 && h < p.H)
-                p.lse[b * p.ldl_b + h] = L == 0.f ? kNegInf : (M + log2f(L)) * kLn2;
+            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, s));
+            top = fmaxf(top, M[j]);
+            const float base = top == kNegInf ? 0.f : top, old = exp2_fast(M[j] - base);
+            f[j] = exp2_fast(f[j] - base);
+            L[j] = fmaf(L[j], old, warp_sum(f[j] * l[j]));
+            M[j] = top;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i][j] *= old;
         }
-        __syncthreads();
-        // This thread's values: v0, and with one thread to a value v0 + 256.
-        const int width = kJoinThreads / share;            // values of a pass
-        const int k0 = t / width, v0 = sub * width + (t - k0 * width), all = p.nblk * 128;
-        auto value_at = [&](int64_t s, int v) -> float4 {  // 128 values of a block, 16 groups of heads each
-            return __ldcs(reinterpret_cast<const float4*>(p.part_o) + ((s * p.nblk + (v >> 7)) * 16 + hl / 4) * 128 + (v & 127));
-        };
-        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-        auto add = [](float4& a, const float4& o, const float4& f) {
-            a.x = fmaf(o.x, f.x, a.x);
-            a.y = fmaf(o.y, f.y, a.y);
-            a.z = fmaf(o.z, f.z, a.z);
-            a.w = fmaf(o.w, f.w, a.w);
-        };
-        if (share == 1) {
-            const bool two = v0 + width < all;
-            if (v0 < all) {
-#pragma unroll 3
-                for (int k = 0; k < np; ++k) {
-                    const int64_t s = slot_of(k);
-                    const float4 o0 = value_at(s, v0), o1 = two ? value_at(s, v0 + width) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    add(acc[0], o0, fac_s[k]);
-                    add(acc[1], o1, fac_s[k]);
+        auto add = [&](int k, const float4 (&x)[4]) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float fk = __shfl_sync(kAll, f[j], k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float v = j == 0 ? x[i].x : j == 1 ? x[i].y : j == 2 ? x[i].z : x[i].w;
+                    acc[i][j] = fmaf(v, fk, acc[i][j]);
                 }
             }
-        } else {
-#pragma unroll 8
-            for (int k = k0; k < np; k += share) add(acc[0], value_at(slot_of(k), v0), fac_s[k]);
-            red[t] = acc[0];
-            __syncthreads();
-            if (k0 == 0) {
-                for (int i = 1; i < share; ++i) add(acc[0], red[t + i * width], make_float4(1.f, 1.f, 1.f, 1.f));
+        };
+        add(0, o[0]);
+        if (cnt > 1) add(1, o[1]);
+#pragma unroll 2
+        for (int k = 2; k < cnt; k += 2) {
+            load(k0 + (c + k) * SHARE, o[0]);
+            if (k + 1 < cnt) load(k0 + (c + k + 1) * SHARE, o[1]);
+            add(k, o[0]);
+            if (k + 1 < cnt) add(k + 1, o[1]);
+        }
+    }
+    if (SHARE > 1) {
+        // The warps' results, merged by warp 0 in the order of the warps.
+        __shared__ float4 red[8][4][32], red_m[8], red_l[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[warp][i][lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        if (lane == 0) {
+            red_m[warp] = make_float4(M[0], M[1], M[2], M[3]);
+            red_l[warp] = make_float4(L[0], L[1], L[2], L[3]);
+        }
+        __syncthreads();
+        if (warp >= 4) return;
+        // Warp i finishes value group i: its quarter of the item's values.
+        float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float4 m = red_m[s];
+            top[0] = fmaxf(top[0], m.x); top[1] = fmaxf(top[1], m.y);
+            top[2] = fmaxf(top[2], m.z); top[3] = fmaxf(top[3], m.w);
+        }
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) L[j] = 0.f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float4 m = red_m[s], q = red_l[s], x = red[s][warp][lane];
+            const float sm[4] = {m.x, m.y, m.z, m.w}, sl[4] = {q.x, q.y, q.z, q.w}, sx[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float fk = exp2_fast(sm[j] - (top[j] == kNegInf ? 0.f : top[j]));
+                L[j] = fmaf(sl[j], fk, L[j]);
+                a[j] = fmaf(sx[j], fk, a[j]);
             }
         }
-        if (k0 == 0 && bounds_ok(b < p.B)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int v = v0 + i * width;
-                if (v >= all || (i == 1 && share != 1)) continue;
-                const float r[4] = {acc[i].x, acc[i].y, acc[i].z, acc[i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (hq * 4 + j < p.H) p.out[b * p.ldo_b + (hq * 4 + j) * p.ldo_h + v] = __float2bfloat16_rn(r[j]);
-            }
+        for (int j = 0; j < 4; ++j) {
+            M[j] = top[j];
+            const int h = hq * 4 + j, v = blk * 128 + (warp >> 1) * 64 + 2 * lane + (warp & 1);
+            const float inv = L[j] > 0.f || L[j] != L[j] ? 1.0f / L[j] : 0.f;
+            if (h < p.H && bounds_ok(b < p.B && v < p.nblk * 128))
+                p.out[b * p.ldo_b + h * p.ldo_h + v] = __float2bfloat16_rn(a[j] * inv);
         }
-        __syncthreads();                                   // the buffers are free for the next item
+        if (warp != 0) return;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int h = hq * 4 + j;
+            const float inv = L[j] > 0.f || L[j] != L[j] ? 1.0f / L[j] : 0.f;
+            if (h >= p.H || !bounds_ok(b < p.B)) continue;
+            __nv_bfloat16* dst = p.out + b * p.ldo_b + h * p.ldo_h + blk * 128 + 2 * lane;
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0][j] * inv, acc[1][j] * inv);
+            *reinterpret_cast<uint32_t*>(dst + 64) = pack_bf16(acc[2][j] * inv, acc[3][j] * inv);
+        }
+    }
+    if (p.lse && blk == 0 && lane < 4 && hq * 4 + lane < p.H) {
+        const float m = lane == 0 ? M[0] : lane == 1 ? M[1] : lane == 2 ? M[2] : M[3];
+        const float l = lane == 0 ? L[0] : lane == 1 ? L[1] : lane == 2 ? L[2] : L[3];
+        p.lse[b * p.ldl_b + hq * 4 + lane] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
     }
 }
 
@@ -1084,8 +1160,14 @@ extern "C" dsnq_status dsnq_paged_latent_attention(
     st = launch_result(launch_kernel(latent_attention_kernel, dim3(static_cast<unsigned>(p.W * G)), dim3(kThreads), smem, s,
                                      mq, mk, mo, p));
     if (st != DSNQ_OK || p.W == 1) return st;
-    const int64_t items = (H + 3) / 4 * p.nblk * 4 * (p.W - 1);
-    const int64_t grid = items < 4 * sms ? items : 4 * sms;
-    return launch_result(launch_kernel(latent_attention_join_kernel, dim3(static_cast<unsigned>(grid)),
-                                       dim3(kJoinThreads), 0, s, p));
+    // Few requests: a request has many parts, so a CTA joins each item.  Many:
+    // a warp does, and no more requests can be split than there are cuts.
+    const int64_t items = (H + 3) / 4 * p.nblk;
+    const int by_cut = B > p.W - 1;
+    const int64_t targets = by_cut ? p.W - 1 : B;
+    if (p.W >= kManyParts * B)
+        return launch_result(launch_kernel(latent_attention_join_kernel<8>, dim3(static_cast<unsigned>(targets * items)),
+                                           dim3(kJoinThreads), 0, s, p, by_cut));
+    return launch_result(launch_kernel(latent_attention_join_kernel<1>, dim3(static_cast<unsigned>(targets * ((items + 7) / 8))),
+                                       dim3(kJoinThreads), 0, s, p, by_cut));
 }
