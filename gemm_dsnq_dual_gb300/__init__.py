@@ -22,6 +22,7 @@ sglang PR #27289 (transpose_scale: column-major activation scales).
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 
 import torch
@@ -48,6 +49,9 @@ __all__ = [
 ]
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, dev) -> int:
     """The stream handle for a call on tensors of device `dev`.  The library
     launches on the current CUDA device (and picks per-device state by it), so
@@ -59,6 +63,8 @@ def _stream(stream, dev) -> int:
         raise ValueError(f"tensors are on {dev} but the current CUDA device is cuda:{cur}; "
                          f"call under torch.cuda.device({dev})")
     if stream is None:
+        if _raw_stream is not None:          # the handle alone, without a Stream object around it
+            return _raw_stream(cur)
         stream = torch.cuda.current_stream(cur)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -365,9 +371,9 @@ def _need(t, name: str, dtype, dim: int, dev=None):
 
 
 def _flat(t, name: str, dtype, n: int, dev):
-    """A contiguous 1-D tensor of n elements; its address."""
-    _need(t, name, dtype, 1, dev)
-    if t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    """The address of a contiguous 1-D tensor of n elements."""
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or t.device != dev:
+        _need(t, name, dtype, 1, dev)
         raise ValueError(f"{name} must be contiguous with {n} elements, got shape {tuple(t.shape)}, strides {t.stride()}")
     return t.data_ptr()
 
@@ -375,15 +381,13 @@ def _flat(t, name: str, dtype, n: int, dev):
 def _strides3(t, name: str):
     """Strides of the two outer dimensions of a 3-D tensor with contiguous
     rows (a dimension of size 1 gets the stride it would have if packed)."""
-    n0, n1, n2 = t.shape
     s0, s1, s2 = t.stride()
+    n0, n1, n2 = t.shape
     if s2 != 1 and n2 > 1:
         raise ValueError(f"{name} must have contiguous rows")
     if n1 == 1:
         s1 = n2
-    if n0 == 1:
-        s0 = n1 * s1
-    return s0, s1
+    return (n1 * s1 if n0 == 1 else s0), s1
 
 
 def _rope_layout(layout) -> int:
@@ -500,6 +504,7 @@ def latent_cache_write(kv, pe, positions, slots, inv_freq, cache, gamma=None, ep
     return cache
 
 
+@functools.lru_cache(maxsize=256)
 def paged_latent_attention_workspace_bytes(B: int, H: int, v_dim: int, table_width: int, page_size: int) -> int:
     """Bytes of paged_latent_attention's workspace (host-only query)."""
     n = C.c_int64()

@@ -5,11 +5,14 @@
 //
 // Rotary positions: the pair (a, b) of frequency i at position p becomes
 //   (a cos t - b sin t, b cos t + a sin t) * rope_scale,   t = p * inv_freq[i].
-// At position 10^6 an fp32 product p * inv_freq is off by up to 0.06 rad, so
-// the angle is formed in fp64 as a number of turns, its whole turns dropped,
-// and only the fraction (|.| <= 1/2) goes to fp32 (sincospif).  The table of a
-// token's angles is formed once per CTA (or warp) in shared memory and used
-// for all its heads.
+// At position 10^6 an fp32 product p * inv_freq is off by up to 0.06 rad.
+// Positions are whole, so only the fraction of a turn that one position adds
+// matters: it is taken from inv_freq once, in fp64, as a 64-bit fixed-point
+// number; times the position modulo 2^64 it is the fraction of a turn at that
+// position (off by 2^-54 per position), and only that goes to fp32
+// (sincospif).  The fp64 units are few, so the products by position are whole
+// numbers; the table of a token's angles is formed once per CTA or warp, in
+// shared memory, and used for all its heads.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -45,20 +48,26 @@ struct Rope {
     float sign;                 // -1 rotates back
 };
 
-// (cos, sin) * scale of frequency i at position pos.
-__device__ __forceinline__ float2 rope_angle(const Rope& r, int64_t pos, int i) {
-    const double turns = static_cast<double>(pos) * r.inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
-    const float frac = static_cast<float>(turns - rint(turns));
+// The turns that one position adds, modulo 1, as a 64-bit fraction.
+__device__ __forceinline__ uint64_t turn_step(double inv_freq) {
+    const double turns = inv_freq * 0.15915494309189533577;   // 1 / (2 pi)
+    return __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
+}
+
+// (cos, sin) * scale at position pos of the frequency with that step.
+__device__ __forceinline__ float2 rope_angle(const Rope& r, uint64_t step, int64_t pos) {
+    const int64_t turn = static_cast<int64_t>(step * static_cast<uint64_t>(pos));   // in [-1/2, 1/2) turns
     float s, c;
-    sincospif(2.0f * frac, &s, &c);
+    sincospif(__ll2float_rn(turn) * 0x1p-63f, &s, &c);
     return make_float2(c * r.scale, s * (r.scale * r.sign));
 }
 
 // The values of a chunk whose first column is `q` of the rotated range, given
 // its own values x and, for the half layout, its partner chunk's values y.
+template <bool HALF>
 __device__ __forceinline__ void rotate_chunk(const Rope& r, const float2* cs, int q, float2 (&x)[4],
                                              const float2 (&y)[4]) {
-    if (!r.half) {
+    if (!HALF) {
         const float2* t = cs + (q >> 1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -114,16 +123,20 @@ struct HeadArgs {
 constexpr int kHeadWarps = 8;
 
 // LPR lanes hold one head's row (CPL chunks of 16 bytes each, chunk
-// lane + j * LPR), so a warp works on 32 / LPR heads at once.  A CTA takes
-// heads of one token: its first dim/2 threads form the token's angles while
-// the first rows are on their way.
-template <int LPR, int CPL>
-__global__ void __launch_bounds__(kHeadWarps * 32)
+// lane + j * LPR), so a warp works on 32 / LPR heads at once, and takes U such
+// rows a step, all requested before the first is worked on.  A CTA takes heads
+// of one token: its first dim/2 threads form the token's angles while the
+// first rows are on their way.  Bound by HBM for many tokens: four CTAs per SM
+// (64 registers) with 64 bytes a thread on their way keep 64 KB in flight.
+// HALF: pairs (i, i + dim/2), whose partner chunk is loaded beside the own one.
+template <int LPR, int CPL, bool HALF>
+__global__ void __launch_bounds__(kHeadWarps * 32, CPL * (HALF ? 2 : 1) <= 2 ? 4 : CPL * (HALF ? 2 : 1) <= 4 ? 2 : 1)
 head_norm_rope_kernel(const HeadArgs a) {
     grid_dependency_wait();
     allow_dependent_launch();
     bounds_self_test(a.inject);
-    constexpr int kRows = 32 / LPR;      // heads per warp and step
+    constexpr int kRows = 32 / LPR;      // heads per warp and row
+    constexpr int U = CPL >= 4 ? 1 : 4 / (CPL * (HALF ? 2 : 1));
     __shared__ float2 cs[kMaxRope / 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % LPR, sub = lane / LPR;
@@ -134,85 +147,89 @@ head_norm_rope_kernel(const HeadArgs a) {
     const int c_lo = a.rope.off / kChunk, c_n = a.rope.dim / kChunk;
 
     bool live[CPL], rot[CPL];
-    int col[CPL], pcol[CPL];
+    int pcol[CPL];
     uint4 graw[CPL], pgraw[CPL];
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
-        const int c = l + j * LPR;
+        const int c = l + j * LPR, q = c - c_lo;
         live[j] = c < chunks;
         rot[j] = live[j] && c >= c_lo && c < c_lo + c_n;
-        col[j] = c * kChunk;
-        const int q = c - c_lo;
-        pcol[j] = (rot[j] && a.rope.half) ? (q < c_n / 2 ? c + c_n / 2 : c - c_n / 2) * kChunk : col[j];
+        pcol[j] = (HALF && rot[j] ? (q < c_n / 2 ? c + c_n / 2 : c - c_n / 2) : c) * kChunk;
         graw[j] = pgraw[j] = make_uint4(0, 0, 0, 0);
         if (a.gamma && live[j]) {
-            graw[j] = *reinterpret_cast<const uint4*>(a.gamma + col[j]);
-            pgraw[j] = *reinterpret_cast<const uint4*>(a.gamma + pcol[j]);
+            graw[j] = *reinterpret_cast<const uint4*>(a.gamma + c * kChunk);
+            if (HALF) pgraw[j] = *reinterpret_cast<const uint4*>(a.gamma + pcol[j]);
         }
     }
 
-    auto load = [&](int h, uint4 (&raw)[CPL], uint4 (&praw)[CPL]) {
-        const __nv_bfloat16* row = a.x + m * a.ldx_tok + h * a.ldx_head;
+    uint4 raw[U][CPL], praw[U][CPL];
+    constexpr int kStep = kHeadWarps * kRows;              // heads of a row of the CTA
+    auto load = [&](int h) {
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            raw[j] = praw[j] = make_uint4(0, 0, 0, 0);
-            if (h < h1 && live[j] && bounds_ok(m < a.M && h < a.H && col[j] + kChunk <= a.D && pcol[j] + kChunk <= a.D)) {
-                raw[j] = *reinterpret_cast<const uint4*>(row + col[j]);
-                if (rot[j] && a.rope.half) praw[j] = *reinterpret_cast<const uint4*>(row + pcol[j]);
+        for (int u = 0; u < U; ++u) {
+            const __nv_bfloat16* row = a.x + m * a.ldx_tok + static_cast<int64_t>(h + u * kStep) * a.ldx_head;
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                raw[u][j] = praw[u][j] = make_uint4(0, 0, 0, 0);
+                const int col = (l + j * LPR) * kChunk;
+                if (h + u * kStep < h1 && live[j] && bounds_ok(m < a.M && h + u * kStep < a.H && col + kChunk <= a.D &&
+                                                               pcol[j] + kChunk <= a.D)) {
+                    raw[u][j] = *reinterpret_cast<const uint4*>(row + col);
+                    if (HALF && rot[j]) praw[u][j] = *reinterpret_cast<const uint4*>(row + pcol[j]);
+                }
             }
         }
     };
 
-    constexpr int kStep = kHeadWarps * kRows;
-    int h = h0 + warp * kRows + sub;
-    uint4 raw[CPL], praw[CPL];
-    load(h, raw, praw);
+    load(h0 + warp * kRows + sub);
     if (threadIdx.x < static_cast<unsigned>(a.rope.dim / 2))
-        cs[threadIdx.x] = rope_angle(a.rope, a.rope.positions[m], threadIdx.x);
+        cs[threadIdx.x] = rope_angle(a.rope, turn_step(a.rope.inv_freq[threadIdx.x]), a.rope.positions[m]);
     __syncthreads();
 
-    for (int base = h0 + warp * kRows; base < h1; base += kStep, h += kStep) {
-        float2 x[CPL][4];
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) unpack8(raw[j], x[j]);
-        float2 y[CPL][4];
-        if (a.rope.half) {
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) unpack8(praw[j], y[j]);
-        }
-        load(h + kStep, raw, praw);      // the next row while this one is worked on
-        if (a.norm) {
-            float ssq = 0.f;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) ssq += sum_squares(x[j]);
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, o);
-            const float r = 1.0f / sqrtf(ssq / a.d_f + a.eps);
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                scale_by(x[j], r, graw[j], a.gamma != nullptr);
-                if (a.rope.half) scale_by(y[j], r, pgraw[j], a.gamma != nullptr);
-            }
-        }
+    for (int base = h0 + warp * kRows; base < h1; base += U * kStep) {
         // In place, a lane's partner chunk is another lane's output: every
         // lane has its rows in registers before any lane stores.
         __syncwarp();
-        if (h < h1) {
-            __nv_bfloat16* row = a.out + m * a.ldo_tok + h * a.ldo_head;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = base + sub + u * kStep;
+            float2 x[CPL][4], y[CPL][4];
 #pragma unroll
             for (int j = 0; j < CPL; ++j) {
-                if (!live[j] || !bounds_ok(m < a.M && h < a.H && col[j] + kChunk <= a.D)) continue;
-                if (rot[j]) rotate_chunk(a.rope, cs, col[j] - a.rope.off, x[j], y[j]);
-                *reinterpret_cast<uint4*>(row + col[j]) = pack8(x[j]);
+                unpack8(raw[u][j], x[j]);
+                if (HALF) unpack8(praw[u][j], y[j]);
+            }
+            if (a.norm) {
+                float ssq = 0.f;
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) ssq += sum_squares(x[j]);
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) ssq += __shfl_xor_sync(0xffffffffu, ssq, o);
+                const float r = 1.0f / sqrtf(ssq / a.d_f + a.eps);
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) {
+                    scale_by(x[j], r, graw[j], a.gamma != nullptr);
+                    if (HALF) scale_by(y[j], r, pgraw[j], a.gamma != nullptr);
+                }
+            }
+            if (h >= h1) continue;
+            __nv_bfloat16* row = a.out + m * a.ldo_tok + static_cast<int64_t>(h) * a.ldo_head;
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                const int col = (l + j * LPR) * kChunk;
+                if (!live[j] || !bounds_ok(m < a.M && h < a.H && col + kChunk <= a.D)) continue;
+                if (rot[j]) rotate_chunk<HALF>(a.rope, cs, col - a.rope.off, x[j], y[j]);
+                *reinterpret_cast<uint4*>(row + col) = pack8(x[j]);
             }
         }
+        if (base + U * kStep < h1) load(base + U * kStep + sub);
     }
 }
 
 template <int LPR, int CPL>
 dsnq_status launch_heads(HeadArgs& a, int sms, cudaStream_t s) {
-    // Heads per CTA: one step of its warps when tokens are few (a decode row
-    // is bound by latency), the whole token once the tokens alone fill the GPU.
+    // Heads per CTA: one row of its warps when tokens are few (a decode row is
+    // bound by latency), the whole token once the tokens alone fill the GPU.
     const int step = kHeadWarps * (32 / LPR);
     int64_t blocks = (a.H + step - 1) / step;
     const int64_t want = (8LL * sms + a.M - 1) / a.M;      // CTAs per token that give every SM eight
@@ -222,8 +239,8 @@ dsnq_status launch_heads(HeadArgs& a, int sms, cudaStream_t s) {
     a.head_blocks = (a.H + a.heads_per_block - 1) / a.heads_per_block;
     const int64_t grid = a.M * a.head_blocks;
     if (grid > 0x7fffffffLL) return DSNQ_ERR_UNSUPPORTED;
-    return launch_result(launch_kernel(head_norm_rope_kernel<LPR, CPL>, dim3(static_cast<unsigned>(grid)),
-                                       dim3(kHeadWarps * 32), 0, s, a));
+    return launch_result(launch_kernel(a.rope.half ? head_norm_rope_kernel<LPR, CPL, true> : head_norm_rope_kernel<LPR, CPL, false>,
+                                       dim3(static_cast<unsigned>(grid)), dim3(kHeadWarps * 32), 0, s, a));
 }
 
 // --------------------------------------------------------- latent cache write
@@ -246,71 +263,81 @@ struct WriteArgs {
 
 constexpr int kWriteWarps = 4;
 
-// One warp per row; lane l holds chunks l, l + 32, ... of the concatenated row.
-template <int CPL>
-__global__ void __launch_bounds__(kWriteWarps * 32)
+// One warp per row; lane l holds chunks l, l + 32, ... of the concatenated
+// row.  The row is requested before its slot and position are known (they
+// decide only where and by how much), so a row costs one trip to memory; four
+// CTAs or more per SM hide it.
+template <int CPL, bool HALF>
+__global__ void __launch_bounds__(kWriteWarps * 32, HALF ? 4 : 6)
 latent_cache_write_kernel(const WriteArgs a) {
     grid_dependency_wait();
     allow_dependent_launch();
     bounds_self_test(a.inject);
     __shared__ float2 cs_all[kWriteWarps][kMaxRope / 2];
+    __shared__ uint64_t steps[kMaxRope / 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float2* cs = cs_all[warp];
     const int64_t m = static_cast<int64_t>(blockIdx.x) * kWriteWarps + warp;
-    if (m >= a.M) return;
-    const int64_t slot = a.slots[m];
-    if (slot < 0) return;                // a padded row
-    if (slot >= a.num_slots) {
-        if (lane == 0) atomicOr(&g_rope_status, kStatusBounds);
-        return;
-    }
+    const bool in = m < a.M;
     const int c_lo = a.rope.off / kChunk, c_n = a.rope.dim / kChunk;
     bool live[CPL], rot[CPL];
-    float2 x[CPL][4], y[CPL][4];
-    uint4 graw[CPL], pgraw[CPL];
+    uint4 raw[CPL], praw[CPL], graw[CPL], pgraw[CPL];
     int pcol[CPL];
+    const int64_t slot = in ? a.slots[m] : -1;
+    const int64_t pos = in && a.rope.dim ? a.rope.positions[m] : 0;
     auto at = [&](int col) {
         return col < a.K ? a.kv + m * a.ldkv + col : a.pe + m * a.ldpe + (col - a.K);
     };
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
-        const int c = lane + j * 32, col = c * kChunk;
+        const int c = lane + j * 32, col = c * kChunk, q = c - c_lo;
         live[j] = col < a.W;
         rot[j] = live[j] && c >= c_lo && c < c_lo + c_n;
-        const int q = c - c_lo;
-        pcol[j] = (rot[j] && a.rope.half) ? (q < c_n / 2 ? c + c_n / 2 : c - c_n / 2) * kChunk : col;
-        uint4 raw = make_uint4(0, 0, 0, 0), praw = raw;
-        graw[j] = pgraw[j] = raw;
-        if (live[j] && bounds_ok(col + kChunk <= a.W && pcol[j] + kChunk <= a.W)) {
-            raw = *reinterpret_cast<const uint4*>(at(col));
-            if (rot[j] && a.rope.half) praw = *reinterpret_cast<const uint4*>(at(pcol[j]));
+        pcol[j] = HALF && rot[j] ? (q < c_n / 2 ? c + c_n / 2 : c - c_n / 2) * kChunk : col;
+        raw[j] = praw[j] = graw[j] = pgraw[j] = make_uint4(0, 0, 0, 0);
+        if (in && live[j] && bounds_ok(col + kChunk <= a.W && pcol[j] + kChunk <= a.W)) {
+            raw[j] = *reinterpret_cast<const uint4*>(at(col));
+            if (HALF && rot[j]) praw[j] = *reinterpret_cast<const uint4*>(at(pcol[j]));
             if (a.gamma && col < a.K) graw[j] = *reinterpret_cast<const uint4*>(a.gamma + col);
-            if (a.gamma && pcol[j] < a.K) pgraw[j] = *reinterpret_cast<const uint4*>(a.gamma + pcol[j]);
+            if (HALF && a.gamma && pcol[j] < a.K) pgraw[j] = *reinterpret_cast<const uint4*>(a.gamma + pcol[j]);
         }
-        unpack8(raw, x[j]);
-        unpack8(praw, y[j]);
     }
-    for (int i = lane; i < a.rope.dim / 2; i += 32) cs[i] = rope_angle(a.rope, a.rope.positions[m], i);
+    for (int i = threadIdx.x; i < a.rope.dim / 2; i += kWriteWarps * 32) steps[i] = turn_step(a.rope.inv_freq[i]);
+    __syncthreads();
+    if (slot < 0) return;                // a padded row, or none
+    if (slot >= a.num_slots) {
+        if (lane == 0) atomicOr(&g_rope_status, kStatusBounds);
+        return;
+    }
+    for (int i = lane; i < a.rope.dim / 2; i += 32) cs[i] = rope_angle(a.rope, steps[i], pos);
     __syncwarp();
+    float2 x[CPL][4];
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) unpack8(raw[j], x[j]);
+    float r = 1.f;
     if (a.norm) {
         float ssq = 0.f;
 #pragma unroll
         for (int j = 0; j < CPL; ++j)
             if ((lane + j * 32) * kChunk < a.K) ssq += sum_squares(x[j]);
-        const float r = 1.0f / sqrtf(warp_sum(ssq) / a.k_f + a.eps);
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-            if ((lane + j * 32) * kChunk < a.K) scale_by(x[j], r, graw[j], a.gamma != nullptr);
-            if (pcol[j] < a.K) scale_by(y[j], r, pgraw[j], a.gamma != nullptr);
-        }
+        r = 1.0f / sqrtf(warp_sum(ssq) / a.k_f + a.eps);
     }
-    const int64_t page = slot / a.page_size;
+    // Slots mostly fit 32 bits, whose division is a fraction of the 64-bit one.
+    const int64_t page = slot <= 0xffffffffLL ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page_size) : slot / a.page_size;
     __nv_bfloat16* row = a.cache + page * a.ld_page + (slot - page * a.page_size) * a.ld_row;
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
         const int col = (lane + j * 32) * kChunk;
         if (!live[j] || !bounds_ok(col + kChunk <= a.W)) continue;
-        if (rot[j]) rotate_chunk(a.rope, cs, col - a.rope.off, x[j], y[j]);
+        if (a.norm && col < a.K) scale_by(x[j], r, graw[j], a.gamma != nullptr);
+        if (rot[j]) {
+            float2 y[4];
+            if (HALF) {
+                unpack8(praw[j], y);
+                if (a.norm && pcol[j] < a.K) scale_by(y, r, pgraw[j], a.gamma != nullptr);
+            }
+            rotate_chunk<HALF>(a.rope, cs, col - a.rope.off, x[j], y);
+        }
         *reinterpret_cast<uint4*>(row + col) = pack8(x[j]);
     }
 }
@@ -335,6 +362,7 @@ struct ExtendArgs {
 constexpr int kExtendThreads = 512;
 
 // Exclusive sum of one value per thread over the CTA; *total gets the sum.
+// One barrier: every thread adds the warps' sums before its own itself.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t inc = v;
@@ -345,47 +373,14 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
     }
     if (lane == 31) warp_sums[warp] = inc;
     __syncthreads();
-    if (warp == 0) {
-        int64_t w = lane < kExtendThreads / 32 ? warp_sums[lane] : 0;
+    int64_t before = inc - v, sum = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += u;
-        }
-        if (lane < kExtendThreads / 32) warp_sums[lane] = w;
+    for (int i = 0; i < kExtendThreads / 32; ++i) {
+        if (i < warp) before += warp_sums[i];
+        sum += warp_sums[i];
     }
-    __syncthreads();
-    const int64_t before = warp ? warp_sums[warp - 1] : 0;
-    *total = warp_sums[kExtendThreads / 32 - 1];
-    __syncthreads();
-    return before + inc - v;
-}
-
-struct Request {
-    int old_len, want, held;             // tokens so far, tokens asked for, pages held
-};
-
-__device__ __forceinline__ Request read_request(const ExtendArgs& a, int b) {
-    Request r;
-    const int64_t cap = static_cast<int64_t>(a.width) * a.page_size;
-    const int32_t len = a.seq_lens[b];
-    r.old_len = static_cast<int>(len < 0 ? 0 : (len > cap ? cap : len));
-    const int32_t n = a.new_tokens ? a.new_tokens[b] : 1;
-    r.want = n < 0 ? 0 : n;
-    r.held = static_cast<int>((static_cast<int64_t>(r.old_len) + a.page_size - 1) / a.page_size);
-    return r;
-}
-
-// Pages request r needs for the tokens that have a row (rows - start) and a
-// place in the table; *fit gets their number.
-__device__ __forceinline__ int pages_needed(const ExtendArgs& a, const Request& r, int64_t start, int* fit) {
-    const int64_t cap = static_cast<int64_t>(a.width) * a.page_size;
-    int64_t f = r.want;
-    const int64_t room = a.rows > start ? a.rows - start : 0;
-    if (f > room) f = room;
-    if (f > cap - r.old_len) f = cap - r.old_len;
-    *fit = static_cast<int>(f);
-    return static_cast<int>((r.old_len + f + a.page_size - 1) / a.page_size) - r.held;
+    *total = sum;
+    return before;
 }
 
 // Every CTA forms the sums over all requests in shared memory (they are few
@@ -393,38 +388,53 @@ __device__ __forceinline__ int pages_needed(const ExtendArgs& a, const Request& 
 // requests (table, lengths) and of the token rows (positions, slots).  A
 // row's page is read from the entries the request already held, or straight
 // from the free list, never from an entry that another CTA writes.
+// Bound by latency: two trips to memory (lengths, then page ids) and two
+// barriers; 3 to 4 us a call in a graph for tens of requests.
 __global__ void __launch_bounds__(kExtendThreads)
 extend_tables_kernel(const ExtendArgs a) {
     grid_dependency_wait();
     allow_dependent_launch();
     bounds_self_test(a.inject);
-    extern __shared__ int32_t sums[];    // [B] first row (at most rows), [B] first free page (at most F)
-    int32_t* first_row = sums;
-    int32_t* first_page = sums + a.B;
-    __shared__ int64_t warp_sums[kExtendThreads / 32];
+    extern __shared__ int32_t sums[];
+    int32_t* old_s = sums;               // [B] tokens so far
+    int32_t* row_s = old_s + a.B;        // [B] first row, at most `rows`
+    int32_t* page_s = row_s + a.B;       // [B] first free page, at most F
+    int32_t* new_s = page_s + a.B;       // [B] tokens after the step
+    __shared__ int64_t warp_rows[kExtendThreads / 32], warp_pages[kExtendThreads / 32];
     const int t = threadIdx.x, lane = t & 31;
     const int per = (a.B + kExtendThreads - 1) / kExtendThreads;
     const int b0 = min(t * per, a.B), b1 = min(b0 + per, a.B);
+    const int64_t cap = static_cast<int64_t>(a.width) * a.page_size;     // below 2^31
+    const uint32_t ps = a.page_size;
+    auto pages_of = [&](int32_t len) -> int32_t { return static_cast<int32_t>((static_cast<uint32_t>(len) + ps - 1) / ps); };
 
+    // Each thread works on its own requests' entries up to the last barrier.
     int64_t n = 0, total_rows, total_pages;
-    for (int b = b0; b < b1; ++b) n += read_request(a, b).want;
-    const int64_t start0 = block_scan(n, warp_sums, &total_rows);
-    int64_t start = start0, pages = 0;
     for (int b = b0; b < b1; ++b) {
-        const Request r = read_request(a, b);
-        int fit;
-        first_row[b] = static_cast<int32_t>(start < a.rows ? start : a.rows);
-        pages += pages_needed(a, r, start, &fit);
-        start += r.want;
+        const int32_t len = a.seq_lens[b], want = a.new_tokens ? a.new_tokens[b] : 1;
+        old_s[b] = static_cast<int32_t>(len < 0 ? 0 : (len > cap ? cap : len));
+        row_s[b] = want < 0 ? 0 : want;
+        n += row_s[b];
     }
-    int64_t page = block_scan(pages, warp_sums, &total_pages);
-    start = start0;
+    int64_t start = block_scan(n, warp_rows, &total_rows), pages = 0;
     for (int b = b0; b < b1; ++b) {
-        const Request r = read_request(a, b);
-        int fit;
-        first_page[b] = static_cast<int32_t>(page < a.F ? page : a.F);
-        page += pages_needed(a, r, start, &fit);
-        start += r.want;
+        const int32_t want = row_s[b], len = old_s[b];
+        row_s[b] = static_cast<int32_t>(start < a.rows ? start : a.rows);
+        // The tokens that have a row and a place in the table.
+        const int64_t fit = min(static_cast<int64_t>(min(want, a.rows - row_s[b])), cap - len);
+        new_s[b] = static_cast<int32_t>(len + fit);
+        page_s[b] = pages_of(new_s[b]) - pages_of(len);
+        pages += page_s[b];
+        start += want;
+    }
+    int64_t page = block_scan(pages, warp_pages, &total_pages);
+    for (int b = b0; b < b1; ++b) {
+        const int32_t need = page_s[b];
+        page_s[b] = static_cast<int32_t>(page < a.F ? page : a.F);
+        page += need;
+        const int32_t got = min(need, a.F - page_s[b]);
+        const int64_t backed = static_cast<int64_t>(pages_of(old_s[b]) + got) * ps;
+        if (backed < new_s[b]) new_s[b] = static_cast<int32_t>(backed);
     }
     __syncthreads();
     const int live_rows = static_cast<int>(total_rows < a.rows ? total_rows : a.rows);
@@ -435,22 +445,45 @@ extend_tables_kernel(const ExtendArgs a) {
         a.counts[1] = static_cast<int32_t>(total_pages < 0x7fffffff ? total_pages : 0x7fffffff);
     }
 
+    // Token rows.
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kExtendThreads + t; r < a.rows;
+         r += static_cast<int64_t>(gridDim.x) * kExtendThreads) {
+        const int row = static_cast<int>(r);
+        int64_t pos = 0, slot = -1;
+        if (row < live_rows) {
+            // The last request whose first row is at most `row` (requests
+            // without tokens share their successor's first row and lose).
+            int lo = 0, hi = a.B;        // row_s[lo] <= row, row_s[hi] > row
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (row_s[mid] <= row) lo = mid;
+                else hi = mid;
+            }
+            const int32_t len = old_s[lo];
+            pos = static_cast<int64_t>(len) + (row - row_s[lo]);
+            if (pos < new_s[lo]) {
+                const int32_t p = static_cast<int32_t>(static_cast<uint32_t>(pos) / ps), k = p - pages_of(len);
+                int32_t id = -1;
+                if (bounds_ok(p < a.width && page_s[lo] + k < a.F + (k < 0 ? 0x40000000 : 0)))
+                    id = k < 0 ? a.table[lo * a.ld_table + p] : a.free_pages[page_s[lo] + k];
+                if (id >= 0) slot = static_cast<int64_t>(id) * ps + (pos - static_cast<int64_t>(p) * ps);
+            }
+        }
+        a.positions[row] = pos;
+        a.slots[row] = slot;
+    }
+
     // Requests: one per thread; a request's new pages are stored by its whole
     // warp when they are many (a prompt), by its thread otherwise.
-    for (int bw = (blockIdx.x * kExtendThreads + (t & ~31)); bw < a.B; bw += gridDim.x * kExtendThreads) {
+    for (int bw = blockIdx.x * kExtendThreads + (t & ~31); bw < a.B; bw += gridDim.x * kExtendThreads) {
         const int b = bw + lane;
         int got = 0, held = 0, from = 0;
         if (b < a.B) {
-            const Request r = read_request(a, b);
-            int fit;
-            const int need = pages_needed(a, r, first_row[b], &fit);
-            from = first_page[b];
-            got = min(need, a.F - from);
-            held = r.held;
-            const int64_t end = static_cast<int64_t>(r.old_len) + fit;
-            const int64_t backed = static_cast<int64_t>(held + got) * a.page_size;
-            a.new_lens[b] = static_cast<int32_t>(end < backed ? end : backed);
-            a.row_starts[b] = first_row[b];
+            held = pages_of(old_s[b]);
+            from = page_s[b];
+            got = pages_of(new_s[b]) - held;
+            a.new_lens[b] = new_s[b];
+            a.row_starts[b] = row_s[b];
             if (got <= 2)
                 for (int k = 0; k < got; ++k)
                     if (bounds_ok(held + k < a.width && from + k < a.F))
@@ -466,40 +499,6 @@ extend_tables_kernel(const ExtendArgs a) {
                 if (bounds_ok(hd + k < a.width && f + k < a.F))
                     a.table[(bw + src) * a.ld_table + hd + k] = a.free_pages[f + k];
         }
-    }
-
-    // Token rows.
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kExtendThreads + t; r0 < a.rows;
-         r0 += static_cast<int64_t>(gridDim.x) * kExtendThreads) {
-        const int row = static_cast<int>(r0);
-        int64_t pos = 0, slot = -1;
-        if (row < live_rows) {
-            // The last request whose first row is at most `row` (requests
-            // without tokens share their successor's first row and lose).
-            int lo = 0, hi = a.B;        // first_row[lo] <= row, first_row[hi] > row
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (first_row[mid] <= row) lo = mid;
-                else hi = mid;
-            }
-            const Request r = read_request(a, lo);
-            int fit;
-            const int need = pages_needed(a, r, first_row[lo], &fit);
-            const int from = first_page[lo];
-            const int got = min(need, a.F - from);
-            const int j = row - first_row[lo];
-            pos = static_cast<int64_t>(r.old_len) + j;
-            const int64_t p = pos / a.page_size;
-            if (j < fit && p < r.held + got) {
-                const int k = static_cast<int>(p) - r.held;
-                int32_t id = -1;
-                if (bounds_ok(p < a.width && from + k < a.F))
-                    id = k < 0 ? a.table[lo * a.ld_table + p] : a.free_pages[from + k];
-                if (id >= 0) slot = static_cast<int64_t>(id) * a.page_size + (pos - p * a.page_size);
-            }
-        }
-        a.positions[row] = pos;
-        a.slots[row] = slot;
     }
 }
 
@@ -614,10 +613,12 @@ extern "C" dsnq_status dsnq_latent_cache_write(
     a.inject = debug_inject_flags();
     const dim3 grid(static_cast<unsigned>((M + kWriteWarps - 1) / kWriteWarps)), block(kWriteWarps * 32);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (W <= 256) return launch_result(launch_kernel(latent_cache_write_kernel<1>, grid, block, 0, s, a));
-    if (W <= 512) return launch_result(launch_kernel(latent_cache_write_kernel<2>, grid, block, 0, s, a));
-    if (W <= 768) return launch_result(launch_kernel(latent_cache_write_kernel<3>, grid, block, 0, s, a));
-    return launch_result(launch_kernel(latent_cache_write_kernel<4>, grid, block, 0, s, a));
+    const bool half = layout == DSNQ_ROPE_HALF;
+    void (*kern)(WriteArgs) = W <= 256   ? (half ? latent_cache_write_kernel<1, true> : latent_cache_write_kernel<1, false>)
+                              : W <= 512 ? (half ? latent_cache_write_kernel<2, true> : latent_cache_write_kernel<2, false>)
+                              : W <= 768 ? (half ? latent_cache_write_kernel<3, true> : latent_cache_write_kernel<3, false>)
+                                         : (half ? latent_cache_write_kernel<4, true> : latent_cache_write_kernel<4, false>);
+    return launch_result(launch_kernel(kern, grid, block, 0, s, a));
 }
 
 extern "C" dsnq_status dsnq_extend_block_tables(
@@ -654,8 +655,8 @@ extern "C" dsnq_status dsnq_extend_block_tables(
     }
     int64_t grid = ((rows > B ? rows : B) + kExtendThreads - 1) / kExtendThreads;
     grid = grid < 1 ? 1 : (grid > sms ? sms : grid);
-    const size_t smem = static_cast<size_t>(2 * B) * sizeof(int32_t);
-    static_assert(2 * DSNQ_MAX_REQUESTS * sizeof(int32_t) <= 128 * 1024, "two words per request in shared memory");
+    const size_t smem = static_cast<size_t>(4 * B) * sizeof(int32_t);
+    static_assert(4 * DSNQ_MAX_REQUESTS * sizeof(int32_t) <= 128 * 1024, "four words per request in shared memory");
     if (smem > 48 * 1024 && !set_smem_attr(reinterpret_cast<const void*>(extend_tables_kernel), smem)) return DSNQ_ERR_CUDA;
     return launch_result(launch_kernel(extend_tables_kernel, dim3(static_cast<unsigned>(grid)), dim3(kExtendThreads), smem,
                                        static_cast<cudaStream_t>(stream), a));

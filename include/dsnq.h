@@ -391,7 +391,7 @@ DSNQ_API dsnq_status dsnq_fused_norm_quant_gemm_dual(
 
 /* Most requests of one call of dsnq_extend_block_tables and
  * dsnq_paged_latent_attention. */
-#define DSNQ_MAX_REQUESTS 16384
+#define DSNQ_MAX_REQUESTS 8192
 
 /* Pairing of the rotated columns x[0 .. R): pair i is (x[2i], x[2i+1]) or
  * (x[i], x[i + R/2]). */
