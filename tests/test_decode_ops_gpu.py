@@ -611,7 +611,7 @@ def test_decode_step_in_a_graph():
         q, _, lens, _, _, _, counts = m.step(m.x, m.lens, None, m.free)
         out, lse = dsnq.paged_latent_attention(q, m.cache, m.table, lens, 512, m.scale, workspace=m.ws)
         m.lens.copy_(lens)
-            idx = (torch.arange(m.free.numel(), device=DEV) + counts[0]) % m.free.numel()
+        idx = (torch.arange(m.free.numel(), device=DEV) + counts[0]) % m.free.numel()
         m.free.copy_(m.free[idx])
         return out, lse
 
