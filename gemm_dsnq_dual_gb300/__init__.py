@@ -359,41 +359,60 @@ def fused_norm_quant_gemm_dual(q, kv, gamma_q, gamma_kv, eps, w1_fp8, w1_scale, 
     return out1, out2, kv_out, q_fp8, q_scale
 
 
-def _need(t, name: str, dtype, dim: int, dev=None):
-    """Checks a tensor argument's type, rank and device."""
+_BF16, _F32, _F64, _I32, _I64 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.int64
+
+
+def _refuse(t, name: str, dtype, dim: int, dev, why: str):
+    """Says what is wrong with a tensor argument."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
-    if dev is not None and t.device != dev:
+    if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    return t
+    raise ValueError(f"{name} {why}, got shape {tuple(t.shape)}, strides {t.stride()}")
 
 
-def _flat(t, name: str, dtype, n: int, dev):
+# One function per rank checks a tensor and gives what the library takes of
+# it: small calls are bound by this host work.
+
+def _vec(t, name: str, dtype, n: int, dev) -> int:
     """The address of a contiguous 1-D tensor of n elements."""
     if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or t.device != dev:
-        _need(t, name, dtype, 1, dev)
-        raise ValueError(f"{name} must be contiguous with {n} elements, got shape {tuple(t.shape)}, strides {t.stride()}")
+        _refuse(t, name, dtype, 1, dev, f"must be contiguous with {n} elements")
     return t.data_ptr()
 
 
-def _strides3(t, name: str):
-    """Strides of the two outer dimensions of a 3-D tensor with contiguous
-    rows (a dimension of size 1 gets the stride it would have if packed)."""
-    s0, s1, s2 = t.stride()
+def _mat(t, name: str, dtype, dev):
+    """(rows, columns, row stride, address) of a 2-D tensor with contiguous rows."""
+    if t.dtype is not dtype or t.dim() != 2 or t.device != dev:
+        _refuse(t, name, dtype, 2, dev, "")
+    n0, n1 = t.shape
+    s0, s1 = t.stride()
+    if s1 != 1 and n1 > 1:
+        _refuse(t, name, dtype, 2, dev, "must have contiguous rows")
+    return n0, n1, (s0 if n0 > 1 else max(s0, n1)), t.data_ptr()
+
+
+def _cube(t, name: str, dtype, dev):
+    """(three sizes, two outer strides, address) of a 3-D tensor with
+    contiguous rows (a dimension of size 1 gets the stride it would have if
+    packed)."""
+    if t.dtype is not dtype or t.dim() != 3 or t.device != dev:
+        _refuse(t, name, dtype, 3, dev, "")
     n0, n1, n2 = t.shape
+    s0, s1, s2 = t.stride()
     if s2 != 1 and n2 > 1:
-        raise ValueError(f"{name} must have contiguous rows")
+        _refuse(t, name, dtype, 3, dev, "must have contiguous rows")
     if n1 == 1:
         s1 = n2
-    return (n1 * s1 if n0 == 1 else s0), s1
+    return n0, n1, n2, (n1 * s1 if n0 == 1 else s0), s1, t.data_ptr()
 
 
 def _rope_layout(layout) -> int:
-    if layout in (ROPE_INTERLEAVED, "interleaved"):
+    if layout == "interleaved" or layout == ROPE_INTERLEAVED:
         return ROPE_INTERLEAVED
-    if layout in (ROPE_HALF, "half"):
+    if layout == "half" or layout == ROPE_HALF:
         return ROPE_HALF
     raise ValueError(f"unknown rotary layout {layout!r}")
 
@@ -432,23 +451,22 @@ def extend_block_tables(seq_lens, new_tokens, free_pages, block_table, page_size
     `out` supplies those five.  Padded rows and tokens without a place have
     slot -1."""
     B, dev = seq_lens.shape[0], seq_lens.device
-    _need(block_table, "block_table", torch.int32, 2, dev)
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table has {block_table.shape[0]} rows for {B} requests")
+    tb, width, ld, table = _mat(block_table, "block_table", _I32, dev)
+    if tb != B:
+        raise ValueError(f"block_table has {tb} rows for {B} requests")
     if out is None:
-        out = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B + 1, dtype=torch.int32, device=dev),
-               torch.empty(rows, dtype=torch.int64, device=dev), torch.empty(rows, dtype=torch.int64, device=dev),
-               torch.empty(2, dtype=torch.int32, device=dev))
+        out = (torch.empty(B, dtype=_I32, device=dev), torch.empty(B + 1, dtype=_I32, device=dev),
+               torch.empty(rows, dtype=_I64, device=dev), torch.empty(rows, dtype=_I64, device=dev),
+               torch.empty(2, dtype=_I32, device=dev))
     new_lens, row_starts, positions, slots, counts = out
     F = free_pages.shape[0]
     check(lib().dsnq_extend_block_tables(
-        B, rows, page_size, _flat(seq_lens, "seq_lens", torch.int32, B, dev),
-        None if new_tokens is None else _flat(new_tokens, "new_tokens", torch.int32, B, dev),
-        _flat(free_pages, "free_pages", torch.int32, F, dev), F,
-        block_table.data_ptr(), block_table.shape[1], _row_view_ok(block_table, "block_table"),
-        _flat(new_lens, "new_lens", torch.int32, B, dev), _flat(row_starts, "row_starts", torch.int32, B + 1, dev),
-        _flat(positions, "positions", torch.int64, rows, dev), _flat(slots, "slots", torch.int64, rows, dev),
-        _flat(counts, "counts", torch.int32, 2, dev), _stream(stream, dev)), "dsnq_extend_block_tables")
+        B, rows, page_size, _vec(seq_lens, "seq_lens", _I32, B, dev),
+        None if new_tokens is None else _vec(new_tokens, "new_tokens", _I32, B, dev),
+        _vec(free_pages, "free_pages", _I32, F, dev), F, table, width, ld,
+        _vec(new_lens, "new_lens", _I32, B, dev), _vec(row_starts, "row_starts", _I32, B + 1, dev),
+        _vec(positions, "positions", _I64, rows, dev), _vec(slots, "slots", _I64, rows, dev),
+        _vec(counts, "counts", _I32, 2, dev), _stream(stream, dev)), "dsnq_extend_block_tables")
     return new_lens, row_starts, positions, slots, counts
 
 
@@ -458,20 +476,19 @@ def head_rmsnorm_rope(x, positions, inv_freq, gamma=None, eps: float = 1e-6, nor
     and rotation of its columns [rope_offset, rope_offset + 2 * len(inv_freq))
     (default: the last ones) by positions [M] int64 times inv_freq float64,
     one rounding.  `out` may be x.  Returns out [M,H,D]."""
-    M, H, D = _need(x, "x", torch.bfloat16, 3).shape
     dev = x.device
+    M, H, D, xt, xh, xp = _cube(x, "x", _BF16, dev)
     if out is None:
-        out = torch.empty(M, H, D, dtype=torch.bfloat16, device=dev)
-    elif _need(out, "out", torch.bfloat16, 3, dev).shape != x.shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
+        out = torch.empty(M, H, D, dtype=_BF16, device=dev)
+    oM, oH, oD, ot, oh, op = _cube(out, "out", _BF16, dev)
+    if oM != M or oH != H or oD != D:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, H, D)}")
     pairs = inv_freq.shape[0]
-    sx, so = _strides3(x, "x"), _strides3(out, "out")
     check(lib().dsnq_head_rmsnorm_rope(
-        M, H, D, x.data_ptr(), sx[0], sx[1], 1 if normalize else 0,
-        None if gamma is None else _flat(gamma, "gamma", torch.bfloat16, D, dev), float(eps),
-        _flat(positions, "positions", torch.int64, M, dev), _flat(inv_freq, "inv_freq", torch.float64, pairs, dev),
-        D - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), float(rope_scale),
-        1 if inverse else 0, out.data_ptr(), so[0], so[1], _stream(stream, dev)), "dsnq_head_rmsnorm_rope")
+        M, H, D, xp, xt, xh, 1 if normalize else 0, None if gamma is None else _vec(gamma, "gamma", _BF16, D, dev), eps,
+        _vec(positions, "positions", _I64, M, dev), _vec(inv_freq, "inv_freq", _F64, pairs, dev),
+        D - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), rope_scale,
+        1 if inverse else 0, op, ot, oh, _stream(stream, dev)), "dsnq_head_rmsnorm_rope")
     return out
 
 
@@ -482,25 +499,24 @@ def latent_cache_write(kv, pe, positions, slots, inv_freq, cache, gamma=None, ep
     `normalize`, columns [rope_offset, + 2 * len(inv_freq)) of the row
     (default: the last ones) rotated.  Negative slots are skipped; the slots
     of a call must be distinct.  Returns cache."""
-    M, K = _need(kv, "kv", torch.bfloat16, 2).shape
     dev = kv.device
-    P = 0
+    M, K, ldkv, kvp = _mat(kv, "kv", _BF16, dev)
+    P = ldpe = 0
+    pep = None
     if pe is not None:
-        P = _need(pe, "pe", torch.bfloat16, 2, dev).shape[1]
-        if pe.shape[0] != M:
-            raise ValueError(f"pe has {pe.shape[0]} rows, kv {M}")
-    pages, page_size, W = _need(cache, "cache", torch.bfloat16, 3, dev).shape
+        rows, P, ldpe, pep = _mat(pe, "pe", _BF16, dev)
+        if rows != M:
+            raise ValueError(f"pe has {rows} rows, kv {M}")
+    pages, page_size, W, ld_page, ld_row, cp = _cube(cache, "cache", _BF16, dev)
     if W != K + P:
         raise ValueError(f"cache rows have {W} columns, kv and pe {K + P}")
     pairs = inv_freq.shape[0]
-    sc = _strides3(cache, "cache")
     check(lib().dsnq_latent_cache_write(
-        M, K, P, kv.data_ptr(), _row_view_ok(kv, "kv"), pe.data_ptr() if P else None, _row_view_ok(pe, "pe") if P else 0,
-        1 if normalize else 0, None if gamma is None else _flat(gamma, "gamma", torch.bfloat16, K, dev), float(eps),
-        _flat(positions, "positions", torch.int64, M, dev), _flat(inv_freq, "inv_freq", torch.float64, pairs, dev),
-        W - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), float(rope_scale),
-        _flat(slots, "slots", torch.int64, M, dev), cache.data_ptr(), pages, page_size, sc[0], sc[1],
-        _stream(stream, dev)), "dsnq_latent_cache_write")
+        M, K, P, kvp, ldkv, pep, ldpe, 1 if normalize else 0, None if gamma is None else _vec(gamma, "gamma", _BF16, K, dev),
+        eps, _vec(positions, "positions", _I64, M, dev), _vec(inv_freq, "inv_freq", _F64, pairs, dev),
+        W - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), rope_scale,
+        _vec(slots, "slots", _I64, M, dev), cp, pages, page_size, ld_page, ld_row, _stream(stream, dev)),
+        "dsnq_latent_cache_write")
     return cache
 
 
@@ -520,34 +536,33 @@ def paged_latent_attention(q, cache, block_table, seq_lens, v_dim: int, scale: f
     [pages, page_size, DK], whose pages block_table [B, width] (int32) names.
     The value of a row is its first v_dim columns.  Returns (out [B,H,v_dim]
     bf16, lse [B,H] fp32).  The uint8 `workspace` is allocated if omitted."""
-    B, H, DK = _need(q, "q", torch.bfloat16, 3).shape
     dev = q.device
-    pages, page_size, W = _need(cache, "cache", torch.bfloat16, 3, dev).shape
+    B, H, DK, qt, qh, qp = _cube(q, "q", _BF16, dev)
+    pages, page_size, W, ld_page, ld_row, cp = _cube(cache, "cache", _BF16, dev)
     if W != DK:
         raise ValueError(f"cache rows have {W} columns, q {DK}")
-    _need(block_table, "block_table", torch.int32, 2, dev)
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table has {block_table.shape[0]} rows for {B} requests")
-    width = block_table.shape[1]
+    tb, width, ldt, table = _mat(block_table, "block_table", _I32, dev)
+    if tb != B:
+        raise ValueError(f"block_table has {tb} rows for {B} requests")
     if out is None:
-        out = torch.empty(B, H, v_dim, dtype=torch.bfloat16, device=dev)
-    elif _need(out, "out", torch.bfloat16, 3, dev).shape != (B, H, v_dim):
+        out = torch.empty(B, H, v_dim, dtype=_BF16, device=dev)
+    oB, oH, oD, ot, oh, op = _cube(out, "out", _BF16, dev)
+    if oB != B or oH != H or oD != v_dim:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(B, H, v_dim)}")
     if lse is None:
-        lse = torch.empty(B, H, dtype=torch.float32, device=dev)
-    elif _need(lse, "lse", torch.float32, 2, dev).shape != (B, H):
+        lse = torch.empty(B, H, dtype=_F32, device=dev)
+    lB, lH, ldl, lp = _mat(lse, "lse", _F32, dev)
+    if lB != B or lH != H:
         raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(B, H)}")
     if workspace is None:
-        workspace = torch.empty(paged_latent_attention_workspace_bytes(B, H, v_dim, width, page_size), dtype=torch.uint8,
-                                device=dev)
-    elif _need(workspace, "workspace", torch.uint8, 1, dev).stride(0) != 1:
-        raise ValueError("workspace must be contiguous")
-    sq, sc, so = _strides3(q, "q"), _strides3(cache, "cache"), _strides3(out, "out")
+        size = paged_latent_attention_workspace_bytes(B, H, v_dim, width, page_size)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    else:
+        size = workspace.numel()
     check(lib().dsnq_paged_latent_attention(
-        B, H, DK, v_dim, q.data_ptr(), sq[0], sq[1], cache.data_ptr(), pages, page_size, sc[0], sc[1],
-        block_table.data_ptr(), width, _row_view_ok(block_table, "block_table"), _flat(seq_lens, "seq_lens", torch.int32, B, dev),
-        float(scale), out.data_ptr(), so[0], so[1], lse.data_ptr(), _row_view_ok(lse, "lse"), workspace.data_ptr(),
-        workspace.numel(), _stream(stream, dev)), "dsnq_paged_latent_attention")
+        B, H, DK, v_dim, qp, qt, qh, cp, pages, page_size, ld_page, ld_row, table, width, ldt,
+        _vec(seq_lens, "seq_lens", _I32, B, dev), scale, op, ot, oh, lp, ldl,
+        _vec(workspace, "workspace", torch.uint8, size, dev), size, _stream(stream, dev)), "dsnq_paged_latent_attention")
     return out, lse
 
 

@@ -1,6 +1,7 @@
 // Internal helpers shared by the CUDA translation units of libdsnq.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <utility>
 #include <cuda_runtime.h>
@@ -46,10 +47,15 @@ inline dsnq_status launch_result(cudaError_t e) {
     return (e == cudaSuccess && last == cudaSuccess) ? DSNQ_OK : DSNQ_ERR_CUDA;
 }
 
+// SMs of the current device (0 on error), looked up once per device.
 inline int device_sm_count() {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < kDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
