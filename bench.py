@@ -876,6 +876,45 @@ def allreduce_max(x: float, world, dev):
     return float(t.item())
 
 
+def decode_ops(which, M, dev):
+    """A call of one operator of the decode step on M rows: `tables` for M
+    requests, `head_rope` on the attention heads of wq_b's output (128 of 192
+    columns, the last 64 rotated), `cache_write` of the kv latent and its
+    position columns, `attention` of M requests of 1024 tokens each with 128
+    heads over the 576-column cache."""
+    import torch
+    import gemm_dsnq_dual_gb300 as dsnq
+    g = torch.Generator(device=dev).manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=dev).to(torch.bfloat16)
+    ints = lambda n, hi: torch.randint(0, hi, (n,), generator=g, device=dev)
+    page, tokens = 64, 1024
+    pages = M * (tokens // page + 1)
+    ids = torch.randperm(pages, generator=g, device=dev).to(torch.int32)
+    f, scale = dsnq.rope_frequencies(64, device=dev)
+    if which == "tables":
+        table = torch.full((M, tokens // page + 1), -1, dtype=torch.int32, device=dev)
+        table[:, :tokens // page] = ids[:M * (tokens // page)].view(M, -1)
+        lens = torch.full((M,), tokens, dtype=torch.int32, device=dev)
+        return lambda: dsnq.extend_block_tables(lens, None, ids[M * (tokens // page):], table, page, M)
+    if which == "head_rope":
+        x, pos = rnd(M, N_ATTN).view(M, 128, 192), ints(M, 1 << 17)
+        out = torch.empty_like(x)
+        return lambda: dsnq.head_rmsnorm_rope(x, pos, f, normalize=False, rope_scale=scale, out=out)
+    cache = rnd(pages, page, KKV + 64)
+    if which == "cache_write":
+        row, pos = rnd(M, KQ + KKV + 64), ints(M, 1 << 17)
+        slots = torch.randperm(pages * page, generator=g, device=dev)[:M]
+        gamma = rnd(KKV)
+        return lambda: dsnq.latent_cache_write(row[:, KQ:KQ + KKV], row[:, KQ + KKV:], pos, slots, f, cache, gamma=gamma,
+                                               normalize=True, rope_scale=scale)
+    q, table = rnd(M, 128, KKV + 64), ids.view(M, -1)
+    lens = torch.full((M,), tokens, dtype=torch.int32, device=dev)
+    return lambda: dsnq.paged_latent_attention(q, cache, table, lens, KKV, 192 ** -0.5)
+
+
+DECODE_OPS = ["tables", "head_rope", "cache_write", "attention"]
+
+
 def run_kernel_only(args):
     """A few launches of one kernel on the configured workload, for profilers
     (ncu): `--kernel-only gemm` runs the dual GEMM, `norm_quant` the fused
@@ -883,13 +922,21 @@ def run_kernel_only(args):
     `unfused` the unfused baseline's three launches (norm to bf16, then the
     quant of q twice), `fused_step` the one-launch norm+quant+GEMM (a few
     decode rows), `bf16a` the dual GEMM on the bf16 q rows (quantized inside
-    the GEMM for a few rows); no timing, no JSON line.  Every mode first runs one fused
-    norm+quant to make its inputs."""
+    the GEMM for a few rows), and the operators of decode_ops(); no timing, no
+    JSON line.  The modes of the pre-projection first run one fused norm+quant
+    to make their inputs."""
     import torch
     import gemm_dsnq_dual_gb300 as dsnq
     from gemm_dsnq_dual_gb300 import inputs
     dev = torch.device("cuda", 0)
     M = args.M
+    if args.kernel_only in DECODE_OPS:
+        fn = decode_ops(args.kernel_only, M, dev)
+        for _ in range(args.launches):
+            fn()
+        torch.cuda.synchronize()
+        print(f"kernel-only {args.kernel_only} M={M}: {args.launches} launches ok")
+        return
     lat = inputs.full_path_batch(M, seed=3)
     q, kv = lat.q.to(dev), lat.kv.to(dev)
     gq, gkv = lat.gamma_q.to(dev), lat.gamma_kv.to(dev)
@@ -938,7 +985,7 @@ def main():
     ap.add_argument("--no-long-context", dest="long_context", action="store_false",
                     help="skip the M=32768 long-context GEMM of the side measurements")
     ap.add_argument("--no-cpu-baseline", action="store_true")
-    ap.add_argument("--kernel-only", choices=["gemm", "norm_quant", "single_latent", "unfused", "fused_step", "bf16a"],
+    ap.add_argument("--kernel-only", choices=["gemm", "norm_quant", "single_latent", "unfused", "fused_step", "bf16a", *DECODE_OPS],
                     default=None,
                     help="profiling aid: launch one kernel --launches times and exit")
     ap.add_argument("--launches", type=int, default=3)
