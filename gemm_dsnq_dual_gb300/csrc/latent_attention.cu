@@ -25,7 +25,7 @@
 // O is kept transposed because TMEM has 512 columns: 64 heads x 512 values take
 // DV/128 x 64 = 256 of them at full use of its 128 lanes, which leaves room for
 // two S buffers; heads x DV at M = 64 would take all 512.
-// P is rounded to bf16 (half a step, 2^-9 relative) because the tensor core
+// P is rounded to bf16 (half a step, 2^-8 relative) because the tensor core
 // takes bf16; sums, maxima and O stay in fp32, and the sum is of the unrounded p.
 // Warps: 0 copies tiles (TMA), 1 issues the products Q K^T, 6 the products P V,
 // 2..5 do the softmax, the rescaling of O and the output.  S(n+1) is computed
@@ -396,9 +396,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     const int b_first = run.b;
     if (threadIdx.x == 0 && g == 0) p.meta[w] = make_int2(run.b, run.t0);
 
-    // The issuing warps' wait: the vote makes the result, and so the control
-    // flow after it, uniform to the compiler, which then keeps descriptors in
-    // uniform registers, where tcgen05.mma takes them.
+    // A whole warp's wait: all of its lanes go on or none (warp-wide
+    // instructions follow), and the compiler sees that it is so.
     auto wait_uniform = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_bounded<true>(bar, parity, abort_flag, tmo));
     };
@@ -576,7 +575,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
             for (int i = 0; i < run.n; ++i, ++n) {
                 const int valid = min(kTile, run.len - (run.t0 + i) * kTile);
-                ok = ok && wait_bounded<true>(smem_u32(&sfull[n & 1]), (n >> 1) & 1, abort_flag, tmo);
+                ok = ok && wait_uniform(smem_u32(&sfull[n & 1]), (n >> 1) & 1);
                 tc_fence_after();
                 float s[2][16];                            // [row][8 k + column]
                 {
@@ -601,7 +600,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 }
                 // Whether product n - 1 is done (then P's buffer and O are this
                 // tile's) is looked at early: the test takes long, and mostly it is.
-                bool pv_done = n == 0 || mbar_test(smem_u32(pempty), (n & 1) ^ 1);
+                bool pv_done = n == 0 || __all_sync(0xffffffffu, mbar_test(smem_u32(pempty), (n & 1) ^ 1));
                 bool raise = false;
                 float top[2];
 #pragma unroll
@@ -632,7 +631,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                         if ((lane & 3) == 0) alpha_s[row0 + 8 * a] = alpha;
                     }
                     soft_sync_or(false);
-                    if (!pv_done) ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
+                    if (!pv_done) ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
                     pv_done = true;
                     tc_fence_after();
                     for (int c = 0; ok && c < p.nblk * kHeads; c += 16) {
@@ -649,28 +648,28 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 uint32_t pk[2][8];
                 if (mine) {
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                    const float off = m[a] == kNegInf ? 0.f : m[a] * p.scale_log2;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int a = 0; a < 2; ++a) {
+                        const float off = m[a] == kNegInf ? 0.f : m[a] * p.scale_log2;
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float e0 = exp2_fast(fmaf(s[a][2 * j], p.scale_log2, -off));
-                        const float e1 = exp2_fast(fmaf(s[a][2 * j + 1], p.scale_log2, -off));
-                        sum[j & 1] += e0;
-                        sum[2 + (j & 1)] += e1;
-                        pk[a][j] = pack_bf16(e0, e1);
+                        for (int j = 0; j < 8; ++j) {
+                            const float e0 = exp2_fast(fmaf(s[a][2 * j], p.scale_log2, -off));
+                            const float e1 = exp2_fast(fmaf(s[a][2 * j + 1], p.scale_log2, -off));
+                            sum[j & 1] += e0;
+                            sum[2 + (j & 1)] += e1;
+                            pk[a][j] = pack_bf16(e0, e1);
+                        }
+                        l[a] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     }
-                    l[a] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
-                }
-                if (!pv_done) ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
+                if (!pv_done) ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
                 __syncwarp();
                 if (ok) {
                     if (mine) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        stmatrix_x4(p_addr + (((2 * j + p_grp) ^ p_swz) << 4), pk[0][2 * j], pk[1][2 * j], pk[0][2 * j + 1],
-                                    pk[1][2 * j + 1]);
+                        for (int j = 0; j < 4; ++j)
+                            stmatrix_x4(p_addr + (((2 * j + p_grp) ^ p_swz) << 4), pk[0][2 * j], pk[1][2 * j], pk[0][2 * j + 1],
+                                        pk[1][2 * j + 1]);
                     }
                     if (valid < kTile) {
                         // Rows past the length hold whatever the page or the
@@ -694,7 +693,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 if (lane == 0) mbar_arrive(smem_u32(pfull));
             }
             // ---- output of the request (or of this worker's part of it)
-            ok = ok && wait_bounded<true>(smem_u32(pempty), (n & 1) ^ 1, abort_flag, tmo);
+            ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
             tc_fence_after();
             const int64_t slot = (static_cast<int64_t>(w) * 2 + (b == b_first ? 0 : 1)) * p.G + g;
 #pragma unroll
