@@ -405,7 +405,8 @@ def test_attention_lengths_around_every_tile_border():
 
 
 @pytest.mark.parametrize("lens,H", [([20000], 16), ([9000, 3], 128), ([0, 5000, 0, 1], 64), ([1] * 400, 8), ([64] * 160 + [0] * 30, 65),
-                                    ([700] * 3 + [10000] + [5] * 40, 128), ([0] * 5, 128), ([0], 1)])
+                                    ([700] * 3 + [10000] + [5] * 40, 128), ([0] * 5, 128), ([0], 1),
+                                    ([600, 590, 0, 610] * 17, 128), ([300] * 16, 64), ([130, 0, 1] * 50, 16)])
 def test_attention_work_splits(lens, H):
     """One request over every worker, many to a worker, empty ones between."""
     check_attention(*attention_case(lens, H, 576, 64, seed=len(lens)), 512, 576 ** -0.5)
