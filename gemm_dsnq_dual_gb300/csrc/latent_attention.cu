@@ -35,6 +35,18 @@
 // spends more time on the polls than the tensor core on the products.
 // The running maximum is raised (and O rescaled) only when a row's maximum
 // grew by more than 2^8: until then p <= 2^8 is harmless in fp32 and bf16.
+// Shared memory (227 KB) holds q (72 KB at 64 heads x 576), P and two tiles and
+// more: tiles come in pairs of 64-column chunks, each freed as soon as its
+// product with P is done, so that the next tile's copies start early.
+//
+// Measured on GB300, 576 columns: 1.64 us per tile and CTA at 16 heads, 1.72 at
+// 64 (6.7 and 6.4 TB/s over 152 CTAs: HBM bounds it), 1.63 at 128 heads, where
+// two CTAs read each tile (the products bound it: 38 to 49 cycles each of the
+// 36 of Q K^T, 51 each of the 16 of P V).  Per call in a graph: 2 requests of
+// 131071 tokens at 16 heads 63 us (floor 45), 128 of 8000 at 48 heads, 512
+// columns, 196 us (159), 96 of mixed lengths at 128 heads 107 us (44), one of
+// 701 at 128 heads 13 us: ~1.8 us to the first copy, ~2.5 us to the first
+// product and 4 to 7 us for parts and join do not shrink with the work.
 
 #include <cuda.h>
 #include <cuda_bf16.h>

