@@ -485,9 +485,9 @@ def head_rmsnorm_rope(x, positions, inv_freq, gamma=None, eps: float = 1e-6, nor
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, H, D)}")
     pairs = inv_freq.shape[0]
     check(lib().dsnq_head_rmsnorm_rope(
-        M, H, D, xp, xt, xh, 1 if normalize else 0, None if gamma is None else _vec(gamma, "gamma", _BF16, D, dev), eps,
+        M, H, D, xp, xt, xh, 1 if normalize else 0, None if gamma is None else _vec(gamma, "gamma", _BF16, D, dev), float(eps),
         _vec(positions, "positions", _I64, M, dev), _vec(inv_freq, "inv_freq", _F64, pairs, dev),
-        D - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), rope_scale,
+        D - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), float(rope_scale),
         1 if inverse else 0, op, ot, oh, _stream(stream, dev)), "dsnq_head_rmsnorm_rope")
     return out
 
@@ -513,8 +513,8 @@ def latent_cache_write(kv, pe, positions, slots, inv_freq, cache, gamma=None, ep
     pairs = inv_freq.shape[0]
     check(lib().dsnq_latent_cache_write(
         M, K, P, kvp, ldkv, pep, ldpe, 1 if normalize else 0, None if gamma is None else _vec(gamma, "gamma", _BF16, K, dev),
-        eps, _vec(positions, "positions", _I64, M, dev), _vec(inv_freq, "inv_freq", _F64, pairs, dev),
-        W - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), rope_scale,
+        float(eps), _vec(positions, "positions", _I64, M, dev), _vec(inv_freq, "inv_freq", _F64, pairs, dev),
+        W - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), float(rope_scale),
         _vec(slots, "slots", _I64, M, dev), cp, pages, page_size, ld_page, ld_row, _stream(stream, dev)),
         "dsnq_latent_cache_write")
     return cache
@@ -561,7 +561,7 @@ def paged_latent_attention(q, cache, block_table, seq_lens, v_dim: int, scale: f
         size = workspace.numel()
     check(lib().dsnq_paged_latent_attention(
         B, H, DK, v_dim, qp, qt, qh, cp, pages, page_size, ld_page, ld_row, table, width, ldt,
-        _vec(seq_lens, "seq_lens", _I32, B, dev), scale, op, ot, oh, lp, ldl,
+        _vec(seq_lens, "seq_lens", _I32, B, dev), float(scale), op, ot, oh, lp, ldl,
         _vec(workspace, "workspace", torch.uint8, size, dev), size, _stream(stream, dev)), "dsnq_paged_latent_attention")
     return out, lse
 

@@ -1125,7 +1125,10 @@ extern "C" dsnq_status dsnq_paged_latent_attention(
     dsnq_status st = check_sizes(B, H, DK, DV, table_width, page_size);
     if (st != DSNQ_OK) return st;
     if (num_pages < 1 || !(scale > 0.f && scale < 1.0e30f) || workspace_bytes < 0) return DSNQ_ERR_INVALID_ARG;
-    if (num_pages > 0x7ffffffeLL || ld_row > (1LL << 36) || ld_page > (1LL << 38)) return DSNQ_ERR_UNSUPPORTED;
+    // Strides of a tensor map are below 2^40 bytes (the cache's 8-row groups: 16 ld_row).
+    if (num_pages > 0x7ffffffeLL || ld_row >= (1LL << 36) || ld_page >= (1LL << 39) || ldq_tok >= (1LL << 39) ||
+        ldq_head >= (1LL << 39))
+        return DSNQ_ERR_UNSUPPORTED;
     if (B == 0) return DSNQ_OK;
     if (!q || !out || !seq_lens || !workspace || !cache || (table_width && !block_table))
         return DSNQ_ERR_INVALID_ARG;

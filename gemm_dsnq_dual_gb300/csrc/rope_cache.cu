@@ -467,7 +467,7 @@ extend_tables_kernel(const ExtendArgs a) {
             if (pos < new_s[lo]) {
                 const int32_t p = static_cast<int32_t>(static_cast<uint32_t>(pos) / ps), k = p - pages_of(len);
                 int32_t id = -1;
-                if (bounds_ok(p < a.width && page_s[lo] + k < a.F + (k < 0 ? 0x40000000 : 0)))
+                if (bounds_ok(p < a.width && (k < 0 || page_s[lo] + k < a.F)))
                     id = k < 0 ? a.table[lo * a.ld_table + p] : a.free_pages[page_s[lo] + k];
                 if (id >= 0) slot = static_cast<int64_t>(id) * ps + (pos - static_cast<int64_t>(p) * ps);
             }
@@ -548,6 +548,8 @@ extern "C" dsnq_status dsnq_head_rmsnorm_rope(
     if (M == 0) return DSNQ_OK;
     if (!x || !out || (rope_dim && (!positions || !inv_freq))) return DSNQ_ERR_INVALID_ARG;
     if ((H > 1 && (ldx_head < D || ldo_head < D)) || (M > 1 && (ldx_tok < D || ldo_tok < D))) return DSNQ_ERR_INVALID_ARG;
+    // In place only row by row: with other strides a row would meet another's output.
+    if (x == out && ((H > 1 && ldx_head != ldo_head) || (M > 1 && ldx_tok != ldo_tok))) return DSNQ_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(out, 16) || ldx_tok % kChunk || ldx_head % kChunk || ldo_tok % kChunk ||
         ldo_head % kChunk || (gamma && !aligned(gamma, 16)) || !aligned(positions, 8) || !aligned(inv_freq, 8))
         return DSNQ_ERR_MISALIGNED;
@@ -639,6 +641,7 @@ extern "C" dsnq_status dsnq_extend_block_tables(
     // Every CTA reads the lengths, so no output may take their place.
     if (B && (new_lens == seq_lens || new_lens == new_tokens || row_starts == seq_lens || row_starts == new_tokens))
         return DSNQ_ERR_INVALID_ARG;
+    if ((rows && positions == slots) || (B && new_lens == row_starts)) return DSNQ_ERR_INVALID_ARG;
     if (!aligned(seq_lens, 4) || !aligned(new_tokens, 4) || !aligned(free_pages, 4) || !aligned(block_table, 4) ||
         !aligned(new_lens, 4) || !aligned(row_starts, 4) || !aligned(positions, 8) || !aligned(slots, 8) ||
         !aligned(counts, 4))
@@ -660,7 +663,8 @@ extern "C" dsnq_status dsnq_extend_block_tables(
     grid = grid < 1 ? 1 : (grid > sms ? sms : grid);
     const size_t smem = static_cast<size_t>(4 * B) * sizeof(int32_t);
     static_assert(4 * DSNQ_MAX_REQUESTS * sizeof(int32_t) <= 128 * 1024, "four words per request in shared memory");
-    if (smem > 48 * 1024 && !set_smem_attr(reinterpret_cast<const void*>(extend_tables_kernel), smem)) return DSNQ_ERR_CUDA;
+    // The limit without the attribute is 48 KB with the static part.
+    if (smem > 32 * 1024 && !set_smem_attr(reinterpret_cast<const void*>(extend_tables_kernel), smem)) return DSNQ_ERR_CUDA;
     return launch_result(launch_kernel(extend_tables_kernel, dim3(static_cast<unsigned>(grid)), dim3(kExtendThreads), smem,
                                        static_cast<cudaStream_t>(stream), a));
 }

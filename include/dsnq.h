@@ -425,8 +425,9 @@ typedef enum {
  * A token gets no place when its row would lie past `rows`, its request's
  * table is full, or the free list is used up (counts[1] > num_free); new_lens
  * counts the tokens that got one.  table_width * page_size < 2^31.
- * The outputs must not overlap the inputs or each other (new_lens and
- * row_starts equal to seq_lens or new_tokens: DSNQ_ERR_INVALID_ARG).
+ * The outputs must not overlap the inputs or each other (new_lens or
+ * row_starts equal to seq_lens, new_tokens or one another, and positions equal
+ * to slots: DSNQ_ERR_INVALID_ARG).
  */
 DSNQ_API dsnq_status dsnq_extend_block_tables(
     int64_t B, int64_t rows, int64_t page_size,
@@ -454,7 +455,8 @@ DSNQ_API dsnq_status dsnq_extend_block_tables(
  *                 rope_dim == 0.
  *   rope_offset : multiple of 8; rope_dim : multiple of 16, <= 256.
  *   out, ldo_tok, ldo_head : bf16 [M, H, D]; may be x itself with the same
- *                 strides, otherwise must not overlap it.
+ *                 strides (others: DSNQ_ERR_INVALID_ARG), otherwise must not
+ *                 overlap it.
  * Alignment: x, out, gamma 16 bytes, strides multiples of 8; positions and
  * inv_freq 8 bytes.
  */

@@ -101,7 +101,7 @@ def test_rope_frequencies():
 
 def test_extend_argument_checks(lib):
     def call(B=4, rows=8, ps=16, lens=A, new=A + 64, free=A, F=10, table=A, width=8, ld=8, nl=A + 256, rs=A + 512, pos=A,
-             slots=A, counts=A):
+             slots=A + 1024, counts=A):
         return lib.dsnq_extend_block_tables(B, rows, ps, lens, new, free, F, table, width, ld, nl, rs, pos, slots, counts, None)
 
     assert call(B=-1) == INVALID and call(rows=-1) == INVALID and call(ps=0) == INVALID and call(F=-1) == INVALID
@@ -117,19 +117,20 @@ def test_extend_argument_checks(lib):
     assert call(nl=A) == INVALID                              # the lengths in place
     assert call(rs=A) == INVALID
     assert call(nl=A + 64) == INVALID                         # the counts in place
+    assert call(slots=A) == INVALID and call(rs=A + 256) == INVALID        # two outputs in one place
     assert call(lens=A + 2) == MISALIGNED and call(slots=A + 4) == MISALIGNED and call(pos=A + 4) == MISALIGNED
 
 
 def test_head_norm_rope_argument_checks(lib):
     def call(M=4, H=3, D=64, x=A, lt=192, lh=64, norm=1, gamma=None, eps=1e-6, pos=A, f=A, off=0, dim=64, lay=0, scale=1.0,
-             inv=0, out=A, ot=192, oh=64):
+             inv=0, out=2 * A, ot=192, oh=64):
         return lib.dsnq_head_rmsnorm_rope(M, H, D, x, lt, lh, norm, gamma, eps, pos, f, off, dim, lay, scale, inv, out, ot, oh, None)
 
     assert call(M=0) == OK and call(M=0, x=None, out=None, pos=None, f=None) == OK
     assert call(M=-1) == INVALID and call(H=0) == INVALID and call(D=0) == INVALID
     assert call(eps=-1.0) == INVALID and call(eps=float("nan")) == INVALID
     assert call(norm=0, gamma=A) == INVALID                   # a weight without a norm
-    assert call(D=60) == UNSUPPORTED and call(D=1032, lh=1032, lt=3096, oh=1032, ot=3096) == UNSUPPORTED
+    assert call(D=60) == UNSUPPORTED and call(D=1032, lh=1032, lt=3 * 1032, oh=1032, ot=3 * 1032) == UNSUPPORTED
     assert call(H=65536) == UNSUPPORTED
     assert call(off=8) == INVALID and call(off=-8) == INVALID and call(dim=-16) == INVALID     # outside the head
     assert call(off=1 << 62) == INVALID
@@ -138,6 +139,7 @@ def test_head_norm_rope_argument_checks(lib):
     assert call(lay=2) == INVALID and call(scale=float("inf")) == INVALID and call(scale=float("nan")) == INVALID
     assert call(x=None) == INVALID and call(out=None) == INVALID and call(pos=None) == INVALID and call(f=None) == INVALID
     assert call(lh=56) == INVALID and call(ot=56) == INVALID
+    assert call(out=A, ot=256) == INVALID and call(out=A, oh=128, ot=384) == INVALID           # in place, other strides
     assert call(x=A + 8) == MISALIGNED and call(lt=196) == MISALIGNED and call(gamma=A + 2) == MISALIGNED
     assert call(pos=A + 4) == MISALIGNED and call(f=A + 4) == MISALIGNED
 
@@ -179,6 +181,8 @@ def test_attention_argument_checks(lib):
     assert call(DK=560) == UNSUPPORTED and call(DK=640, qh=640, qt=128 * 640, lr=640, lp=64 * 640) == UNSUPPORTED
     assert call(DV=448) == UNSUPPORTED and call(H=1025) == UNSUPPORTED and call(B=8193) == UNSUPPORTED
     assert call(ps=60) == UNSUPPORTED and call(ps=4) == UNSUPPORTED
+    assert call(lr=1 << 20, lp=1 << 21) == INVALID            # pages that overlap
+    assert call(ps=8, lr=1 << 36, lp=1 << 39, width=1, ldt=1) == UNSUPPORTED and call(qt=1 << 39) == UNSUPPORTED
     assert call(width=1 << 26, ldt=1 << 26) == UNSUPPORTED    # tokens of a request beyond int32
     assert call(scale=0.0) == INVALID and call(scale=-1.0) == INVALID and call(scale=float("nan")) == INVALID
     for name in ("q", "cache", "table", "lens", "out", "w"):

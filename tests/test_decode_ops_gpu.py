@@ -117,6 +117,9 @@ def test_extend_large_prompt_and_largest_batch():
     held = -(-lens // 16)
     need = int((-(-(lens + new) // 16) - held).sum())
     check_extend(lens, new, np.arange(10000, 10000 + need), t, 16, int(new.sum()))
+    for B in (2047, 2049, 4097):                             # around where the sums outgrow 32 and 48 KB
+        t = np.arange(2 * B).reshape(B, 2)
+        check_extend(np.arange(B) % 13, None, [], t, 16, B)
     B = 8192
     lens = np.arange(B) % 33
     t = np.full((B, 4), -1)
@@ -412,6 +415,25 @@ def test_attention_work_splits(lens, H):
     check_attention(*attention_case(lens, H, 576, 64, seed=len(lens)), 512, 576 ** -0.5)
 
 
+def test_attention_most_heads_requests_and_a_table_of_no_columns():
+    """The largest batch and head count taken, no requests, no columns."""
+    check_attention(*attention_case([70, 0, 3], 1024, 128, 8, seed=60), 128, 0.1)
+    check_attention(*attention_case([5, 64], 513, 192, 64, seed=61), 128, 0.1)
+    check_attention(*attention_case([k % 4 for k in range(8192)], 3, 128, 8, seed=62, poison=False), 128, 0.1)
+    q, cache, table, lens = attention_case([9, 9], 20, 576, 64, seed=63)
+    out, lse = dsnq.paged_latent_attention(q, cache, table[:, :0], lens, 512, 0.05)
+    assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+    out, lse = dsnq.paged_latent_attention(q[:0], cache, table[:0], lens[:0], 512, 0.05)
+    assert out.shape == (0, 20, 512) and lse.shape == (0, 20)
+    assert dsnq.debug_status() == OK
+
+
+@pytest.mark.parametrize("DK,DV", [(128, 128), (192, 128), (576, 128), (512, 256)])
+def test_attention_long_narrow_rows(DK, DV):
+    """Many tiles in the ring (narrow rows), and pairs of chunks that hold no value."""
+    check_attention(*attention_case([7000, 130], 20, DK, 32, seed=DK), DV, DK ** -0.5)
+
+
 def test_attention_no_request_sees_all_of_a_wide_table():
     """A table much wider than the lengths: idle workers."""
     check_attention(*attention_case([100, 5], 16, 576, 64, seed=10, extra=500), 512, 0.05)
@@ -655,6 +677,74 @@ def test_launch_overlap_changes_nothing():
     finally:
         dsnq.set_launch_overlap(True)
     assert all(torch.equal(a, b) for a, b in zip(on, off))
+
+
+_FIRST_CALLS_IN_CAPTURE = """
+import torch
+import gemm_dsnq_dual_gb300 as dsnq
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+f, _ = dsnq.rope_frequencies(64)
+kv, q = torch.randn(3, 512, device="cuda").bfloat16(), torch.randn(2, 48, 512, device="cuda").bfloat16()
+cache = torch.zeros(8, 64, 512, dtype=torch.bfloat16, device="cuda")
+
+def step():
+    table = torch.full((2, 3), -1, dtype=torch.int32, device="cuda")
+    lens, _, pos, slots, _ = dsnq.extend_block_tables(lens0, new, free, table, 64, 3)
+    dsnq.latent_cache_write(kv, None, pos, slots, f, cache)
+    qr = dsnq.head_rmsnorm_rope(q, pos[:2], f)
+    return dsnq.paged_latent_attention(qr, cache, table, lens, 512, 0.05)
+
+lens0, new, free = i32([0, 0]), i32([2, 1]), i32([5, 6])
+torch.cuda.synchronize()
+g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(g, stream=s):
+    out = step()
+g.replay()
+torch.cuda.synchronize()
+want = step()
+assert dsnq.debug_status() == 0
+assert all(torch.equal(a, b) for a, b in zip(out, want)) and bool(out[0].isfinite().all()) and bool((out[0] != 0).any())
+print("captured ok")
+"""
+
+
+def test_first_calls_may_be_captured():
+    """In a fresh process: each operator's first call is made under capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_two_graphs_at_once():
+    """Two captured calls, replayed at the same time on two streams: each has
+    its own workspace from its graph's pool."""
+    cases = [attention_case([4000, 77, 900], 64, 576, 64, seed=70 + i) for i in range(2)]
+    want = [dsnq.paged_latent_attention(*c, 512, 0.05) for c in cases]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in cases]
+    for c, s in zip(cases, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(dsnq.paged_latent_attention(*c, 512, 0.05))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
+def test_empty_calls():
+    e = torch.empty(0, 512, dtype=torch.bfloat16, device=DEV)
+    i = torch.empty(0, dtype=torch.int64, device=DEV)
+    cache = torch.ones(2, 8, 512, dtype=torch.bfloat16, device=DEV)
+    dsnq.latent_cache_write(e, None, i, i, FREQ(64), cache)
+    assert bool((cache == 1).all()) and dsnq.debug_status() == OK
 
 
 def test_other_device_is_refused():
