@@ -21,9 +21,11 @@ sglang PR #27289 (transpose_scale: column-major activation scales).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import functools
 import math
+import threading
 
 import torch
 
@@ -409,6 +411,38 @@ def _cube(t, name: str, dtype, dev):
     return n0, n1, n2, (n1 * s1 if n0 == 1 else s0), s1, t.data_ptr()
 
 
+def _allocating_on(stream):
+    """Context in which memory for a call on `stream` is allocated: on that
+    stream, since memory of another one may still be in use there."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+_kept = threading.local()
+
+
+def _workspace(size: int, dev, stream, handle: int):
+    """A uint8 tensor of at least `size` bytes for one call on the stream
+    `handle`.  Calls of one thread on one stream run one after the other, so
+    outside a capture the last such tensor serves again (an allocation took 5
+    of a small call's 19 us on the host); of the streams a thread used, the
+    last four keep theirs.  A capture gets a tensor of its graph's pool, a
+    call with an explicit stream one of that stream."""
+    if stream is not None or torch.cuda.is_current_stream_capturing():
+        with _allocating_on(stream):
+            return torch.empty(size, dtype=torch.uint8, device=dev)
+    kept = _kept.__dict__
+    key = (torch.cuda.current_device(), handle)
+    t = kept.get(key)
+    if t is None or t.numel() < size:
+        kept.pop(key, None)
+        while len(kept) >= 4:
+            kept.pop(next(iter(kept)))
+        kept[key] = t = torch.empty(size, dtype=torch.uint8, device=dev)
+    return t
+
+
 def _rope_layout(layout) -> int:
     if layout == "interleaved" or layout == ROPE_INTERLEAVED:
         return ROPE_INTERLEAVED
@@ -455,9 +489,10 @@ def extend_block_tables(seq_lens, new_tokens, free_pages, block_table, page_size
     if tb != B:
         raise ValueError(f"block_table has {tb} rows for {B} requests")
     if out is None:
-        out = (torch.empty(B, dtype=_I32, device=dev), torch.empty(B + 1, dtype=_I32, device=dev),
-               torch.empty(rows, dtype=_I64, device=dev), torch.empty(rows, dtype=_I64, device=dev),
-               torch.empty(2, dtype=_I32, device=dev))
+        with _allocating_on(stream):
+            out = (torch.empty(B, dtype=_I32, device=dev), torch.empty(B + 1, dtype=_I32, device=dev),
+                   torch.empty(rows, dtype=_I64, device=dev), torch.empty(rows, dtype=_I64, device=dev),
+                   torch.empty(2, dtype=_I32, device=dev))
     new_lens, row_starts, positions, slots, counts = out
     F = free_pages.shape[0]
     check(lib().dsnq_extend_block_tables(
@@ -479,7 +514,8 @@ def head_rmsnorm_rope(x, positions, inv_freq, gamma=None, eps: float = 1e-6, nor
     dev = x.device
     M, H, D, xt, xh, xp = _cube(x, "x", _BF16, dev)
     if out is None:
-        out = torch.empty(M, H, D, dtype=_BF16, device=dev)
+        with _allocating_on(stream):
+            out = torch.empty(M, H, D, dtype=_BF16, device=dev)
     oM, oH, oD, ot, oh, op = _cube(out, "out", _BF16, dev)
     if oM != M or oH != H or oD != D:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, H, D)}")
@@ -535,7 +571,9 @@ def paged_latent_attention(q, cache, block_table, seq_lens, v_dim: int, scale: f
     first seq_lens[b] (int32) tokens of each request in the paged cache
     [pages, page_size, DK], whose pages block_table [B, width] (int32) names.
     The value of a row is its first v_dim columns.  Returns (out [B,H,v_dim]
-    bf16, lse [B,H] fp32).  The uint8 `workspace` is allocated if omitted."""
+    bf16, lse [B,H] fp32).  The uint8 `workspace` is the binding's own if
+    omitted: one per thread and stream, and one of its own in a capture (with
+    streams that are destroyed while work is pending, pass one)."""
     dev = q.device
     B, H, DK, qt, qh, qp = _cube(q, "q", _BF16, dev)
     pages, page_size, W, ld_page, ld_row, cp = _cube(cache, "cache", _BF16, dev)
@@ -545,24 +583,25 @@ def paged_latent_attention(q, cache, block_table, seq_lens, v_dim: int, scale: f
     if tb != B:
         raise ValueError(f"block_table has {tb} rows for {B} requests")
     if out is None:
-        out = torch.empty(B, H, v_dim, dtype=_BF16, device=dev)
+        with _allocating_on(stream):
+            out = torch.empty(B, H, v_dim, dtype=_BF16, device=dev)
     oB, oH, oD, ot, oh, op = _cube(out, "out", _BF16, dev)
     if oB != B or oH != H or oD != v_dim:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(B, H, v_dim)}")
     if lse is None:
-        lse = torch.empty(B, H, dtype=_F32, device=dev)
+        with _allocating_on(stream):
+            lse = torch.empty(B, H, dtype=_F32, device=dev)
     lB, lH, ldl, lp = _mat(lse, "lse", _F32, dev)
     if lB != B or lH != H:
         raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(B, H)}")
+    handle = _stream(stream, dev)
     if workspace is None:
-        size = paged_latent_attention_workspace_bytes(B, H, v_dim, width, page_size)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    else:
-        size = workspace.numel()
+        workspace = _workspace(paged_latent_attention_workspace_bytes(B, H, v_dim, width, page_size), dev, stream, handle)
+    size = workspace.numel()
     check(lib().dsnq_paged_latent_attention(
         B, H, DK, v_dim, qp, qt, qh, cp, pages, page_size, ld_page, ld_row, table, width, ldt,
         _vec(seq_lens, "seq_lens", _I32, B, dev), float(scale), op, ot, oh, lp, ldl,
-        _vec(workspace, "workspace", torch.uint8, size, dev), size, _stream(stream, dev)), "dsnq_paged_latent_attention")
+        _vec(workspace, "workspace", torch.uint8, size, dev), size, handle), "dsnq_paged_latent_attention")
     return out, lse
 
 

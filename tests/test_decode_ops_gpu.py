@@ -538,6 +538,42 @@ def test_attention_two_streams_at_once():
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
 
+def test_attention_on_an_explicit_stream_and_from_threads():
+    """A Stream, its handle, and two threads on one stream: the same results."""
+    import threading
+    cases = [attention_case([2500, 33, 800], 48, 576, 64, seed=80 + i) for i in range(2)]
+    want = [dsnq.paged_latent_attention(*c, 512, 0.05) for c in cases]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream, 0):
+        got = dsnq.paged_latent_attention(*cases[0], 512, 0.05, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0][0]) and torch.equal(got[1], want[0][1])
+    outs = [[], []]
+
+    def work(i):
+        for _ in range(50):
+            outs[i].append(dsnq.paged_latent_attention(*cases[i], 512, 0.05))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        assert len(got) == 50 and all(torch.equal(g[0], w[0]) and torch.equal(g[1], w[1]) for g in got)
+    assert dsnq.debug_status() == OK
+
+
+def test_attention_kept_workspace_grows():
+    """Small, large and small again on one stream; five streams in turn."""
+    for i in range(5):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for lens, H in (([3], 16), ([9000, 10], 64), ([70], 16)):
+                check_attention(*attention_case(lens, H, 576, 64, seed=90 + i), 512, 0.05)
+
+
 def test_attention_wait_runs_out_and_is_reported():
     """A copy that never comes: the waits run out, the kernel returns, the
     status is read and cleared, and the next call is right."""
