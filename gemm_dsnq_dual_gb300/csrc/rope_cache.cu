@@ -7,12 +7,11 @@
 //   (a cos t - b sin t, b cos t + a sin t) * rope_scale,   t = p * inv_freq[i].
 // At position 10^6 an fp32 product p * inv_freq is off by up to 0.06 rad.
 // Positions are whole, so only the fraction of a turn that one position adds
-// matters: it is taken from inv_freq once, in fp64, as a 64-bit fixed-point
-// number; times the position modulo 2^64 it is the fraction of a turn at that
-// position (off by 2^-54 per position), and only that goes to fp32
-// (sincospif).  The fp64 units are few, so the products by position are whole
-// numbers; the table of a token's angles is formed once per CTA or warp, in
-// shared memory, and used for all its heads.
+// matters: it is taken from inv_freq once, as a 64-bit fixed-point number;
+// times the position modulo 2^64 it is the fraction of a turn at that position
+// (off by 2^-64 per position), and only that goes to fp32 (sincospif).  The
+// table of a token's angles is formed once per CTA or warp, in shared memory,
+// and used for all its heads.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -48,10 +47,21 @@ struct Rope {
     float sign;                 // -1 rotates back
 };
 
-// The turns that one position adds, modulo 1, as a 64-bit fraction.
+// The turns that one position adds, modulo 1, as a 64-bit fraction: the
+// frequency's 53-bit mantissa times round(2^66 / (2 pi)), shifted by its
+// exponent.  In whole numbers, since the fp64 units are few (in fp64 it was a
+// seventh of the time of a prompt's cache write: 8191 rows in 6.9 us, now 6.0).
 __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
-    const double turns = inv_freq * 0.15915494309189533577;   // 1 / (2 pi)
-    return __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
+    constexpr uint64_t kTurn = 11743562013128004906ull;
+    const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(inv_freq));
+    const int exp = static_cast<int>(bits >> 52) & 0x7ff;
+    if (exp == 0) return 0;                        // below 2^-1022
+    const uint64_t mant = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+    const uint64_t hi = __umul64hi(mant, kTurn), lo = mant * kTurn;
+    const int shift = 54 - (exp - 1023);           // turns * 2^64 = (hi:lo) >> shift
+    const uint64_t f = shift >= 128 ? 0 : shift >= 64 ? hi >> (shift - 64) : shift > 0 ? (hi << (64 - shift)) | (lo >> shift)
+                       : shift > -64 ? lo << -shift : 0;
+    return bits >> 63 ? 0 - f : f;
 }
 
 // (cos, sin) * scale at position pos of the frequency with that step.
@@ -268,8 +278,10 @@ constexpr int kWriteWarps = 4;
 // One warp per row; lane l holds chunks l, l + 32, ... of the concatenated
 // row.  The row is requested before its slot and position are known (they
 // decide only where and by how much), so a row costs one trip to memory; four
-// CTAs or more per SM hide it.  Measured: 8191 normalized rows of 576 in 6.9 us
-// (2.7 TB/s: two and a quarter waves of one trip each), 32 rows in 2.3 us.
+// CTAs or more per SM hide it.  Measured: 8191 normalized rows of 576 in 6.0 us
+// (3.1 TB/s: two and a quarter waves of one trip each), 32768 in 20.6 us, 32
+// in 2.3 us.  Warps that stride over the rows and request the next one early
+// need registers of a CTA per SM and are slower up to 8191 rows (6.7 us).
 template <int CPL, bool HALF>
 __global__ void __launch_bounds__(kWriteWarps * 32, HALF ? 4 : 6)
 latent_cache_write_kernel(const WriteArgs a) {

@@ -443,7 +443,7 @@ DSNQ_API dsnq_status dsnq_extend_block_tables(
  *       normalize; gamma == NULL: no weight)
  *   pairs (a, b) of columns [rope_offset, rope_offset + rope_dim) of y:
  *       (a cos t - b sin t, b cos t + a sin t) * rope_scale,
- *       t = positions[m] * inv_freq[i]   (angle in fp64; -t with inverse)
+ *       t = positions[m] * inv_freq[i]   (as a 64-bit fraction of a turn; -t with inverse)
  *   out = bf16_rn(y), one rounding.
  * Scaled rotary positions (long contexts) are a matter of inv_freq and
  * rope_scale, which the caller prepares once.
@@ -451,8 +451,8 @@ DSNQ_API dsnq_status dsnq_extend_block_tables(
  *                 dsnq_block_scaled_fp8_gemm with ldx_head = D; D a multiple
  *                 of 8, <= 1024; H <= 65535.
  *   gamma       : bf16 [D] or NULL (must be NULL without normalize).
- *   positions   : int64 [M]; inv_freq : fp64 [rope_dim / 2].  May be NULL when
- *                 rope_dim == 0.
+ *   positions   : int64 [M]; inv_freq : fp64 [rope_dim / 2], finite.  May be
+ *                 NULL when rope_dim == 0.
  *   rope_offset : multiple of 8; rope_dim : multiple of 16, <= 256.
  *   out, ldo_tok, ldo_head : bf16 [M, H, D]; may be x itself with the same
  *                 strides (others: DSNQ_ERR_INVALID_ARG), otherwise must not

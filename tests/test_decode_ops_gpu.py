@@ -250,6 +250,26 @@ def test_rope_zero_rows_and_non_finite():
     assert torch.equal(z[keep], y[keep]) and not bool(torch.isfinite(z[2, 3]).any())
 
 
+def test_rope_frequencies_of_every_size():
+    """Zero, subnormal, tiny, negative and large frequencies against exact
+    fractions of a turn.  The 64-bit step is off by |f| + 1 units of 2^-64
+    turns, the turn by that times the position: 2^-21 turns at 2^30 and 5000,
+    so 2^-18 rad beside the fp32 and bf16 steps of the other tests."""
+    from fractions import Fraction
+    per_turn = Fraction("0.159154943091895335768883763372514362034459645740456448747667344")   # 1 / (2 pi)
+    f = [0.0, 5e-324, 1e-300, 2.0**-64, -2.0**-40, 1e-5, 0.3, -0.7, 1.0, 6.28318530717958, 33.3, -1000.1, 2.0**20 + 0.1,
+         -(2.0**30), 2.0**30 - 0.5, 0.75]
+    pos = [0, 1, 4999, -3]
+    x = torch.zeros(len(pos), 2, 32, dtype=torch.bfloat16, device=DEV)
+    x[:, 0, 0::2] = 1
+    x[:, 1, 1::2] = 1
+    got = val(dsnq.head_rmsnorm_rope(x, torch.tensor(pos, device=DEV), torch.tensor(f, dtype=torch.float64, device=DEV),
+                                     normalize=False))
+    t = np.array([[float((p * Fraction(w) * per_turn) % 1) for w in f] for p in pos]) * 2 * np.pi
+    want = np.stack([np.stack([np.cos(t), np.sin(t)], -1), np.stack([-np.sin(t), np.cos(t)], -1)], 1).reshape(got.shape)
+    assert np.all(np.abs(got - want) <= 2.0**-8 * np.abs(want) + 2.0**-18 + 2.0**-14)
+
+
 def test_rope_no_tokens():
     e = torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV)
     assert dsnq.head_rmsnorm_rope(e, torch.empty(0, dtype=torch.int64, device=DEV), FREQ(64)).shape == (0, 4, 64)
