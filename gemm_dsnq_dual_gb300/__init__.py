@@ -21,7 +21,6 @@ sglang PR #27289 (transpose_scale: column-major activation scales).
 
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import functools
 import math
@@ -411,12 +410,13 @@ def _cube(t, name: str, dtype, dev):
     return n0, n1, n2, (n1 * s1 if n0 == 1 else s0), s1, t.data_ptr()
 
 
-def _allocating_on(stream):
-    """Context in which memory for a call on `stream` is allocated: on that
-    stream, since memory of another one may still be in use there."""
+def _new(shape, dtype, dev, stream):
+    """An uninitialized tensor for a call on `stream`, of that stream's
+    memory: memory of another one may still be in use there."""
     if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 _kept = threading.local()
@@ -430,10 +430,9 @@ def _workspace(size: int, dev, stream, handle: int):
     last four keep theirs.  A capture gets a tensor of its graph's pool, a
     call with an explicit stream one of that stream."""
     if stream is not None or torch.cuda.is_current_stream_capturing():
-        with _allocating_on(stream):
-            return torch.empty(size, dtype=torch.uint8, device=dev)
+        return _new(size, torch.uint8, dev, stream)
     kept = _kept.__dict__
-    key = (torch.cuda.current_device(), handle)
+    key = (dev.index, handle)
     t = kept.get(key)
     if t is None or t.numel() < size:
         kept.pop(key, None)
@@ -489,10 +488,8 @@ def extend_block_tables(seq_lens, new_tokens, free_pages, block_table, page_size
     if tb != B:
         raise ValueError(f"block_table has {tb} rows for {B} requests")
     if out is None:
-        with _allocating_on(stream):
-            out = (torch.empty(B, dtype=_I32, device=dev), torch.empty(B + 1, dtype=_I32, device=dev),
-                   torch.empty(rows, dtype=_I64, device=dev), torch.empty(rows, dtype=_I64, device=dev),
-                   torch.empty(2, dtype=_I32, device=dev))
+        out = (_new(B, _I32, dev, stream), _new(B + 1, _I32, dev, stream), _new(rows, _I64, dev, stream),
+               _new(rows, _I64, dev, stream), _new(2, _I32, dev, stream))
     new_lens, row_starts, positions, slots, counts = out
     F = free_pages.shape[0]
     check(lib().dsnq_extend_block_tables(
@@ -514,8 +511,7 @@ def head_rmsnorm_rope(x, positions, inv_freq, gamma=None, eps: float = 1e-6, nor
     dev = x.device
     M, H, D, xt, xh, xp = _cube(x, "x", _BF16, dev)
     if out is None:
-        with _allocating_on(stream):
-            out = torch.empty(M, H, D, dtype=_BF16, device=dev)
+        out = _new((M, H, D), _BF16, dev, stream)
     oM, oH, oD, ot, oh, op = _cube(out, "out", _BF16, dev)
     if oM != M or oH != H or oD != D:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, H, D)}")
@@ -583,14 +579,12 @@ def paged_latent_attention(q, cache, block_table, seq_lens, v_dim: int, scale: f
     if tb != B:
         raise ValueError(f"block_table has {tb} rows for {B} requests")
     if out is None:
-        with _allocating_on(stream):
-            out = torch.empty(B, H, v_dim, dtype=_BF16, device=dev)
+        out = _new((B, H, v_dim), _BF16, dev, stream)
     oB, oH, oD, ot, oh, op = _cube(out, "out", _BF16, dev)
     if oB != B or oH != H or oD != v_dim:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(B, H, v_dim)}")
     if lse is None:
-        with _allocating_on(stream):
-            lse = torch.empty(B, H, dtype=_F32, device=dev)
+        lse = _new((B, H), _F32, dev, stream)
     lB, lH, ldl, lp = _mat(lse, "lse", _F32, dev)
     if lB != B or lH != H:
         raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(B, H)}")
