@@ -435,6 +435,10 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     auto wait_uniform = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_bounded<true>(bar, parity, abort_flag, tmo));
     };
+    // The same, asleep between polls: for the copying warp, which is ahead.
+    auto wait_uniform_asleep = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, tmo));
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
@@ -447,7 +451,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             if (run.len == 0) continue;
             const int32_t* row = p.table + run.b * p.ld_table;
             int ids = 0;
-            ok = wait_bounded(smem_u32(qempty), (nq & 1) ^ 1, abort_flag, tmo);
+            ok = wait_uniform_asleep(smem_u32(qempty), (nq & 1) ^ 1);
             if (!ok) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(smem_u32(qfull), q_bytes);
@@ -473,7 +477,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 const int id = __shfl_sync(0xffffffffu, ids, (i % batch) * pieces + (lane & (pieces - 1)));
                 const int group = (tok0 + lane * p.box_rows) % p.page_size / 8;
                 if (odd) {
-                    ok = wait_bounded(smem_u32(&oempty[po.i]), po.pass ^ 1, abort_flag, tmo);
+                    ok = wait_uniform_asleep(smem_u32(&oempty[po.i]), po.pass ^ 1);
                     if (!ok) break;
                     const uint32_t fb = smem_u32(&ofull[po.i]);
                     if (lane == 0) mbar_arrive_expect_tx(fb, live * p.box_rows * 128);
@@ -483,7 +487,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     po.step(p.odd_slots);
                 }
                 for (int j = 0; j < pairs; ++j) {
-                    ok = wait_bounded(smem_u32(&empty[pp.i]), pp.pass ^ 1, abort_flag, tmo);
+                    ok = wait_uniform_asleep(smem_u32(&empty[pp.i]), pp.pass ^ 1);
                     if (!ok) break;
                     const uint32_t fb = smem_u32(&full[pp.i]);
                     if (!skip) {                           // test hook: the first pair never comes, the waits on it run out

@@ -611,6 +611,24 @@ def test_attention_wait_runs_out_and_is_reported():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("page", [8, 16])
+def test_attention_wait_runs_out_with_many_copies_a_tile(page):
+    """Every lane of the copying warp gives up together, whatever it was
+    waiting for: long requests in small pages, on every worker."""
+    q, cache, table, lens = attention_case([9000, 40, 20000, 0, 700], 80, 576, page, seed=23)
+    want = dsnq.paged_latent_attention(q, cache, table, lens, 512, 0.05)
+    torch.cuda.synchronize()
+    dsnq.debug_set(1, 5_000_000)
+    try:
+        for _ in range(3):
+            dsnq.paged_latent_attention(q, cache, table, lens, 512, 0.05)
+            assert dsnq.debug_status() == TIMEOUT
+    finally:
+        dsnq.debug_set(0, 0)
+    got = dsnq.paged_latent_attention(q, cache, table, lens, 512, 0.05)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and dsnq.debug_status() == OK
+
+
 # -------------------------------------------------------- a run of them together
 
 class Model:
