@@ -43,7 +43,7 @@
 // 64 (6.7 and 6.4 TB/s over 152 CTAs: HBM bounds it), 1.63 at 128 heads, where
 // two CTAs read each tile (the products bound it: 38 to 49 cycles each of the
 // 36 of Q K^T, 51 each of the 16 of P V).  Per call in a graph: 2 requests of
-// 131071 tokens at 16 heads 63 us (floor 45), 128 of 8000 at 48 heads, 512
+// 131071 tokens at 16 heads 62 us (floor 45), 128 of 8000 at 48 heads, 512
 // columns, 196 us (159), 96 of mixed lengths at 128 heads 107 us (44), one of
 // 701 at 128 heads 13 us: ~1.8 us to the first copy, ~2.5 us to the first
 // product and 4 to 7 us for parts and join do not shrink with the work.
@@ -855,13 +855,14 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 // item is four heads of one block of 128 values: SHARE = 1 gives it to one
 // warp, for the few parts of a request in a large batch; SHARE = 8 gives it to
 // the eight warps of a CTA, which take the parts in turn, for long requests
-// that many workers share.
+// that many workers share.  A warp has AHEAD parts on their way: the kernel
+// takes as long as its trips to memory.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kManyParts = 4;         // workers per request from which a CTA joins an item
 
-template <int SHARE>
-__global__ void __launch_bounds__(kJoinThreads)
+template <int SHARE, int AHEAD>
+__global__ void __launch_bounds__(kJoinThreads, AHEAD > 2 ? 1 : 2)
 latent_attention_join_kernel(const Params p, const int by_cut) {
     grid_dependency_wait();
     allow_dependent_launch();
@@ -921,9 +922,10 @@ latent_attention_join_kernel(const Params p, const int by_cut) {
     }
     for (int c = 0; c < mine; c += 32) {                   // 32 parts at a time, one's (max, sum) per lane
         const int cnt = min(32, mine - c);
-        float4 o[2][4];
-        load(k0 + c * SHARE, o[0]);                        // on their way while the factors are formed
-        if (cnt > 1) load(k0 + (c + 1) * SHARE, o[1]);
+        float4 o[AHEAD][4];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)                   // on their way while the factors are formed
+            if (u < cnt) load(k0 + (c + u) * SHARE, o[u]);
         float f[4] = {kNegInf, kNegInf, kNegInf, kNegInf}, l[4] = {0.f, 0.f, 0.f, 0.f};
         if (lane < cnt) {
             const float4* ml = reinterpret_cast<const float4*>(p.part_ml + slot_of(k0 + (c + lane) * SHARE) * kHeads + hl);
@@ -955,14 +957,13 @@ latent_attention_join_kernel(const Params p, const int by_cut) {
                 }
             }
         };
-        add(0, o[0]);
-        if (cnt > 1) add(1, o[1]);
-#pragma unroll 2
-        for (int k = 2; k < cnt; k += 2) {
-            load(k0 + (c + k) * SHARE, o[0]);
-            if (k + 1 < cnt) load(k0 + (c + k + 1) * SHARE, o[1]);
-            add(k, o[0]);
-            if (k + 1 < cnt) add(k + 1, o[1]);
+        for (int k = 0; k < cnt; k += AHEAD) {
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (k + u < cnt) add(k + u, o[u]);
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (k + AHEAD + u < cnt) load(k0 + (c + k + AHEAD + u) * SHARE, o[u]);
         }
     }
     if (SHARE > 1) {
@@ -1202,12 +1203,19 @@ extern "C" dsnq_status dsnq_paged_latent_attention(
     if (st != DSNQ_OK || p.W == 1) return st;
     // Few requests: a request has many parts, so a CTA joins each item.  Many:
     // a warp does, and no more requests can be split than there are cuts.
+    // While all CTAs find room at once, each keeps more parts on their way
+    // (registers, so fewer CTAs on an SM).  Measured, 2 parts ahead against 4:
+    // 20 requests up to 8000 tokens, 128 heads (320 CTAs) 26.8 against 23.9 us,
+    // 40 up to 4096 (640 CTAs) 31.5 against 33.4, 256 of 500, 16 heads (two
+    // parts a request) 42.8 against 44.6; against 5, one request of 9000, 128
+    // heads (128 CTAs) 19.4 against 18.0, eight up to 16000 (1024) 22.2 against 27.2.
     const int64_t items = (H + 3) / 4 * p.nblk;
     const int by_cut = B > p.W - 1;
     const int64_t targets = by_cut ? p.W - 1 : B;
-    if (p.W >= kManyParts * B)
-        return launch_result(launch_kernel(latent_attention_join_kernel<8>, dim3(static_cast<unsigned>(targets * items)),
-                                           dim3(kJoinThreads), 0, s, p, by_cut));
-    return launch_result(launch_kernel(latent_attention_join_kernel<1>, dim3(static_cast<unsigned>(targets * ((items + 7) / 8))),
-                                       dim3(kJoinThreads), 0, s, p, by_cut));
+    const bool share = p.W >= kManyParts * B;
+    const int64_t grid = targets * (share ? items : (items + 7) / 8);
+    void (*join)(Params, int);
+    if (share) join = p.W > 16 * B && grid <= sms ? latent_attention_join_kernel<8, 5> : latent_attention_join_kernel<8, 2>;
+    else join = !by_cut && grid <= 3 * sms ? latent_attention_join_kernel<1, 4> : latent_attention_join_kernel<1, 2>;
+    return launch_result(launch_kernel(join, dim3(static_cast<unsigned>(grid)), dim3(kJoinThreads), 0, s, p, by_cut));
 }
