@@ -44,7 +44,7 @@
 // two CTAs read each tile (the products bound it: 38 to 49 cycles each of the
 // 36 of Q K^T, 51 each of the 16 of P V).  Per call in a graph: 2 requests of
 // 131071 tokens at 16 heads 62 us (floor 45), 128 of 8000 at 48 heads, 512
-// columns, 196 us (159), 96 of mixed lengths at 128 heads 107 us (44), one of
+// columns, 198 us (159), 96 of mixed lengths at 128 heads 107 us (44), one of
 // 701 at 128 heads 13 us: ~1.8 us to the first copy, ~2.5 us to the first
 // product and 4 to 7 us for parts and join do not shrink with the work.
 
