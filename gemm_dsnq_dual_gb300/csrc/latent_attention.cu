@@ -44,7 +44,7 @@
 // two CTAs read each tile (the products bound it: 38 to 49 cycles each of the
 // 36 of Q K^T, 51 each of the 16 of P V).  Per call in a graph: 2 requests of
 // 131071 tokens at 16 heads 62 us (floor 45), 128 of 8000 at 48 heads, 512
-// columns, 198 us (159), 96 of mixed lengths at 128 heads 107 us (44), one of
+// columns, 198 us (159), 96 of mixed lengths at 128 heads 105 us (44), one of
 // 701 at 128 heads 13 us: ~1.8 us to the first copy, ~2.5 us to the first
 // product and 4 to 7 us for parts and join do not shrink with the work.
 
@@ -75,7 +75,7 @@ constexpr int kTmemCols = 512;
 constexpr int kTmemS = 256;           // first column of the two S buffers
 constexpr float kRaise = 8.0f;        // log2 by which a maximum may grow before O is rescaled
 constexpr int kMiscBytes = 2048;
-constexpr int kRequestUnits = 3;      // what a request costs a worker beside its tiles, in tiles, at most
+constexpr int kRequestUnits = 2;      // what a request costs a worker beside its tiles, in tiles, at most
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -101,10 +101,10 @@ struct Params {
     uint32_t inject;
 };
 
-__device__ __forceinline__ int request_len(const Params& p, int b) {
-    const int64_t n = p.seq_lens[b];
-    return static_cast<int>(n < 0 ? 0 : (n > p.cap ? p.cap : n));
+__device__ __forceinline__ int clamp_len(const Params& p, int32_t n) {
+    return n < 0 ? 0 : (n > p.cap ? static_cast<int>(p.cap) : n);
 }
+__device__ __forceinline__ int request_len(const Params& p, int b) { return clamp_len(p, p.seq_lens[b]); }
 // Tiles of a request; an empty one counts as one (somebody writes its zeros).
 __device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len + kTile - 1) / kTile : 1; }
 
@@ -263,10 +263,12 @@ __device__ __forceinline__ bool soft_sync_or(bool v) {
 // to (not including) tile t_end of request b_end.
 struct Run {
     int b, t0, b_end, t_end;
+    int32_t ahead;                    // seq_lens of request b: a trip to memory ahead of its use
     int len, tiles, n;                // of the current request: tokens, tiles, tiles of this run
     __device__ __forceinline__ bool next(const Params& p) {
         if (b > b_end || (b == b_end && t0 >= t_end)) return false;
-        len = request_len(p, b);
+        len = clamp_len(p, ahead);
+        if (b + 1 < p.B) ahead = p.seq_lens[b + 1];
         tiles = tiles_of(len);
         n = (b == b_end ? t_end : tiles) - t0;
         return true;
@@ -351,9 +353,10 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     // among a request's leading units is a cut before its first tile.  Thread
     // t sums requests [t * per, (t + 1) * per).  The leading units stand for
     // what a request costs beside its tiles (queries, pipeline fill, output:
-    // ~4 us against ~1.4 us a tile); with less than that many tiles per worker
+    // ~3 us against ~1.5 us a tile); with less than that many tiles per worker
     // they would only leave workers idle.  Measured: 96 requests of mixed
-    // lengths 109 us with 3 units, 160 with none; one request of 701 tokens
+    // lengths 105 us with 2 units, 107 with 3, 108 with 4, 160 with none; 200 up
+    // to 1000 tokens, 16 heads, 23.0, 24.9 and 26.8; one request of 701 tokens
     // 14.2 us with 3, 12.8 with none.
     {
         const int per = (p.B + kThreads - 1) / kThreads;
@@ -427,6 +430,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     run.t0 = run_s[1];
     run.b_end = run_s[2];
     run.t_end = run_s[3];
+    if (run.b < p.B) run.ahead = p.seq_lens[run.b];
     const int b_first = run.b;
     if (threadIdx.x == 0 && g == 0) p.meta[w] = make_int2(run.b, run.t0);
 
@@ -713,13 +717,13 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                         // Rows past the length hold whatever the page or the
                         // buffer held: 0 * NaN would reach O, so they become 0.
                         // (S of this tile is done, so its pairs have landed.)
-                        const int words = p.nblk * 16;     // 16-byte words of a row's value
-                        for (int e = st; e < (kTile - valid) * words; e += 128) {
-                            const int r = valid + e / words, v = e % words;
-                            int slot = zslot + (v >> 4);
-                            if (slot >= p.pair_slots) slot -= p.pair_slots;
-                            *reinterpret_cast<uint4*>(pair_s + slot * kPairBytes + (r >> 3) * 2048 + ((v >> 3) & 1) * 1024 +
-                                                      (r & 7) * 128 + (v & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int r = valid + (st >> 4); r < kTile; r += 8) {
+                            int slot = zslot;
+                            uint8_t* at = pair_s + (r >> 3) * 2048 + ((st >> 3) & 1) * 1024 + (r & 7) * 128 + (st & 7) * 16;
+                            for (int j = 0; j < p.nblk; ++j) {
+                                *reinterpret_cast<uint4*>(at + slot * kPairBytes) = make_uint4(0, 0, 0, 0);
+                                if (++slot == p.pair_slots) slot = 0;
+                            }
                         }
                     }
                 }
