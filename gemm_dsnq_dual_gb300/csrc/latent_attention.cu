@@ -865,14 +865,14 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 constexpr int kJoinThreads = 256;
 constexpr int kManyParts = 4;         // workers per request from which a CTA joins an item
 
-template <int SHARE, int AHEAD>
-__global__ void __launch_bounds__(kJoinThreads, AHEAD > 2 ? 1 : 2)
+template <int SHARE, int AHEAD, int CTAS>
+__global__ void __launch_bounds__(kJoinThreads, CTAS)
 latent_attention_join_kernel(const Params p, const int by_cut) {
     grid_dependency_wait();
     allow_dependent_launch();
     bounds_self_test(p.inject);
     constexpr unsigned kAll = 0xffffffffu;
-    __shared__ int first_s, parts_s;
+    __shared__ int first_s, parts_s, request_s[kJoinThreads];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = threadIdx.x;
     const float kNegInf = __int_as_float(0xff800000);
     const int quads = (p.H + 3) / 4, items = quads * p.nblk;
@@ -884,12 +884,13 @@ latent_attention_join_kernel(const Params p, const int by_cut) {
     // meta[k] = (b, > 0); the cuts of a request are neighbours.
     static_assert(kMaxCtas <= kJoinThreads, "one thread per worker");
     const int2 me = t < p.W ? p.meta[t] : make_int2(-1, 0);
+    request_s[t] = me.x;
     if (t == 0) {
         first_s = p.W;
         parts_s = 0;
     }
     __syncthreads();
-    const int b = by_cut ? p.meta[what + 1].x : what;
+    const int b = by_cut ? request_s[what + 1] : what;
     const bool cut = me.x == b && me.y > 0 && b < p.B;
     const unsigned votes = __ballot_sync(kAll, cut);
     if (lane == 0 && votes) {
@@ -904,7 +905,7 @@ latent_attention_join_kernel(const Params p, const int by_cut) {
     if (item >= items) return;                             // SHARE = 8: the whole CTA
     const int hq = item / p.nblk, blk = item - hq * p.nblk;
     const int g = hq * 4 / kHeads, hl = hq * 4 - g * kHeads;
-    const int left_slot = p.meta[w - 1].x == b ? 0 : 1;
+    const int left_slot = request_s[w - 1] == b ? 0 : 1;
     auto slot_of = [&](int k) -> int64_t {                 // part k's place in the workspace
         return static_cast<int64_t>(k == 0 ? (w - 1) * 2 + left_slot : (w + k - 1) * 2) * p.G + g;
     };
@@ -1213,13 +1214,16 @@ extern "C" dsnq_status dsnq_paged_latent_attention(
     // 40 up to 4096 (640 CTAs) 31.5 against 33.4, 256 of 500, 16 heads (two
     // parts a request) 42.8 against 44.6; against 5, one request of 9000, 128
     // heads (128 CTAs) 19.4 against 18.0, eight up to 16000 (1024) 22.2 against 27.2.
+    // With more CTAs than find room, three on an SM instead of two: 256 of 500,
+    // 128 heads (1200 CTAs) 77.9 against 76.9 us, 40 up to 4096 (640) 30.3 against 30.9.
     const int64_t items = (H + 3) / 4 * p.nblk;
     const int by_cut = B > p.W - 1;
     const int64_t targets = by_cut ? p.W - 1 : B;
     const bool share = p.W >= kManyParts * B;
     const int64_t grid = targets * (share ? items : (items + 7) / 8);
     void (*join)(Params, int);
-    if (share) join = p.W > 16 * B && grid <= sms ? latent_attention_join_kernel<8, 5> : latent_attention_join_kernel<8, 2>;
-    else join = !by_cut && grid <= 3 * sms ? latent_attention_join_kernel<1, 4> : latent_attention_join_kernel<1, 2>;
+    if (share) join = p.W > 16 * B && grid <= sms ? latent_attention_join_kernel<8, 5, 1> : latent_attention_join_kernel<8, 2, 2>;
+    else if (!by_cut && grid <= 3 * sms) join = latent_attention_join_kernel<1, 4, 1>;
+    else join = grid <= 5 * sms ? latent_attention_join_kernel<1, 2, 2> : latent_attention_join_kernel<1, 2, 3>;
     return launch_result(launch_kernel(join, dim3(static_cast<unsigned>(grid)), dim3(kJoinThreads), 0, s, p, by_cut));
 }
