@@ -43,8 +43,8 @@
 // 64 (6.7 and 6.4 TB/s over 152 CTAs: HBM bounds it), 1.63 at 128 heads, where
 // two CTAs read each tile (the products bound it: 38 to 49 cycles each of the
 // 36 of Q K^T, 51 each of the 16 of P V).  Per call in a graph: 2 requests of
-// 131071 tokens at 16 heads 62 us (floor 45), 128 of 8000 at 48 heads, 512
-// columns, 198 us (159), 96 of mixed lengths at 128 heads 105 us (44), one of
+// 131071 tokens at 16 heads 59 us (floor 45), 128 of 8000 at 48 heads, 512
+// columns, 189 us (159), 96 of mixed lengths at 128 heads 104 us (44), one of
 // 701 at 128 heads 13 us: ~1.8 us to the first copy, ~2.5 us to the first
 // product and 4 to 7 us for parts and join do not shrink with the work.
 
@@ -116,11 +116,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t chunk, int32_t group,
-                                            int32_t page) {
+                                            int32_t page, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(chunk), "r"(group), "r"(page)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(chunk), "r"(group), "r"(page), "l"(policy)
         : "memory");
 }
 
@@ -446,6 +446,13 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
+        // Tiles pass through L2 once (twice for two head groups), the parts are
+        // to stay there for the join: with normal priority the parts of long
+        // requests went to HBM (128 x 8000 tokens 197 against 189 us; two of
+        // 131071 wrote 5.2 MB there, now 1.3, and every third pass over three
+        // caches in turn finds 15% of its rows still in L2).
+        uint64_t policy;
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
         const int pieces = kTile / p.box_rows;             // copies of a tile (1, 2, 4 or 8)
         const int batch = 32 / pieces;                     // tiles whose table entries the lanes hold
         uint32_t nq = 0;
@@ -487,7 +494,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     if (lane == 0) mbar_arrive_expect_tx(fb, live * p.box_rows * 128);
                     __syncwarp();
                     if (lane < live)
-                        tma_load_5d(smem_u32(odd_s) + po.i * kChunkBytes + lane * p.box_rows * 128, &map_odd, fb, p.ck - 1, group, id);
+                        tma_load_5d(smem_u32(odd_s) + po.i * kChunkBytes + lane * p.box_rows * 128, &map_odd, fb, p.ck - 1, group, id,
+                                    policy);
                     po.step(p.odd_slots);
                 }
                 for (int j = 0; j < pairs; ++j) {
@@ -499,7 +507,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                         __syncwarp();
                         if (lane < live)
                             tma_load_5d(smem_u32(pair_s) + pp.i * kPairBytes + lane * p.box_rows * 256, &map_pair, fb, 2 * j, group,
-                                        id);
+                                        id, policy);
                     }
                     skip = false;
                     pp.step(p.pair_slots);
