@@ -385,14 +385,15 @@ def _vec(t, name: str, dtype, n: int, dev) -> int:
 
 
 def _mat(t, name: str, dtype, dev):
-    """(rows, columns, row stride, address) of a 2-D tensor with contiguous rows."""
+    """(rows, columns, row stride, address) of a 2-D tensor with contiguous
+    rows (a lone row's stride is its length, whatever the view's is)."""
     if t.dtype is not dtype or t.dim() != 2 or t.device != dev:
         _refuse(t, name, dtype, 2, dev, "")
     n0, n1 = t.shape
     s0, s1 = t.stride()
     if s1 != 1 and n1 > 1:
         _refuse(t, name, dtype, 2, dev, "must have contiguous rows")
-    return n0, n1, (s0 if n0 > 1 else max(s0, n1)), t.data_ptr()
+    return n0, n1, (s0 if n0 > 1 else n1), t.data_ptr()
 
 
 def _cube(t, name: str, dtype, dev):

@@ -110,6 +110,17 @@ def test_extend_hands_on(library):
     assert library.calls[0][1][4] is None
 
 
+def test_a_lone_row_has_no_stride(library):
+    """One row of a buffer whose rows are no multiple of 8 apart: the stride is
+    never used, so it must not reach the library, which would refuse it."""
+    a = write_args()
+    row = z(1, 2113)
+    a.update(kv=row[:, :512], pe=row[:, 512:576], positions=a["positions"][:1], slots=a["slots"][:1])
+    dsnq.latent_cache_write(**a)
+    c = library.calls[0][1]
+    assert c[0] == 1 and c[4] == 512 and c[6] == 64
+
+
 # ------------------------------------------------------------------- refusals
 
 def out_with(i, t):
