@@ -427,19 +427,19 @@ def _workspace(size: int, dev, stream, handle: int):
     """A uint8 tensor of at least `size` bytes for one call on the stream
     `handle`.  Calls of one thread on one stream run one after the other, so
     outside a capture the last such tensor serves again (an allocation took 5
-    of a small call's 19 us on the host); of the streams a thread used, the
-    last four keep theirs.  A capture gets a tensor of its graph's pool, a
-    call with an explicit stream one of that stream."""
+    of a small call's 19 us on the host); on each device, the four streams
+    that the thread used last keep theirs.  A capture gets a tensor of its
+    graph's pool, a call with an explicit stream one of that stream."""
     if stream is not None or torch.cuda.is_current_stream_capturing():
         return _new(size, torch.uint8, dev, stream)
-    kept = _kept.__dict__
-    key = (dev.index, handle)
-    t = kept.get(key)
+    kept = _kept.__dict__.setdefault(dev.index, {})          # in the order of their last use
+    t = kept.pop(handle, None)
     if t is None or t.numel() < size:
-        kept.pop(key, None)
+        t = None
         while len(kept) >= 4:
             kept.pop(next(iter(kept)))
-        kept[key] = t = torch.empty(size, dtype=torch.uint8, device=dev)
+        t = torch.empty(size, dtype=torch.uint8, device=dev)
+    kept[handle] = t
     return t
 
 

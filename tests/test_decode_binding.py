@@ -222,3 +222,51 @@ def test_tensors_of_another_device_are_refused_by_name(library, op, name):
     with pytest.raises(ValueError, match=r"is on cpu, expected meta" if name == first else f"{name} is on meta, expected cpu"):
         fn(**a)
     assert library.calls == []
+
+
+# ------------------------------------------------------------- kept workspaces
+
+CPU = torch.device("cpu")
+
+
+@pytest.fixture
+def eager(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    dsnq._kept.__dict__.clear()
+    yield
+    dsnq._kept.__dict__.clear()
+
+
+def test_a_stream_in_use_keeps_its_workspace(eager):
+    """The four streams used last keep theirs: one that every other call uses
+    is never among those that lose it, the others go in turn."""
+    mine = dsnq._workspace(100, CPU, None, 1)
+    others = {}
+    for h in range(2, 12):
+        others[h] = dsnq._workspace(100, CPU, None, h)
+        assert dsnq._workspace(100, CPU, None, 1) is mine
+    assert dsnq._workspace(100, CPU, None, 11) is others[11]
+    assert dsnq._workspace(100, CPU, None, 10) is others[10]
+    assert dsnq._workspace(100, CPU, None, 9) is others[9]
+    assert dsnq._workspace(100, CPU, None, 8) is not others[8]
+
+
+def test_workspaces_of_devices_are_counted_apart(eager, monkeypatch):
+    """Five devices with a stream each: all keep theirs."""
+    class Device(str):
+        index = property(lambda self: int(self[4:]))
+
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: empty(n, dtype=dtype))
+    devs = [Device(f"cuda{i}") for i in range(5)]
+    kept = [dsnq._workspace(10, d, None, 7) for d in devs]
+    assert all(dsnq._workspace(10, d, None, 7) is t for d, t in zip(devs, kept))
+    assert len({t.data_ptr() for t in kept}) == 5
+
+
+def test_captures_and_explicit_streams_keep_none(eager, monkeypatch):
+    monkeypatch.setattr(dsnq, "_new", lambda shape, dtype, dev, stream: torch.empty(shape, dtype=dtype, device=dev))
+    assert dsnq._workspace(10, CPU, 5, 5) is not dsnq._workspace(10, CPU, 5, 5)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    assert dsnq._workspace(10, CPU, None, 5) is not dsnq._workspace(10, CPU, None, 5)
+    assert not dsnq._kept.__dict__
