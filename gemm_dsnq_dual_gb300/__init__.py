@@ -45,6 +45,7 @@ __all__ = [
     "fused_norm_quant_gemm_dual",
     "ROPE_INTERLEAVED", "ROPE_HALF", "rope_frequencies", "extend_block_tables", "head_rmsnorm_rope",
     "latent_cache_write", "paged_latent_attention", "paged_latent_attention_workspace_bytes",
+    "release_workspaces",
     "quant_output_sizes", "debug_status", "debug_set", "set_launch_overlap", "scale_layout_of", "scale_ld_for",
     "empty_scales",
 ]
@@ -443,6 +444,14 @@ def _workspace(size: int, dev, stream, handle: int):
     return t
 
 
+def release_workspaces() -> None:
+    """Gives the workspaces that paged_latent_attention keeps for the calling
+    thread (up to 42 MB for each of four streams of a device) back to torch's
+    allocator.  Calls still running may go on using theirs: the memory goes to
+    later work of the same stream only."""
+    _kept.__dict__.clear()
+
+
 def _rope_layout(layout) -> int:
     if layout == "interleaved" or layout == ROPE_INTERLEAVED:
         return ROPE_INTERLEAVED
@@ -569,8 +578,9 @@ def paged_latent_attention(q, cache, block_table, seq_lens, v_dim: int, scale: f
     [pages, page_size, DK], whose pages block_table [B, width] (int32) names.
     The value of a row is its first v_dim columns.  Returns (out [B,H,v_dim]
     bf16, lse [B,H] fp32).  The uint8 `workspace` is the binding's own if
-    omitted: one per thread and stream, and one of its own in a capture (with
-    streams that are destroyed while work is pending, pass one)."""
+    omitted: one per thread and stream, kept until release_workspaces(), and
+    one of its own in a capture (with streams that are destroyed while work is
+    pending, pass one)."""
     dev = q.device
     B, H, DK, qt, qh, qp = _cube(q, "q", _BF16, dev)
     pages, page_size, W, ld_page, ld_row, cp = _cube(cache, "cache", _BF16, dev)

@@ -232,9 +232,9 @@ CPU = torch.device("cpu")
 @pytest.fixture
 def eager(monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
-    dsnq._kept.__dict__.clear()
+    dsnq.release_workspaces()
     yield
-    dsnq._kept.__dict__.clear()
+    dsnq.release_workspaces()
 
 
 def test_a_stream_in_use_keeps_its_workspace(eager):
@@ -262,6 +262,20 @@ def test_workspaces_of_devices_are_counted_apart(eager, monkeypatch):
     kept = [dsnq._workspace(10, d, None, 7) for d in devs]
     assert all(dsnq._workspace(10, d, None, 7) is t for d, t in zip(devs, kept))
     assert len({t.data_ptr() for t in kept}) == 5
+
+
+def test_a_workspace_grows_and_is_given_back(eager):
+    import gc
+    import weakref
+    small = dsnq._workspace(10, CPU, None, 1)
+    assert dsnq._workspace(5, CPU, None, 1) is small
+    large = dsnq._workspace(20, CPU, None, 1)
+    assert large is not small and large.numel() == 20 and dsnq._workspace(10, CPU, None, 1) is large
+    ref = weakref.ref(large)
+    del small, large
+    dsnq.release_workspaces()
+    gc.collect()
+    assert ref() is None
 
 
 def test_captures_and_explicit_streams_keep_none(eager, monkeypatch):
