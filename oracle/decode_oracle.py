@@ -61,15 +61,37 @@ def extend_block_tables(seq_lens, new_tokens, free_pages, table, page_size, rows
             np.array([taken, wanted], np.int64), table)
 
 
+def _inverse_turn(bits):
+    """floor(2^bits / (2 pi)), from Machin's pi = 16 atan(1/5) - 4 atan(1/239)."""
+    one = 1 << (2 * bits)
+
+    def atan_inverse(n):
+        total, term, k = 0, one // n, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term //= n * n
+            k += 2
+        return total
+
+    return (one << bits) // (2 * (16 * atan_inverse(5) - 4 * atan_inverse(239)))
+
+
+_TURN_BITS = 1300                        # beyond the exponents of fp64 frequencies and positions
+_PER_TURN = _inverse_turn(_TURN_BITS)
+
+
+def _angle(position, freq):
+    """position * freq modulo one turn: the exact product's fraction of a turn
+    (Python integers), rounded to fp64 once."""
+    num, den = float(freq).as_integer_ratio()
+    scale = den << _TURN_BITS
+    return int(position) * num * _PER_TURN % scale / scale * (2.0 * np.pi)
+
+
 def rope_rotate(x, positions, inv_freq, layout, scale=1.0, inverse=False):
     """x [..., tokens on axis 0, ..., R] with its pairs rotated, fp64."""
     x = np.asarray(x, np.float64)
-    # The angle modulo one turn, from the exact product of a whole position
-    # and the fp64 frequency (Python integers: no rounding before the fraction).
-    ang = np.empty((len(positions), len(inv_freq)))
-    for i, p in enumerate(positions):
-        for j, f in enumerate(inv_freq):
-            ang[i, j] = np.float64(int(p)) * np.float64(f)
+    ang = np.array([[_angle(p, f) for f in inv_freq] for p in positions]).reshape(len(positions), len(inv_freq))
     c, s = np.cos(ang) * scale, np.sin(ang) * scale * (-1.0 if inverse else 1.0)
     shape = (len(positions),) + (1,) * (x.ndim - 2) + (len(inv_freq),)
     c, s = c.reshape(shape), s.reshape(shape)

@@ -61,6 +61,21 @@ def test_rotation_is_a_complex_product():
     assert np.allclose(oracle.rope_rotate(h, pos, f, "half", inverse=True), x, atol=1e-9)
 
 
+def test_rotation_at_far_positions_is_exact():
+    """The angle is the exact product's: at 2^50 an fp64 product is off by up
+    to 2^-4 rad, the exact fraction of a turn, rounded once to fp64, by 2^-51."""
+    from fractions import Fraction
+    per_turn = Fraction("0.159154943091895335768883763372514362034459645740456448747667344")   # 1 / (2 pi)
+    pos, f = [2**50 + 1, -(2**50) - 12345, 2**62 - 1, 2**31 - 1, 3], [0.1, 1.0, 1e-5, 0.7320508]
+    x = np.zeros((len(pos), 8))
+    x[:, 0::2] = 1
+    y = oracle.rope_rotate(x, pos, f, "interleaved")
+    for i, p in enumerate(pos):
+        for j, w in enumerate(f):
+            t = float((p * Fraction(w) * per_turn) % 1) * 2 * math.pi
+            assert abs(y[i, 2 * j] - math.cos(t)) < 1e-14 and abs(y[i, 2 * j + 1] - math.sin(t)) < 1e-14
+
+
 def test_norm_agrees_with_torch():
     x, g = torch.randn(4, 3, 32, dtype=torch.float64), torch.rand(32, dtype=torch.float64)
     y = oracle.head_rmsnorm_rope(x.numpy(), [0] * 4, [], g.numpy(), 1e-5)
