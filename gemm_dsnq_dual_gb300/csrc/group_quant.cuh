@@ -18,6 +18,7 @@ constexpr float kE4M3Max = 448.0f;  // largest finite E4M3FN value
 
 // ---- packed fp32 pairs: the f32x2 arithmetic of sm_100+ through the CUDA
 // builtins (one instruction per pair).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 

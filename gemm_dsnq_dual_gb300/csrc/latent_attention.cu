@@ -15,7 +15,7 @@
 // whole.  Every CTA works the cut out from the lengths on
 // the device, so nothing is planned on the host and the call can be captured.
 // A run that covers a whole request writes its output; the others leave
-// (sum, max, unnormalized output) in fp32 in the workspace, at two slots per
+// (sum, max, output times that sum) in fp32 in the workspace, at two slots per
 // worker, and a second kernel joins them in the order of the tokens (no
 // atomics: results do not depend on timing).
 //
@@ -27,7 +27,10 @@
 // DV/128 x 64 = 256 of them at full use of its 128 lanes, which leaves room for
 // two S buffers; heads x DV at M = 64 would take all 512.
 // P is rounded to bf16 (half a step, 2^-8 relative) because the tensor core
-// takes bf16; sums, maxima and O stay in fp32, and the sum is of the unrounded p.
+// takes bf16; sums, maxima and O stay in fp32.  O is divided by the sum of the
+// rounded p, so that the weights add up to one and an output lies among the
+// values it is made of; lse, and the weight of a part among the others, is of
+// the unrounded sum.
 // Warps: 0 copies tiles (TMA), 1 issues the products Q K^T, 6 the products P V,
 // 2..5 do the softmax, the rescaling of O and the output.  S(n+1) is computed
 // while softmax(n) runs.  Two issuing warps, because the two products wait for
@@ -621,8 +624,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 continue;
             }
             // Of the two rows: maximum of the raw scores in use, and this
-            // thread's share of the sum of p.
-            float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+            // thread's share of the sums of p, unrounded and rounded.
+            float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
             for (int i = 0; i < run.n; ++i, ++n) {
                 const int valid = min(kTile, run.len - (run.t0 + i) * kTile);
                 ok = ok && wait_uniform(smem_u32(&sfull[n & 1]), (n >> 1) & 1);
@@ -677,6 +680,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                             alpha = exp2_fast((m[a] - top[a]) * p.scale_log2);
                             m[a] = top[a];
                             l[a] *= alpha;
+                            lr[a] *= alpha;
                         }
                         if ((lane & 3) == 0) alpha_s[row0 + 8 * a] = alpha;
                     }
@@ -700,16 +704,15 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
                         const float off = m[a] == kNegInf ? 0.f : m[a] * p.scale_log2;
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float e0 = exp2_fast(fmaf(s[a][2 * j], p.scale_log2, -off));
                             const float e1 = exp2_fast(fmaf(s[a][2 * j + 1], p.scale_log2, -off));
-                            sum[j & 1] += e0;
-                            sum[2 + (j & 1)] += e1;
+                            sum[j & 1] = add2(sum[j & 1], make_float2(e0, e1));
                             pk[a][j] = pack_bf16(e0, e1);
                         }
-                        l[a] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        l[a] += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                     }
                 }
                 if (!pv_done) ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
@@ -741,6 +744,18 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(pfull));
+                if (mine) {
+                    // The rounded sum, while the product runs.
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        float2 sum[2] = {make_float2(lr[a], 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            sum[j & 1] = add2(sum[j & 1], make_float2(__uint_as_float(pk[a][j] << 16),
+                                                                      __uint_as_float(pk[a][j] & 0xffff0000u)));
+                        lr[a] = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+                    }
+                }
             }
             // ---- output of the request (or of this worker's part of it)
             ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
@@ -749,8 +764,12 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 l[a] += __shfl_xor_sync(0xffffffffu, l[a], 1);
+                lr[a] += __shfl_xor_sync(0xffffffffu, lr[a], 1);
                 l[a] += __shfl_xor_sync(0xffffffffu, l[a], 2);
-                if ((lane & 3) == 0) inv_s[row0 + 8 * a] = l[a] > 0.f || l[a] != l[a] ? __fdividef(1.0f, l[a]) : 0.f;
+                lr[a] += __shfl_xor_sync(0xffffffffu, lr[a], 2);
+                // A part's weights add up to its unrounded sum, which the join divides by.
+                if ((lane & 3) == 0)
+                    inv_s[row0 + 8 * a] = lr[a] > 0.f || lr[a] != lr[a] ? __fdividef(whole ? 1.0f : l[a], lr[a]) : 0.f;
             }
             soft_sync_or(false);                           // inv_s is next written after another tile's barrier
             __syncwarp();
@@ -814,28 +833,35 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                     put(it + 1, r[1]);
                 }
             } else {
-                // A part, in the order the registers hold it: 512 bytes a store.
+                // A part, in the order the registers hold it: 512 bytes a store,
+                // 16 heads at a time with their factors in registers (read from
+                // shared memory between the stores they cost 1.5 us a part).
                 float4* o = reinterpret_cast<float4*>(p.part_o) + slot * p.nblk * 16 * 128 + quad * 32 + lane;
-                const int per = (heads + 15) >> 4, its = p.nblk * per;       // 16 heads a step
-                uint32_t r[2][16];
-                auto fetch = [&](int it, uint32_t (&x)[16]) { tmem_ld16_issue(tl + (it / per) * kHeads + (it % per) * 16, x); };
-                auto put = [&](int it, const uint32_t (&x)[16]) {
-                    const int c = (it / per) * 16 + (it % per) * 4;
+                for (int hg = 0; hg < heads; hg += 16) {
+                    float4 f[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (bounds_ok(w < p.W && c + j < p.nblk * 16))
-                            o[(c + j) * 128] = make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]),
-                                                           __uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3]));
-                };
-                fetch(0, r[0]);
-                for (int it = 0; it < its; it += 2) {
-                    tmem_ld16_wait(r[0]);
-                    if (it + 1 < its) fetch(it + 1, r[1]);
-                    put(it, r[0]);
-                    if (it + 1 >= its) break;
-                    tmem_ld16_wait(r[1]);
-                    if (it + 2 < its) fetch(it + 2, r[0]);
-                    put(it + 1, r[1]);
+                    for (int j = 0; j < 4; ++j) f[j] = reinterpret_cast<const float4*>(inv_s + hg)[j];
+                    uint32_t r[2][16];
+                    auto fetch = [&](int blk, uint32_t (&x)[16]) { tmem_ld16_issue(tl + blk * kHeads + hg, x); };
+                    auto put = [&](int blk, const uint32_t (&x)[16]) {
+                        const int c = blk * 16 + hg / 4;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (bounds_ok(w < p.W && c + j < p.nblk * 16))
+                                o[(c + j) * 128] =
+                                    make_float4(__uint_as_float(x[4 * j]) * f[j].x, __uint_as_float(x[4 * j + 1]) * f[j].y,
+                                                __uint_as_float(x[4 * j + 2]) * f[j].z, __uint_as_float(x[4 * j + 3]) * f[j].w);
+                    };
+                    fetch(0, r[0]);
+                    for (int blk = 0; blk < p.nblk; blk += 2) {
+                        tmem_ld16_wait(r[0]);
+                        if (blk + 1 < p.nblk) fetch(blk + 1, r[1]);
+                        put(blk, r[0]);
+                        if (blk + 1 >= p.nblk) break;
+                        tmem_ld16_wait(r[1]);
+                        if (blk + 2 < p.nblk) fetch(blk + 2, r[0]);
+                        put(blk + 1, r[1]);
+                    }
                 }
             }
 #pragma unroll

@@ -511,7 +511,9 @@ DSNQ_API dsnq_status dsnq_paged_latent_attention_workspace_bytes(int64_t B, int6
  *   z_j = scale * q[b,h] . c_j,   j < seq_lens[b]
  *   out[b,h,:] = sum_j softmax(z)_j c_j[0:DV],   lse[b,h] = log sum_j exp z_j
  * fp32 scores, sums and accumulation; the probabilities are rounded to bf16
- * for the second product.  An empty request gets zeros and lse = -infinity.
+ * for the second product, whose result is divided by the sum of the rounded
+ * ones (the weights add up to one); lse is of the unrounded sum.  An empty
+ * request gets zeros and lse = -infinity.
  *   B, H, DK, DV : requests (<= DSNQ_MAX_REQUESTS), heads (<= 1024), key and value
  *                 width: DK a multiple of 64, <= 576; DV a multiple of 128,
  *                 <= 512 and <= DK.
