@@ -78,6 +78,7 @@ constexpr int kTmemCols = 512;
 constexpr int kTmemS = 256;           // first column of the two S buffers
 constexpr float kRaise = 8.0f;        // log2 by which a maximum may grow before O is rescaled
 constexpr int kMiscBytes = 2048;
+constexpr int kManyParts = 4;         // workers per request from which a CTA joins an item
 constexpr int kRequestUnits = 2;      // what a request costs a worker beside its tiles, in tiles, at most
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -87,6 +88,7 @@ struct Params {
     const int32_t* table;
     int64_t ld_table;
     int B, H, G, W;                   // requests, heads, head groups, workers
+    int W_full;                       // workers that the GPU has room for, whatever the tables hold
     int width, page_size, box_rows, num_pages;   // box_rows: tokens of one copy
     int64_t cap;                      // tokens the table can hold per request
     int ck, nblk;                     // 64-column chunks of a row, 128-column blocks of the value
@@ -389,12 +391,23 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             tiles += sums[i];
             most = max(most, longest[i]);
         }
-        // Requests about as long as a worker's share go one to a worker, uncut:
-        // cutting saves less than the parts (fp32, the dearer the more heads)
-        // and their join cost.  Measured, uncut against cut: 64 requests of
-        // 1000 tokens, 128 heads (16 tiles, share 13) 38.8 against 49.3 us;
-        // 16 of 300, 16 heads (5 tiles, share 0) 16.4 against 13.2 us.
-        const bool uncut = p.B <= p.W && most <= tiles / p.W + 3 + min(p.H, kHeads) / 12;
+        // Requests a little longer than a worker's share go one to a worker,
+        // uncut: cutting saves less than the parts and their join cost.  That
+        // cost grows with the requests and heads that a join has to look at
+        // (in tiles, one with an idle GPU, up to 10 with a fifth of it taken);
+        // with less than kManyParts workers a request the join is the one of
+        // few parts, at most 3 to 5 tiles.  Measured, cut against uncut, at
+        // 128 heads (76 workers): one request of 2 tiles 12.3 and 12.5 us, of 3
+        // 12.0 and 14.0, of 8 12.4 and 22.1; 4 of 3 15.2 and 14.8, of 5 15.6 and 18.0;
+        // 16 of 10 30.9 and 29.3, of 16 32.8 and 39.4; 32 of 8 24.2 and 23.8, of 12
+        // 26.2 and 30.8; 64 of 24 56.9 and 52.5.  At 16 heads (152): one of 2
+        // 10.7 and 10.9, of 3 10.7 and 12.3; 64 of 4 15.7 and 14.8, of 7 17.8 and 19.6.  Over
+        // 3660 mixes of 1 to 152 requests of 2 to 32 tiles the rule's choice
+        // takes 1.2% more than the better one on average; a slack of 3 + h / 12,
+        // whatever the number of requests, took 4%.
+        const int h = min(p.H, kHeads), joined = 5 * p.B * h / (8 * p.W_full);
+        const int slack = max(1, p.W < kManyParts * p.B ? min(joined, 3 + h / 32) : joined);
+        const bool uncut = p.B <= p.W && most <= (tiles + p.W - 1) / p.W + slack;
         const int lead = tiles / p.W < kRequestUnits ? static_cast<int>(tiles / p.W) : kRequestUnits;
         const int64_t total = tiles + static_cast<int64_t>(lead) * p.B;
         before += static_cast<int64_t>(lead) * b0;
@@ -897,7 +910,6 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 // takes as long as its trips to memory.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
-constexpr int kManyParts = 4;         // workers per request from which a CTA joins an item
 
 template <int SHARE, int AHEAD, int CTAS>
 __global__ void __launch_bounds__(kJoinThreads, CTAS)
@@ -1192,7 +1204,9 @@ extern "C" dsnq_status dsnq_paged_latent_attention(
         return DSNQ_ERR_CUDA;
     }
     Params p{};
-    p.W = static_cast<int>(workers_for(B, G, cap, sms < kMaxCtas ? sms : kMaxCtas));
+    const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+    p.W = static_cast<int>(workers_for(B, G, cap, ctas));
+    p.W_full = ctas > G ? static_cast<int>(ctas / G) : 1;
     p.seq_lens = seq_lens;
     p.table = block_table;
     p.ld_table = ld_table;
