@@ -28,6 +28,9 @@ The JSON line also reports, measured in the same run:
     consecutive steps overlap on three streams, as a serving loop runs them);
   * cpu_baseline: the fp64 CPU oracle timed on the whole M=8192 workload.
 
+`--decode-ops` times the other operators of the decode step instead, case by
+case (perf/operators.py).
+
 `--impl reference` times the CPU oracle alone on the same metric (bounded
 samples of rows and output columns so the run ends within minutes).
 Multi-GPU: rows are independent, so each rank runs its own batch (weak
@@ -876,18 +879,18 @@ def allreduce_max(x: float, world, dev):
     return float(t.item())
 
 
-def decode_ops(which, M, dev):
+def decode_ops(which, M, dev, tokens=1024, heads=128):
     """A call of one operator of the decode step on M rows: `tables` for M
     requests, `head_rope` on the attention heads of wq_b's output (128 of 192
     columns, the last 64 rotated), `cache_write` of the kv latent and its
-    position columns, `attention` of M requests of 1024 tokens each with 128
-    heads over the 576-column cache."""
+    position columns, `attention` of M requests of `tokens` tokens each with
+    `heads` heads over the 576-column cache."""
     import torch
     import gemm_dsnq_dual_gb300 as dsnq
     g = torch.Generator(device=dev).manual_seed(5)
     rnd = lambda *s: torch.randn(*s, generator=g, device=dev).to(torch.bfloat16)
     ints = lambda n, hi: torch.randint(0, hi, (n,), generator=g, device=dev)
-    page, tokens = 64, 1024
+    page = 64
     pages = M * (tokens // page + 1)
     ids = torch.randperm(pages, generator=g, device=dev).to(torch.int32)
     f, scale = dsnq.rope_frequencies(64, device=dev)
@@ -907,12 +910,63 @@ def decode_ops(which, M, dev):
         gamma = rnd(KKV)
         return lambda: dsnq.latent_cache_write(row[:, KQ:KQ + KKV], row[:, KQ + KKV:], pos, slots, f, cache, gamma=gamma,
                                                normalize=True, rope_scale=scale)
-    q, table = rnd(M, 128, KKV + 64), ids.view(M, -1)
+    q, table = rnd(M, heads, KKV + 64), ids.view(M, -1)
     lens = torch.full((M,), tokens, dtype=torch.int32, device=dev)
     return lambda: dsnq.paged_latent_attention(q, cache, table, lens, KKV, 192 ** -0.5)
 
 
 DECODE_OPS = ["tables", "head_rope", "cache_write", "attention"]
+
+
+def run_decode_ops(args):
+    """Times the library's call of every listed case of perf/operators.py and
+    of a few more and prints one JSON line: `graph_us` per call in a CUDA graph
+    over distinct inputs, each visited once per replay with L2 flushed before
+    the replay (so nothing of a case is found in L2), `call_us` per call of an
+    eager loop over the same inputs, `floor_us` from the bytes and operations
+    that the case cannot do without, at the measured rates."""
+    import importlib.util
+    import torch
+    import gemm_dsnq_dual_gb300 as dsnq
+    spec = importlib.util.spec_from_file_location("decode_cases", os.path.join(ROOT, "perf", "operators.py"))
+    cases = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(cases)
+    cases.own = True
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(0)
+    stream = torch.cuda.current_stream()
+    flush = L2Flush(torch, dev)
+    hbm_gbs, bf16, _, source = load_peaks()
+    by_name = {c["name"]: c for c in cases.listed()}
+    more = [dict(by_name["rope prompt 4096"], name="rope prompt 4096, half pairs", layout="half"),
+            dict(by_name["write prompt 8191"], name="write prompt 32768", M=32768, pad=0),
+            dict(by_name["write prompt 8191"], name="write prompt 32768, half pairs", M=32768, pad=0, layout="half"),
+            dict(by_name["attention 1 x 701"], name="attention 4 x 200", B=4, maxlen=200),
+            dict(by_name["attention 1 x 701"], name="attention 64 x 1000", B=64, maxlen=1000)]
+    out = {}
+    with ClockSampler(0) as clk:
+        for c in [*by_name.values(), *more]:
+            w = cases.work(c)
+            sets = 24 if w["bytes"] < 64 << 20 else 6
+            states = [cases.prepare(c, 100 + i) for i in range(sets)]
+            calls = [lambda s=s: cases.run(s) for s in states]
+            graph = timed_graph_calls(torch, stream, calls, flush, reps=max(args.side_reps, 5))
+            n = sets * max(1, 240 // sets if graph < 1000 else 1)
+            torch.cuda.synchronize()
+            t0 = time.perf_counter()
+            for i in range(n):
+                calls[i % sets]()
+            torch.cuda.synchronize()
+            call = (time.perf_counter() - t0) / n * 1e6
+            floor = max(w["bytes"] / hbm_gbs / 1e3, w["flops"] / bf16 / 1e6)
+            out[c["name"]] = {"floor_us": round(floor, 4), "graph_us": round(graph, 2), "call_us": round(call, 1), "sets": sets}
+            print(f"{c['name']:32s} floor {floor:9.4f}  graph {graph:8.2f}  call {call:8.1f} us", file=sys.stderr, flush=True)
+            del states, calls
+            torch.cuda.empty_cache()
+        status = dsnq.debug_status()
+    if status != 0:
+        raise RuntimeError(f"device status {status} after the timed calls")
+    print(json.dumps({"decode_ops": out, "peaks": source, "hbm_gbs": hbm_gbs, "bf16_tflops": bf16, "clocks": clk.summary()}))
 
 
 def run_kernel_only(args):
@@ -931,7 +985,7 @@ def run_kernel_only(args):
     dev = torch.device("cuda", 0)
     M = args.M
     if args.kernel_only in DECODE_OPS:
-        fn = decode_ops(args.kernel_only, M, dev)
+        fn = decode_ops(args.kernel_only, M, dev, args.tokens, args.heads)
         for _ in range(args.launches):
             fn()
         torch.cuda.synchronize()
@@ -989,6 +1043,10 @@ def main():
                     default=None,
                     help="profiling aid: launch one kernel --launches times and exit")
     ap.add_argument("--launches", type=int, default=3)
+    ap.add_argument("--tokens", type=int, default=1024, help="tokens per request of --kernel-only attention (a multiple of 64)")
+    ap.add_argument("--heads", type=int, default=128, help="heads of --kernel-only attention")
+    ap.add_argument("--decode-ops", action="store_true",
+                    help="time the decode-step operators around the pre-projection, case by case, and exit")
     ap.add_argument("--oracle-child", type=int, default=0, help=argparse.SUPPRESS)
     args = ap.parse_args()
     if args.oracle_child:
@@ -996,6 +1054,9 @@ def main():
         return
     if args.kernel_only:
         run_kernel_only(args)
+        return
+    if args.decode_ops:
+        run_decode_ops(args)
         return
     if args.warmup < 3:
         ap.error("--warmup must be at least 3")
