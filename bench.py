@@ -921,9 +921,10 @@ DECODE_OPS = ["tables", "head_rope", "cache_write", "attention"]
 def run_decode_ops(args):
     """Times the library's call of every listed case of perf/operators.py and
     of a few more and prints one JSON line: `graph_us` per call in a CUDA graph
-    over distinct inputs, each visited once per replay with L2 flushed before
-    the replay (so nothing of a case is found in L2), `call_us` per call of an
-    eager loop over the same inputs, `floor_us` from the bytes and operations
+    of DECODE_GRAPH_CALLS calls (a quarter of that from 64 MB a call on) over
+    distinct inputs, L2 flushed before each replay and gigabytes of other
+    inputs between two visits of one (so nothing of it is found in L2),
+    `call_us` per call of an eager loop over the same inputs, `floor_us` from the bytes and operations
     that the case cannot do without, at the measured rates."""
     import importlib.util
     import torch
@@ -947,11 +948,12 @@ def run_decode_ops(args):
     with ClockSampler(0) as clk:
         for c in [*by_name.values(), *more]:
             w = cases.work(c)
-            sets = 24 if w["bytes"] < 64 << 20 else 6
+            sets = DECODE_GRAPH_CALLS if w["bytes"] < 16 << 20 else 25 if w["bytes"] < 64 << 20 else 5
+            in_graph = DECODE_GRAPH_CALLS if w["bytes"] < 64 << 20 else DECODE_GRAPH_CALLS // 4
             states = [cases.prepare(c, 100 + i) for i in range(sets)]
             calls = [lambda s=s: cases.run(s) for s in states]
-            graph = timed_graph_calls(torch, stream, calls, flush, reps=max(args.side_reps, 5))
-            n = sets * max(1, 240 // sets if graph < 1000 else 1)
+            graph = timed_graph_calls(torch, stream, [calls[i % sets] for i in range(in_graph)], flush, reps=max(args.side_reps, 5))
+            n = 2 * in_graph
             torch.cuda.synchronize()
             t0 = time.perf_counter()
             for i in range(n):

@@ -467,7 +467,8 @@ def rope_frequencies(rope_dim: int, base: float = 10000.0, factor: float = 1.0, 
     original_length) the frequencies of fewer than beta_slow turns over the
     original length are divided by it, those of more than beta_fast kept, the
     ones between blended (the YaRN scheme), and rope_scale is its attention
-    factor 0.1 ln(factor) + 1.  Any other table serves as well."""
+    factor 0.1 ln(factor) + 1.  Any other table serves as well.  Those two take
+    rope_dim = 2 * len(inv_freq) of multiples of 16 up to 256."""
     if rope_dim <= 0 or rope_dim % 2:
         raise ValueError(f"rope_dim must be even and positive, got {rope_dim}")
     i = torch.arange(0, rope_dim, 2, dtype=torch.float64)
@@ -514,10 +515,12 @@ def extend_block_tables(seq_lens, new_tokens, free_pages, block_table, page_size
 
 def head_rmsnorm_rope(x, positions, inv_freq, gamma=None, eps: float = 1e-6, normalize: bool = True, rope_offset=None,
                       layout="interleaved", rope_scale: float = 1.0, inverse: bool = False, out=None, stream=None):
-    """RMSNorm of each head of x [M,H,D] (bf16, token and head strides free)
-    and rotation of its columns [rope_offset, rope_offset + 2 * len(inv_freq))
-    (default: the last ones) by positions [M] int64 times inv_freq float64,
-    one rounding.  `out` may be x.  Returns out [M,H,D]."""
+    """RMSNorm of each head of x [M,H,D] (bf16; token and head strides are
+    free multiples of 8, at least D) and rotation of its columns [rope_offset,
+    rope_offset + 2 * len(inv_freq)) (default: the last ones; an offset that is
+    a multiple of 8, a width that is one of 16, up to 256) by positions [M]
+    int64 times inv_freq float64, one rounding.  `out` may be x.  Returns out
+    [M,H,D]."""
     dev = x.device
     M, H, D, xt, xh, xp = _cube(x, "x", _BF16, dev)
     if out is None:
@@ -539,8 +542,9 @@ def latent_cache_write(kv, pe, positions, slots, inv_freq, cache, gamma=None, ep
     """Stores row m = [kv[m] | pe[m]] (bf16; pe [M,P] or None) at slots[m] of
     the paged cache [pages, page_size, K+P], kv RMSNormed first when
     `normalize`, columns [rope_offset, + 2 * len(inv_freq)) of the row
-    (default: the last ones) rotated.  Negative slots are skipped; the slots
-    of a call must be distinct.  Returns cache."""
+    (default: the last ones; multiples of 8 and 16 as above) rotated.
+    Negative slots are skipped; the slots of a call must be distinct.  Returns
+    cache."""
     dev = kv.device
     M, K, ldkv, kvp = _mat(kv, "kv", _BF16, dev)
     P = ldpe = 0

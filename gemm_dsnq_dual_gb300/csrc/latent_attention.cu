@@ -42,14 +42,17 @@
 // more: tiles come in pairs of 64-column chunks, each freed as soon as its
 // product with P is done, so that the next tile's copies start early.
 //
-// Measured on GB300, 576 columns: 1.64 us per tile and CTA at 16 heads, 1.72 at
-// 64 (6.7 and 6.4 TB/s over 152 CTAs: HBM bounds it), 1.63 at 128 heads, where
-// two CTAs read each tile (the products bound it: 38 to 49 cycles each of the
-// 36 of Q K^T, 51 each of the 16 of P V).  Per call in a graph: 2 requests of
-// 131071 tokens at 16 heads 59 us (floor 45), 128 of 8000 at 48 heads, 512
-// columns, 189 us (159), 96 of mixed lengths at 128 heads 104 us (44), one of
-// 701 at 128 heads 13 us: ~1.8 us to the first copy, ~2.5 us to the first
-// product and 4 to 7 us for parts and join do not shrink with the work.
+// Measured on GB300, 576 columns, between requests of 2048 and 8192 tokens, one
+// to a worker: 1.61 us per tile and CTA at 16 heads, 1.73 at 64 (7.0 and 6.5
+// TB/s over 152 CTAs: HBM bounds it), 1.70 at 128 heads, where two CTAs read
+// each tile (3.3 TB/s).  There the products bound it: alone on an SM one of Q
+// K^T takes 48 cycles and one of P V 61, so the 36 and 16 of a tile 2704 of its
+// ~3500; the rest is the ring of two tiles, which refills as P V frees it.  Per
+// call in a graph: 2 requests of 131071 tokens at 16 heads 59 us (floor 45), 128
+// of 8000 at 48 heads, 512 columns, 191 us (159), 96 of mixed lengths at 128
+// heads 105 us (44), one of 701 at 128 heads 13 us: ~1.8 us to the first copy,
+// ~2.5 us to the first product and 4 to 7 us for parts and join do not shrink
+// with the work.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -464,9 +467,10 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         // ------------------------------------------------------- TMA producer
         // Tiles pass through L2 once (twice for two head groups), the parts are
         // to stay there for the join: with normal priority the parts of long
-        // requests went to HBM (128 x 8000 tokens 197 against 189 us; two of
-        // 131071 wrote 5.2 MB there, now 1.3, and every third pass over three
-        // caches in turn finds 15% of its rows still in L2).
+        // requests went to HBM (two of 131071 tokens wrote 5.2 MB there, now
+        // 1.3).  Over eight caches in turn 128 x 8000 tokens take 191.3 us
+        // against 196.7, two of 131071 59.3 against 62.0; over three caches in
+        // turn, where a pass finds some of its rows still in L2, 189.4 and 59.1.
         uint64_t policy;
         asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
         const int pieces = kTile / p.box_rows;             // copies of a tile (1, 2, 4 or 8)

@@ -140,7 +140,9 @@ constexpr int kHeadWarps = 8;
 // (64 registers) with 64 bytes a thread on their way keep 64 KB in flight.
 // Measured: 4096 x 48 x 512 in 61.5 us (6.5 TB/s, 98% of the copy bandwidth;
 // 86 us with one row a warp in flight), 1 x 128 x 192 in 2.1 us.
-// HALF: pairs (i, i + dim/2), whose partner chunk is loaded beside the own one.
+// HALF: pairs (i, i + dim/2), whose partner chunk is loaded beside the own one,
+// in registers of its own: at 257 to 512 columns a warp then has one row in
+// flight and an SM two CTAs, and 4096 x 48 x 512 take 108 us (3.7 TB/s).
 template <int LPR, int CPL, bool HALF>
 __global__ void __launch_bounds__(kHeadWarps * 32, CPL * (HALF ? 2 : 1) <= 2 ? 4 : CPL * (HALF ? 2 : 1) <= 4 ? 2 : 1)
 head_norm_rope_kernel(const HeadArgs a) {
@@ -280,8 +282,12 @@ constexpr int kWriteWarps = 4;
 // decide only where and by how much), so a row costs one trip to memory; four
 // CTAs or more per SM hide it.  Measured: 8191 normalized rows of 576 in 6.0 us
 // (3.1 TB/s: two and a quarter waves of one trip each), 32768 in 20.6 us, 32
-// in 2.3 us.  Warps that stride over the rows and request the next one early
-// need registers of a CTA per SM and are slower up to 8191 rows (6.7 us).
+// in 2.3 us; half pairs, whose partner chunks are loaded a second time, 7.9 us
+// for 8191 rows and 28.5 for 32768.  For many rows the instructions bound it
+// (~520 a row: the third of a row's three passes holds 8 chunks of 32, and the
+// angles take a pass of their own).  Warps that stride over the rows and request
+// the next one early need registers of a CTA per SM: 6.7 us at 8191 rows, 19.9
+// at 32768.
 template <int CPL, bool HALF>
 __global__ void __launch_bounds__(kWriteWarps * 32, HALF ? 4 : 6)
 latent_cache_write_kernel(const WriteArgs a) {
@@ -403,7 +409,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
 // requests (table, lengths) and of the token rows (positions, slots).  A
 // row's page is read from the entries the request already held, or straight
 // from the free list, never from an entry that another CTA writes.
-// Bound by latency: two trips to memory (lengths, then page ids) and two
+// Bound by latency: two trips to memory (lengths, then page ids) and three
 // barriers.  Measured: 48 requests 3.7 us, 1000 requests with 20000 rows 6.2 us.
 __global__ void __launch_bounds__(kExtendThreads)
 extend_tables_kernel(const ExtendArgs a) {
