@@ -922,8 +922,8 @@ def run_decode_ops(args):
     """Times the library's call of every listed case of perf/operators.py and
     of a few more and prints one JSON line: `graph_us` per call in a CUDA graph
     of DECODE_GRAPH_CALLS calls (a quarter of that from 64 MB a call on) over
-    distinct inputs, L2 flushed before each replay and gigabytes of other
-    inputs between two visits of one (so nothing of it is found in L2),
+    distinct inputs, L2 flushed before each replay; an input that a graph visits
+    again has a gigabyte or more of others in between (so none is found in L2),
     `call_us` per call of an eager loop over the same inputs, `floor_us` from the bytes and operations
     that the case cannot do without, at the measured rates."""
     import importlib.util
