@@ -1,5 +1,6 @@
-"""Which requests of the paged latent attention are cut over workers: the
-workspace begins with each worker's first request and its first tile there."""
+"""Which requests of the paged latent attention are cut over workers (the
+workspace begins with each worker's first request and its first tile there),
+kept workspaces that are given back, and a lone row of the cache write."""
 
 import pytest
 import torch
@@ -62,3 +63,41 @@ def test_requests_of_about_a_workers_share_stay_whole():
 def test_a_long_request_among_short_ones_is_cut():
     inside, working = cuts([9000] + [100] * 20, 64)
     assert inside > 100
+
+
+def test_workspaces_may_be_released_between_calls():
+    """Given back while a call still runs, and between a capture and its
+    replays: the memory goes to later work of the same stream only."""
+    lens, H = [3000, 70, 900], 64
+    g = torch.Generator(device=DEV).manual_seed(2)
+    cache = torch.randn(70, 64, 576, generator=g, device=DEV).to(torch.bfloat16)
+    table = torch.randperm(70, generator=g, device=DEV)[:70].to(torch.int32).view(1, 70)[:, :47].expand(3, 47).contiguous()
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    q = torch.randn(3, H, 576, generator=g, device=DEV).to(torch.bfloat16)
+    want = dsnq.paged_latent_attention(q, cache, table, n, 512, 0.05)
+    junk = []
+    for _ in range(20):
+        got = dsnq.paged_latent_attention(q, cache, table, n, 512, 0.05)
+        dsnq.release_workspaces()
+        junk.append(torch.full((1 << 20,), float("nan"), device=DEV))        # may take the memory
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = dsnq.paged_latent_attention(q, cache, table, n, 512, 0.05)
+    dsnq.release_workspaces()
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert dsnq.debug_status() == 0
+
+
+def test_a_lone_row_of_a_buffer_with_an_odd_stride():
+    """One kv row of a buffer whose rows are 2113 apart: the stride is never used."""
+    row = torch.randn(1, 2113, device=DEV).to(torch.bfloat16)
+    cache = torch.zeros(2, 8, 576, dtype=torch.bfloat16, device=DEV)
+    i64 = lambda x: torch.tensor(x, device=DEV)
+    f = torch.zeros(0, dtype=torch.float64, device=DEV)
+    dsnq.latent_cache_write(row[:, 1536:2048], row[:, 2048:2112], i64([5]), i64([11]), f, cache)
+    assert torch.equal(cache[1, 3], row[0, 1536:2112]) and int((cache != 0).any(-1).sum()) == 1
+    assert dsnq.debug_status() == 0
