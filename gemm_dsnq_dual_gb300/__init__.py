@@ -13,6 +13,9 @@ kernels.  Output tensors are allocated here with torch when not supplied.
   head_rmsnorm_rope               -- per-head RMSNorm and rotary positions in one pass
   latent_cache_write              -- normalized, rotated latent rows into the paged cache
   paged_latent_attention          -- one new token per request over the paged latent cache
+  latent_cache_write_fp8, latent_cache_read_fp8 -- the cache in 8 bits: rows in, and back
+  paged_latent_attention_fp8      -- one new token per request over it
+  shared_prefix_latent_attention_fp8 -- the same behind a prefix that all requests share
 
 Method: vLLM PR #53540 (fused_qk_rmsnorm_group_quant feeding
 apply_pre_quantized_block_scaled_mm for the attention and indexer wq_b) and
@@ -45,6 +48,8 @@ __all__ = [
     "fused_norm_quant_gemm_dual",
     "ROPE_INTERLEAVED", "ROPE_HALF", "rope_frequencies", "extend_block_tables", "head_rmsnorm_rope",
     "latent_cache_write", "paged_latent_attention", "paged_latent_attention_workspace_bytes",
+    "latent_cache_write_fp8", "latent_cache_read_fp8", "paged_latent_attention_fp8", "paged_latent_attention_fp8_workspace_bytes",
+    "shared_prefix_latent_attention_fp8", "shared_prefix_latent_attention_fp8_workspace_bytes",
     "release_workspaces",
     "quant_output_sizes", "debug_status", "debug_set", "set_launch_overlap", "scale_layout_of", "scale_ld_for",
     "empty_scales",
@@ -361,7 +366,7 @@ def fused_norm_quant_gemm_dual(q, kv, gamma_q, gamma_kv, eps, w1_fp8, w1_scale, 
     return out1, out2, kv_out, q_fp8, q_scale
 
 
-_BF16, _F32, _F64, _I32, _I64 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.int64
+_BF16, _F32, _F64, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.int64, torch.uint8
 
 
 def _refuse(t, name: str, dtype, dim: int, dev, why: str):
@@ -445,9 +450,10 @@ def _workspace(size: int, dev, stream, handle: int):
 
 
 def release_workspaces() -> None:
-    """Gives the workspaces that paged_latent_attention keeps for the calling
-    thread (up to 42 MB for each of four streams of a device) back to torch's
-    allocator.  Calls still running may go on using theirs: the memory goes to
+    """Gives the workspaces that the attention calls keep for the calling thread
+    (one for each of four streams of a device: up to 42 MB after
+    paged_latent_attention, more after shared_prefix_latent_attention_fp8) back
+    to torch's allocator.  Calls still running may go on using theirs: the memory goes to
     later work of the same stream only."""
     _kept.__dict__.clear()
 
@@ -612,6 +618,146 @@ def paged_latent_attention(q, cache, block_table, seq_lens, v_dim: int, scale: f
         _vec(seq_lens, "seq_lens", _I32, B, dev), float(scale), op, ot, oh, lp, ldl,
         _vec(workspace, "workspace", torch.uint8, size, dev), size, handle), "dsnq_paged_latent_attention")
     return out, lse
+
+
+def _cache_fp8(cache, scales, dev):
+    """(pages, page size, row bytes, page and row strides, address; stride and
+    address of the scales) of a cache in 8 bits."""
+    pages, page_size, W, ld_page, ld_row, cp = _cube(cache, "cache", _U8, dev)
+    sp, ss, lds, scp = _mat(scales, "scales", _F32, dev)
+    if sp != pages or ss != page_size:
+        raise ValueError(f"scales has shape {tuple(scales.shape)}, expected {(pages, page_size)}")
+    return pages, page_size, W, ld_page, ld_row, cp, lds, scp
+
+
+def latent_cache_write_fp8(kv, pe, positions, slots, inv_freq, cache, scales, gamma=None, eps: float = 1e-6, normalize: bool = False,
+                           rope_offset=None, layout="interleaved", rope_scale: float = 1.0, stream=None):
+    """latent_cache_write into a cache in 8 bits: uint8 [pages, page_size, K +
+    2 P], of each row K e4m3 codes and P bf16 position columns, and fp32 scales
+    [pages, page_size] by which both are multiplied.  The scale is the rotated
+    latent's largest magnitude / 448 (at least 2^-60).  K a multiple of 16.
+    Returns (cache, scales)."""
+    dev = kv.device
+    M, K, ldkv, kvp = _mat(kv, "kv", _BF16, dev)
+    P = ldpe = 0
+    pep = None
+    if pe is not None:
+        rows, P, ldpe, pep = _mat(pe, "pe", _BF16, dev)
+        if rows != M:
+            raise ValueError(f"pe has {rows} rows, kv {M}")
+    pages, page_size, W, ld_page, ld_row, cp, lds, scp = _cache_fp8(cache, scales, dev)
+    if W != K + 2 * P:
+        raise ValueError(f"cache rows have {W} bytes, kv and pe make {K + 2 * P}")
+    pairs = inv_freq.shape[0]
+    check(lib().dsnq_latent_cache_write_fp8(
+        M, K, P, kvp, ldkv, pep, ldpe, 1 if normalize else 0, None if gamma is None else _vec(gamma, "gamma", _BF16, K, dev),
+        float(eps), _vec(positions, "positions", _I64, M, dev), _vec(inv_freq, "inv_freq", _F64, pairs, dev),
+        K + P - 2 * pairs if rope_offset is None else rope_offset, 2 * pairs, _rope_layout(layout), float(rope_scale),
+        _vec(slots, "slots", _I64, M, dev), cp, pages, page_size, ld_page, ld_row, scp, lds, _stream(stream, dev)),
+        "dsnq_latent_cache_write_fp8")
+    return cache, scales
+
+
+def latent_cache_read_fp8(cache, scales, latent_dim: int, block_table, row_starts, rows: int, first=None, out=None, stream=None):
+    """Reads tokens of a cache in 8 bits (latent_cache_write_fp8; K =
+    latent_dim) back as bf16 rows [rows, K + P], request after request: row r of
+    [row_starts[b], row_starts[b + 1]) (int32 [B + 1]) is token first[b] + r -
+    row_starts[b] (int32 [B]; None: 0) of request b of block_table [B, width]
+    (int32).  Rows from row_starts[B] on are left as they were.  Returns out."""
+    dev = cache.device
+    pages, page_size, W, ld_page, ld_row, cp, lds, scp = _cache_fp8(cache, scales, dev)
+    P = (W - latent_dim) // 2
+    if latent_dim <= 0 or latent_dim + 2 * P != W or P < 0:
+        raise ValueError(f"cache rows of {W} bytes do not hold {latent_dim} codes and bf16 position columns")
+    B, width, ldt, table = _mat(block_table, "block_table", _I32, dev)
+    if out is None:
+        out = _new((rows, latent_dim + P), _BF16, dev, stream)
+    oR, oW, ldo, op = _mat(out, "out", _BF16, dev)
+    if oR != rows or oW != latent_dim + P:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(rows, latent_dim + P)}")
+    check(lib().dsnq_latent_cache_read_fp8(
+        B, rows, latent_dim, P, cp, pages, page_size, ld_page, ld_row, scp, lds, table, width, ldt,
+        _vec(row_starts, "row_starts", _I32, B + 1, dev), None if first is None else _vec(first, "first", _I32, B, dev), op, ldo,
+        _stream(stream, dev)), "dsnq_latent_cache_read_fp8")
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def paged_latent_attention_fp8_workspace_bytes(B: int, H: int, v_dim: int, table_width: int, page_size: int) -> int:
+    """Bytes of paged_latent_attention_fp8's workspace (host-only query)."""
+    n = C.c_int64()
+    check(lib().dsnq_paged_latent_attention_fp8_workspace_bytes(B, H, v_dim, table_width, page_size, C.byref(n)),
+          "dsnq_paged_latent_attention_fp8_workspace_bytes")
+    return n.value
+
+
+@functools.lru_cache(maxsize=256)
+def shared_prefix_latent_attention_fp8_workspace_bytes(B: int, H: int, v_dim: int, prefix_width: int, table_width: int,
+                                                       page_size: int) -> int:
+    """Bytes of shared_prefix_latent_attention_fp8's workspace (host-only query)."""
+    n = C.c_int64()
+    check(lib().dsnq_shared_prefix_latent_attention_fp8_workspace_bytes(B, H, v_dim, prefix_width, table_width, page_size, C.byref(n)),
+          "dsnq_shared_prefix_latent_attention_fp8_workspace_bytes")
+    return n.value
+
+
+def _attention_fp8(q, cache, scales, prefix_table, prefix_len, block_table, seq_lens, v_dim, scale, out, lse, workspace, stream):
+    dev = q.device
+    B, H, DK, qt, qh, qp = _cube(q, "q", _BF16, dev)
+    pages, page_size, W, ld_page, ld_row, cp, lds, scp = _cache_fp8(cache, scales, dev)
+    P, K = W - DK, 2 * DK - W
+    if P < 0 or K <= 0:
+        raise ValueError(f"cache rows of {W} bytes do not fit q's {DK} columns")
+    tb, width, ldt, table = _mat(block_table, "block_table", _I32, dev)
+    if tb != B:
+        raise ValueError(f"block_table has {tb} rows for {B} requests")
+    if out is None:
+        out = _new((B, H, v_dim), _BF16, dev, stream)
+    oB, oH, oD, ot, oh, op = _cube(out, "out", _BF16, dev)
+    if oB != B or oH != H or oD != v_dim:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(B, H, v_dim)}")
+    if lse is None:
+        lse = _new((B, H), _F32, dev, stream)
+    lB, lH, ldl, lp = _mat(lse, "lse", _F32, dev)
+    if lB != B or lH != H:
+        raise ValueError(f"lse has shape {tuple(lse.shape)}, expected {(B, H)}")
+    handle = _stream(stream, dev)
+    lens = _vec(seq_lens, "seq_lens", _I32, B, dev)
+    if prefix_table is None:
+        front, entry = (), "dsnq_paged_latent_attention_fp8"
+    else:
+        pw = prefix_table.shape[0] if prefix_table.dim() else 0
+        front = (_vec(prefix_table, "prefix_table", _I32, pw, dev), pw, _vec(prefix_len, "prefix_len", _I32, 1, dev))
+        entry = "dsnq_shared_prefix_latent_attention_fp8"
+    if workspace is None:
+        size = (shared_prefix_latent_attention_fp8_workspace_bytes(B, H, v_dim, pw, width, page_size) if front else
+                paged_latent_attention_fp8_workspace_bytes(B, H, v_dim, width, page_size))
+        workspace = _workspace(size, dev, stream, handle)
+    size = workspace.numel()
+    check(getattr(lib(), entry)(
+        B, H, K, P, v_dim, qp, qt, qh, cp, pages, page_size, ld_page, ld_row, scp, lds, *front, table, width, ldt, lens, float(scale),
+        op, ot, oh, lp, ldl, _vec(workspace, "workspace", _U8, size, dev), size, handle), entry)
+    return out, lse
+
+
+def paged_latent_attention_fp8(q, cache, scales, block_table, seq_lens, v_dim: int, scale: float, out=None, lse=None, workspace=None,
+                               stream=None):
+    """paged_latent_attention over a cache in 8 bits (latent_cache_write_fp8):
+    uint8 [pages, page_size, K + 2 P] and fp32 scales [pages, page_size], q
+    [B,H,K+P]; K a multiple of 128 up to 512, P 0 or 64, v_dim a multiple of 128
+    up to K.  Returns (out [B,H,v_dim] bf16, lse [B,H] fp32).  The workspace is
+    handled as in paged_latent_attention."""
+    return _attention_fp8(q, cache, scales, None, None, block_table, seq_lens, v_dim, scale, out, lse, workspace, stream)
+
+
+def shared_prefix_latent_attention_fp8(q, cache, scales, prefix_table, prefix_len, block_table, seq_lens, v_dim: int, scale: float,
+                                       out=None, lse=None, workspace=None, stream=None):
+    """paged_latent_attention_fp8 for requests that all begin with the first
+    prefix_len (int32 [1]) tokens of prefix_table [width] (int32 page ids), each
+    followed by seq_lens[b] tokens of its own row of block_table.  The prefix is
+    read and multiplied once for every 64 (request, head) pairs of the batch.
+    The workspace grows with the batch (about 8 v_dim bytes a pair)."""
+    return _attention_fp8(q, cache, scales, prefix_table, prefix_len, block_table, seq_lens, v_dim, scale, out, lse, workspace, stream)
 
 
 def debug_status(stream=None) -> int:

@@ -73,6 +73,19 @@ SIGNATURES = {
     "dsnq_paged_latent_attention": (
         i32, [i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, i64, i64, vp, i64, i64, vp, f32,
               vp, i64, i64, vp, i64, vp, i64, vp]),
+    "dsnq_latent_cache_write_fp8": (
+        i32, [i64, i64, i64, vp, i64, vp, i64, i32, vp, f32, vp, vp, i64, i64, i32, f32,
+              vp, vp, i64, i64, i64, i64, vp, i64, vp]),
+    "dsnq_latent_cache_read_fp8": (
+        i32, [i64, i64, i64, i64, vp, i64, i64, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, vp]),
+    "dsnq_paged_latent_attention_fp8_workspace_bytes": (i32, [i64, i64, i64, i64, i64, pi64]),
+    "dsnq_shared_prefix_latent_attention_fp8_workspace_bytes": (i32, [i64, i64, i64, i64, i64, i64, pi64]),
+    "dsnq_paged_latent_attention_fp8": (
+        i32, [i64, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, i64, i64, vp, i64, vp, i64, i64, vp, f32,
+              vp, i64, i64, vp, i64, vp, i64, vp]),
+    "dsnq_shared_prefix_latent_attention_fp8": (
+        i32, [i64, i64, i64, i64, i64, vp, i64, i64, vp, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, i64, i64, vp, f32,
+              vp, i64, i64, vp, i64, vp, i64, vp]),
     "dsnq_debug_status": (i32, [vp]),
     "dsnq_debug_build": (i32, []),
     "dsnq_debug_set": (None, [u32, u64]),

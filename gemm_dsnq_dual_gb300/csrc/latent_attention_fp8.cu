@@ -1,0 +1,1500 @@
+// Attention of one new token per request over a paged latent cache held in 8
+// bits, and the same for a batch whose requests begin with the same tokens.
+//
+//   row j of the cache: s_j (codes_j | pe_j), codes e4m3, pe bf16, s_j fp32
+//   out[b, h, :] = sum_j p_j s_j codes_j[0:DV],  p = softmax_j(scale * s_j q[b, h] . (codes_j | pe_j))
+//
+// The codes go to the tensor cores as they are; nothing is widened to 16 bits,
+// neither in memory nor in shared memory, so a row costs its 8-bit bytes on the
+// way in and in every read of it by a product.  What multiplies them is split
+// instead, into two e4m3 numbers, x = hi + lo / 32, hi = e4m3(x), lo =
+// e4m3(32 (x - hi)): eight significant bits, as many as bf16 has.
+//   q: divided by a power of two per head (exact) so that it is below 256; hi and
+//      lo then hold a bf16 exactly down to 2^-7 (hi's last bit is 2^-9 there, lo's
+//      2^-14), that is to 2^-15 of the head's largest; what is smaller is off by
+//      at most 2^-15, 2^-23 of the largest.  hi and lo are stacked along N, so a
+//      product reads a tile of the cache once.
+//   p s: x = p_j s_j 2^-T with T a power of two per head and block of 32 tokens
+//      such that the block's largest x lies in (128, 256]; the products put 2^T
+//      back (block scales along K).  Rounded by at most 2^-8 of x (2^-4 of hi's
+//      remainder, which is at most 2^-4 of x) or 2^-15 (half of lo's last bit),
+//      less than 2^-22 of the block's largest.
+// The position columns are a bf16 product into the same accumulators.  Scores,
+// softmax statistics and outputs are fp32.  The outputs are divided by the sum
+// of the p that the rounded x stand for, so that the weights add up to one
+// (those with x below 2^-6 count unrounded: a token whose scale is far below its
+// neighbours' may have a large p and no value to speak of).
+//
+// One CTA, 64 heads, tiles of 128 tokens:
+//   S^T [128 tokens x (64 hi | 64 lo)]  = C Q^T        M = 128: a thread has a token
+//   O^T [DV x 64 heads]                += C^T (p s)^T   M = 128, block-scaled; C^T is the
+//                                                       same tile read column-major
+// TMEM: O^T takes DV/128 x 64 columns, S^T 128, the block scales 8.  Measured
+// alone on an SM, one product of S^T takes 69 cycles at 64 heads (52 at 16) and
+// one of O^T 52 (45): 2900 cycles a tile at 64 heads and 576 columns, where the
+// copy of a tile takes 3600 at this GPU's share of HBM per SM.
+//
+// Work split: jobs (a request, or 64 rows of the whole batch against the common
+// prefix) are laid end to end as tiles and cut into equal runs, one per worker
+// (one CTA per group of 64 heads), on the device, from the lengths.  A run that
+// covers a whole request writes its output; otherwise, and for all jobs of a
+// batch with a common prefix, (max, sum, output times that sum) go to the
+// workspace in fp32, and a second kernel joins them in the order of the tokens
+// (no atomics: results do not depend on timing).
+// The prefix: its rows are the (request, head) pairs of the batch laid end to
+// end, so every tile of the prefix serves 64 rows whatever the number of heads.
+//
+// Warps: 0 copies tiles (TMA), 1 issues S^T, 2 issues O^T, 4..11 do the softmax:
+// warp w has tokens 32 (w % 4) .. of a tile (the TMEM lanes it can reach, and one
+// block of 32 of the scales) and one half of the heads.  They also split q, for
+// the next job while the last product of this one runs, and write the output.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "debug_check.cuh"
+#include "group_quant.cuh"
+#include "dsnq_internal.h"
+#include "latent_tiles.cuh"
+#include "tensor_host.h"
+#include "tensor_ptx.cuh"
+
+namespace dsnq {
+namespace attn8 {
+
+using namespace attn;
+
+constexpr int kHeads = 64;                  // rows (heads) of a CTA
+constexpr int kTile = 128;                  // tokens of a tile
+constexpr int kChunkBytes = kTile * 128;    // 128 bytes of each row of a tile
+constexpr int kThreads = 384;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSoftWarp0 = 4, kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
+constexpr int kMaxSlots = 13;               // slots of the ring of chunks
+constexpr int kScaleSlots = 4;              // tiles whose row scales are kept; the ring holds at most three tiles
+constexpr int kMaxCtas = 160;               // bound of workers x head groups
+constexpr int kTmemCols = 512;
+constexpr int kTmemS = 256;                 // first column of S^T
+constexpr int kTmemSfa = 384, kTmemSfb = 388;   // block scales of C^T (ones) and of p s
+constexpr float kRaise = 32.0f;             // log2 by which a block may exceed the reference before O is rescaled
+constexpr float kLeastScale = 0x1p-60f;
+constexpr int kMiscBytes = 7168;
+constexpr int kPBytes = kTile * 64;         // hi (or lo) of p s of a tile: 64 bytes a token
+constexpr int kManyParts = 4;               // workers per job from which a CTA joins an item
+
+struct Params {
+    const __nv_bfloat16* q;
+    int64_t ldq_b, ldq_h;
+    const float* scales;
+    int64_t ld_scale;                 // of a page
+    const int32_t* seq_lens;
+    const int32_t* table;
+    int64_t ld_table;
+    const int32_t* prefix_table;
+    const int32_t* prefix_len;        // NULL: no common prefix
+    int B, H, G, W;                   // requests, heads, head groups, workers
+    int W_full;                       // workers that the GPU has room for, whatever the tables hold
+    int HR;                           // rows of a request against the prefix: heads, a multiple of 4
+    int R, NP;                        // rows against the prefix; jobs of them (G groups of 64 rows each)
+    int width, prefix_width, page_size, box_rows, num_pages;   // box_rows: tokens of one copy
+    int64_t cap, prefix_cap;          // tokens the tables can hold
+    int cc, pe, nblk;                 // 128-code chunks of a row, position chunk, 128-column blocks of the value
+    int q_rows;                       // rows of hi (and of lo) that a chunk of q has room for
+    int slots, twin;                  // slots of the ring; 1: position columns share a slot with the last codes
+    float scale_log2;
+    __nv_bfloat16* out;
+    int64_t ldo_b, ldo_h;
+    float* lse;                       // NULL: not written
+    int64_t ldl_b;
+    int2* meta;                       // [W] first job of the worker and its first tile there
+    float2* part_ml;                  // [part][64] (reference in log2 units, sum)
+    float* part_o;                    // [part][nblk][16][128][4]: value block, four heads, value, head
+    uint64_t timeout_ns;
+    uint32_t inject;
+};
+
+__device__ __forceinline__ int clamp_len(int64_t cap, int32_t n) {
+    return n < 0 ? 0 : (n > cap ? static_cast<int>(cap) : n);
+}
+// Tiles of a request; an empty one counts as one (somebody writes its zeros).
+__device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len + kTile - 1) / kTile : 1; }
+
+// Place of the part that worker w leaves of job j in the workspace.  With a
+// prefix every job leaves its parts: along the runs j + w grows from part to
+// part.  Otherwise only the first and the last job of a run can be cut.
+__device__ __forceinline__ int64_t part_slot(const Params& p, int w, int j, bool first, int g) {
+    return (p.prefix_len ? static_cast<int64_t>(j) + w : static_cast<int64_t>(w) * 2 + (first ? 0 : 1)) * p.G + g;
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t chunk, int32_t group,
+                                            int32_t page, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(chunk), "r"(group), "r"(page), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// Instruction descriptors: D fp32, M = 128.  e4m3 x e4m3, both K-major; bf16 x
+// bf16; and block-scaled e4m3 x e4m3 with both operands column-major, scales as
+// powers of two, `block` the byte of B's scale words that holds this block's.
+__device__ __forceinline__ uint32_t idesc_s(int n) { return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24); }
+__device__ __forceinline__ uint32_t idesc_pe(int n) { return idesc_s(n) | (1u << 7) | (1u << 10); }
+__device__ __forceinline__ uint32_t idesc_o(int n) {
+    return (1u << 15) | (1u << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (8u << 24);
+}
+
+// Four steps of D (+)= A B^T along the 128 bytes of a chunk's rows, issued by
+// one elected lane; the first overwrites D when !accumulate.
+#define DSNQ_MMA4(KIND)                                                                                                \
+    asm volatile(                                                                                                      \
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b;\n\t"                                                              \
+        "setp.ne.b32 p, %4, 0;\n\t"                                                                                    \
+        "setp.eq.b32 t, 0, 0;\n\t"                                                                                     \
+        "elect.sync _|e, 0xffffffff;\n\t"                                                                              \
+        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], %1, %2, %3, p;\n\t"                                          \
+        "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"                                                                   \
+        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, t;\n\t"                                            \
+        "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"                                                                   \
+        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, t;\n\t"                                            \
+        "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"                                                                   \
+        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),                            \
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)                                                          \
+        : "memory")
+__device__ __forceinline__ void tc_mma4_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    DSNQ_MMA4("f8f6f4");
+}
+__device__ __forceinline__ void tc_mma4_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    DSNQ_MMA4("f16");
+}
+#undef DSNQ_MMA4
+
+// O^T (+)= C^T (p s)^T of one chunk of codes: four blocks of 32 tokens (4 KB of
+// the tile, 2 KB of p s apart), of each the product with hi and the one with
+// lo (8 KB on), whose scales lie two columns on.
+__device__ __forceinline__ void tc_mma8_scaled(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                               uint32_t sfb, uint32_t accumulate) {
+#define DSNQ_MX "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+#define DSNQ_STEP(A, B, BL, ID)                                                                                        \
+    "add.u64 a, %1, " A ";\n\tadd.u64 b, %2, " B ";\n\tadd.u64 l, %2, " BL ";\n\tadd.u32 i, %3, " ID ";\n\t"            \
+    DSNQ_MX "[%0], a, b, i, [%4], [%5], t;\n\t" DSNQ_MX "[%0], a, l, i, [%4], [%6], t;\n\t"
+    asm volatile(
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b, l;\n\t.reg .b32 i;\n\t"
+        "setp.ne.b32 p, %7, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "add.u64 l, %2, 512;\n\t"
+        DSNQ_MX "[%0], %1, %2, %3, [%4], [%5], p;\n\t"
+        DSNQ_MX "[%0], %1, l, %3, [%4], [%6], t;\n\t"
+        DSNQ_STEP("256", "128", "640", "16")
+        DSNQ_STEP("512", "256", "768", "32")
+        DSNQ_STEP("768", "384", "896", "48")
+        "}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(sfb + 2), "r"(accumulate)
+        : "memory");
+#undef DSNQ_STEP
+#undef DSNQ_MX
+}
+
+// 512 bytes of block scales into four TMEM columns of all lane quarters.
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(desc)
+        : "memory");
+}
+
+// Descriptors: p s with its 64-byte rows (64-byte swizzle, eight rows 512 bytes
+// on), and the scales as rows of 16 bytes (no swizzle).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t swizzle) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | static_cast<uint64_t>((lead >> 4) & 0x3FFF) << 16 |
+           static_cast<uint64_t>((stride >> 4) & 0x3FFF) << 32 | static_cast<uint64_t>(1) << 46 |
+           static_cast<uint64_t>(swizzle) << 61;
+}
+
+__device__ __forceinline__ void tmem_ld8_issue(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld8_wait(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// hi = e4m3(x), lo = e4m3(32 (x - hi)) of two numbers (|x| <= 256: x - hi is
+// exact and at most 8); `sum` gets hi + lo / 32.
+__device__ __forceinline__ uint32_t e4m3x2_of(__half2 x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+    return r;
+}
+__device__ __forceinline__ __half2 half2_of(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+    return *reinterpret_cast<const __half2*>(&r);
+}
+__device__ __forceinline__ void split2(__half2 x, uint32_t& hi, uint32_t& lo, __half2& sum) {
+    hi = e4m3x2_of(x);
+    const __half2 h = half2_of(hi);
+    lo = e4m3x2_of(__hmul2(__hsub2(x, h), __float2half2_rn(32.f)));
+    sum = __hfma2(half2_of(lo), __float2half2_rn(0.03125f), h);
+}
+
+// Barrier of the softmax warps; returns whether any thread passed true.  A
+// named barrier has no time limit, so every softmax warp reaches every one of
+// them whether or not its waits succeeded (the counts depend on the run alone).
+__device__ __forceinline__ bool soft_sync_or(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return r != 0;
+}
+
+// Where the chunks of the worker's n-th tile lie: chunk c of a tile is its first
+// codes (c = 0), its position columns (c = 1, if any), its other codes.  They go
+// around the ring one after the other; S^T of a tile needs all of them while
+// the codes of the tile before wait for its product with p s, so there must be
+// room for two tiles.  With 512 codes, position columns and more than 32 heads
+// there is not, by one slot: there (`twin`) a tile has four slots, and the last
+// codes follow the position columns, which S^T is done with early, in one slot.
+struct Chunks {
+    int i = 0;
+    uint32_t pass = 0, n = 0;
+    __device__ __forceinline__ void at(const Params& p, int c, int& slot, uint32_t& parity) const {
+        if (p.twin) {
+            const int pos = c == 4 ? 1 : c;
+            slot = static_cast<int>(n & 1) * 4 + pos;
+            parity = pos == 1 ? (c == 4) : (n >> 1) & 1;
+            return;
+        }
+        slot = i + c;
+        parity = pass;
+        if (slot >= p.slots) {
+            slot -= p.slots;
+            parity ^= 1;
+        }
+    }
+    __device__ __forceinline__ void next(const Params& p) {
+        ++n;
+        if (p.twin) return;
+        i += p.cc + p.pe;
+        if (i >= p.slots) {
+            i -= p.slots;
+            pass ^= 1;
+        }
+    }
+};
+
+// A worker's run of tiles, job by job: from tile t0 of job j up to (not
+// including) tile t_end of job j_end.  Jobs below NP are rows against the
+// prefix, job NP + b is request b.
+struct Run {
+    int j, t0, j_end, t_end;
+    int plen;                         // tokens of the prefix
+    int32_t ahead;                    // seq_lens of the next request: a trip to memory ahead of its use
+    int len, tiles, n;                // of the current job: tokens, tiles, tiles of this run
+    int count, hp;                    // its rows in this CTA, and their number up to a multiple of 16
+    __device__ __forceinline__ bool next(const Params& p, int g) {
+        if (j > j_end || (j == j_end && t0 >= t_end)) return false;
+        const bool prefix = j < p.NP;
+        len = prefix ? plen : clamp_len(p.cap, ahead);
+        if (j + 1 >= p.NP && j + 1 < p.NP + p.B) ahead = p.seq_lens[j + 1 - p.NP];
+        tiles = tiles_of(len);
+        n = (j == j_end ? t_end : tiles) - t0;
+        const int rows = prefix ? p.R - (j * p.G + g) * kHeads : p.H - g * kHeads;
+        count = max(0, min(kHeads, rows));
+        hp = (count + 15) & ~15;
+        return true;
+    }
+    __device__ __forceinline__ bool live() const { return len > 0 && count > 0; }
+    __device__ __forceinline__ void advance() {
+        ++j;
+        t0 = 0;
+    }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int q_chunk = 2 * p.q_rows * 128;                // bytes of a code chunk of q: hi, then lo
+    const int cpt = p.cc + p.pe;                           // chunks of a tile
+    uint8_t* q_s = smem;                                   // [cc][2 q_rows][128 B]
+    uint8_t* qpe_s = q_s + p.cc * q_chunk;                 // [pe][q_rows][128 B]
+    uint8_t* p_s = qpe_s + p.pe * p.q_rows * 128;          // hi, lo: [128 tokens][64 B]
+    uint8_t* ring = p_s + 2 * kPBytes;                     // [slots][128 tokens][128 B]
+    uint8_t* misc = ring + p.slots * kChunkBytes;
+    uint8_t* sf_s = misc;                                  // [32][16 B] block scales of p s
+    float* sc_s = reinterpret_cast<float*>(sf_s + 512);    // [kScaleSlots][128] row scales
+    float* cq_s = sc_s + kScaleSlots * kTile;              // [2][64] factor of a head's scores
+    float* bc_s = cq_s + 2 * kHeads;                       // [8 warps][32]{T, 2^(T - M)}; at a job's end [2 halves][4][32]{l, lr}
+    float* mx_s = bc_s + kSoftWarps * 64;                  // [2 halves][4][32]
+    float* al_s = mx_s + kSoftWarps * 32;                  // [64] factors of O
+    uint64_t* full = reinterpret_cast<uint64_t*>(al_s + kHeads);   // [kMaxSlots]
+    uint64_t* empty = full + kMaxSlots;                    // [kMaxSlots]
+    uint64_t* qfull = empty + kMaxSlots;
+    uint64_t* sfull = qfull + 1;
+    uint64_t* sempty = sfull + 1;
+    uint64_t* pfull = sempty + 1;
+    uint64_t* pempty = pfull + 1;
+    uint64_t* drain = pempty + 1;                          // [2] abort: products already issued
+    int64_t* sums = reinterpret_cast<int64_t*>(drain + 2); // [kWarps]
+    int* longest = reinterpret_cast<int*>(sums + kWarps);  // [kWarps]
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(longest + kWarps);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    int* run_s = reinterpret_cast<int*>(tmem_holder + 2);  // [4] first job and tile, end job and tile
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = blockIdx.x / p.G, g = blockIdx.x - w * p.G;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMaxSlots; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(qfull), kSoftWarps);
+        mbar_init(smem_u32(sfull), 1);
+        mbar_init(smem_u32(sempty), kSoftWarps);
+        mbar_init(smem_u32(pfull), kSoftWarps);
+        mbar_init(smem_u32(pempty), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&drain[i]), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch_desc(&map_c);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    grid_dependency_wait();
+    allow_dependent_launch();
+    bounds_self_test(p.inject);
+
+    // The worker's run.  Each job counts `lead` units (what it costs beside its
+    // tiles: queries, pipeline fill, output), then one per tile; worker w takes
+    // units [w U / workers, (w + 1) U / workers), and a cut among a job's
+    // leading units is a cut before its first tile.  Thread t sums requests
+    // [t * per, (t + 1) * per); the jobs against the prefix come first.
+    const int plen = p.prefix_len ? clamp_len(p.prefix_cap, *p.prefix_len) : 0;
+    {
+        const int per = (p.B + kThreads - 1) / kThreads;
+        const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
+        int64_t mine = 0;
+        int most = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int t = tiles_of(clamp_len(p.cap, p.seq_lens[b]));
+            mine += t;
+            most = max(most, t);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        int64_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (lane == 31) {
+            sums[warp] = inc;
+            longest[warp] = most;
+        }
+        __syncthreads();
+        int64_t before = inc - mine, tiles = 0;
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) before += sums[i];
+            tiles += sums[i];
+            most = max(most, longest[i]);
+        }
+        const int ptiles = plen > 0 ? tiles_of(plen) : 0, pjobs = plen > 0 ? p.NP : 0;
+        tiles += static_cast<int64_t>(pjobs) * ptiles;
+        // Requests a little longer than a worker's share go one to a worker, uncut.
+        const int h = min(p.H, kHeads), joined = 5 * p.B * h / (16 * p.W_full);
+        const int slack = max(1, p.W < kManyParts * p.B ? min(joined, 2 + h / 64) : joined);
+        const bool uncut = !p.prefix_len && p.B <= p.W && most <= (tiles + p.W - 1) / p.W + slack;
+        const int lead = tiles >= p.W ? 1 : 0;
+        const int64_t front = static_cast<int64_t>(pjobs) * (lead + ptiles);   // units of the prefix
+        const int64_t total = tiles + static_cast<int64_t>(lead) * (p.B + pjobs);
+        before += front + static_cast<int64_t>(lead) * b0;
+        mine += static_cast<int64_t>(lead) * (b1 - b0);
+        const int64_t workers = total < p.W ? total : p.W;
+        if (uncut && threadIdx.x < 2) {
+            run_s[2 * threadIdx.x] = p.NP + min(w + static_cast<int>(threadIdx.x), p.B);
+            run_s[2 * threadIdx.x + 1] = 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 2 && !uncut; ++e) {
+            const int64_t u = w + e < workers ? (w + e) * total / workers : total;
+            if (threadIdx.x == 0) {
+                if (u == total) {
+                    run_s[2 * e] = p.NP + p.B;
+                    run_s[2 * e + 1] = 0;
+                } else if (u < front) {
+                    const int j = static_cast<int>(u / (lead + ptiles));
+                    run_s[2 * e] = j;
+                    run_s[2 * e + 1] = max(static_cast<int>(u - static_cast<int64_t>(j) * (lead + ptiles)) - lead, 0);
+                }
+            }
+            if (u >= before && u < before + mine) {
+                int64_t at = before;
+                int b = b0, n = lead + tiles_of(clamp_len(p.cap, p.seq_lens[b]));
+                while (at + n <= u) {
+                    at += n;
+                    n = lead + tiles_of(clamp_len(p.cap, p.seq_lens[++b]));
+                }
+                run_s[2 * e] = p.NP + b;
+                run_s[2 * e + 1] = max(static_cast<int>(u - at) - lead, 0);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    if (warp >= kSoftWarp0 && warp < kSoftWarp0 + 4) {     // the scales of C^T are ones
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                         tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmemSfa),
+                     "r"(0x7f7f7f7f)
+                     : "memory");
+        tmem_wait_st();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint64_t tmo = p.timeout_ns;
+    Run run;
+    run.j = run_s[0];
+    run.t0 = run_s[1];
+    run.j_end = run_s[2];
+    run.t_end = run_s[3];
+    run.plen = plen;
+    run.ahead = 0;
+    if (run.j >= p.NP && run.j < p.NP + p.B) run.ahead = p.seq_lens[run.j - p.NP];
+    const int j_first = run.j;
+    if (threadIdx.x == 0 && g == 0) p.meta[w] = make_int2(run.j, run.t0);
+
+    // A whole warp's wait: all of its lanes go on or none (warp-wide
+    // instructions follow), and the compiler sees that it is so.
+    auto wait_uniform = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_bounded<true>(bar, parity, abort_flag, tmo));
+    };
+    // The same, asleep between polls: for the copying warp, which is ahead.
+    auto wait_uniform_asleep = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, tmo));
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------- TMA producer
+        // Chunks in the order of their use by S^T: the first codes (with the
+        // tile's row scales), the position columns, whose slot is free again
+        // when S^T is done with them, the other codes.  A request's tiles pass
+        // through L2 once, so they leave it first; the prefix's are read by
+        // every group of rows.
+        uint64_t once, again;
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+        asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(again));
+        const int pieces = kTile / p.box_rows;             // copies of a chunk (1, 2, 4, 8 or 16)
+        const int batch = 32 / pieces;                     // tiles whose table entries the lanes hold
+        Chunks ch;
+        bool ok = true, skip = (p.inject & kInjectSkipLoad) != 0;
+        for (; ok && run.next(p, g); run.advance()) {
+            if (!run.live()) continue;
+            const bool prefix = run.j < p.NP;
+            const int32_t* row = prefix ? p.prefix_table : p.table + (run.j - p.NP) * p.ld_table;
+            const int width = prefix ? p.prefix_width : p.width;
+            const uint64_t policy = prefix ? again : once;
+            int ids = 0;
+            for (int i = 0; ok && i < run.n; ++i, ch.next(p)) {
+                const int tile = run.t0 + i;
+                if (i % batch == 0) {
+                    const int64_t tok = static_cast<int64_t>(tile) * kTile + static_cast<int64_t>(lane) * p.box_rows;
+                    ids = 0;
+                    if (tok < run.len) {
+                        const int64_t e = tok / p.page_size;
+                        if (bounds_ok(e < width)) ids = row[e];
+                        if (ids < 0 || ids >= p.num_pages) {   // such pages read as zeros
+                            atomicOr(&g_status, kStatusBounds);
+                            ids = p.num_pages;
+                        }
+                    }
+                }
+                const int tok0 = tile * kTile;
+                const int live = min(pieces, (run.len - tok0 + p.box_rows - 1) / p.box_rows);
+                const int id = __shfl_sync(0xffffffffu, ids, (i % batch) * pieces + (lane & (pieces - 1)));
+                const int in_page = (tok0 + lane * p.box_rows) % p.page_size;
+                const unsigned good = __ballot_sync(0xffffffffu, lane < live && id < p.num_pages);
+                for (int c = 0; c < cpt; ++c) {
+                    const int chunk = c == 0 ? 0 : !p.pe ? c : c == 1 ? p.cc : c - 1;
+                    int slot;
+                    uint32_t parity;
+                    ch.at(p, c, slot, parity);
+                    ok = wait_uniform_asleep(smem_u32(&empty[slot]), parity ^ 1);
+                    if (!ok) break;
+                    const uint32_t fb = smem_u32(&full[slot]);
+                    if (!skip) {                           // test hook: the first chunk never comes, the waits on it run out
+                        float* sc = sc_s + (ch.n & (kScaleSlots - 1)) * kTile + lane * p.box_rows;
+                        if (c == 0 && lane < live && id >= p.num_pages)
+                            for (int k = 0; k < p.box_rows; ++k) sc[k] = 0.f;
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(fb, live * p.box_rows * 128 + (c == 0 ? __popc(good) * p.box_rows * 4 : 0));
+                        __syncwarp();
+                        if (lane < live) {
+                            tma_load_5d(smem_u32(ring) + slot * kChunkBytes + lane * p.box_rows * 128, &map_c, fb, chunk, in_page / 8, id,
+                                        policy);
+                            if (c == 0 && id < p.num_pages)
+                                bulk_load(smem_u32(sc), p.scales + static_cast<int64_t>(id) * p.ld_scale + in_page, p.box_rows * 4, fb,
+                                          policy);
+                        }
+                    }
+                    skip = false;
+                }
+            }
+        }
+        if (!ok) settle_ns(kAbortSettleNs);                // copies already issued land before the CTA goes
+    } else if (warp == 1) {
+        // ---------------------------------------------- products S^T = C Q^T
+        // Chunk by chunk as they land.
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(q_s), 16, 1024), pe_desc = smem_desc_sw128(smem_u32(qpe_s), 16, 1024);
+        const uint32_t d = tmem + kTmemS;
+        Chunks ch;
+        uint32_t nq = 0;
+        bool ok = true;
+        for (; ok && run.next(p, g); run.advance()) {
+            if (!run.live()) continue;
+            const uint32_t id_s = idesc_s(2 * run.hp), id_pe = idesc_pe(run.hp);
+            ok = wait_uniform(smem_u32(qfull), nq & 1);
+            ++nq;
+            for (int i = 0; ok && i < run.n; ++i, ch.next(p)) {
+                ok = wait_uniform(smem_u32(sempty), (ch.n & 1) ^ 1);
+                tc_fence_after();
+                for (int c = 0; ok && c < cpt; ++c) {
+                    int slot;
+                    uint32_t parity;
+                    ch.at(p, c, slot, parity);
+                    ok = wait_uniform(smem_u32(&full[slot]), parity);
+                    if (!ok) break;
+                    const uint64_t a = smem_desc_sw128(smem_u32(ring) + slot * kChunkBytes, 16, 1024);
+                    const int code = c == 0 || !p.pe ? c : c - 1;
+                    if (p.pe && c == 1) {
+                        tc_mma4_bf16(d, a, pe_desc, id_pe, 1);
+                        tc_commit(smem_u32(&empty[slot]));
+                    } else {
+                        tc_mma4_e4m3(d, a, q_desc + static_cast<uint32_t>(code * q_chunk >> 4), id_s, c > 0);
+                        if (code >= p.nblk) tc_commit(smem_u32(&empty[slot]));   // no part of the value
+                    }
+                }
+                if (!ok) break;
+                tc_commit(smem_u32(sfull));
+            }
+        }
+        if (!ok) {                                         // products already issued end before their memory goes
+            tc_commit(smem_u32(&drain[0]));
+            wait_drain(smem_u32(&drain[0]), 0, tmo);
+        }
+    } else if (warp == 2) {
+        // ----------------------------------------- products O^T += C^T (p s)^T
+        // They free the chunks one by one.
+        const uint64_t p_desc = smem_desc(smem_u32(p_s), kPBytes, 512, 4);
+        const uint64_t sf_desc = smem_desc(smem_u32(sf_s), 0, 128, 0);
+        Chunks ch;
+        bool ok = true;
+        for (; ok && run.next(p, g); run.advance()) {
+            if (!run.live()) continue;
+            const uint32_t id_o = idesc_o(run.hp);
+            for (int i = 0; i < run.n; ++i, ch.next(p)) {
+                ok = wait_uniform(smem_u32(pfull), ch.n & 1);
+                if (!ok) break;
+                tc_fence_after();
+                tc_copy_scales(tmem + kTmemSfb, sf_desc);
+                for (int c = 0; c < cpt; ++c) {
+                    const int code = c == 0 || !p.pe ? c : c - 1;
+                    if ((p.pe && c == 1) || code >= p.nblk) continue;
+                    int slot;
+                    uint32_t parity;
+                    ch.at(p, c, slot, parity);
+                    tc_mma8_scaled(tmem + code * kHeads, smem_desc_sw128(smem_u32(ring) + slot * kChunkBytes, kChunkBytes, 1024), p_desc,
+                                   id_o, tmem + kTmemSfa, tmem + kTmemSfb, i > 0);
+                    tc_commit(smem_u32(&empty[slot]));
+                }
+                tc_commit(smem_u32(pempty));
+            }
+        }
+        if (!ok) {
+            tc_commit(smem_u32(&drain[1]));
+            wait_drain(smem_u32(&drain[1]), 0, tmo);
+        }
+    } else if (warp >= kSoftWarp0) {
+        // ------------------------------------- softmax, splitting q, output
+        const int quad = warp & 3, sw = warp - kSoftWarp0, half = sw >> 2;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const int st = threadIdx.x - kSoftWarp0 * 32;      // 0..255
+        const float kNegInf = __int_as_float(0xff800000);
+        const int tok = quad * 32 + lane;                  // this thread's token of a tile
+        const int DV = p.nblk * 128;
+        float* bc = bc_s + sw * 64;
+        uint32_t n = 0, nq = 0;
+        Chunks ch;
+        bool ok = true;                                    // false: only the barriers are kept up
+
+        // Splits the queries of the job r into shared memory, and leaves the
+        // factors of their scores.  Warp sw takes rows sw, sw + 8, ...; a lane 16
+        // codes, lanes 0..7 also eight position columns.
+        auto split_q = [&](const Run& r, int buf) {
+            const bool prefix = r.j < p.NP;
+            const int row0 = prefix ? (r.j * p.G + g) * kHeads : g * kHeads;
+            constexpr int kAhead = 4;
+            for (int i0 = sw; i0 < r.hp; i0 += kAhead * kSoftWarps) {
+                uint4 x[kAhead][2], e[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u * kSoftWarps;
+                    x[u][0] = x[u][1] = e[u] = make_uint4(0, 0, 0, 0);
+                    int b = r.j - p.NP, h = row0 + i;
+                    if (prefix) {
+                        b = (row0 + i) / p.HR;
+                        h = row0 + i - b * p.HR;
+                    }
+                    if (i >= r.count || h >= p.H || !bounds_ok(b >= 0 && b < p.B)) continue;
+                    const __nv_bfloat16* src = p.q + b * p.ldq_b + h * p.ldq_h;
+                    if (lane * 16 < p.cc * 128) {
+                        x[u][0] = *reinterpret_cast<const uint4*>(src + lane * 16);
+                        x[u][1] = *reinterpret_cast<const uint4*>(src + lane * 16 + 8);
+                    }
+                    if (p.pe && lane < 8) e[u] = *reinterpret_cast<const uint4*>(src + p.cc * 128 + lane * 8);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u * kSoftWarps;
+                    if (i >= r.hp) break;
+                    // The largest magnitude, as the bits of a bf16 (infinities and NaN above all others).
+                    const uint32_t* xw = reinterpret_cast<const uint32_t*>(x[u]);
+                    const uint32_t* ew = reinterpret_cast<const uint32_t*>(&e[u]);
+                    uint32_t top = 0, etop = 0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = max(top, max(xw[k] & 0x7fff, (xw[k] >> 16) & 0x7fff));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) etop = max(etop, max(ew[k] & 0x7fff, (ew[k] >> 16) & 0x7fff));
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    if (p.pe) etop = __reduce_max_sync(0xffffffffu, etop);
+                    // 2^ex > largest / 256, so that 32 (x - hi) <= 256; and the position columns divided by it stay finite.
+                    int ex = static_cast<int>(top >> 7) - 127 - 7;
+                    ex = max(max(ex, -100), static_cast<int>(etop >> 7) - 127 - 100);
+                    const bool finite = max(top, etop) < 0x7f80;
+                    if (!finite) ex = 0;
+                    const float inv = __int_as_float((127 - ex) << 23);
+                    if (lane == 0)
+                        cq_s[buf * kHeads + i] = finite ? __int_as_float((127 + ex) << 23) * p.scale_log2 : __int_as_float(0x7fffffff);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t h0, h1, l0, l1;
+                        __half2 s;
+                        const uint32_t a = xw[2 * k], b = xw[2 * k + 1];
+                        split2(__floats2half2_rn(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv), h0, l0, s);
+                        split2(__floats2half2_rn(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv), h1, l1, s);
+                        hi[k] = h0 | h1 << 16;
+                        lo[k] = l0 | l1 << 16;
+                    }
+                    if (lane * 16 < p.cc * 128) {
+                        uint8_t* at = q_s + (lane >> 3) * q_chunk + (((lane & 7) ^ (i & 7)) << 4);
+                        *reinterpret_cast<uint4*>(at + i * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(at + (r.hp + i) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    if (p.pe && lane < 8) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = pack_bf16(__uint_as_float(ew[k] << 16) * inv, __uint_as_float(ew[k] & 0xffff0000u) * inv);
+                        *reinterpret_cast<uint4*>(qpe_s + i * 128 + ((lane ^ (i & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(qfull));
+        };
+        // The next job of the run that has tiles and rows, from r on.
+        auto seek = [&](Run& r) {
+            for (; r.next(p, g); r.advance())
+                if (r.live()) return true;
+            return false;
+        };
+        {
+            Run r = run;
+            if (seek(r)) split_q(r, 0);
+        }
+
+        for (; run.next(p, g); run.advance()) {
+            const int b = run.j - p.NP;
+            const bool whole = !p.prefix_len && run.t0 == 0 && run.n == run.tiles;
+            if (!run.live()) {
+                if (p.prefix_len || run.len > 0) continue; // no part; the join knows
+                // An empty request: zeros, and the logarithm of an empty sum.
+                for (int e = st; e < kHeads * (DV / 8); e += kSoftThreads) {
+                    const int h = g * kHeads + e / (DV / 8), c = e % (DV / 8);
+                    if (h < p.H && bounds_ok(b >= 0 && b < p.B))
+                        *reinterpret_cast<uint4*>(p.out + b * p.ldo_b + h * p.ldo_h + c * 8) = make_uint4(0, 0, 0, 0);
+                }
+                if (p.lse && st < kHeads && g * kHeads + st < p.H) p.lse[b * p.ldl_b + g * kHeads + st] = kNegInf;
+                continue;
+            }
+            const int ng = run.hp >> 4;                    // groups of eight heads of this half
+            const int h0 = half * 8 * ng;                  // its first head
+            const float* cq = cq_s + (nq & 1) * kHeads + h0;
+            float l[32], lr[32];                           // per head, this token's share of the sums of p: unrounded, rounded
+#pragma unroll
+            for (int k = 0; k < 32; ++k) l[k] = lr[k] = 0.f;
+            float M = 0.f;                                 // of head h0 + lane: what O and the sums are relative to (log2)
+            for (int i = 0; i < run.n; ++i, ++n, ch.next(p)) {
+                const int valid = min(kTile, run.len - (run.t0 + i) * kTile);
+                int slot0;
+                uint32_t parity0;
+                ch.at(p, 0, slot0, parity0);
+                ok = ok && wait_uniform(smem_u32(&full[slot0]), parity0);
+                const bool in = tok < valid;
+                const float sj = ok && in ? sc_s[(n & (kScaleSlots - 1)) * kTile + tok] : 1.f;
+                const float sl = fmaxf(sj, kLeastScale), lg = log2f(sl), inv_s = 1.0f / sl;
+                ok = ok && wait_uniform(smem_u32(sfull), n & 1);
+                tc_fence_after();
+                float z[32];                               // log2 of p s, up to the reference
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= ng) break;
+                    uint32_t a[8], c[8];
+                    tmem_ld8_issue(tl + kTmemS + h0 + 8 * k, a);
+                    tmem_ld8_issue(tl + kTmemS + run.hp + h0 + 8 * k, c);
+                    const float4 f0 = *reinterpret_cast<const float4*>(cq + 8 * k), f1 = *reinterpret_cast<const float4*>(cq + 8 * k + 4);
+                    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                    tmem_ld8_wait(a);
+                    tmem_ld8_wait(c);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float s = fmaf(__uint_as_float(c[j]), 0.03125f, __uint_as_float(a[j]));
+                        z[8 * k + j] = in ? fmaf(s, f[j] * sj, lg) : kNegInf;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(sempty));
+                // The block's largest value of each head, head h0 + k's in lane k.
+                float top = kNegInf;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    if (k >= 8 * ng) break;
+                    const float t = redux_max(z[k]);
+                    top = lane == k ? t : top;
+                }
+                // x = 2^(z - T) <= 256
+                float T = top == kNegInf ? kNegInf : ceilf(top) - 8.f;
+                const bool mine = lane < 8 * ng;
+                if (i == 0) {
+                    mx_s[sw * 32 + lane] = T;
+                    soft_sync_or(false);
+                    const float* mx = mx_s + half * 128 + lane;
+                    M = fmaxf(fmaxf(mx[0], mx[32]), fmaxf(mx[64], mx[96]));
+                    if (M == kNegInf) M = 0.f;
+                } else if (soft_sync_or(mine && T - M > kRaise)) {
+                    // Rare: some block grew too far; O and the sums follow.
+                    mx_s[sw * 32 + lane] = T;
+                    soft_sync_or(false);
+                    const float* mx = mx_s + half * 128 + lane;
+                    const float to = fmaxf(fmaxf(mx[0], mx[32]), fmaxf(mx[64], mx[96]));
+                    float alpha = 1.f;
+                    if (mine && to - M > kRaise) {
+                        alpha = exp2_fast(M - to);
+                        M = to;
+                    }
+                    if (mine) al_s[h0 + lane] = alpha;     // the same from each of the half's four warps
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (k >= 8 * ng) break;
+                        l[k] *= al_s[h0 + k];
+                        lr[k] *= al_s[h0 + k];
+                    }
+                    ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
+                    tc_fence_after();
+                    for (int blk = 0; ok && blk < p.nblk; ++blk)
+                        for (int k = 0; k < ng; ++k) {
+                            uint32_t r[8];
+                            const uint32_t at = tl + blk * kHeads + h0 + 8 * k;
+                            tmem_ld8_issue(at, r);
+                            tmem_ld8_wait(r);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * al_s[h0 + 8 * k + j]);
+                            tmem_st8(at, r);
+                        }
+                    tmem_wait_st();
+                }
+                if (T == kNegInf) T = M;                   // nothing in this block: x = 0
+                const int up = static_cast<int>(fmaxf(fminf(T - M, 127.f), -126.f));
+                bc[lane] = T;
+                bc[32 + lane] = __int_as_float((up + 127) << 23);
+                __syncwarp();
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= ng) break;
+                    const float4 t0 = *reinterpret_cast<const float4*>(bc + 8 * k), t1 = *reinterpret_cast<const float4*>(bc + 8 * k + 4);
+                    const float4 f0 = *reinterpret_cast<const float4*>(bc + 32 + 8 * k), f1 = *reinterpret_cast<const float4*>(bc + 36 + 8 * k);
+                    const float t[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+                    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const float x0 = exp2_fast(z[8 * k + j] - t[j]), x1 = exp2_fast(z[8 * k + j + 1] - t[j + 1]);
+                        uint32_t a, c;
+                        __half2 s;
+                        split2(__floats2half2_rn(x0, x1), a, c, s);
+                        const float2 r = __half22float2(s);
+                        const int at = 2 * k + (j >> 2);
+                        hi[at] = j & 2 ? hi[at] | a << 16 : a;
+                        lo[at] = j & 2 ? lo[at] | c << 16 : c;
+                        const float w0 = f[j] * inv_s, w1 = f[j + 1] * inv_s;
+                        l[8 * k + j] = fmaf(x0, w0, l[8 * k + j]);
+                        l[8 * k + j + 1] = fmaf(x1, w1, l[8 * k + j + 1]);
+                        lr[8 * k + j] = fmaf(x0 < 0x1p-6f ? x0 : r.x, w0, lr[8 * k + j]);
+                        lr[8 * k + j + 1] = fmaf(x1 < 0x1p-6f ? x1 : r.y, w1, lr[8 * k + j + 1]);
+                    }
+                }
+                if (n > 0) ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
+                __syncwarp();
+                if (ok) {
+                    uint8_t* at = p_s + tok * 64;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k >= ng) break;
+                        const int v = half * ng + k;       // eight heads: eight bytes
+                        const int off = (((v >> 1) ^ ((tok >> 1) & 3)) << 4) + (v & 1) * 8;
+                        *reinterpret_cast<uint2*>(at + off) = make_uint2(hi[2 * k], hi[2 * k + 1]);
+                        *reinterpret_cast<uint2*>(at + kPBytes + off) = make_uint2(lo[2 * k], lo[2 * k + 1]);
+                    }
+                    if (mine) {
+                        const int h = h0 + lane;
+                        uint8_t* sf = sf_s + (h & 31) * 16 + (h >> 5) * 4 + quad;
+                        sf[0] = static_cast<uint8_t>(up + 127);
+                        sf[8] = static_cast<uint8_t>(max(up + 127 - 5, 0));
+                    }
+                    if (valid < kTile) {
+                        // Rows past the length hold whatever the page or the
+                        // buffer held: 0 * NaN would reach O, so their codes become 0.
+                        // (S^T of this tile is done, so its chunks have landed.)
+                        for (int r = valid + (st >> 3); r < kTile; r += kSoftThreads / 8) {
+                            for (int j = 0; j < p.nblk; ++j) {
+                                int slot;
+                                uint32_t parity;
+                                ch.at(p, j == 0 ? 0 : j + p.pe, slot, parity);
+                                *reinterpret_cast<uint4*>(ring + slot * kChunkBytes + r * 128 + (st & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(pfull));
+            }
+            // S^T of the last tile is done with q: the next job's takes its place
+            // while the last product runs.
+            ++nq;
+            {
+                Run r = run;
+                r.advance();
+                if (seek(r) && ok) split_q(r, nq & 1);
+            }
+            // ---- output of the job (or of this worker's part of it)
+            // Sums over the tokens: lane k gets head h0 + k's.
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < o; ++k) {
+                    const bool hi_half = lane & o;
+                    const float a = hi_half ? l[k] : l[k + o], c = hi_half ? lr[k] : lr[k + o];
+                    l[k] = (hi_half ? l[k + o] : l[k]) + __shfl_xor_sync(0xffffffffu, a, o);
+                    lr[k] = (hi_half ? lr[k + o] : lr[k]) + __shfl_xor_sync(0xffffffffu, c, o);
+                }
+            bc[lane] = l[0];
+            bc[32 + lane] = lr[0];
+            soft_sync_or(false);                           // bc is next written after another tile's barrier
+            float ls = 0.f, lrs = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                ls += bc_s[(half * 4 + q) * 64 + lane];
+                lrs += bc_s[(half * 4 + q) * 64 + 32 + lane];
+            }
+            // A part's weights add up to its unrounded sum, which the join divides by.
+            if (lane < 8 * ng) al_s[h0 + lane] = lrs > 0.f || lrs != lrs ? __fdividef(whole ? 1.0f : ls, lrs) : 0.f;
+            __syncwarp();                                  // the same from each of the half's four warps
+            ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
+            tc_fence_after();
+            if (!ok) continue;
+            if (whole) {
+                // 32 values x 32 heads at a time, through the warp's own 2 KB of
+                // p's buffers: stmatrix turns the fragments into rows of 32 values
+                // (16-byte chunks, chunk ^ (row / 2) % 4), which leave as 16-byte
+                // stores, 64 bytes of each of eight heads at once.
+                const uint32_t stage = smem_u32(p_s) + sw * 2048;
+                const int col0 = 2 * (lane & 3);
+                for (int blk = 0; blk < p.nblk; ++blk) {
+                    uint32_t x[2][16];
+                    const uint32_t src = tl + blk * kHeads + h0;
+                    tmem_ld_frag32(src, x[0]);
+                    tmem_ld_frag32(src + (16u << 16), x[1]);
+                    tmem_ld16_wait(x[0]);
+                    tmem_ld16_wait(x[1]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {          // eight heads
+                        if (q >= ng) break;
+                        const float2 f = *reinterpret_cast<const float2*>(al_s + h0 + q * 8 + col0);
+                        uint32_t v[4];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d)        // eight values
+                            v[d] = pack_bf16(__uint_as_float(x[d >> 1][q * 4 + (d & 1) * 2]) * f.x,
+                                             __uint_as_float(x[d >> 1][q * 4 + (d & 1) * 2 + 1]) * f.y);
+                        const int hl = q * 8 + (lane & 7), d = lane >> 3;
+                        stmatrix_x4_trans(stage + hl * 64 + ((d ^ ((hl >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
+                    }
+                    __syncwarp();
+                    __nv_bfloat16* o = p.out + b * p.ldo_b + blk * 128 + quad * 32 + (lane & 3) * 8;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int hl = j * 8 + (lane >> 2), head = h0 + hl;
+                        uint4 v;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(stage + hl * 64 + (((lane & 3) ^ ((hl >> 1) & 3)) << 4))
+                                     : "memory");
+                        if (j < ng && head < run.count && bounds_ok(b >= 0 && b < p.B))
+                            *reinterpret_cast<uint4*>(o + static_cast<int64_t>(g * kHeads + head) * p.ldo_h) = v;
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // A part, in the order the registers hold it: 512 bytes a store.
+                const int64_t slot = part_slot(p, w, run.j, run.j == j_first, g);
+                float4* o = reinterpret_cast<float4*>(p.part_o) + slot * p.nblk * 16 * 128 + quad * 32 + lane;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= ng || h0 + 8 * k >= run.count) break;
+                    const float4 f0 = *reinterpret_cast<const float4*>(al_s + h0 + 8 * k);
+                    const float4 f1 = *reinterpret_cast<const float4*>(al_s + h0 + 8 * k + 4);
+                    for (int blk = 0; blk < p.nblk; ++blk) {
+                        uint32_t x[8];
+                        tmem_ld8_issue(tl + blk * kHeads + h0 + 8 * k, x);
+                        tmem_ld8_wait(x);
+                        float4* at = o + (blk * 16 + (h0 >> 2) + 2 * k) * 128;
+                        at[0] = make_float4(__uint_as_float(x[0]) * f0.x, __uint_as_float(x[1]) * f0.y, __uint_as_float(x[2]) * f0.z,
+                                            __uint_as_float(x[3]) * f0.w);
+                        at[128] = make_float4(__uint_as_float(x[4]) * f1.x, __uint_as_float(x[5]) * f1.y,
+                                              __uint_as_float(x[6]) * f1.z, __uint_as_float(x[7]) * f1.w);
+                    }
+                }
+                if (quad == 0 && lane < 8 * ng) p.part_ml[slot * kHeads + h0 + lane] = make_float2(M, ls);
+            }
+            const int head = g * kHeads + h0 + lane;
+            if (whole && p.lse && quad == 0 && lane < 8 * ng && head < p.H)
+                p.lse[b * p.ldl_b + head] = ls == 0.f ? kNegInf : (M + log2f(ls)) * kLn2;
+            tc_fence_before();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Joins the parts of a job in the order of the tokens, the prefix's before the
+// request's own:
+//   out = sum_k 2^(m_k - M) o_k / sum_k 2^(m_k - M) l_k,  M = max_k m_k
+// The parts of job j are those of the workers from the last one that begins at
+// or before its first tile up to the last one that begins inside it.  Without a
+// prefix only requests with two or more parts are joined (by_cut: found at the
+// first cut inside them); with one, all of them.
+// A part's value is read as it lies: 16 bytes are four heads of one value.  An
+// item is four heads of one block of 128 values: SHARE = 1 gives it to one
+// warp, for few parts; SHARE = 8 gives it to the eight warps of a CTA, which
+// take the parts in turn, for jobs that many workers share.  A warp has AHEAD
+// parts on their way: the kernel takes as long as its trips to memory.
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+
+template <int SHARE, int AHEAD, int CTAS>
+__global__ void __launch_bounds__(kJoinThreads, CTAS)
+latent_attention_fp8_join_kernel(const Params p, const int by_cut) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    bounds_self_test(p.inject);
+    constexpr unsigned kAll = 0xffffffffu;
+    __shared__ int2 meta_s[kJoinThreads];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = threadIdx.x;
+    const float kNegInf = __int_as_float(0xff800000);
+    const int quads = (p.H + 3) / 4, items = quads * p.nblk;
+    const int per = (items + 8 / SHARE - 1) / (8 / SHARE); // CTAs of a request
+    const int what = blockIdx.x / per;
+
+    static_assert(kMaxCtas <= kJoinThreads, "one thread per worker");
+    const int2 me = t < p.W ? p.meta[t] : make_int2(0x7fffffff, 0);
+    meta_s[t] = me;
+    __syncthreads();
+    int b = what;
+    if (by_cut) {                                          // the request of the cut before worker what + 1, at its first cut
+        const int2 cut = meta_s[what + 1];
+        b = cut.x - p.NP;
+        if (b >= p.B || cut.y == 0 || (meta_s[what].x == cut.x && meta_s[what].y > 0)) return;
+    }
+    // First worker and number of parts of a job.
+    auto parts_of = [&](int j, int& w0) {
+        const int before = __syncthreads_count(me.x < j || (me.x == j && me.y == 0));
+        const int upto = __syncthreads_count(me.x <= j);
+        w0 = before - 1;
+        return upto - before + 1;
+    };
+    int w1, w2 = 0, n1 = 0, n2;
+    const int sub = static_cast<int>(blockIdx.x) - what * per;
+    const int item = SHARE == 1 ? sub * 8 + warp : sub;
+    const int hq = min(item, items - 1) / p.nblk, blk = item - hq * p.nblk;
+    int g1 = 0, hl1 = 0, j1 = 0;
+    const int j2 = p.NP + b, g2 = hq * 4 / kHeads, hl2 = hq * 4 - g2 * kHeads;
+    n2 = parts_of(j2, w1);
+    if (p.prefix_len) {
+        w2 = w1;
+        if (clamp_len(p.cap, p.seq_lens[b]) == 0) n2 = 0;  // an empty request leaves none
+        if (clamp_len(p.prefix_cap, *p.prefix_len) > 0) {
+            // The rows of four heads lie in one group; a CTA's items may lie in two
+            // jobs, so each warp finds its own.
+            const int r = b * p.HR + hq * 4, rg = r / kHeads;
+            j1 = rg / p.G;
+            g1 = rg - j1 * p.G;
+            hl1 = r - rg * kHeads;
+            int before = 0, upto = 0;
+            for (int k = lane; k < p.W; k += 32) {
+                const int2 m = meta_s[k];
+                before += m.x < j1 || (m.x == j1 && m.y == 0);
+                upto += m.x <= j1;
+            }
+            before = __reduce_add_sync(kAll, before);
+            upto = __reduce_add_sync(kAll, upto);
+            w1 = before - 1;
+            n1 = upto - before + 1;
+        }
+    } else {
+        w2 = w1;
+        if (n2 < 2) return;
+    }
+    if (item >= items) return;                             // SHARE = 8: the whole CTA
+    const int np = n1 + n2;
+    auto slot_of = [&](int k) -> int64_t {                 // part k's place in the workspace
+        const bool front = k < n1;
+        const int w = front ? w1 + k : w2 + k - n1, j = front ? j1 : j2;
+        return part_slot(p, w, j, meta_s[w].x == j, front ? g1 : g2);
+    };
+    auto row_of = [&](int k) { return k < n1 ? hl1 : hl2; };
+    // Values 2 lane, + 1, 2 lane + 64, + 1 of the block.
+    auto load = [&](int k, float4 (&o)[4]) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((slot_of(k) * p.nblk + blk) * 16 + row_of(k) / 4) * 128 + 2 * lane;
+        o[0] = src[0];
+        o[1] = src[1];
+        o[2] = src[64];
+        o[3] = src[65];
+    };
+    const int k0 = SHARE == 1 ? 0 : warp, mine = np > k0 ? (np - k0 + SHARE - 1) / SHARE : 0;   // parts of this warp
+    float M[4], L[4] = {0.f, 0.f, 0.f, 0.f}, acc[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        M[j] = kNegInf;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i][j] = 0.f;
+    }
+    for (int c = 0; c < mine; c += 32) {                   // 32 parts at a time, one's (max, sum) per lane
+        const int cnt = min(32, mine - c);
+        float4 o[AHEAD][4];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)                    // on their way while the factors are formed
+            if (u < cnt) load(k0 + (c + u) * SHARE, o[u]);
+        float f[4] = {kNegInf, kNegInf, kNegInf, kNegInf}, l[4] = {0.f, 0.f, 0.f, 0.f};
+        if (lane < cnt) {
+            const int k = k0 + (c + lane) * SHARE;
+            const float4* ml = reinterpret_cast<const float4*>(p.part_ml + slot_of(k) * kHeads + row_of(k));
+            const float4 x = ml[0], y = ml[1];
+            f[0] = x.x; f[1] = x.z; f[2] = y.x; f[3] = y.z;
+            l[0] = x.y; l[1] = x.w; l[2] = y.y; l[3] = y.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float top = f[j];
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, s));
+            top = fmaxf(top, M[j]);
+            const float base = top == kNegInf ? 0.f : top, old = exp2_fast(M[j] - base);
+            f[j] = exp2_fast(f[j] - base);
+            L[j] = fmaf(L[j], old, warp_sum(f[j] * l[j]));
+            M[j] = top;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i][j] *= old;
+        }
+        auto add = [&](int k, const float4 (&x)[4]) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float fk = __shfl_sync(kAll, f[j], k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float v = j == 0 ? x[i].x : j == 1 ? x[i].y : j == 2 ? x[i].z : x[i].w;
+                    acc[i][j] = fmaf(v, fk, acc[i][j]);
+                }
+            }
+        };
+        for (int k = 0; k < cnt; k += AHEAD) {
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (k + u < cnt) add(k + u, o[u]);
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (k + AHEAD + u < cnt) load(k0 + (c + k + AHEAD + u) * SHARE, o[u]);
+        }
+    }
+    if (SHARE > 1) {
+        // The warps' results, merged in the order of the warps.
+        __shared__ float4 red[8][4][32], red_m[8], red_l[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[warp][i][lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        if (lane == 0) {
+            red_m[warp] = make_float4(M[0], M[1], M[2], M[3]);
+            red_l[warp] = make_float4(L[0], L[1], L[2], L[3]);
+        }
+        __syncthreads();
+        if (warp >= 4) return;
+        // Warp i finishes value group i: its quarter of the item's values.
+        float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float4 m = red_m[s];
+            top[0] = fmaxf(top[0], m.x); top[1] = fmaxf(top[1], m.y);
+            top[2] = fmaxf(top[2], m.z); top[3] = fmaxf(top[3], m.w);
+        }
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) L[j] = 0.f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float4 m = red_m[s], q = red_l[s], x = red[s][warp][lane];
+            const float sm[4] = {m.x, m.y, m.z, m.w}, sl[4] = {q.x, q.y, q.z, q.w}, sx[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float fk = exp2_fast(sm[j] - (top[j] == kNegInf ? 0.f : top[j]));
+                L[j] = fmaf(sl[j], fk, L[j]);
+                a[j] = fmaf(sx[j], fk, a[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            M[j] = top[j];
+            const int h = hq * 4 + j, v = blk * 128 + (warp >> 1) * 64 + 2 * lane + (warp & 1);
+            const float inv = L[j] > 0.f || L[j] != L[j] ? 1.0f / L[j] : 0.f;
+            if (h < p.H && bounds_ok(b < p.B && v < p.nblk * 128))
+                p.out[b * p.ldo_b + h * p.ldo_h + v] = __float2bfloat16_rn(a[j] * inv);
+        }
+        if (warp != 0) return;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int h = hq * 4 + j;
+            const float inv = L[j] > 0.f || L[j] != L[j] ? 1.0f / L[j] : 0.f;
+            if (h >= p.H || !bounds_ok(b < p.B)) continue;
+            __nv_bfloat16* dst = p.out + b * p.ldo_b + h * p.ldo_h + blk * 128 + 2 * lane;
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0][j] * inv, acc[1][j] * inv);
+            *reinterpret_cast<uint32_t*>(dst + 64) = pack_bf16(acc[2][j] * inv, acc[3][j] * inv);
+        }
+    }
+    if (p.lse && blk == 0 && lane < 4 && hq * 4 + lane < p.H) {
+        const float m = lane == 0 ? M[0] : lane == 1 ? M[1] : lane == 2 ? M[2] : M[3];
+        const float l = lane == 0 ? L[0] : lane == 1 ? L[1] : lane == 2 ? L[2] : L[3];
+        p.lse[b * p.ldl_b + hq * 4 + lane] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+    }
+}
+
+// --------------------------------------------------------------------- host
+
+// The cache as [page][group of 8 tokens][chunk][token][128 bytes]: one copy
+// brings one chunk of `rows` tokens (whole groups) of one page.
+bool make_cache_map(CUtensorMap* m, const void* cache, int64_t pages, int64_t page_size, int64_t chunks, int64_t ld_page,
+                    int64_t ld_row, int rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[5] = {128, 8, static_cast<cuuint64_t>(chunks), static_cast<cuuint64_t>(page_size / 8),
+                                static_cast<cuuint64_t>(pages)};
+    const cuuint64_t strides[4] = {static_cast<cuuint64_t>(ld_row), 128, static_cast<cuuint64_t>(ld_row * 8),
+                                   static_cast<cuuint64_t>(ld_page)};
+    const cuuint32_t box[5] = {128, 8, 1, static_cast<cuuint32_t>(rows / 8), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(cache), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t tiles_for(int64_t cap) { return cap > kTile ? (cap + kTile - 1) / kTile : 1; }
+
+// What a call comes to before anything is known about the lengths.
+struct Shape {
+    int64_t B, H, K, P, DV, width, page_size;
+    bool prefix;
+    int64_t prefix_width;
+};
+struct Plan {
+    int64_t G, HR, R, NP, W, parts;
+};
+Plan plan_of(const Shape& s, int64_t ctas) {
+    Plan x{};
+    x.G = (s.H + kHeads - 1) / kHeads;
+    x.HR = (s.H + 3) / 4 * 4;
+    int64_t tiles = 0;
+    if (s.prefix && s.prefix_width > 0) {
+        x.R = s.B * x.HR;
+        x.NP = ((x.R + kHeads - 1) / kHeads + x.G - 1) / x.G;
+        tiles = x.NP * tiles_for(s.prefix_width * s.page_size);
+    }
+    // Workers: bounded by the device and by the most tiles that the tables can hold.
+    const int64_t per = tiles_for(s.width * s.page_size);
+    x.W = ctas / x.G;
+    if (x.W < 1) x.W = 1;
+    if ((x.W - 1) / per + 1 > s.B) {                       // min(W, tiles + B * per) without overflow
+        tiles += s.B * per;
+        if (tiles < x.W) x.W = tiles;
+    }
+    x.parts = (s.prefix ? x.NP + s.B + x.W : 2 * x.W) * x.G;
+    return x;
+}
+
+struct Layout {
+    int64_t meta, ml, o, total;                            // byte offsets of the workspace's parts
+};
+Layout workspace_layout(const Plan& x, int64_t DV) {
+    Layout L;
+    L.meta = 0;
+    L.ml = (x.W * 8 + 255) / 256 * 256;
+    L.o = (L.ml + x.parts * kHeads * 8 + 255) / 256 * 256;
+    L.total = L.o + x.parts * kHeads * DV * 4;
+    return L;
+}
+
+dsnq_status check_sizes(const Shape& s) {
+    if (s.B < 0 || s.H <= 0 || s.K <= 0 || s.P < 0 || s.DV <= 0 || s.width < 0 || s.prefix_width < 0 || s.page_size <= 0)
+        return DSNQ_ERR_INVALID_ARG;
+    if (s.DV > s.K) return DSNQ_ERR_INVALID_ARG;
+    if (s.K % 128 || s.K > 512 || (s.P != 0 && s.P != 64) || s.DV % 128 || s.H > 1024 || s.B > DSNQ_MAX_REQUESTS || s.page_size % 8 ||
+        s.page_size > (1 << 20) || s.width > 0x7fffffffLL || s.width * s.page_size > 0x7fffff00LL || s.prefix_width > 0x7fffffffLL ||
+        s.prefix_width * s.page_size > 0x7fffff00LL)
+        return DSNQ_ERR_UNSUPPORTED;
+    return DSNQ_OK;
+}
+
+dsnq_status workspace_bytes_of(const Shape& s, int64_t* bytes) {
+    const dsnq_status st = check_sizes(s);
+    if (st != DSNQ_OK) return st;
+    if (bytes) *bytes = s.B == 0 ? 0 : workspace_layout(plan_of(s, kMaxCtas), s.DV).total;
+    return DSNQ_OK;
+}
+
+struct Tensors {
+    const void* q;
+    int64_t ldq_tok, ldq_head;
+    const void* cache;
+    int64_t num_pages, ld_page, ld_row;
+    const float* scales;
+    int64_t ld_scale;
+    const int32_t *prefix_table, *prefix_len, *table;
+    int64_t ld_table;
+    const int32_t* seq_lens;
+    float scale;
+    void* out;
+    int64_t ldo_tok, ldo_head;
+    float* lse;
+    int64_t ldl_tok;
+    void* workspace;
+    int64_t workspace_bytes;
+};
+
+dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
+    dsnq_status st = check_sizes(z);
+    if (st != DSNQ_OK) return st;
+    if (t.num_pages < 1 || !(t.scale > 0.f && t.scale < 1.0e30f) || t.workspace_bytes < 0) return DSNQ_ERR_INVALID_ARG;
+    // Strides of a tensor map are below 2^40 bytes (the cache's 8-row groups: 8 ld_row).
+    if (t.num_pages > 0x7ffffffeLL || t.ld_row >= (1LL << 37) || t.ld_page >= (1LL << 40) || t.ld_scale >= (1LL << 38) ||
+        t.ldq_tok >= (1LL << 39) || t.ldq_head >= (1LL << 39))
+        return DSNQ_ERR_UNSUPPORTED;
+    if (z.B == 0) return DSNQ_OK;
+    if (!t.q || !t.out || !t.seq_lens || !t.workspace || !t.cache || !t.scales || (z.width && !t.table) ||
+        (z.prefix && (!t.prefix_len || (z.prefix_width && !t.prefix_table))))
+        return DSNQ_ERR_INVALID_ARG;
+    const int64_t DK = z.K + z.P, row = z.K + 2 * z.P;
+    if ((z.H > 1 && (t.ldq_head < DK || t.ldo_head < z.DV)) ||
+        (z.B > 1 && (t.ldq_tok < DK || t.ldo_tok < z.DV || t.ld_table < z.width)) || (z.B > 1 && t.lse && t.ldl_tok < z.H) ||
+        t.ld_row < row || t.ld_page < (z.page_size - 1) * t.ld_row + row || (t.num_pages > 1 && t.ld_scale < z.page_size))
+        return DSNQ_ERR_INVALID_ARG;
+    if (!aligned(t.q, 16) || t.ldq_tok % 8 || t.ldq_head % 8 || !aligned(t.cache, 16) || t.ld_page % 16 || t.ld_row % 16 ||
+        !aligned(t.scales, 16) || t.ld_scale % 4 || !aligned(t.out, 16) || t.ldo_tok % 8 || t.ldo_head % 8 || !aligned(t.table, 4) ||
+        !aligned(t.prefix_table, 4) || !aligned(t.prefix_len, 4) || !aligned(t.seq_lens, 4) || !aligned(t.lse, 4) ||
+        !aligned(t.workspace, 16))
+        return DSNQ_ERR_MISALIGNED;
+    if (t.workspace_bytes < workspace_layout(plan_of(z, kMaxCtas), z.DV).total) return DSNQ_ERR_INVALID_ARG;
+    const int sms = device_sm_count();
+    if (sms <= 0) {
+        cudaGetLastError();
+        return DSNQ_ERR_CUDA;
+    }
+    const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+    const Plan x = plan_of(z, ctas);
+    Params p{};
+    p.q = static_cast<const __nv_bfloat16*>(t.q);
+    p.ldq_b = t.ldq_tok; p.ldq_h = t.ldq_head;
+    p.scales = t.scales; p.ld_scale = t.ld_scale;
+    p.seq_lens = t.seq_lens;
+    p.table = t.table; p.ld_table = t.ld_table;
+    p.prefix_table = t.prefix_table;
+    p.prefix_len = z.prefix ? t.prefix_len : nullptr;
+    p.B = static_cast<int>(z.B); p.H = static_cast<int>(z.H); p.G = static_cast<int>(x.G); p.W = static_cast<int>(x.W);
+    p.W_full = ctas > x.G ? static_cast<int>(ctas / x.G) : 1;
+    p.HR = static_cast<int>(x.HR); p.R = static_cast<int>(x.R); p.NP = static_cast<int>(x.NP);
+    p.width = static_cast<int>(z.width);
+    p.prefix_width = static_cast<int>(z.prefix_width);
+    p.page_size = static_cast<int>(z.page_size);
+    p.num_pages = static_cast<int>(t.num_pages);
+    p.cap = z.width * z.page_size;
+    p.prefix_cap = z.prefix_width * z.page_size;
+    p.box_rows = z.page_size % 128 == 0 ? 128 : z.page_size % 64 == 0 ? 64 : z.page_size % 32 == 0 ? 32 : z.page_size % 16 == 0 ? 16 : 8;
+    p.cc = static_cast<int>(z.K / 128);
+    p.pe = z.P ? 1 : 0;
+    p.nblk = static_cast<int>(z.DV / 128);
+    const int64_t rows = x.NP ? x.R : z.H;                 // the most that a CTA can get
+    p.q_rows = static_cast<int>(rows < kHeads ? (rows + 15) / 16 * 16 : kHeads);
+    // Shared memory: q, p s, scales and barriers, and the rest for the ring, up
+    // to the three tiles whose row scales have a place.
+    const int64_t fixed = 1024 + static_cast<int64_t>(2 * p.cc + p.pe) * p.q_rows * 128 + 2 * kPBytes + kMiscBytes;
+    const int cpt = p.cc + p.pe;
+    p.slots = static_cast<int>((227 * 1024 - fixed) / kChunkBytes);
+    if (p.slots > 3 * cpt) p.slots = 3 * cpt;
+    if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+    p.twin = p.slots < 2 * cpt;                            // 512 codes, position columns, more than 32 heads
+    if (p.twin && (cpt != 5 || p.slots < 8)) return DSNQ_ERR_UNSUPPORTED;
+    if (p.twin) p.slots = 8;
+    const size_t smem = static_cast<size_t>(fixed + p.slots * kChunkBytes);
+    p.scale_log2 = t.scale * kLog2e;
+    p.out = static_cast<__nv_bfloat16*>(t.out);
+    p.ldo_b = t.ldo_tok; p.ldo_h = t.ldo_head;
+    p.lse = t.lse; p.ldl_b = t.ldl_tok;
+    const Layout lay = workspace_layout(x, z.DV);
+    uint8_t* ws = static_cast<uint8_t*>(t.workspace);
+    p.meta = reinterpret_cast<int2*>(ws + lay.meta);
+    p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
+    p.part_o = reinterpret_cast<float*>(ws + lay.o);
+    const uint64_t limit = debug_wait_timeout_ns();
+    p.timeout_ns = limit ? limit : kDefaultTimeoutNs;
+    p.inject = debug_inject_flags();
+
+    CUtensorMap mc;
+    if (!make_cache_map(&mc, t.cache, t.num_pages, z.page_size, cpt, t.ld_page, t.ld_row, p.box_rows)) return DSNQ_ERR_CUDA;
+    if (!set_smem_attr(reinterpret_cast<const void*>(latent_attention_fp8_kernel), smem)) return DSNQ_ERR_CUDA;
+    st = launch_result(launch_kernel(latent_attention_fp8_kernel, dim3(static_cast<unsigned>(p.W * p.G)), dim3(kThreads), smem, s, mc, p));
+    if (st != DSNQ_OK || (p.W == 1 && !z.prefix)) return st;
+    // Few jobs: a request has many parts, so a CTA joins each item.  Many: a
+    // warp does, and without a prefix no more requests can be split than there
+    // are cuts.  While all CTAs find room at once, each keeps more parts on
+    // their way (registers, so fewer CTAs on an SM).
+    const int64_t items = (z.H + 3) / 4 * p.nblk, jobs = x.NP + z.B;
+    const int by_cut = !z.prefix && z.B > p.W - 1;
+    const int64_t targets = by_cut ? p.W - 1 : z.B;
+    const bool share = p.W >= kManyParts * jobs;
+    const int64_t grid = targets * (share ? items : (items + 7) / 8);
+    void (*join)(Params, int);
+    if (share) join = p.W > 16 * jobs && grid <= sms ? latent_attention_fp8_join_kernel<8, 5, 1> : latent_attention_fp8_join_kernel<8, 2, 2>;
+    else if (!by_cut && grid <= 3 * sms) join = latent_attention_fp8_join_kernel<1, 4, 1>;
+    else join = grid <= 5 * sms ? latent_attention_fp8_join_kernel<1, 2, 2> : latent_attention_fp8_join_kernel<1, 2, 3>;
+    return launch_result(launch_kernel(join, dim3(static_cast<unsigned>(grid)), dim3(kJoinThreads), 0, s, p, by_cut));
+}
+
+}  // namespace attn8
+
+bool take_attention_fp8_words(cudaStream_t s, unsigned int* v) {
+    unsigned int w = 0, st = 0;
+    const unsigned int zero = 0;
+    if (!take_debug_word(s, &w)) return false;
+    if (cudaMemcpyFromSymbolAsync(&st, g_status, sizeof(st), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    *v = w | st;
+    return true;
+}
+
+}  // namespace dsnq
+
+using namespace dsnq;
+
+extern "C" dsnq_status dsnq_paged_latent_attention_fp8_workspace_bytes(int64_t B, int64_t H, int64_t DV, int64_t table_width,
+                                                                       int64_t page_size, int64_t* bytes) {
+    return attn8::workspace_bytes_of({B, H, DV, 0, DV, table_width, page_size, false, 0}, bytes);
+}
+
+extern "C" dsnq_status dsnq_shared_prefix_latent_attention_fp8_workspace_bytes(
+    int64_t B, int64_t H, int64_t DV, int64_t prefix_width, int64_t table_width, int64_t page_size, int64_t* bytes) {
+    return attn8::workspace_bytes_of({B, H, DV, 0, DV, table_width, page_size, true, prefix_width}, bytes);
+}
+
+extern "C" dsnq_status dsnq_paged_latent_attention_fp8(
+    int64_t B, int64_t H, int64_t K, int64_t P, int64_t DV, const void* q, int64_t ldq_tok, int64_t ldq_head, const void* cache,
+    int64_t num_pages, int64_t page_size, int64_t ld_page, int64_t ld_row, const float* scales, int64_t ld_scale,
+    const int32_t* block_table, int64_t table_width, int64_t ld_table, const int32_t* seq_lens, float scale, void* out, int64_t ldo_tok,
+    int64_t ldo_head, float* lse, int64_t ldl_tok, void* workspace, int64_t workspace_bytes, void* stream) {
+    return attn8::attention({B, H, K, P, DV, table_width, page_size, false, 0},
+                            {q, ldq_tok, ldq_head, cache, num_pages, ld_page, ld_row, scales, ld_scale, nullptr, nullptr, block_table,
+                             ld_table, seq_lens, scale, out, ldo_tok, ldo_head, lse, ldl_tok, workspace, workspace_bytes},
+                            static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dsnq_status dsnq_shared_prefix_latent_attention_fp8(
+    int64_t B, int64_t H, int64_t K, int64_t P, int64_t DV, const void* q, int64_t ldq_tok, int64_t ldq_head, const void* cache,
+    int64_t num_pages, int64_t page_size, int64_t ld_page, int64_t ld_row, const float* scales, int64_t ld_scale,
+    const int32_t* prefix_table, int64_t prefix_width, const int32_t* prefix_len, const int32_t* block_table, int64_t table_width,
+    int64_t ld_table, const int32_t* seq_lens, float scale, void* out, int64_t ldo_tok, int64_t ldo_head, float* lse, int64_t ldl_tok,
+    void* workspace, int64_t workspace_bytes, void* stream) {
+    return attn8::attention({B, H, K, P, DV, table_width, page_size, true, prefix_width},
+                            {q, ldq_tok, ldq_head, cache, num_pages, ld_page, ld_row, scales, ld_scale, prefix_table, prefix_len,
+                             block_table, ld_table, seq_lens, scale, out, ldo_tok, ldo_head, lse, ldl_tok, workspace, workspace_bytes},
+                            static_cast<cudaStream_t>(stream));
+}

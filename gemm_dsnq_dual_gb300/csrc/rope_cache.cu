@@ -1,7 +1,7 @@
 // The steps between the pre-projection and the attention of a decode step:
 // block tables and slots from request lengths, per-head RMSNorm with rotary
 // positions, and the write of normalized, rotated latent rows into the paged
-// cache.
+// cache, in bf16 or in 8 bits, with the way back from 8 bits.
 //
 // Rotary positions: the pair (a, b) of frequency i at position p becomes
 //   (a cos t - b sin t, b cos t + a sin t) * rope_scale,   t = p * inv_freq[i].
@@ -266,8 +266,10 @@ struct WriteArgs {
     int64_t M;
     int K, W;                            // latent columns, row columns (latent + position part)
     const int64_t* slots;
-    __nv_bfloat16* cache;
-    int64_t ld_page, ld_row, num_slots;
+    void* cache;                         // bf16, or bytes: K codes, then the position columns as bf16
+    int64_t ld_page, ld_row, num_slots;  // strides in elements of the cache
+    float* scales;                       // 8 bits: one a row
+    int64_t ld_scale;
     int page_size;
     int norm;
     float k_f, eps;
@@ -276,6 +278,7 @@ struct WriteArgs {
 };
 
 constexpr int kWriteWarps = 4;
+constexpr float kLeastScale = 0x1p-60f;  // of a row in 8 bits: an all-zero latent leaves its position columns finite
 
 // One warp per row; lane l holds chunks l, l + 32, ... of the concatenated
 // row.  The row is requested before its slot and position are known (they
@@ -288,7 +291,13 @@ constexpr int kWriteWarps = 4;
 // angles take a pass of their own).  Warps that stride over the rows and request
 // the next one early need registers of a CTA per SM: 6.7 us at 8191 rows, 19.9
 // at 32768.
-template <int CPL, bool HALF>
+//
+// FP8: the row leaves as s (codes | position columns / s), s = max |latent| /
+// 448 of the rotated row, in fp32; one scale a row, since the attention's
+// products sum over the whole row before a factor can be applied, and e4m3
+// keeps its 4 bits down to 2^-15 of the largest.  Codes are those of the IEEE
+// quotient; the position columns' quotients are rounded once to bf16.
+template <int CPL, bool HALF, bool FP8>
 __global__ void __launch_bounds__(kWriteWarps * 32, HALF ? 4 : 6)
 latent_cache_write_kernel(const WriteArgs a) {
     grid_dependency_wait();
@@ -345,7 +354,8 @@ latent_cache_write_kernel(const WriteArgs a) {
     }
     // Slots mostly fit 32 bits, whose division is a fraction of the 64-bit one.
     const int64_t page = slot <= 0xffffffffLL ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page_size) : slot / a.page_size;
-    __nv_bfloat16* row = a.cache + page * a.ld_page + (slot - page * a.page_size) * a.ld_row;
+    const int64_t in_page = slot - page * a.page_size, at_row = page * a.ld_page + in_page * a.ld_row;
+    uint32_t top = 0;                    // largest magnitude among the latent columns, as bits (NaN above all)
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
         const int col = (lane + j * 32) * kChunk;
@@ -359,7 +369,142 @@ latent_cache_write_kernel(const WriteArgs a) {
             }
             rotate_chunk<HALF>(a.rope, cs, col - a.rope.off, x[j], y);
         }
-        *reinterpret_cast<uint4*>(row + col) = pack8(x[j]);
+        if (!FP8) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.cache) + at_row + col) = pack8(x[j]);
+        if (FP8 && col < a.K) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                top = max(top, max(__float_as_uint(x[j][i].x) & 0x7fffffffu, __float_as_uint(x[j][i].y) & 0x7fffffffu));
+        }
+    }
+    if (!FP8) return;
+    top = __reduce_max_sync(0xffffffffu, top);
+    // A NaN or an infinity among the latent columns makes the row NaN.
+    const float scale = top < 0x7f800000u ? fmaxf(group_scale(__uint_as_float(top)), kLeastScale) : __int_as_float(0x7fffffff);
+    const GroupQuant gq = group_quant_from(scale, group_recip(scale));
+    uint8_t* row = static_cast<uint8_t*>(a.cache) + at_row;
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) {
+        const int col = (lane + j * 32) * kChunk;
+        if (!live[j] || !bounds_ok(col + kChunk <= a.W)) continue;
+        if (col < a.K) {
+            bool ok;
+            uint2 codes = quant8_bracket(x[j], gq, ok);
+            if (!ok) codes = quant8_divide(x[j], scale);
+            *reinterpret_cast<uint2*>(row + col) = codes;
+        } else {
+            float2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = make_float2(__fdiv_rn(x[j][i].x, scale), __fdiv_rn(x[j][i].y, scale));
+            *reinterpret_cast<uint4*>(row + a.K + (col - a.K) * 2) = pack8(v);
+        }
+    }
+    if (lane == 0) a.scales[page * a.ld_scale + in_page] = scale;
+}
+
+// -------------------------------------------------- latent cache read (8 bits)
+struct ReadArgs {
+    const uint8_t* cache;
+    const float* scales;
+    int64_t ld_page, ld_row, ld_scale;   // bytes, bytes, floats
+    int num_pages, page_size;
+    int K, W;                            // latent columns, columns of an output row
+    const int32_t* table;
+    int64_t ld_table;
+    int B, width;
+    const int32_t* row_starts;           // [B + 1]
+    const int32_t* first;                // first token of each request, NULL: 0
+    __nv_bfloat16* out;
+    int64_t ldo;
+    int64_t rows;
+    uint32_t recip;                      // ceil(2^32 / chunks of a row)
+    uint32_t inject;
+};
+
+constexpr int kReadThreads = 256;
+constexpr int kReadRows = 32;            // rows of a CTA
+
+// A CTA takes 32 rows of the output: each of its first threads finds one row's
+// request (the last that begins at or before it), page and scale, then all of
+// them take the rows' chunks of 8 columns one after the other, several on
+// their way at once.  Bound by HBM: 1.8 KB a row in and out.
+__global__ void __launch_bounds__(kReadThreads)
+latent_cache_read_fp8_kernel(const ReadArgs a) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    bounds_self_test(a.inject);
+    __shared__ int64_t at_s[kReadRows];  // byte offset of the row in the cache, -1: zeros, -2: not written
+    __shared__ float scale_s[kReadRows];
+    const int t = threadIdx.x;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kReadRows;
+    if (t < kReadRows) {
+        const int64_t r = r0 + t;
+        int64_t at = -2;
+        float scale = 0.f;
+        if (r < a.rows && r >= a.row_starts[0] && r < a.row_starts[a.B]) {
+            int lo = 0, hi = a.B;        // row_starts[lo] <= r < row_starts[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (a.row_starts[mid] <= r) lo = mid;
+                else hi = mid;
+            }
+            const int64_t tok = r - a.row_starts[lo] + (a.first ? a.first[lo] : 0);
+            int id = -1;
+            if (tok >= 0 && tok < static_cast<int64_t>(a.width) * a.page_size) id = a.table[lo * a.ld_table + tok / a.page_size];
+            at = -1;
+            if (id >= 0 && id < a.num_pages) {
+                const int64_t in_page = tok % a.page_size;
+                at = id * a.ld_page + in_page * a.ld_row;
+                scale = a.scales[id * a.ld_scale + in_page];
+            } else {
+                atomicOr(&g_rope_status, kStatusBounds);
+            }
+        }
+        at_s[t] = at;
+        scale_s[t] = scale;
+    }
+    __syncthreads();
+    const int chunks = a.W / kChunk, items = kReadRows * chunks;
+    constexpr int U = 6;
+    for (int base = t; base < items; base += U * kReadThreads) {
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = base + u * kReadThreads;
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (e >= items) continue;
+            const int row = static_cast<int>(__umulhi(static_cast<uint32_t>(e), a.recip)), col = (e - row * chunks) * kChunk;
+            const int64_t at = at_s[row];
+            if (at < 0 || !bounds_ok(col + kChunk <= a.W)) continue;
+            if (col < a.K) {
+                const uint2 v = *reinterpret_cast<const uint2*>(a.cache + at + col);
+                raw[u].x = v.x;
+                raw[u].y = v.y;
+            } else {
+                raw[u] = *reinterpret_cast<const uint4*>(a.cache + at + a.K + (col - a.K) * 2);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = base + u * kReadThreads;
+            if (e >= items) continue;
+            const int row = static_cast<int>(__umulhi(static_cast<uint32_t>(e), a.recip)), col = (e - row * chunks) * kChunk;
+            if (at_s[row] == -2) continue;
+            const float2 s = make_float2(scale_s[row], scale_s[row]);
+            float2 f[4];
+            if (col < a.K) {
+                const uint32_t w[2] = {raw[u].x, raw[u].y};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (i & 1) * 16), __NV_E4M3);
+                    f[i] = __half22float2(__half2(h));
+                }
+            } else {
+                unpack8(raw[u], f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], s);
+            *reinterpret_cast<uint4*>(a.out + (r0 + row) * a.ldo + col) = pack8(f);
+        }
     }
 }
 
@@ -595,11 +740,15 @@ extern "C" dsnq_status dsnq_head_rmsnorm_rope(
     return launch_heads<32, 4>(a, sms, s);
 }
 
-extern "C" dsnq_status dsnq_latent_cache_write(
-    int64_t M, int64_t K, int64_t P, const void* kv, int64_t ldkv, const void* pe, int64_t ldpe, int32_t normalize,
-    const void* gamma, float eps, const int64_t* positions, const double* inv_freq, int64_t rope_offset,
-    int64_t rope_dim, dsnq_rope_layout layout, float rope_scale, const int64_t* slots, void* cache, int64_t num_pages,
-    int64_t page_size, int64_t ld_page, int64_t ld_row, void* stream) {
+namespace dsnq {
+namespace {
+
+// What the writes in bf16 and in 8 bits have in common; `row` is the length of
+// a cache row and `unit` the multiple of its strides, in elements of the cache.
+dsnq_status check_write(WriteArgs& a, int64_t M, int64_t K, int64_t P, const void* kv, int64_t ldkv, const void* pe, int64_t ldpe,
+                        int32_t normalize, const void* gamma, float eps, const int64_t* positions, const double* inv_freq,
+                        int64_t rope_offset, int64_t rope_dim, dsnq_rope_layout layout, float rope_scale, const int64_t* slots,
+                        void* cache, int64_t num_pages, int64_t page_size, int64_t ld_page, int64_t ld_row, int64_t row, int64_t unit) {
     if (M < 0 || K <= 0 || P < 0 || num_pages < 0 || page_size <= 0) return DSNQ_ERR_INVALID_ARG;
     if (normalize && (!(eps >= 0.f) || eps > 3.0e38f)) return DSNQ_ERR_INVALID_ARG;   // also rejects NaN
     if (!normalize && gamma) return DSNQ_ERR_INVALID_ARG;
@@ -612,20 +761,19 @@ extern "C" dsnq_status dsnq_latent_cache_write(
     if (M == 0) return DSNQ_OK;
     if (!kv || (P && !pe) || !slots || (num_pages && !cache) || (rope_dim && (!positions || !inv_freq)))
         return DSNQ_ERR_INVALID_ARG;
-    if ((M > 1 && (ldkv < K || (P && ldpe < P))) || ld_row < W || ld_page < (page_size - 1) * ld_row + W)
+    if ((M > 1 && (ldkv < K || (P && ldpe < P))) || ld_row < row || ld_page < (page_size - 1) * ld_row + row)
         return DSNQ_ERR_INVALID_ARG;
     if (!aligned(kv, 16) || ldkv % kChunk || (P && (!aligned(pe, 16) || ldpe % kChunk)) || !aligned(cache, 16) ||
-        ld_page % kChunk || ld_row % kChunk || (gamma && !aligned(gamma, 16)) || !aligned(slots, 8) ||
+        ld_page % unit || ld_row % unit || (gamma && !aligned(gamma, 16)) || !aligned(slots, 8) ||
         !aligned(positions, 8) || !aligned(inv_freq, 8))
         return DSNQ_ERR_MISALIGNED;
-    WriteArgs a{};
     a.kv = static_cast<const __nv_bfloat16*>(kv);
     a.pe = static_cast<const __nv_bfloat16*>(pe);
     a.gamma = static_cast<const __nv_bfloat16*>(gamma);
     a.ldkv = ldkv; a.ldpe = ldpe;
     a.M = M; a.K = static_cast<int>(K); a.W = static_cast<int>(W);
     a.slots = slots;
-    a.cache = static_cast<__nv_bfloat16*>(cache);
+    a.cache = cache;
     a.ld_page = ld_page; a.ld_row = ld_row;
     a.num_slots = num_pages * page_size;
     a.page_size = static_cast<int>(page_size);
@@ -634,14 +782,90 @@ extern "C" dsnq_status dsnq_latent_cache_write(
     a.rope = Rope{positions, inv_freq, static_cast<int>(rope_offset), static_cast<int>(rope_dim),
                   layout == DSNQ_ROPE_HALF, rope_scale, 1.0f};
     a.inject = debug_inject_flags();
-    const dim3 grid(static_cast<unsigned>((M + kWriteWarps - 1) / kWriteWarps)), block(kWriteWarps * 32);
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool half = layout == DSNQ_ROPE_HALF;
-    void (*kern)(WriteArgs) = W <= 256   ? (half ? latent_cache_write_kernel<1, true> : latent_cache_write_kernel<1, false>)
-                              : W <= 512 ? (half ? latent_cache_write_kernel<2, true> : latent_cache_write_kernel<2, false>)
-                              : W <= 768 ? (half ? latent_cache_write_kernel<3, true> : latent_cache_write_kernel<3, false>)
-                                         : (half ? latent_cache_write_kernel<4, true> : latent_cache_write_kernel<4, false>);
+    return DSNQ_OK;
+}
+
+template <bool HALF, bool FP8>
+dsnq_status launch_write(const WriteArgs& a, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>((a.M + kWriteWarps - 1) / kWriteWarps)), block(kWriteWarps * 32);
+    void (*kern)(WriteArgs) = a.W <= 256   ? latent_cache_write_kernel<1, HALF, FP8>
+                              : a.W <= 512 ? latent_cache_write_kernel<2, HALF, FP8>
+                              : a.W <= 768 ? latent_cache_write_kernel<3, HALF, FP8>
+                                           : latent_cache_write_kernel<4, HALF, FP8>;
     return launch_result(launch_kernel(kern, grid, block, 0, s, a));
+}
+
+}  // namespace
+}  // namespace dsnq
+
+extern "C" dsnq_status dsnq_latent_cache_write(
+    int64_t M, int64_t K, int64_t P, const void* kv, int64_t ldkv, const void* pe, int64_t ldpe, int32_t normalize,
+    const void* gamma, float eps, const int64_t* positions, const double* inv_freq, int64_t rope_offset,
+    int64_t rope_dim, dsnq_rope_layout layout, float rope_scale, const int64_t* slots, void* cache, int64_t num_pages,
+    int64_t page_size, int64_t ld_page, int64_t ld_row, void* stream) {
+    WriteArgs a{};
+    const dsnq_status st = check_write(a, M, K, P, kv, ldkv, pe, ldpe, normalize, gamma, eps, positions, inv_freq, rope_offset, rope_dim,
+                                       layout, rope_scale, slots, cache, num_pages, page_size, ld_page, ld_row, K + P, kChunk);
+    if (st != DSNQ_OK || M == 0) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return layout == DSNQ_ROPE_HALF ? launch_write<true, false>(a, s) : launch_write<false, false>(a, s);
+}
+
+extern "C" dsnq_status dsnq_latent_cache_write_fp8(
+    int64_t M, int64_t K, int64_t P, const void* kv, int64_t ldkv, const void* pe, int64_t ldpe, int32_t normalize,
+    const void* gamma, float eps, const int64_t* positions, const double* inv_freq, int64_t rope_offset,
+    int64_t rope_dim, dsnq_rope_layout layout, float rope_scale, const int64_t* slots, void* cache, int64_t num_pages,
+    int64_t page_size, int64_t ld_page, int64_t ld_row, float* scales, int64_t ld_scale, void* stream) {
+    WriteArgs a{};
+    const dsnq_status st = check_write(a, M, K, P, kv, ldkv, pe, ldpe, normalize, gamma, eps, positions, inv_freq, rope_offset, rope_dim,
+                                       layout, rope_scale, slots, cache, num_pages, page_size, ld_page, ld_row, K + 2 * P, 16);
+    if (st != DSNQ_OK) return st;
+    if (K % 16) return DSNQ_ERR_UNSUPPORTED;
+    if (M == 0) return DSNQ_OK;
+    if (num_pages && !scales) return DSNQ_ERR_INVALID_ARG;
+    if (num_pages > 1 && ld_scale < page_size) return DSNQ_ERR_INVALID_ARG;
+    if (!aligned(scales, 4)) return DSNQ_ERR_MISALIGNED;
+    a.scales = scales;
+    a.ld_scale = ld_scale;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return layout == DSNQ_ROPE_HALF ? launch_write<true, true>(a, s) : launch_write<false, true>(a, s);
+}
+
+extern "C" dsnq_status dsnq_latent_cache_read_fp8(
+    int64_t B, int64_t rows, int64_t K, int64_t P, const void* cache, int64_t num_pages, int64_t page_size, int64_t ld_page,
+    int64_t ld_row, const float* scales, int64_t ld_scale, const int32_t* block_table, int64_t table_width, int64_t ld_table,
+    const int32_t* row_starts, const int32_t* first, void* out, int64_t ldo, void* stream) {
+    if (B < 0 || rows < 0 || K <= 0 || P < 0 || num_pages < 0 || page_size <= 0 || table_width < 0) return DSNQ_ERR_INVALID_ARG;
+    if (K % 16 || P % kChunk || K > kMaxWidth || P > kMaxWidth || K + P > kMaxWidth || B > DSNQ_MAX_REQUESTS || rows > 0x7fffffffLL ||
+        page_size > (1 << 20) || num_pages > 0x7fffffffLL || table_width > 0x7fffffffLL || table_width * page_size > 0x7fffffffLL ||
+        ld_row > (1LL << 40))
+        return DSNQ_ERR_UNSUPPORTED;
+    if (B == 0 || rows == 0) return DSNQ_OK;
+    const int64_t row = K + 2 * P, W = K + P;
+    if (!row_starts || !out || (num_pages && (!cache || !scales)) || (table_width && !block_table)) return DSNQ_ERR_INVALID_ARG;
+    if ((rows > 1 && ldo < W) || (B > 1 && ld_table < table_width) || ld_row < row || ld_page < (page_size - 1) * ld_row + row ||
+        (num_pages > 1 && ld_scale < page_size))
+        return DSNQ_ERR_INVALID_ARG;
+    if (!aligned(cache, 16) || ld_page % 16 || ld_row % 16 || !aligned(scales, 4) || !aligned(block_table, 4) || !aligned(row_starts, 4) ||
+        !aligned(first, 4) || !aligned(out, 16) || ldo % kChunk)
+        return DSNQ_ERR_MISALIGNED;
+    ReadArgs a{};
+    a.cache = static_cast<const uint8_t*>(cache);
+    a.scales = scales;
+    a.ld_page = ld_page; a.ld_row = ld_row; a.ld_scale = ld_scale;
+    a.num_pages = static_cast<int>(num_pages); a.page_size = static_cast<int>(page_size);
+    a.K = static_cast<int>(K); a.W = static_cast<int>(W);
+    a.table = block_table; a.ld_table = ld_table;
+    a.B = static_cast<int>(B); a.width = static_cast<int>(table_width);
+    a.row_starts = row_starts;
+    a.first = first;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.ldo = ldo; a.rows = rows;
+    const uint32_t chunks = static_cast<uint32_t>(W / kChunk);
+    a.recip = static_cast<uint32_t>((0x100000000ull + chunks - 1) / chunks);   // exact for the few thousand items of a CTA
+    a.inject = debug_inject_flags();
+    return launch_result(launch_kernel(latent_cache_read_fp8_kernel, dim3(static_cast<unsigned>((rows + kReadRows - 1) / kReadRows)),
+                                       dim3(kReadThreads), 0, static_cast<cudaStream_t>(stream), a));
 }
 
 extern "C" dsnq_status dsnq_extend_block_tables(

@@ -546,13 +546,138 @@ DSNQ_API dsnq_status dsnq_paged_latent_attention(
     void* stream);
 
 /*
+ * ---- The same cache in 8 bits ----
+ *
+ * A row of the cache stands for s (codes[0:K] | pe[0:P]): K e4m3 codes, P bf16
+ * numbers and one fp32 factor s for all of them.  `cache` holds rows of K + 2 P
+ * bytes, the codes, then the position columns (pages and rows at strides in
+ * bytes); `scales` the factors, row i of page p at scales[p * ld_scale + i].
+ * With 512 latent and 64 position columns a row takes 644 bytes instead of
+ * 1152.  The calls below are this implementation's own.
+ */
+
+/*
+ * dsnq_latent_cache_write into such a cache: the row is formed as there (norm,
+ * rotation) in fp32 and leaves as
+ *   s      = max(max_k |row[k]| / 448, 2^-60),  k < K   (IEEE division)
+ *   code_k = e4m3_rn_satfinite(fp32(row[k] / s)),  pe_k = bf16_rn(fp32(row[K + k] / s))
+ * (a NaN or an infinity among the latent columns makes s NaN, so that the whole
+ * row reads back as NaN; position columns stay finite up to 2^67).
+ *   K            : multiple of 16; P: multiple of 8; K + P <= 1024.
+ *   cache, num_pages, page_size, ld_page, ld_row : bytes, ld_row >= K + 2 P;
+ *                16-byte aligned, strides multiples of 16.
+ *   scales, ld_scale : fp32, ld_scale >= page_size, 4-byte aligned.
+ * Other arguments, alignment and rules as in dsnq_latent_cache_write.
+ */
+DSNQ_API dsnq_status dsnq_latent_cache_write_fp8(
+    int64_t M, int64_t K, int64_t P,
+    const void* kv, int64_t ldkv, const void* pe, int64_t ldpe,
+    int32_t normalize, const void* gamma, float eps,
+    const int64_t* positions, const double* inv_freq,
+    int64_t rope_offset, int64_t rope_dim, dsnq_rope_layout layout, float rope_scale,
+    const int64_t* slots, void* cache, int64_t num_pages, int64_t page_size, int64_t ld_page, int64_t ld_row,
+    float* scales, int64_t ld_scale,
+    void* stream);
+
+/*
+ * Rows of such a cache read back as bf16, request after request: row r with
+ * row_starts[b] <= r < row_starts[b + 1] is token first[b] + r - row_starts[b]
+ * of request b, out[r] = bf16_rn(s * (codes | pe)).  Rows from row_starts[B] on
+ * are left as they were.
+ *   B, rows     : requests (<= DSNQ_MAX_REQUESTS), rows of out.
+ *   K, P        : as in the write.
+ *   block_table, table_width, ld_table : int32 [B, table_width],
+ *                 table_width * page_size < 2^31.
+ *   row_starts  : int32 [B + 1], not decreasing; first: int32 [B], or NULL: 0.
+ *   out, ldo    : bf16 [rows, K + P], 16-byte aligned, ldo a multiple of 8.
+ * A token outside its request's table, or on a page outside [0, num_pages),
+ * reads as zeros and is reported by dsnq_debug_status as DSNQ_ERR_BOUNDS.  out
+ * must not overlap the cache.
+ */
+DSNQ_API dsnq_status dsnq_latent_cache_read_fp8(
+    int64_t B, int64_t rows, int64_t K, int64_t P,
+    const void* cache, int64_t num_pages, int64_t page_size, int64_t ld_page, int64_t ld_row,
+    const float* scales, int64_t ld_scale,
+    const int32_t* block_table, int64_t table_width, int64_t ld_table,
+    const int32_t* row_starts, const int32_t* first,
+    void* out, int64_t ldo,
+    void* stream);
+
+/* Host-only queries: bytes of the workspaces of the two calls below.  Errors as
+ * in those calls.  `bytes` may be NULL. */
+DSNQ_API dsnq_status dsnq_paged_latent_attention_fp8_workspace_bytes(int64_t B, int64_t H, int64_t DV, int64_t table_width,
+                                                                     int64_t page_size, int64_t* bytes);
+DSNQ_API dsnq_status dsnq_shared_prefix_latent_attention_fp8_workspace_bytes(int64_t B, int64_t H, int64_t DV, int64_t prefix_width,
+                                                                             int64_t table_width, int64_t page_size, int64_t* bytes);
+
+/*
+ * dsnq_paged_latent_attention over such a cache:
+ *   z_j = scale * s_j * q[b,h] . (codes_j | pe_j),   j < seq_lens[b]
+ *   out[b,h,:] = sum_j softmax(z)_j s_j codes_j[0:DV],   lse[b,h] = log sum_j exp z_j
+ * q's latent columns are split into two e4m3 numbers each (exact down to 2^-15 of
+ * the head's largest, off by at most 2^-23 of that below); the probabilities
+ * times s_j are rounded to two e4m3 numbers (off by at most 2^-8 of themselves,
+ * as bf16 would be, or 2^-22 of the largest among 32 neighbouring tokens), and
+ * the outputs divided by the sum of the rounded ones; fp32 scores, sums and
+ * accumulation.  An empty request gets zeros
+ * and lse = -infinity.
+ *   K, P, DV    : K a multiple of 128, <= 512; P 0 or 64; DV a multiple of 128,
+ *                 <= K.  A key is K + P columns wide.
+ *   q, ldq_tok, ldq_head : bf16 [B, H, K + P]; a non-finite value makes its head
+ *                 NaN.
+ *   cache, num_pages, page_size, ld_page, ld_row, scales, ld_scale : as above,
+ *                 num_pages >= 1, page_size a multiple of 8, scales 16-byte
+ *                 aligned, ld_scale a multiple of 4.  Scales are in [2^-60,
+ *                 2^119], as the write leaves them (0 counts as a zero row).
+ * Other arguments, page ids outside the cache, workspace and launches as in
+ * dsnq_paged_latent_attention.
+ */
+DSNQ_API dsnq_status dsnq_paged_latent_attention_fp8(
+    int64_t B, int64_t H, int64_t K, int64_t P, int64_t DV,
+    const void* q, int64_t ldq_tok, int64_t ldq_head,
+    const void* cache, int64_t num_pages, int64_t page_size, int64_t ld_page, int64_t ld_row,
+    const float* scales, int64_t ld_scale,
+    const int32_t* block_table, int64_t table_width, int64_t ld_table,
+    const int32_t* seq_lens, float scale,
+    void* out, int64_t ldo_tok, int64_t ldo_head, float* lse, int64_t ldl_tok,
+    void* workspace, int64_t workspace_bytes,
+    void* stream);
+
+/*
+ * The same for a batch whose requests all begin with the same tokens: request
+ * b's tokens are the first prefix_len[0] of prefix_table (int32
+ * [prefix_width]), then the first seq_lens[b] of its own row of block_table.
+ * The prefix is read and multiplied for all requests at once: 64 (request,
+ * head) pairs share each pass over it, so with few heads it costs a fraction of
+ * B separate passes.
+ *   prefix_len  : int32 [1] in device memory, taken as within [0, prefix_width
+ *                 * page_size]; 0: no prefix.
+ *   seq_lens    : tokens behind the prefix; may be 0.
+ *   workspace   : at least dsnq_shared_prefix_latent_attention_fp8_workspace_bytes:
+ *                 the batch's partial results, 4 DV bytes for each (request,
+ *                 head) pair, twice, and some for each worker.
+ * Two launches.  Other arguments as in dsnq_paged_latent_attention_fp8.
+ */
+DSNQ_API dsnq_status dsnq_shared_prefix_latent_attention_fp8(
+    int64_t B, int64_t H, int64_t K, int64_t P, int64_t DV,
+    const void* q, int64_t ldq_tok, int64_t ldq_head,
+    const void* cache, int64_t num_pages, int64_t page_size, int64_t ld_page, int64_t ld_row,
+    const float* scales, int64_t ld_scale,
+    const int32_t* prefix_table, int64_t prefix_width, const int32_t* prefix_len,
+    const int32_t* block_table, int64_t table_width, int64_t ld_table,
+    const int32_t* seq_lens, float scale,
+    void* out, int64_t ldo_tok, int64_t ldo_head, float* lse, int64_t ldl_tok,
+    void* workspace, int64_t workspace_bytes,
+    void* stream);
+
+/*
  * Device status words.  Kernels with bounded waits (the mbarrier waits
  * of the GEMM and the attention) record a timeout there instead of hanging.  In the debug build
  * (libdsnq_debug.so, compiled with DSNQ_DEBUG) every kernel also checks the
  * indices of its memory accesses against the buffer extents its arguments
  * describe; a failed check skips the access and records a bounds error.
  * In both builds a cache slot or page id that lies outside the cache records
- * one too (dsnq_latent_cache_write, dsnq_paged_latent_attention).
+ * one too (the calls that write, read or attend to a cache).
  * This call synchronizes `stream`, reads the words of the current device,
  * clears them and returns DSNQ_OK, DSNQ_ERR_TIMEOUT, DSNQ_ERR_BOUNDS (a
  * timeout takes precedence when both are recorded), or DSNQ_ERR_CUDA if the
