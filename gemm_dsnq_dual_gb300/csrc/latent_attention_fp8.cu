@@ -15,15 +15,15 @@
 //      at most 2^-15, 2^-23 of the largest.  hi and lo are stacked along N, so a
 //      product reads a tile of the cache once.
 //   p s: x = p_j s_j 2^-T with T a power of two per head and block of 32 tokens
-//      such that the block's largest x lies in (128, 256]; the products put 2^T
+//      such that the block's largest x lies in [64, 256]; the products put 2^T
 //      back (block scales along K).  Rounded by at most 2^-8 of x (2^-4 of hi's
 //      remainder, which is at most 2^-4 of x) or 2^-15 (half of lo's last bit),
-//      less than 2^-22 of the block's largest.
+//      at most 2^-21 of the block's largest.
 // The position columns are a bf16 product into the same accumulators.  Scores,
 // softmax statistics and outputs are fp32.  The outputs are divided by the sum
 // of the p that the rounded x stand for, so that the weights add up to one
-// (those with x below 2^-6 count unrounded: a token whose scale is far below its
-// neighbours' may have a large p and no value to speak of).
+// (those of tokens whose scale is below 2^-8 of their block's largest count
+// unrounded: they may have a large p and no value to speak of).
 //
 // One CTA, 64 heads, tiles of 128 tokens:
 //   S^T [128 tokens x (64 hi | 64 lo)]  = C Q^T        M = 128: a thread has a token
@@ -46,8 +46,9 @@
 //
 // Warps: 0 copies tiles (TMA), 1 issues S^T, 2 issues O^T, 4..11 do the softmax:
 // warp w has tokens 32 (w % 4) .. of a tile (the TMEM lanes it can reach, and one
-// block of 32 of the scales) and one half of the heads.  They also split q, for
-// the next job while the last product of this one runs, and write the output.
+// block of 32 of the scales) and one half of the heads.  They also split q,
+// for the next job while the last product of this one runs, and write the
+// output.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -221,24 +222,18 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
            static_cast<uint64_t>(swizzle) << 61;
 }
 
-__device__ __forceinline__ void tmem_ld8_issue(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(taddr)
                  : "memory");
 }
-__device__ __forceinline__ void tmem_ld8_wait(uint32_t (&r)[8]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-                 :
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
-                 : "memory");
-}
-
 __device__ __forceinline__ float redux_max(float v) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -247,35 +242,50 @@ __device__ __forceinline__ float redux_max(float v) {
 
 // hi = e4m3(x), lo = e4m3(32 (x - hi)) of two numbers (|x| <= 256: x - hi is
 // exact and at most 8); `sum` gets hi + lo / 32.
-__device__ __forceinline__ uint32_t e4m3x2_of(__half2 x) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
-    return r;
-}
+// (The conversion from fp32 pairs takes a third of the time of the one from half
+// pairs, which the remainder uses because it is one.)
 __device__ __forceinline__ __half2 half2_of(uint32_t codes) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
     return *reinterpret_cast<const __half2*>(&r);
 }
-__device__ __forceinline__ void split2(__half2 x, uint32_t& hi, uint32_t& lo, __half2& sum) {
-    hi = e4m3x2_of(x);
-    const __half2 h = half2_of(hi);
-    lo = e4m3x2_of(__hmul2(__hsub2(x, h), __float2half2_rn(32.f)));
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo, __half2& sum) {
+    uint16_t c;
+    hi = e4m3x2(x);
+    const __half2 h = half2_of(hi), d = __hmul2(__hsub2(__float22half2_rn(x), h), __float2half2_rn(32.f));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<const uint32_t*>(&d)));
+    lo = c;
     sum = __hfma2(half2_of(lo), __float2half2_rn(0.03125f), h);
 }
 
-// Barrier of the softmax warps; returns whether any thread passed true.  A
-// named barrier has no time limit, so every softmax warp reaches every one of
-// them whether or not its waits succeeded (the counts depend on the run alone).
-__device__ __forceinline__ bool soft_sync_or(bool v) {
+// lg2.approx: off by at most 2^-22 here, and its inverse is taken from itself.
+__device__ __forceinline__ float log2_fast(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Registers of a copying or issuing thread and of a softmax thread: together
+// those that the CTA is launched with (168 each).  With less than ~200 the
+// softmax keeps some of its sums in local memory, whose loads wait behind the
+// products' reads of shared memory.
+constexpr int kRegsIssue = 64, kRegsSoft = 216;
+static_assert(128 * kRegsIssue + kSoftThreads * kRegsSoft <= kThreads * 168, "registers of the CTA at its launch");
+
+// Barriers of all softmax warps, and of the four that have the same heads
+// (returns whether any of their threads passed true).  A named barrier has no
+// time limit, so every softmax warp reaches every one of them whether or not
+// its waits succeeded (the counts depend on the run alone).
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool half_sync_or(int half, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(v))
+        : "r"(static_cast<uint32_t>(v)), "r"(2 + half)
         : "memory");
     return r != 0;
 }
@@ -357,8 +367,8 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     uint8_t* sf_s = misc;                                  // [32][16 B] block scales of p s
     float* sc_s = reinterpret_cast<float*>(sf_s + 512);    // [kScaleSlots][128] row scales
     float* cq_s = sc_s + kScaleSlots * kTile;              // [2][64] factor of a head's scores
-    float* bc_s = cq_s + 2 * kHeads;                       // [8 warps][32]{T, 2^(T - M)}; at a job's end [2 halves][4][32]{l, lr}
-    float* mx_s = bc_s + kSoftWarps * 64;                  // [2 halves][4][32]
+    float* bc_s = cq_s + 2 * kHeads;                       // [8 warps][64] 2^(T - M); at a job's end {l, lr}
+    float* mx_s = bc_s + kSoftWarps * 64;                  // [8 warps][32]
     float* al_s = mx_s + kSoftWarps * 32;                  // [64] factors of O
     uint64_t* full = reinterpret_cast<uint64_t*>(al_s + kHeads);   // [kMaxSlots]
     uint64_t* empty = full + kMaxSlots;                    // [kMaxSlots]
@@ -513,6 +523,8 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, tmo));
     };
 
+    if (warp < kSoftWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
         // Chunks in the order of their use by S^T: the first codes (with the
@@ -654,8 +666,10 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             tc_commit(smem_u32(&drain[1]));
             wait_drain(smem_u32(&drain[1]), 0, tmo);
         }
-    } else if (warp >= kSoftWarp0) {
+    }
+    } else {
         // ------------------------------------- softmax, splitting q, output
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         const int quad = warp & 3, sw = warp - kSoftWarp0, half = sw >> 2;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const int st = threadIdx.x - kSoftWarp0 * 32;      // 0..255
@@ -673,7 +687,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         auto split_q = [&](const Run& r, int buf) {
             const bool prefix = r.j < p.NP;
             const int row0 = prefix ? (r.j * p.G + g) * kHeads : g * kHeads;
-            constexpr int kAhead = 4;
+            constexpr int kAhead = 2;
             for (int i0 = sw; i0 < r.hp; i0 += kAhead * kSoftWarps) {
                 uint4 x[kAhead][2], e[kAhead];
 #pragma unroll
@@ -721,8 +735,8 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                         uint32_t h0, h1, l0, l1;
                         __half2 s;
                         const uint32_t a = xw[2 * k], b = xw[2 * k + 1];
-                        split2(__floats2half2_rn(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv), h0, l0, s);
-                        split2(__floats2half2_rn(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv), h1, l1, s);
+                        split2(make_float2(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv), h0, l0, s);
+                        split2(make_float2(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv), h1, l1, s);
                         hi[k] = h0 | h1 << 16;
                         lo[k] = l0 | l1 << 16;
                     }
@@ -771,133 +785,161 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             }
             const int ng = run.hp >> 4;                    // groups of eight heads of this half
             const int h0 = half * 8 * ng;                  // its first head
+            const bool mine = lane < 8 * ng;               // this lane has a head: h0 + lane
             const float* cq = cq_s + (nq & 1) * kHeads + h0;
-            float l[32], lr[32];                           // per head, this token's share of the sums of p: unrounded, rounded
+            float2 l[16], lr[16];                          // per head, this token's share of the sums of p: unrounded, rounded
 #pragma unroll
-            for (int k = 0; k < 32; ++k) l[k] = lr[k] = 0.f;
+            for (int k = 0; k < 16; ++k) l[k] = lr[k] = make_float2(0.f, 0.f);
             float M = 0.f;                                 // of head h0 + lane: what O and the sums are relative to (log2)
             for (int i = 0; i < run.n; ++i, ++n, ch.next(p)) {
                 const int valid = min(kTile, run.len - (run.t0 + i) * kTile);
+                const bool in = tok < valid;
                 int slot0;
                 uint32_t parity0;
                 ch.at(p, 0, slot0, parity0);
-                ok = ok && wait_uniform(smem_u32(&full[slot0]), parity0);
-                const bool in = tok < valid;
-                const float sj = ok && in ? sc_s[(n & (kScaleSlots - 1)) * kTile + tok] : 1.f;
-                const float sl = fmaxf(sj, kLeastScale), lg = log2f(sl), inv_s = 1.0f / sl;
+                // Shared memory answers in hundreds of cycles while the products
+                // read it, so what can be asked for early is, and as little as
+                // possible lies between S^T and the product that waits for p s.
+                const bool landed = mbar_test(smem_u32(&full[slot0]), parity0);
                 ok = ok && wait_uniform(smem_u32(sfull), n & 1);
+                if (!__all_sync(0xffffffffu, landed)) ok = ok && wait_uniform(smem_u32(&full[slot0]), parity0);
                 tc_fence_after();
-                float z[32];                               // log2 of p s, up to the reference
+                float2 z[16];                              // log2 of p s, up to the reference; then x
+                float lg;
+                {
+                    const float sj = ok && in ? sc_s[(n & (kScaleSlots - 1)) * kTile + tok] : 1.f;
+                    lg = log2_fast(fmaxf(sj, kLeastScale));
+                    const float2 s2 = make_float2(sj, sj), lg2 = make_float2(lg, lg), down = make_float2(0.03125f, 0.03125f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k >= ng) break;
-                    uint32_t a[8], c[8];
-                    tmem_ld8_issue(tl + kTmemS + h0 + 8 * k, a);
-                    tmem_ld8_issue(tl + kTmemS + run.hp + h0 + 8 * k, c);
-                    const float4 f0 = *reinterpret_cast<const float4*>(cq + 8 * k), f1 = *reinterpret_cast<const float4*>(cq + 8 * k + 4);
-                    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-                    tmem_ld8_wait(a);
-                    tmem_ld8_wait(c);
+                    for (int k = 0; k < 2; ++k) {
+                        if (2 * k >= ng) break;
+                        uint32_t a[16], c[16];
+                        tmem_ld16_issue(tl + kTmemS + h0 + 16 * k, a);
+                        tmem_ld16_issue(tl + kTmemS + run.hp + h0 + 16 * k, c);
+                        tmem_ld16_wait(a);
+                        tmem_ld16_wait(c);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float s = fmaf(__uint_as_float(c[j]), 0.03125f, __uint_as_float(a[j]));
-                        z[8 * k + j] = in ? fmaf(s, f[j] * sj, lg) : kNegInf;
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 f = *reinterpret_cast<const float4*>(cq + 16 * k + 4 * j);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int e = 4 * j + 2 * u;
+                                const float2 s = fma2(make_float2(__uint_as_float(c[e]), __uint_as_float(c[e + 1])), down,
+                                                      make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])));
+                                z[8 * k + 2 * j + u] = fma2(s, mul2(u ? make_float2(f.z, f.w) : make_float2(f.x, f.y), s2), lg2);
+                            }
+                        }
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(sempty));
-                // The block's largest value of each head, head h0 + k's in lane k.
-                float top = kNegInf;
+                const bool pv_done = n == 0 || mbar_test(smem_u32(pempty), (n & 1) ^ 1);
+                if (valid < kTile) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    if (k >= 8 * ng) break;
-                    const float t = redux_max(z[k]);
-                    top = lane == k ? t : top;
+                    for (int k = 0; k < 16; ++k)
+                        if (!in) z[k] = make_float2(kNegInf, kNegInf);
                 }
-                // x = 2^(z - T) <= 256
-                float T = top == kNegInf ? kNegInf : ceilf(top) - 8.f;
-                const bool mine = lane < 8 * ng;
+                // T of each head: x = 2^(z - T) <= 256, the block's largest at
+                // least 64.  (Rounded to a whole number by adding 1.5 2^23.)
+                uint32_t hi[8], lo[8];                     // four heads each
+                __half2 sum[16];                           // x as rounded
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (k >= 2 * ng) break;
+                    float2 T[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 top = make_float2(redux_max(z[2 * k + j].x), redux_max(z[2 * k + j].y));
+                        T[j] = add2(add2(add2(top, make_float2(-7.5f, -7.5f)), make_float2(0x1.8p23f, 0x1.8p23f)),
+                                    make_float2(-0x1.8p23f, -0x1.8p23f));
+                    }
+                    if (lane == 0) *reinterpret_cast<float4*>(bc + 4 * k) = make_float4(T[0].x, T[0].y, T[1].x, T[1].y);
+                    uint32_t a2[2], c2[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int e = 2 * k + j;
+                        const float2 y = fma2(T[j], make_float2(-1.f, -1.f), z[e]);
+                        z[e] = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                        if (valid < kTile && !in) z[e] = make_float2(0.f, 0.f);   // T may be -infinity too
+                        split2(z[e], a2[j], c2[j], sum[e]);
+                    }
+                    hi[k] = __byte_perm(a2[0], a2[1], 0x5410);
+                    lo[k] = __byte_perm(c2[0], c2[1], 0x5410);
+                }
+                __syncwarp();
+                const float top = mine ? bc[lane] : kNegInf;   // head h0 + lane's
+                // What O and the sums are relative to.
+                bool raise = false;
                 if (i == 0) {
-                    mx_s[sw * 32 + lane] = T;
-                    soft_sync_or(false);
-                    const float* mx = mx_s + half * 128 + lane;
-                    M = fmaxf(fmaxf(mx[0], mx[32]), fmaxf(mx[64], mx[96]));
-                    if (M == kNegInf) M = 0.f;
-                } else if (soft_sync_or(mine && T - M > kRaise)) {
-                    // Rare: some block grew too far; O and the sums follow.
-                    mx_s[sw * 32 + lane] = T;
-                    soft_sync_or(false);
+                    mx_s[sw * 32 + lane] = top;
+                    soft_sync();
+                } else {
+                    raise = half_sync_or(half, top - M > kRaise);
+                    if (raise) {
+                        mx_s[sw * 32 + lane] = top;
+                        half_sync_or(half, false);
+                    }
+                }
+                if (i == 0 || raise) {
                     const float* mx = mx_s + half * 128 + lane;
                     const float to = fmaxf(fmaxf(mx[0], mx[32]), fmaxf(mx[64], mx[96]));
-                    float alpha = 1.f;
-                    if (mine && to - M > kRaise) {
-                        alpha = exp2_fast(M - to);
-                        M = to;
-                    }
-                    if (mine) al_s[h0 + lane] = alpha;     // the same from each of the half's four warps
-                    __syncwarp();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (k >= 8 * ng) break;
-                        l[k] *= al_s[h0 + k];
-                        lr[k] *= al_s[h0 + k];
-                    }
-                    ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
-                    tc_fence_after();
-                    for (int blk = 0; ok && blk < p.nblk; ++blk)
-                        for (int k = 0; k < ng; ++k) {
-                            uint32_t r[8];
-                            const uint32_t at = tl + blk * kHeads + h0 + 8 * k;
-                            tmem_ld8_issue(at, r);
-                            tmem_ld8_wait(r);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * al_s[h0 + 8 * k + j]);
-                            tmem_st8(at, r);
+                    if (i == 0) {
+                        M = to == kNegInf ? 0.f : to;
+                    } else {
+                        // Rare: some block grew too far; O and the sums follow.
+                        float alpha = 1.f;
+                        if (mine && to - M > kRaise) {
+                            alpha = exp2_fast(M - to);
+                            M = to;
                         }
-                    tmem_wait_st();
-                }
-                if (T == kNegInf) T = M;                   // nothing in this block: x = 0
-                const int up = static_cast<int>(fmaxf(fminf(T - M, 127.f), -126.f));
-                bc[lane] = T;
-                bc[32 + lane] = __int_as_float((up + 127) << 23);
-                __syncwarp();
-                uint32_t hi[8], lo[8];
+                        if (mine) al_s[h0 + lane] = alpha; // the same from each of the half's four warps
+                        __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k >= ng) break;
-                    const float4 t0 = *reinterpret_cast<const float4*>(bc + 8 * k), t1 = *reinterpret_cast<const float4*>(bc + 8 * k + 4);
-                    const float4 f0 = *reinterpret_cast<const float4*>(bc + 32 + 8 * k), f1 = *reinterpret_cast<const float4*>(bc + 36 + 8 * k);
-                    const float t[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
-                    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                        for (int k = 0; k < 16; ++k) {
+                            if (k >= 4 * ng) break;
+                            const float2 by = *reinterpret_cast<const float2*>(al_s + h0 + 2 * k);
+                            l[k] = mul2(l[k], by);
+                            lr[k] = mul2(lr[k], by);
+                        }
+                        ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
+                        tc_fence_after();
+                        for (int blk = 0; ok && blk < p.nblk; ++blk)
+                            for (int k = 0; k < 2 * ng; ++k) {
+                                uint32_t r[4];
+                                const uint32_t at = tl + blk * kHeads + h0 + 4 * k;
+                                tmem_ld4(at, r);
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const float x0 = exp2_fast(z[8 * k + j] - t[j]), x1 = exp2_fast(z[8 * k + j + 1] - t[j + 1]);
-                        uint32_t a, c;
-                        __half2 s;
-                        split2(__floats2half2_rn(x0, x1), a, c, s);
-                        const float2 r = __half22float2(s);
-                        const int at = 2 * k + (j >> 2);
-                        hi[at] = j & 2 ? hi[at] | a << 16 : a;
-                        lo[at] = j & 2 ? lo[at] | c << 16 : c;
-                        const float w0 = f[j] * inv_s, w1 = f[j + 1] * inv_s;
-                        l[8 * k + j] = fmaf(x0, w0, l[8 * k + j]);
-                        l[8 * k + j + 1] = fmaf(x1, w1, l[8 * k + j + 1]);
-                        lr[8 * k + j] = fmaf(x0 < 0x1p-6f ? x0 : r.x, w0, lr[8 * k + j]);
-                        lr[8 * k + j + 1] = fmaf(x1 < 0x1p-6f ? x1 : r.y, w1, lr[8 * k + j + 1]);
+                                for (int j = 0; j < 4; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * al_s[h0 + 4 * k + j]);
+                                tmem_st4(at, r);
+                            }
+                        tmem_wait_st();
                     }
                 }
-                if (n > 0) ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
-                __syncwarp();
+                const int up = static_cast<int>(fmaxf(fminf((top == kNegInf ? M : top) - M, 127.f), -126.f));
+                bc[32 + lane] = __int_as_float((up + 127) << 23);
+                if (!__all_sync(0xffffffffu, pv_done)) ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
                 if (ok) {
                     uint8_t* at = p_s + tok * 64;
+                    // A quarter of the warp's lanes fill all banks with 16 bytes each.
+                    const int swz = (tok >> 1) & 3;
+                    if (ng & 1) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k >= ng) break;
-                        const int v = half * ng + k;       // eight heads: eight bytes
-                        const int off = (((v >> 1) ^ ((tok >> 1) & 3)) << 4) + (v & 1) * 8;
-                        *reinterpret_cast<uint2*>(at + off) = make_uint2(hi[2 * k], hi[2 * k + 1]);
-                        *reinterpret_cast<uint2*>(at + kPBytes + off) = make_uint2(lo[2 * k], lo[2 * k + 1]);
+                        for (int k = 0; k < 4; ++k) {
+                            if (k >= ng) break;
+                            const int v = half * ng + k;   // eight heads: eight bytes
+                            const int off = (((v >> 1) ^ swz) << 4) + (v & 1) * 8;
+                            *reinterpret_cast<uint2*>(at + off) = make_uint2(hi[2 * k], hi[2 * k + 1]);
+                            *reinterpret_cast<uint2*>(at + kPBytes + off) = make_uint2(lo[2 * k], lo[2 * k + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if (2 * k >= ng) break;
+                            const int off = ((half * (ng >> 1) + k) ^ swz) << 4;
+                            *reinterpret_cast<uint4*>(at + off) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                            *reinterpret_cast<uint4*>(at + kPBytes + off) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                        }
                     }
                     if (mine) {
                         const int h = h0 + lane;
@@ -923,6 +965,25 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(pfull));
+                // The sums, while the product runs.  Tokens whose values are far
+                // below their neighbours' count unrounded.
+                const bool tiny = lg < redux_max(in ? lg : -1.0e30f) - 8.f, any_tiny = __any_sync(0xffffffffu, tiny);
+                const float inv_s = exp2_fast(-lg);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (k >= 2 * ng) break;
+                    const float4 f = *reinterpret_cast<const float4*>(bc + 32 + 4 * k);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int e = 2 * k + j;
+                        const float2 w = mul2(j ? make_float2(f.z, f.w) : make_float2(f.x, f.y), make_float2(inv_s, inv_s));
+                        float2 r = __half22float2(sum[e]);
+                        if (any_tiny && tiny) r = z[e];
+                        l[e] = fma2(z[e], w, l[e]);
+                        lr[e] = fma2(r, w, lr[e]);
+                    }
+                }
+                __syncwarp();                              // bc is read
             }
             // S^T of the last tile is done with q: the next job's takes its place
             // while the last product runs.
@@ -934,18 +995,24 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             }
             // ---- output of the job (or of this worker's part of it)
             // Sums over the tokens: lane k gets head h0 + k's.
+            float v[32], u[32];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                v[2 * k] = l[k].x; v[2 * k + 1] = l[k].y;
+                u[2 * k] = lr[k].x; u[2 * k + 1] = lr[k].y;
+            }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
                 for (int k = 0; k < o; ++k) {
-                    const bool hi_half = lane & o;
-                    const float a = hi_half ? l[k] : l[k + o], c = hi_half ? lr[k] : lr[k + o];
-                    l[k] = (hi_half ? l[k + o] : l[k]) + __shfl_xor_sync(0xffffffffu, a, o);
-                    lr[k] = (hi_half ? lr[k + o] : lr[k]) + __shfl_xor_sync(0xffffffffu, c, o);
+                    const bool odd = lane & o;
+                    const float a = odd ? v[k] : v[k + o], c = odd ? u[k] : u[k + o];
+                    v[k] = (odd ? v[k + o] : v[k]) + __shfl_xor_sync(0xffffffffu, a, o);
+                    u[k] = (odd ? u[k + o] : u[k]) + __shfl_xor_sync(0xffffffffu, c, o);
                 }
-            bc[lane] = l[0];
-            bc[32 + lane] = lr[0];
-            soft_sync_or(false);                           // bc is next written after another tile's barrier
+            bc[lane] = v[0];
+            bc[32 + lane] = u[0];
+            half_sync_or(half, false);                     // bc is next written after the next job's barrier
             float ls = 0.f, lrs = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -953,7 +1020,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 lrs += bc_s[(half * 4 + q) * 64 + 32 + lane];
             }
             // A part's weights add up to its unrounded sum, which the join divides by.
-            if (lane < 8 * ng) al_s[h0 + lane] = lrs > 0.f || lrs != lrs ? __fdividef(whole ? 1.0f : ls, lrs) : 0.f;
+            if (mine) al_s[h0 + lane] = lrs > 0.f || lrs != lrs ? __fdividef(whole ? 1.0f : ls, lrs) : 0.f;
             __syncwarp();                                  // the same from each of the half's four warps
             ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
             tc_fence_after();
@@ -988,13 +1055,14 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     __nv_bfloat16* o = p.out + b * p.ldo_b + blk * 128 + quad * 32 + (lane & 3) * 8;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        if (j >= ng) break;
                         const int hl = j * 8 + (lane >> 2), head = h0 + hl;
                         uint4 v;
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                                      : "r"(stage + hl * 64 + (((lane & 3) ^ ((hl >> 1) & 3)) << 4))
                                      : "memory");
-                        if (j < ng && head < run.count && bounds_ok(b >= 0 && b < p.B))
+                        if (head < run.count && bounds_ok(b >= 0 && b < p.B))
                             *reinterpret_cast<uint4*>(o + static_cast<int64_t>(g * kHeads + head) * p.ldo_h) = v;
                     }
                     __syncwarp();
@@ -1003,26 +1071,19 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 // A part, in the order the registers hold it: 512 bytes a store.
                 const int64_t slot = part_slot(p, w, run.j, run.j == j_first, g);
                 float4* o = reinterpret_cast<float4*>(p.part_o) + slot * p.nblk * 16 * 128 + quad * 32 + lane;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k >= ng || h0 + 8 * k >= run.count) break;
-                    const float4 f0 = *reinterpret_cast<const float4*>(al_s + h0 + 8 * k);
-                    const float4 f1 = *reinterpret_cast<const float4*>(al_s + h0 + 8 * k + 4);
+                for (int k = 0; k < 2 * ng && h0 + 4 * k < run.count; ++k) {
+                    const float4 f = *reinterpret_cast<const float4*>(al_s + h0 + 4 * k);
                     for (int blk = 0; blk < p.nblk; ++blk) {
-                        uint32_t x[8];
-                        tmem_ld8_issue(tl + blk * kHeads + h0 + 8 * k, x);
-                        tmem_ld8_wait(x);
-                        float4* at = o + (blk * 16 + (h0 >> 2) + 2 * k) * 128;
-                        at[0] = make_float4(__uint_as_float(x[0]) * f0.x, __uint_as_float(x[1]) * f0.y, __uint_as_float(x[2]) * f0.z,
-                                            __uint_as_float(x[3]) * f0.w);
-                        at[128] = make_float4(__uint_as_float(x[4]) * f1.x, __uint_as_float(x[5]) * f1.y,
-                                              __uint_as_float(x[6]) * f1.z, __uint_as_float(x[7]) * f1.w);
+                        uint32_t x[4];
+                        tmem_ld4(tl + blk * kHeads + h0 + 4 * k, x);
+                        o[(blk * 16 + (h0 >> 2) + k) * 128] = make_float4(__uint_as_float(x[0]) * f.x, __uint_as_float(x[1]) * f.y,
+                                                                          __uint_as_float(x[2]) * f.z, __uint_as_float(x[3]) * f.w);
                     }
                 }
-                if (quad == 0 && lane < 8 * ng) p.part_ml[slot * kHeads + h0 + lane] = make_float2(M, ls);
+                if (quad == 0 && mine) p.part_ml[slot * kHeads + h0 + lane] = make_float2(M, ls);
             }
             const int head = g * kHeads + h0 + lane;
-            if (whole && p.lse && quad == 0 && lane < 8 * ng && head < p.H)
+            if (whole && p.lse && quad == 0 && mine && head < p.H)
                 p.lse[b * p.ldl_b + head] = ls == 0.f ? kNegInf : (M + log2f(ls)) * kLn2;
             tc_fence_before();
         }
