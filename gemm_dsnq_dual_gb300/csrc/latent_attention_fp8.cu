@@ -44,7 +44,7 @@
 // The prefix: its rows are the (request, head) pairs of the batch laid end to
 // end, so every tile of the prefix serves 64 rows whatever the number of heads.
 //
-// Warps: 0 copies tiles (TMA), 1 issues S^T, 2 issues O^T, 4..11 do the softmax:
+// Warps: 0 and 3 copy tiles (TMA), 1 issues S^T, 2 issues O^T, 4..11 do the softmax:
 // warp w has tokens 32 (w % 4) .. of a tile (the TMEM lanes it can reach, and one
 // block of 32 of the scales) and one half of the heads.  They also split q,
 // for the next job while the last product of this one runs, and write the
@@ -73,8 +73,8 @@ constexpr int kChunkBytes = kTile * 128;    // 128 bytes of each row of a tile
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSoftWarp0 = 4, kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
-constexpr int kMaxSlots = 13;               // slots of the ring of chunks
-constexpr int kScaleSlots = 4;              // tiles whose row scales are kept; the ring holds at most three tiles
+constexpr int kMaxSlots = 13;               // slots of the rings of chunks
+constexpr int kScaleSlots = 4;              // tiles whose row scales are kept; the rings hold at most three tiles
 constexpr int kMaxCtas = 160;               // bound of workers x head groups
 constexpr int kTmemCols = 512;
 constexpr int kTmemS = 256;                 // first column of S^T
@@ -103,7 +103,8 @@ struct Params {
     int64_t cap, prefix_cap;          // tokens the tables can hold
     int cc, pe, nblk;                 // 128-code chunks of a row, position chunk, 128-column blocks of the value
     int q_rows;                       // rows of hi (and of lo) that a chunk of q has room for
-    int slots, twin;                  // slots of the ring; 1: position columns share a slot with the last codes
+    int slots, odd_slots;             // slots of both rings, and of the odd chunks'
+    int twin;                         // position columns share a slot with the last codes
     float scale_log2;
     __nv_bfloat16* out;
     int64_t ldo_b, ldo_h;
@@ -137,11 +138,13 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(chunk), "r"(group), "r"(page), "l"(policy)
         : "memory");
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
-        : "memory");
+// 16 bytes into shared memory, and an arrival on the barrier when this thread's
+// copies so far are there.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Instruction descriptors: D fp32, M = 128.  e4m3 x e4m3, both K-major; bf16 x
@@ -291,15 +294,18 @@ __device__ __forceinline__ bool half_sync_or(int half, bool v) {
 }
 
 // Where the chunks of the worker's n-th tile lie: chunk c of a tile is its first
-// codes (c = 0), its position columns (c = 1, if any), its other codes.  They go
-// around the ring one after the other; S^T of a tile needs all of them while
-// the codes of the tile before wait for its product with p s, so there must be
-// room for two tiles.  With 512 codes, position columns and more than 32 heads
-// there is not, by one slot: there (`twin`) a tile has four slots, and the last
-// codes follow the position columns, which S^T is done with early, in one slot.
+// codes (c = 0), its position columns (c = 1, if any), its other codes.  Each of
+// the two copying warps has a ring of its own, the even chunks' and the odd
+// ones' (a slot's next copy is then always issued by the warp that waited for
+// the one before: with one ring the parity of a phase would not say which pass
+// it is).  S^T of a tile needs all of its chunks while the codes of the tile
+// before wait for their product with p s, so there must be room for two tiles.
+// With 512 codes, position columns and more than 32 heads there is not, by one
+// slot or two: there (`twin`) a tile has four slots, and the last codes follow
+// the position columns, which S^T is done with early, in one slot.
 struct Chunks {
-    int i = 0;
-    uint32_t pass = 0, n = 0;
+    int i[2] = {0, 0};
+    uint32_t pass[2] = {0, 0}, n = 0;
     __device__ __forceinline__ void at(const Params& p, int c, int& slot, uint32_t& parity) const {
         if (p.twin) {
             const int pos = c == 4 ? 1 : c;
@@ -307,20 +313,30 @@ struct Chunks {
             parity = pos == 1 ? (c == 4) : (n >> 1) & 1;
             return;
         }
-        slot = i + c;
-        parity = pass;
-        if (slot >= p.slots) {
-            slot -= p.slots;
+        const bool odd = c & 1;
+        const int size = odd ? p.odd_slots : p.slots - p.odd_slots;
+        slot = (odd ? i[1] : i[0]) + (c >> 1);
+        parity = odd ? pass[1] : pass[0];
+        if (slot >= size) {
+            slot -= size;
             parity ^= 1;
         }
+        if (odd) slot += p.slots - p.odd_slots;
     }
+    // The copying warp of a chunk.
+    static __device__ __forceinline__ int ring(const Params& p, int c) { return p.twin && c == 4 ? 1 : c & 1; }
     __device__ __forceinline__ void next(const Params& p) {
         ++n;
         if (p.twin) return;
-        i += p.cc + p.pe;
-        if (i >= p.slots) {
-            i -= p.slots;
-            pass ^= 1;
+        const int cpt = p.cc + p.pe;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int size = r ? p.odd_slots : p.slots - p.odd_slots;
+            i[r] += (cpt + 1 - r) >> 1;
+            if (i[r] >= size && size > 0) {
+                i[r] -= size;
+                pass[r] ^= 1;
+            }
         }
     }
 };
@@ -372,7 +388,8 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     float* al_s = mx_s + kSoftWarps * 32;                  // [64] factors of O
     uint64_t* full = reinterpret_cast<uint64_t*>(al_s + kHeads);   // [kMaxSlots]
     uint64_t* empty = full + kMaxSlots;                    // [kMaxSlots]
-    uint64_t* qfull = empty + kMaxSlots;
+    uint64_t* scfull = empty + kMaxSlots;                  // [kScaleSlots]
+    uint64_t* qfull = scfull + kScaleSlots;
     uint64_t* sfull = qfull + 1;
     uint64_t* sempty = sfull + 1;
     uint64_t* pfull = sempty + 1;
@@ -392,6 +409,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
+        for (int s = 0; s < kScaleSlots; ++s) mbar_init(smem_u32(&scfull[s]), 32);
         mbar_init(smem_u32(qfull), kSoftWarps);
         mbar_init(smem_u32(sfull), 1);
         mbar_init(smem_u32(sempty), kSoftWarps);
@@ -525,10 +543,11 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
 
     if (warp < kSoftWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 0) {
-        // ------------------------------------------------------- TMA producer
-        // Chunks in the order of their use by S^T: the first codes (with the
-        // tile's row scales), the position columns, whose slot is free again
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------ TMA producers
+        // Chunks in the order of their use by S^T, every other one from each of
+        // the two warps (a copy takes a warp some 50 cycles, and small pages make
+        // many): the first codes (and the tile's row scales), the position columns, whose slot is free again
         // when S^T is done with them, the other codes.  A request's tiles pass
         // through L2 once, so they leave it first; the prefix's are read by
         // every group of rows.
@@ -538,7 +557,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         const int pieces = kTile / p.box_rows;             // copies of a chunk (1, 2, 4, 8 or 16)
         const int batch = 32 / pieces;                     // tiles whose table entries the lanes hold
         Chunks ch;
-        bool ok = true, skip = (p.inject & kInjectSkipLoad) != 0;
+        bool ok = true, skip = warp == 0 && (p.inject & kInjectSkipLoad) != 0;
         for (; ok && run.next(p, g); run.advance()) {
             if (!run.live()) continue;
             const bool prefix = run.j < p.NP;
@@ -564,8 +583,8 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 const int live = min(pieces, (run.len - tok0 + p.box_rows - 1) / p.box_rows);
                 const int id = __shfl_sync(0xffffffffu, ids, (i % batch) * pieces + (lane & (pieces - 1)));
                 const int in_page = (tok0 + lane * p.box_rows) % p.page_size;
-                const unsigned good = __ballot_sync(0xffffffffu, lane < live && id < p.num_pages);
                 for (int c = 0; c < cpt; ++c) {
+                    if (Chunks::ring(p, c) != (warp == 3)) continue;
                     const int chunk = c == 0 ? 0 : !p.pe ? c : c == 1 ? p.cc : c - 1;
                     int slot;
                     uint32_t parity;
@@ -574,22 +593,28 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     if (!ok) break;
                     const uint32_t fb = smem_u32(&full[slot]);
                     if (!skip) {                           // test hook: the first chunk never comes, the waits on it run out
-                        float* sc = sc_s + (ch.n & (kScaleSlots - 1)) * kTile + lane * p.box_rows;
-                        if (c == 0 && lane < live && id >= p.num_pages)
-                            for (int k = 0; k < p.box_rows; ++k) sc[k] = 0.f;
+                        if (lane == 0) mbar_arrive_expect_tx(fb, live * p.box_rows * 128);
                         __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_expect_tx(fb, live * p.box_rows * 128 + (c == 0 ? __popc(good) * p.box_rows * 4 : 0));
-                        __syncwarp();
-                        if (lane < live) {
+                        if (lane < live)
                             tma_load_5d(smem_u32(ring) + slot * kChunkBytes + lane * p.box_rows * 128, &map_c, fb, chunk, in_page / 8, id,
                                         policy);
-                            if (c == 0 && id < p.num_pages)
-                                bulk_load(smem_u32(sc), p.scales + static_cast<int64_t>(id) * p.ld_scale + in_page, p.box_rows * 4, fb,
-                                          policy);
-                        }
                     }
                     skip = false;
+                    if (c == 0) {
+                        // Four row scales a lane.  (The tile that had their place
+                        // has gone, since this chunk's slot is free.)
+                        const int own = lane * 4 / p.box_rows;
+                        const int page = __shfl_sync(0xffffffffu, id, own), first = __shfl_sync(0xffffffffu, in_page, own);
+                        float* sc = sc_s + (ch.n & (kScaleSlots - 1)) * kTile + lane * 4;
+                        const uint32_t sb = smem_u32(&scfull[ch.n & (kScaleSlots - 1)]);
+                        if (own < live && page < p.num_pages) {
+                            copy16(smem_u32(sc), p.scales + static_cast<int64_t>(page) * p.ld_scale + first + lane * 4 - own * p.box_rows);
+                            copies_arrive(sb);
+                        } else {
+                            *reinterpret_cast<float4*>(sc) = make_float4(0.f, 0.f, 0.f, 0.f);
+                            mbar_arrive(sb);
+                        }
+                    }
                 }
             }
         }
@@ -794,15 +819,13 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             for (int i = 0; i < run.n; ++i, ++n, ch.next(p)) {
                 const int valid = min(kTile, run.len - (run.t0 + i) * kTile);
                 const bool in = tok < valid;
-                int slot0;
-                uint32_t parity0;
-                ch.at(p, 0, slot0, parity0);
+                const uint32_t sb = smem_u32(&scfull[n & (kScaleSlots - 1)]), sp = (n / kScaleSlots) & 1;
                 // Shared memory answers in hundreds of cycles while the products
                 // read it, so what can be asked for early is, and as little as
                 // possible lies between S^T and the product that waits for p s.
-                const bool landed = mbar_test(smem_u32(&full[slot0]), parity0);
+                const bool landed = mbar_test(sb, sp);
                 ok = ok && wait_uniform(smem_u32(sfull), n & 1);
-                if (!__all_sync(0xffffffffu, landed)) ok = ok && wait_uniform(smem_u32(&full[slot0]), parity0);
+                if (!__all_sync(0xffffffffu, landed)) ok = ok && wait_uniform(sb, sp);
                 tc_fence_after();
                 float2 z[16];                              // log2 of p s, up to the reference; then x
                 float lg;
@@ -1461,7 +1484,7 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
     p.nblk = static_cast<int>(z.DV / 128);
     const int64_t rows = x.NP ? x.R : z.H;                 // the most that a CTA can get
     p.q_rows = static_cast<int>(rows < kHeads ? (rows + 15) / 16 * 16 : kHeads);
-    // Shared memory: q, p s, scales and barriers, and the rest for the ring, up
+    // Shared memory: q, p s, scales and barriers, and the rest for the rings, up
     // to the three tiles whose row scales have a place.
     const int64_t fixed = 1024 + static_cast<int64_t>(2 * p.cc + p.pe) * p.q_rows * 128 + 2 * kPBytes + kMiscBytes;
     const int cpt = p.cc + p.pe;
@@ -1471,6 +1494,9 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
     p.twin = p.slots < 2 * cpt;                            // 512 codes, position columns, more than 32 heads
     if (p.twin && (cpt != 5 || p.slots < 8)) return DSNQ_ERR_UNSUPPORTED;
     if (p.twin) p.slots = 8;
+    // The rings hold two tiles or more each.
+    const int odd = cpt / 2, share_odd = p.slots * odd / cpt;
+    p.odd_slots = share_odd > 2 * odd ? share_odd : 2 * odd;
     const size_t smem = static_cast<size_t>(fixed + p.slots * kChunkBytes);
     p.scale_log2 = t.scale * kLog2e;
     p.out = static_cast<__nv_bfloat16*>(t.out);
