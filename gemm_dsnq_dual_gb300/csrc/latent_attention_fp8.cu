@@ -44,9 +44,9 @@
 // The prefix: its rows are the (request, head) pairs of the batch laid end to
 // end, so every tile of the prefix serves 64 rows whatever the number of heads.
 //
-// Warps: 0 and 3 copy tiles (TMA), 1 issues S^T, 2 issues O^T, 4..11 do the softmax:
+// Warps: 0 and 3 copy tiles (TMA), 1 issues S^T, 2 issues O^T, the others do the softmax:
 // warp w has tokens 32 (w % 4) .. of a tile (the TMEM lanes it can reach, and one
-// block of 32 of the scales) and one half of the heads.  They also split q,
+// block of 32 of the scales) and one part of the heads.  They also split q,
 // for the next job while the last product of this one runs, and write the
 // output.
 
@@ -70,17 +70,21 @@ using namespace attn;
 constexpr int kHeads = 64;                  // rows (heads) of a CTA
 constexpr int kTile = 128;                  // tokens of a tile
 constexpr int kChunkBytes = kTile * 128;    // 128 bytes of each row of a tile
-constexpr int kThreads = 384;
+constexpr int kPer = 32;                    // heads of a softmax warp, at most
+constexpr int kParts = kHeads / kPer;
+constexpr int kSoftWarp0 = 4, kSoftWarps = 4 * kParts, kSoftThreads = kSoftWarps * 32;
+constexpr int kThreads = kSoftWarp0 * 32 + kSoftThreads;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSoftWarp0 = 4, kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
 constexpr int kMaxSlots = 13;               // slots of the rings of chunks
 constexpr int kScaleSlots = 4;              // tiles whose row scales are kept; the rings hold at most three tiles
 constexpr int kMaxCtas = 160;               // bound of workers x head groups
 constexpr int kTmemCols = 512;
 constexpr int kTmemS = 256;                 // first column of S^T
 constexpr int kTmemSfa = 384, kTmemSfb = 388;   // block scales of C^T (ones) and of p s
+constexpr int kStacked = 32;                // heads up to which hi and lo of p s stand side by side too
 constexpr float kRaise = 32.0f;             // log2 by which a block may exceed the reference before O is rescaled
 constexpr float kLeastScale = 0x1p-60f;
+constexpr float kNothing = -1.0e30f;         // log2 of p s of a token past the length
 constexpr int kMiscBytes = 7168;
 constexpr int kPBytes = kTile * 64;         // hi (or lo) of p s of a tile: 64 bytes a token
 constexpr int kManyParts = 4;               // workers per job from which a CTA joins an item
@@ -130,6 +134,15 @@ __device__ __forceinline__ int64_t part_slot(const Params& p, int w, int j, bool
     return (p.prefix_len ? static_cast<int64_t>(j) + w : static_cast<int64_t>(w) * 2 + (first ? 0 : 1)) * p.G + g;
 }
 
+// The same value, of which the compiler knows nothing: it would otherwise make
+// copies of a loop for either outcome of a test in it (the softmax had four, and
+// the warps' code no room in the instruction cache).
+__device__ __forceinline__ bool opaque(bool v) {
+    uint32_t u = v;
+    asm volatile("" : "+r"(u));
+    return u != 0;
+}
+
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t chunk, int32_t group,
                                             int32_t page, uint64_t policy) {
     asm volatile(
@@ -156,55 +169,67 @@ __device__ __forceinline__ uint32_t idesc_o(int n) {
     return (1u << 15) | (1u << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (8u << 24);
 }
 
+// Shared-memory descriptors as two words, of which the steps of a product change
+// the lower one only.  The upper one: eight rows `stride` bytes on, version 1,
+// swizzle code.
+constexpr uint32_t desc_high(uint32_t stride, uint32_t swizzle) { return (stride >> 4) | 1u << 14 | swizzle << 29; }
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { return ((addr >> 4) & 0x3FFF) | (lead >> 4) << 16; }
+constexpr uint32_t kHighSw128 = desc_high(1024, 2);   // 128-byte rows and swizzle: chunks of the tile and of q
+constexpr uint32_t kHighSw64 = desc_high(512, 4);     // 64-byte rows and swizzle: p s
+constexpr uint32_t kHighRows16 = desc_high(128, 0);   // 16-byte rows: block scales
+
 // Four steps of D (+)= A B^T along the 128 bytes of a chunk's rows, issued by
 // one elected lane; the first overwrites D when !accumulate.
+#define DSNQ_STEP(KIND, K)                                                                                             \
+    "add.u32 x, %1, " K ";\n\tadd.u32 y, %2, " K ";\n\tmov.b64 a, {x, %5};\n\tmov.b64 b, {y, %5};\n\t"                \
+    "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, t;\n\t"
 #define DSNQ_MMA4(KIND)                                                                                                \
     asm volatile(                                                                                                      \
-        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b;\n\t"                                                              \
-        "setp.ne.b32 p, %4, 0;\n\t"                                                                                    \
-        "setp.eq.b32 t, 0, 0;\n\t"                                                                                     \
-        "elect.sync _|e, 0xffffffff;\n\t"                                                                              \
-        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], %1, %2, %3, p;\n\t"                                          \
-        "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"                                                                   \
-        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, t;\n\t"                                            \
-        "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"                                                                   \
-        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, t;\n\t"                                            \
-        "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"                                                                   \
-        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),                            \
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)                                                          \
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"                                           \
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"                            \
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"                                                            \
+        "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, p;\n\t"                                           \
+        DSNQ_STEP(KIND, "2") DSNQ_STEP(KIND, "4") DSNQ_STEP(KIND, "6") "}" ::"r"(d_tmem),                              \
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "n"(kHighSw128)                                           \
         : "memory")
-__device__ __forceinline__ void tc_mma4_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma4_e4m3(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
     DSNQ_MMA4("f8f6f4");
 }
-__device__ __forceinline__ void tc_mma4_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma4_bf16(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
     DSNQ_MMA4("f16");
 }
 #undef DSNQ_MMA4
+#undef DSNQ_STEP
 
 // O^T (+)= C^T (p s)^T of one chunk of codes: four blocks of 32 tokens (4 KB of
-// the tile, 2 KB of p s apart), of each the product with hi and the one with
-// lo (8 KB on), whose scales lie two columns on.
-__device__ __forceinline__ void tc_mma8_scaled(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
-                                               uint32_t sfb, uint32_t accumulate) {
+// the tile, 2 KB of p s apart).  PAIR: of each block the product with hi and the
+// one with lo (8 KB on), whose scales lie two columns on; otherwise one product
+// with both, side by side.
+template <bool PAIR>
+__device__ __forceinline__ void tc_mma_scaled(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t sfa,
+                                              uint32_t sfb, uint32_t accumulate) {
 #define DSNQ_MX "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
-#define DSNQ_STEP(A, B, BL, ID)                                                                                        \
-    "add.u64 a, %1, " A ";\n\tadd.u64 b, %2, " B ";\n\tadd.u64 l, %2, " BL ";\n\tadd.u32 i, %3, " ID ";\n\t"            \
-    DSNQ_MX "[%0], a, b, i, [%4], [%5], t;\n\t" DSNQ_MX "[%0], a, l, i, [%4], [%6], t;\n\t"
-    asm volatile(
-        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b, l;\n\t.reg .b32 i;\n\t"
-        "setp.ne.b32 p, %7, 0;\n\t"
-        "setp.eq.b32 t, 0, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "add.u64 l, %2, 512;\n\t"
-        DSNQ_MX "[%0], %1, %2, %3, [%4], [%5], p;\n\t"
-        DSNQ_MX "[%0], %1, l, %3, [%4], [%6], t;\n\t"
-        DSNQ_STEP("256", "128", "640", "16")
-        DSNQ_STEP("512", "256", "768", "32")
-        DSNQ_STEP("768", "384", "896", "48")
-        "}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(sfb + 2), "r"(accumulate)
-        : "memory");
+#define DSNQ_B(B) "add.u32 y, %2, " B ";\n\tmov.b64 b, {y, %9};\n\t"
+#define DSNQ_STEP(A, B, ID)                                                                                            \
+    "add.u32 x, %1, " A ";\n\tmov.b64 a, {x, %8};\n\tadd.u32 i, %3, " ID ";\n\t" DSNQ_B(B) DSNQ_MX "[%0], a, b, i, [%4], [%5], t;\n\t"
+#define DSNQ_LOW(B) DSNQ_B(B) DSNQ_MX "[%0], a, b, i, [%4], [%6], t;\n\t"
+#define DSNQ_ASM(STEPS)                                                                                                \
+    asm volatile(                                                                                                      \
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b;\n\t.reg .b32 i, x, y;\n\t"                                        \
+        "setp.ne.b32 p, %7, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"                            \
+        "mov.b64 a, {%1, %8};\n\tmov.b64 b, {%2, %9};\n\tmov.b32 i, %3;\n\t" DSNQ_MX "[%0], a, b, i, [%4], [%5], p;\n\t" \
+        STEPS "}" ::"r"(d_tmem),                                                                                       \
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(sfa), "r"(sfb), "r"(sfb + 2), "r"(accumulate), "n"(kHighSw128), "n"(kHighSw64) \
+        : "memory")
+    if (PAIR)
+        DSNQ_ASM(DSNQ_LOW("512") DSNQ_STEP("256", "128", "16") DSNQ_LOW("640") DSNQ_STEP("512", "256", "32") DSNQ_LOW("768")
+                     DSNQ_STEP("768", "384", "48") DSNQ_LOW("896"));
+    else
+        DSNQ_ASM(DSNQ_STEP("256", "128", "16") DSNQ_STEP("512", "256", "32") DSNQ_STEP("768", "384", "48"));
+#undef DSNQ_ASM
+#undef DSNQ_LOW
 #undef DSNQ_STEP
+#undef DSNQ_B
 #undef DSNQ_MX
 }
 
@@ -217,14 +242,19 @@ __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
         : "memory");
 }
 
-// Descriptors: p s with its 64-byte rows (64-byte swizzle, eight rows 512 bytes
-// on), and the scales as rows of 16 bytes (no swizzle).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t swizzle) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | static_cast<uint64_t>((lead >> 4) & 0x3FFF) << 16 |
-           static_cast<uint64_t>((stride >> 4) & 0x3FFF) << 32 | static_cast<uint64_t>(1) << 46 |
-           static_cast<uint64_t>(swizzle) << 61;
+// 16 lanes x 16 columns of TMEM as matrix fragments (tmem_ld_frag32).
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
 }
-
+__device__ __forceinline__ void tmem_ld8_wait(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
@@ -243,10 +273,10 @@ __device__ __forceinline__ float redux_max(float v) {
     return r;
 }
 
-// hi = e4m3(x), lo = e4m3(32 (x - hi)) of two numbers (|x| <= 256: x - hi is
-// exact and at most 8); `sum` gets hi + lo / 32.
-// (The conversion from fp32 pairs takes a third of the time of the one from half
-// pairs, which the remainder uses because it is one.)
+// hi = e4m3(x), lo = e4m3(32 (x - hi)) of two numbers (|x| <= 256: x - hi is at
+// most 8, in half precision); `sum` gets hi + lo / 32.  (The conversion from
+// fp32 pairs takes a third of the time of the one from half pairs, which the
+// remainder uses because it is one.)
 __device__ __forceinline__ __half2 half2_of(uint32_t codes) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
@@ -260,6 +290,7 @@ __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo, __h
     lo = c;
     sum = __hfma2(half2_of(lo), __float2half2_rn(0.03125f), h);
 }
+__device__ __forceinline__ float2 unpack_bf16(uint32_t v) { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
 
 // lg2.approx: off by at most 2^-22 here, and its inverse is taken from itself.
 __device__ __forceinline__ float log2_fast(float x) {
@@ -269,18 +300,37 @@ __device__ __forceinline__ float log2_fast(float x) {
 }
 
 // Registers of a copying or issuing thread and of a softmax thread: together
-// those that the CTA is launched with (168 each).  With less than ~200 the
-// softmax keeps some of its sums in local memory, whose loads wait behind the
-// products' reads of shared memory.
-constexpr int kRegsIssue = 64, kRegsSoft = 216;
-static_assert(128 * kRegsIssue + kSoftThreads * kRegsSoft <= kThreads * 168, "registers of the CTA at its launch");
+// those that the CTA is launched with.  What does not fit goes to local memory,
+// whose loads wait behind the products' reads of shared memory.
+constexpr int kRegsIssue = kPer == 16 ? 56 : 72, kRegsSoft = kPer == 16 ? 104 : 216;
+static_assert(128 * kRegsIssue + kSoftThreads * kRegsSoft <= kThreads * (kPer == 16 ? 96 : 168), "registers of the CTA at its launch");
+
+// wait_bounded<true> in a few instructions: the clock is first read after 64
+// polls.  (The kernel's code has to stay small: the issuing warps run theirs
+// once a tile, between passes of the softmax warps through theirs.)
+__device__ __forceinline__ bool wait_polled(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+        if (n & 63) continue;
+        if (*abort) return false;
+        const uint64_t now = now_ns();
+        if (n == 64) t0 = now;
+        if (now - t0 > timeout_ns) {
+            *abort = 1;
+            atomicOr(&g_status, kStatusTimeout);
+            return false;
+        }
+    }
+    return true;
+}
 
 // Barriers of all softmax warps, and of the four that have the same heads
 // (returns whether any of their threads passed true).  A named barrier has no
 // time limit, so every softmax warp reaches every one of them whether or not
 // its waits succeeded (the counts depend on the run alone).
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ bool half_sync_or(int half, bool v) {
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
+__device__ __forceinline__ bool part_sync_or(int part, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -288,7 +338,7 @@ __device__ __forceinline__ bool half_sync_or(int half, bool v) {
         "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(v)), "r"(2 + half)
+        : "r"(static_cast<uint32_t>(v)), "r"(2 + part)
         : "memory");
     return r != 0;
 }
@@ -307,7 +357,7 @@ struct Chunks {
     int i[2] = {0, 0};
     uint32_t pass[2] = {0, 0}, n = 0;
     __device__ __forceinline__ void at(const Params& p, int c, int& slot, uint32_t& parity) const {
-        if (p.twin) {
+        if (opaque(p.twin)) {
             const int pos = c == 4 ? 1 : c;
             slot = static_cast<int>(n & 1) * 4 + pos;
             parity = pos == 1 ? (c == 4) : (n >> 1) & 1;
@@ -323,11 +373,9 @@ struct Chunks {
         }
         if (odd) slot += p.slots - p.odd_slots;
     }
-    // The copying warp of a chunk.
-    static __device__ __forceinline__ int ring(const Params& p, int c) { return p.twin && c == 4 ? 1 : c & 1; }
     __device__ __forceinline__ void next(const Params& p) {
         ++n;
-        if (p.twin) return;
+        if (opaque(p.twin)) return;
         const int cpt = p.cc + p.pe;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -349,7 +397,7 @@ struct Run {
     int plen;                         // tokens of the prefix
     int32_t ahead;                    // seq_lens of the next request: a trip to memory ahead of its use
     int len, tiles, n;                // of the current job: tokens, tiles, tiles of this run
-    int count, hp;                    // its rows in this CTA, and their number up to a multiple of 16
+    int count;                        // its rows in this CTA
     __device__ __forceinline__ bool next(const Params& p, int g) {
         if (j > j_end || (j == j_end && t0 >= t_end)) return false;
         const bool prefix = j < p.NP;
@@ -359,7 +407,6 @@ struct Run {
         n = (j == j_end ? t_end : tiles) - t0;
         const int rows = prefix ? p.R - (j * p.G + g) * kHeads : p.H - g * kHeads;
         count = max(0, min(kHeads, rows));
-        hp = (count + 15) & ~15;
         return true;
     }
     __device__ __forceinline__ bool live() const { return len > 0 && count > 0; }
@@ -369,8 +416,13 @@ struct Run {
     }
 };
 
+template <int NG>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Params p) {
+    constexpr int HP = 16 * NG;                            // rows (heads) of a job, with those that pad it
+    constexpr bool kPair = HP > kStacked;
+    constexpr uint32_t kLow = kPair ? 0 : HP;              // columns from hi's part of O to lo's
+    constexpr int hpp = HP / kParts;                       // heads of a softmax warp, a multiple of four
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int q_chunk = 2 * p.q_rows * 128;                // bytes of a code chunk of q: hi, then lo
@@ -383,9 +435,9 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     uint8_t* sf_s = misc;                                  // [32][16 B] block scales of p s
     float* sc_s = reinterpret_cast<float*>(sf_s + 512);    // [kScaleSlots][128] row scales
     float* cq_s = sc_s + kScaleSlots * kTile;              // [2][64] factor of a head's scores
-    float* bc_s = cq_s + 2 * kHeads;                       // [8 warps][64] 2^(T - M); at a job's end {l, lr}
-    float* mx_s = bc_s + kSoftWarps * 64;                  // [8 warps][32]
-    float* al_s = mx_s + kSoftWarps * 32;                  // [64] factors of O
+    float* bc_s = cq_s + 2 * kHeads;                       // [kSoftWarps][kPer]{T, 2^(T - M)}; at a job's end {l, lr}
+    float* mx_s = bc_s + kSoftWarps * 2 * kPer;            // [kSoftWarps][kPer]
+    float* al_s = mx_s + kSoftWarps * kPer;                // [64] factors of O
     uint64_t* full = reinterpret_cast<uint64_t*>(al_s + kHeads);   // [kMaxSlots]
     uint64_t* empty = full + kMaxSlots;                    // [kMaxSlots]
     uint64_t* scfull = empty + kMaxSlots;                  // [kScaleSlots]
@@ -441,6 +493,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
         int64_t mine = 0;
         int most = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int t = tiles_of(clamp_len(p.cap, p.seq_lens[b]));
             mine += t;
@@ -534,7 +587,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     // A whole warp's wait: all of its lanes go on or none (warp-wide
     // instructions follow), and the compiler sees that it is so.
     auto wait_uniform = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_bounded<true>(bar, parity, abort_flag, tmo));
+        return __all_sync(0xffffffffu, wait_polled(bar, parity, abort_flag, tmo));
     };
     // The same, asleep between polls: for the copying warp, which is ahead.
     auto wait_uniform_asleep = [&](uint32_t bar, uint32_t parity) {
@@ -547,8 +600,8 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         // ------------------------------------------------------ TMA producers
         // Chunks in the order of their use by S^T, every other one from each of
         // the two warps (a copy takes a warp some 50 cycles, and small pages make
-        // many): the first codes (and the tile's row scales), the position columns, whose slot is free again
-        // when S^T is done with them, the other codes.  A request's tiles pass
+        // many): the first codes (and the tile's row scales), the position columns,
+        // whose slot is free again when S^T is done with them, the other codes.  A request's tiles pass
         // through L2 once, so they leave it first; the prefix's are read by
         // every group of rows.
         uint64_t once, again;
@@ -556,22 +609,26 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(again));
         const int pieces = kTile / p.box_rows;             // copies of a chunk (1, 2, 4, 8 or 16)
         const int batch = 32 / pieces;                     // tiles whose table entries the lanes hold
+        const int odd = warp == 3;
         Chunks ch;
-        bool ok = true, skip = warp == 0 && (p.inject & kInjectSkipLoad) != 0;
+        bool ok = true, skip = !odd && (p.inject & kInjectSkipLoad) != 0;
+#pragma unroll 1
         for (; ok && run.next(p, g); run.advance()) {
             if (!run.live()) continue;
             const bool prefix = run.j < p.NP;
             const int32_t* row = prefix ? p.prefix_table : p.table + (run.j - p.NP) * p.ld_table;
             const int width = prefix ? p.prefix_width : p.width;
             const uint64_t policy = prefix ? again : once;
-            int ids = 0;
+            int ids = 0, offs = 0;
+#pragma unroll 1
             for (int i = 0; ok && i < run.n; ++i, ch.next(p)) {
                 const int tile = run.t0 + i;
                 if (i % batch == 0) {
                     const int64_t tok = static_cast<int64_t>(tile) * kTile + static_cast<int64_t>(lane) * p.box_rows;
-                    ids = 0;
+                    ids = offs = 0;
                     if (tok < run.len) {
-                        const int64_t e = tok / p.page_size;
+                        const int e = static_cast<int>(tok) / p.page_size;
+                        offs = static_cast<int>(tok) - e * p.page_size;
                         if (bounds_ok(e < width)) ids = row[e];
                         if (ids < 0 || ids >= p.num_pages) {   // such pages read as zeros
                             atomicOr(&g_status, kStatusBounds);
@@ -579,12 +636,13 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                         }
                     }
                 }
-                const int tok0 = tile * kTile;
-                const int live = min(pieces, (run.len - tok0 + p.box_rows - 1) / p.box_rows);
-                const int id = __shfl_sync(0xffffffffu, ids, (i % batch) * pieces + (lane & (pieces - 1)));
-                const int in_page = (tok0 + lane * p.box_rows) % p.page_size;
-                for (int c = 0; c < cpt; ++c) {
-                    if (Chunks::ring(p, c) != (warp == 3)) continue;
+                const int live = min(pieces, (run.len - tile * kTile + p.box_rows - 1) / p.box_rows);
+                const int from = (i % batch) * pieces + (lane & (pieces - 1));
+                const int id = __shfl_sync(0xffffffffu, ids, from), in_page = __shfl_sync(0xffffffffu, offs, from);
+#pragma unroll 1
+                for (int k = 0; k < 3; ++k) {
+                    const int c = k == 2 && opaque(p.twin) ? (odd ? 4 : 5) : 2 * k + odd;
+                    if (c >= cpt) break;
                     const int chunk = c == 0 ? 0 : !p.pe ? c : c == 1 ? p.cc : c - 1;
                     int slot;
                     uint32_t parity;
@@ -622,34 +680,33 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     } else if (warp == 1) {
         // ---------------------------------------------- products S^T = C Q^T
         // Chunk by chunk as they land.
-        const uint64_t q_desc = smem_desc_sw128(smem_u32(q_s), 16, 1024), pe_desc = smem_desc_sw128(smem_u32(qpe_s), 16, 1024);
+        const uint32_t q_low = desc_low(smem_u32(q_s), 16), pe_low = desc_low(smem_u32(qpe_s), 16);
         const uint32_t d = tmem + kTmemS;
         Chunks ch;
         uint32_t nq = 0;
         bool ok = true;
+#pragma unroll 1
         for (; ok && run.next(p, g); run.advance()) {
             if (!run.live()) continue;
-            const uint32_t id_s = idesc_s(2 * run.hp), id_pe = idesc_pe(run.hp);
             ok = wait_uniform(smem_u32(qfull), nq & 1);
             ++nq;
+#pragma unroll 1
             for (int i = 0; ok && i < run.n; ++i, ch.next(p)) {
                 ok = wait_uniform(smem_u32(sempty), (ch.n & 1) ^ 1);
                 tc_fence_after();
+#pragma unroll 1
                 for (int c = 0; ok && c < cpt; ++c) {
                     int slot;
                     uint32_t parity;
                     ch.at(p, c, slot, parity);
+                    const int code = c == 0 ? 0 : c - p.pe;
+                    const bool pe = c == 1 && opaque(p.pe);
+                    const uint32_t a = desc_low(smem_u32(ring) + slot * kChunkBytes, 16);
                     ok = wait_uniform(smem_u32(&full[slot]), parity);
                     if (!ok) break;
-                    const uint64_t a = smem_desc_sw128(smem_u32(ring) + slot * kChunkBytes, 16, 1024);
-                    const int code = c == 0 || !p.pe ? c : c - 1;
-                    if (p.pe && c == 1) {
-                        tc_mma4_bf16(d, a, pe_desc, id_pe, 1);
-                        tc_commit(smem_u32(&empty[slot]));
-                    } else {
-                        tc_mma4_e4m3(d, a, q_desc + static_cast<uint32_t>(code * q_chunk >> 4), id_s, c > 0);
-                        if (code >= p.nblk) tc_commit(smem_u32(&empty[slot]));   // no part of the value
-                    }
+                    if (pe) tc_mma4_bf16(d, a, pe_low, idesc_pe(HP), 1);
+                    else tc_mma4_e4m3(d, a, q_low + static_cast<uint32_t>(code * q_chunk >> 4), idesc_s(2 * HP), c > 0);
+                    if (pe || code >= p.nblk) tc_commit(smem_u32(&empty[slot]));   // no part of the value
                 }
                 if (!ok) break;
                 tc_commit(smem_u32(sfull));
@@ -662,26 +719,26 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     } else if (warp == 2) {
         // ----------------------------------------- products O^T += C^T (p s)^T
         // They free the chunks one by one.
-        const uint64_t p_desc = smem_desc(smem_u32(p_s), kPBytes, 512, 4);
-        const uint64_t sf_desc = smem_desc(smem_u32(sf_s), 0, 128, 0);
+        const uint32_t p_low = desc_low(smem_u32(p_s), kPBytes);
+        const uint64_t sf_desc = static_cast<uint64_t>(kHighRows16) << 32 | desc_low(smem_u32(sf_s), 0);
         Chunks ch;
         bool ok = true;
+#pragma unroll 1
         for (; ok && run.next(p, g); run.advance()) {
             if (!run.live()) continue;
-            const uint32_t id_o = idesc_o(run.hp);
+#pragma unroll 1
             for (int i = 0; i < run.n; ++i, ch.next(p)) {
                 ok = wait_uniform(smem_u32(pfull), ch.n & 1);
                 if (!ok) break;
                 tc_fence_after();
                 tc_copy_scales(tmem + kTmemSfb, sf_desc);
-                for (int c = 0; c < cpt; ++c) {
-                    const int code = c == 0 || !p.pe ? c : c - 1;
-                    if ((p.pe && c == 1) || code >= p.nblk) continue;
+#pragma unroll 1
+                for (int k = 0; k < p.nblk; ++k) {
                     int slot;
                     uint32_t parity;
-                    ch.at(p, c, slot, parity);
-                    tc_mma8_scaled(tmem + code * kHeads, smem_desc_sw128(smem_u32(ring) + slot * kChunkBytes, kChunkBytes, 1024), p_desc,
-                                   id_o, tmem + kTmemSfa, tmem + kTmemSfb, i > 0);
+                    ch.at(p, k == 0 ? 0 : k + p.pe, slot, parity);
+                    tc_mma_scaled<kPair>(tmem + k * kHeads, desc_low(smem_u32(ring) + slot * kChunkBytes, kChunkBytes), p_low,
+                                         idesc_o(kPair ? HP : 2 * HP), tmem + kTmemSfa, tmem + kTmemSfb, i > 0);
                     tc_commit(smem_u32(&empty[slot]));
                 }
                 tc_commit(smem_u32(pempty));
@@ -695,25 +752,26 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     } else {
         // ------------------------------------- softmax, splitting q, output
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-        const int quad = warp & 3, sw = warp - kSoftWarp0, half = sw >> 2;
+        const int quad = warp & 3, sw = warp - kSoftWarp0, part = sw >> 2;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const int st = threadIdx.x - kSoftWarp0 * 32;      // 0..255
+        const int st = threadIdx.x - kSoftWarp0 * 32;      // 0 .. kSoftThreads - 1
         const float kNegInf = __int_as_float(0xff800000);
         const int tok = quad * 32 + lane;                  // this thread's token of a tile
         const int DV = p.nblk * 128;
-        float* bc = bc_s + sw * 64;
+        float* bc = bc_s + sw * 2 * kPer;
         uint32_t n = 0, nq = 0;
         Chunks ch;
         bool ok = true;                                    // false: only the barriers are kept up
 
         // Splits the queries of the job r into shared memory, and leaves the
-        // factors of their scores.  Warp sw takes rows sw, sw + 8, ...; a lane 16
-        // codes, lanes 0..7 also eight position columns.
+        // factors of their scores.  Warp sw takes rows sw, sw + kSoftWarps, ...; a lane
+        // 16 codes, lanes 0..7 also eight position columns.
         auto split_q = [&](const Run& r, int buf) {
             const bool prefix = r.j < p.NP;
             const int row0 = prefix ? (r.j * p.G + g) * kHeads : g * kHeads;
             constexpr int kAhead = 2;
-            for (int i0 = sw; i0 < r.hp; i0 += kAhead * kSoftWarps) {
+#pragma unroll 1
+            for (int i0 = sw; i0 < HP; i0 += kAhead * kSoftWarps) {
                 uint4 x[kAhead][2], e[kAhead];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
@@ -735,7 +793,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int i = i0 + u * kSoftWarps;
-                    if (i >= r.hp) break;
+                    if (i >= HP) break;
                     // The largest magnitude, as the bits of a bf16 (infinities and NaN above all others).
                     const uint32_t* xw = reinterpret_cast<const uint32_t*>(x[u]);
                     const uint32_t* ew = reinterpret_cast<const uint32_t*>(&e[u]);
@@ -759,16 +817,16 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     for (int k = 0; k < 4; ++k) {
                         uint32_t h0, h1, l0, l1;
                         __half2 s;
-                        const uint32_t a = xw[2 * k], b = xw[2 * k + 1];
-                        split2(make_float2(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv), h0, l0, s);
-                        split2(make_float2(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv), h1, l1, s);
+                        const float2 a = unpack_bf16(xw[2 * k]), b = unpack_bf16(xw[2 * k + 1]);
+                        split2(make_float2(a.x * inv, a.y * inv), h0, l0, s);
+                        split2(make_float2(b.x * inv, b.y * inv), h1, l1, s);
                         hi[k] = h0 | h1 << 16;
                         lo[k] = l0 | l1 << 16;
                     }
                     if (lane * 16 < p.cc * 128) {
                         uint8_t* at = q_s + (lane >> 3) * q_chunk + (((lane & 7) ^ (i & 7)) << 4);
                         *reinterpret_cast<uint4*>(at + i * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(at + (r.hp + i) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4*>(at + (HP + i) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                     if (p.pe && lane < 8) {
                         uint32_t v[4];
@@ -783,39 +841,161 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(qfull));
         };
-        // The next job of the run that has tiles and rows, from r on.
-        auto seek = [&](Run& r) {
-            for (; r.next(p, g); r.advance())
-                if (r.live()) return true;
-            return false;
-        };
-        {
-            Run r = run;
-            if (seek(r)) split_q(r, 0);
-        }
-
-        for (; run.next(p, g); run.advance()) {
-            const int b = run.j - p.NP;
-            const bool whole = !p.prefix_len && run.t0 == 0 && run.n == run.tiles;
-            if (!run.live()) {
-                if (p.prefix_len || run.len > 0) continue; // no part; the join knows
+        // Job by job: the queries of the next one, while the last product of the
+        // one before runs; that one's output; the next one's tiles.
+        Run next = run;
+        bool started = false;
+        float2 l[kPer / 2], lr[kPer / 2];                  // per head, this token's share of the sums of p: unrounded, rounded
+        float M = 0.f;                                     // of head h0 + lane: what O and the sums are relative to (log2)
+#pragma unroll 1
+        while (true) {
+            // The next job with tiles and rows.
+            bool more = false;
+#pragma unroll 1
+            for (; next.next(p, g); next.advance()) {
+                more = next.live();
+                if (more) break;
+                if (p.prefix_len || next.len > 0) continue;   // no part; the join knows
                 // An empty request: zeros, and the logarithm of an empty sum.
+                const int b = next.j - p.NP;
+#pragma unroll 1
                 for (int e = st; e < kHeads * (DV / 8); e += kSoftThreads) {
                     const int h = g * kHeads + e / (DV / 8), c = e % (DV / 8);
                     if (h < p.H && bounds_ok(b >= 0 && b < p.B))
                         *reinterpret_cast<uint4*>(p.out + b * p.ldo_b + h * p.ldo_h + c * 8) = make_uint4(0, 0, 0, 0);
                 }
                 if (p.lse && st < kHeads && g * kHeads + st < p.H) p.lse[b * p.ldl_b + g * kHeads + st] = kNegInf;
-                continue;
             }
-            const int ng = run.hp >> 4;                    // groups of eight heads of this half
-            const int h0 = half * 8 * ng;                  // its first head
-            const bool mine = lane < 8 * ng;               // this lane has a head: h0 + lane
-            const float* cq = cq_s + (nq & 1) * kHeads + h0;
-            float2 l[16], lr[16];                          // per head, this token's share of the sums of p: unrounded, rounded
+            if (more && ok) split_q(next, nq & 1);
+            if (started) {
+                // ---- output of the job (or of this worker's part of it)
+                const int b = run.j - p.NP, h0 = part * hpp;
+                const bool whole = !p.prefix_len && run.t0 == 0 && run.n == run.tiles, mine = lane < hpp;
+                // Sums over the tokens: lane k gets head h0 + k's.
+                float v[kPer], u[kPer];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) l[k] = lr[k] = make_float2(0.f, 0.f);
-            float M = 0.f;                                 // of head h0 + lane: what O and the sums are relative to (log2)
+                for (int k = 0; k < kPer / 2; ++k) {
+                    v[2 * k] = l[k].x; v[2 * k + 1] = l[k].y;
+                    u[2 * k] = lr[k].x; u[2 * k + 1] = lr[k].y;
+                }
+#pragma unroll
+                for (int o = kPer / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int k = 0; k < o; ++k) {
+                        const bool odd = lane & o;
+                        const float a = odd ? v[k] : v[k + o], c = odd ? u[k] : u[k + o];
+                        v[k] = (odd ? v[k + o] : v[k]) + __shfl_xor_sync(0xffffffffu, a, o);
+                        u[k] = (odd ? u[k + o] : u[k]) + __shfl_xor_sync(0xffffffffu, c, o);
+                    }
+#pragma unroll
+                for (int o = kPer; o < 32; o <<= 1) {
+                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+                    u[0] += __shfl_xor_sync(0xffffffffu, u[0], o);
+                }
+                if (lane < kPer) {
+                    bc[lane] = v[0];
+                    bc[kPer + lane] = u[0];
+                }
+                part_sync_or(part, false);                     // bc is next written after the next job's S^T
+                float ls = 0.f, lrs = 0.f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    ls += bc_s[(part * 4 + q) * 2 * kPer + (lane & (kPer - 1))];
+                    lrs += bc_s[(part * 4 + q) * 2 * kPer + kPer + (lane & (kPer - 1))];
+                }
+                // A part's weights add up to its unrounded sum, which the join divides by.
+                if (mine) al_s[h0 + lane] = lrs > 0.f || lrs != lrs ? __fdividef(whole ? 1.0f : ls, lrs) : 0.f;
+                __syncwarp();                                  // the same from each of the part's four warps
+                ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
+                tc_fence_after();
+                if (ok && whole) {
+                    // 32 values x 16 heads at a time, through 1 KB of p's buffers
+                    // for each warp: stmatrix turns the fragments into rows of 32
+                    // values (16-byte chunks, chunk ^ (row / 2) % 4), which leave as
+                    // 16-byte stores, 64 bytes of each of eight heads at once.
+                    const uint32_t stage = smem_u32(p_s) + sw * 1024;
+                    const int col0 = 2 * (lane & 3);
+#pragma unroll 1
+                    for (int c = 0; c < p.nblk * (kPer / 16); ++c) {
+                        const int blk = c / (kPer / 16), hb = c % (kPer / 16) * 16;   // value block, first head
+                        if (hb >= hpp) continue;
+                        uint32_t x[2][8];
+                        const uint32_t src = tl + blk * kHeads + h0 + hb;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            tmem_ld_frag16(src + (u * 16u << 16), x[u]);
+                            tmem_ld8_wait(x[u]);
+                            if (!kLow) continue;
+                            uint32_t y[8];
+                            tmem_ld_frag16(src + kLow + (u * 16u << 16), y);
+                            tmem_ld8_wait(y);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) x[u][k] = __float_as_uint(__uint_as_float(x[u][k]) + __uint_as_float(y[k]));
+                        }
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {          // eight heads; those past this part's are not stored
+                            const float2 f = *reinterpret_cast<const float2*>(al_s + min(h0 + hb + q * 8 + col0, kHeads - 2));
+                            uint32_t v[4];
+#pragma unroll
+                            for (int d = 0; d < 4; ++d)        // eight values
+                                v[d] = pack_bf16(__uint_as_float(x[d >> 1][q * 4 + (d & 1) * 2]) * f.x,
+                                                 __uint_as_float(x[d >> 1][q * 4 + (d & 1) * 2 + 1]) * f.y);
+                            const int hl = q * 8 + (lane & 7), d = lane >> 3;
+                            stmatrix_x4_trans(stage + hl * 64 + ((d ^ ((hl >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
+                        }
+                        __syncwarp();
+                        __nv_bfloat16* o = p.out + b * p.ldo_b + blk * 128 + quad * 32 + (lane & 3) * 8;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int hl = j * 8 + (lane >> 2), head = h0 + hb + hl;
+                            uint4 v;
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                         : "r"(stage + hl * 64 + (((lane & 3) ^ ((hl >> 1) & 3)) << 4))
+                                         : "memory");
+                            if (hb + hl < hpp && head < run.count && bounds_ok(b >= 0 && b < p.B))
+                                *reinterpret_cast<uint4*>(o + static_cast<int64_t>(g * kHeads + head) * p.ldo_h) = v;
+                        }
+                        __syncwarp();
+                    }
+                } else if (ok) {
+                    // A part, in the order the registers hold it: 512 bytes a store.
+                    const int64_t slot = part_slot(p, w, run.j, run.j == j_first, g);
+                    float4* o = reinterpret_cast<float4*>(p.part_o) + slot * p.nblk * 16 * 128 + quad * 32 + lane;
+#pragma unroll 1
+                    for (int k = 0; 4 * k < hpp && h0 + 4 * k < run.count; ++k) {
+                        const float4 f = *reinterpret_cast<const float4*>(al_s + h0 + 4 * k);
+#pragma unroll 1
+                        for (int blk = 0; blk < p.nblk; ++blk) {
+                            uint32_t x[4];
+                            tmem_ld4(tl + blk * kHeads + h0 + 4 * k, x);
+                            if (kLow) {
+                                uint32_t y[4];
+                                tmem_ld4(tl + blk * kHeads + kLow + h0 + 4 * k, y);
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) + __uint_as_float(y[u]));
+                            }
+                            o[(blk * 16 + (h0 >> 2) + k) * 128] = make_float4(__uint_as_float(x[0]) * f.x, __uint_as_float(x[1]) * f.y,
+                                                                              __uint_as_float(x[2]) * f.z, __uint_as_float(x[3]) * f.w);
+                        }
+                    }
+                    if (quad == 0 && mine) p.part_ml[slot * kHeads + h0 + lane] = make_float2(M, ls);
+                }
+                const int head = g * kHeads + h0 + lane;
+                if (ok && whole && p.lse && quad == 0 && mine && head < p.H)
+                    p.lse[b * p.ldl_b + head] = ls == 0.f ? kNegInf : (M + log2f(ls)) * kLn2;
+                tc_fence_before();
+            }
+            if (!more) break;
+            run = next;
+            next.advance();
+            started = true;
+            const int h0 = part * hpp;                     // this warp's first head
+            const bool mine = lane < hpp;                  // this lane has a head: h0 + lane
+            const float* cq = cq_s + (nq & 1) * kHeads + h0;
+#pragma unroll
+            for (int k = 0; k < kPer / 2; ++k) l[k] = lr[k] = make_float2(0.f, 0.f);
+#pragma unroll 1
             for (int i = 0; i < run.n; ++i, ++n, ch.next(p)) {
                 const int valid = min(kTile, run.len - (run.t0 + i) * kTile);
                 const bool in = tok < valid;
@@ -824,21 +1004,21 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 // read it, so what can be asked for early is, and as little as
                 // possible lies between S^T and the product that waits for p s.
                 const bool landed = mbar_test(sb, sp);
-                ok = ok && wait_uniform(smem_u32(sfull), n & 1);
-                if (!__all_sync(0xffffffffu, landed)) ok = ok && wait_uniform(sb, sp);
+                ok = opaque(ok && wait_uniform(smem_u32(sfull), n & 1));
+                if (!__all_sync(0xffffffffu, landed)) ok = opaque(ok && wait_uniform(sb, sp));
                 tc_fence_after();
-                float2 z[16];                              // log2 of p s, up to the reference; then x
+                float2 z[kPer / 2];                        // log2 of p s, up to the reference; then x
                 float lg;
                 {
                     const float sj = ok && in ? sc_s[(n & (kScaleSlots - 1)) * kTile + tok] : 1.f;
                     lg = log2_fast(fmaxf(sj, kLeastScale));
                     const float2 s2 = make_float2(sj, sj), lg2 = make_float2(lg, lg), down = make_float2(0.03125f, 0.03125f);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        if (2 * k >= ng) break;
+                    for (int k = 0; k < kPer / 16; ++k) {
+                        if (16 * k >= hpp) break;
                         uint32_t a[16], c[16];
                         tmem_ld16_issue(tl + kTmemS + h0 + 16 * k, a);
-                        tmem_ld16_issue(tl + kTmemS + run.hp + h0 + 16 * k, c);
+                        tmem_ld16_issue(tl + kTmemS + HP + h0 + 16 * k, c);
                         tmem_ld16_wait(a);
                         tmem_ld16_wait(c);
 #pragma unroll
@@ -858,18 +1038,18 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(sempty));
                 const bool pv_done = n == 0 || mbar_test(smem_u32(pempty), (n & 1) ^ 1);
-                if (valid < kTile) {
+                if (opaque(valid < kTile)) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (!in) z[k] = make_float2(kNegInf, kNegInf);
+                    for (int k = 0; k < kPer / 2; ++k)
+                        if (!in) z[k] = make_float2(kNothing, kNothing);
                 }
                 // T of each head: x = 2^(z - T) <= 256, the block's largest at
                 // least 64.  (Rounded to a whole number by adding 1.5 2^23.)
-                uint32_t hi[8], lo[8];                     // four heads each
-                __half2 sum[16];                           // x as rounded
+                uint32_t hi[kPer / 4], lo[kPer / 4];       // four heads each
+                __half2 sum[kPer / 2];                     // x as rounded
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (k >= 2 * ng) break;
+                for (int k = 0; k < kPer / 4; ++k) {
+                    if (4 * k >= hpp) break;
                     float2 T[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -884,31 +1064,30 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                         const int e = 2 * k + j;
                         const float2 y = fma2(T[j], make_float2(-1.f, -1.f), z[e]);
                         z[e] = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                        if (valid < kTile && !in) z[e] = make_float2(0.f, 0.f);   // T may be -infinity too
                         split2(z[e], a2[j], c2[j], sum[e]);
                     }
                     hi[k] = __byte_perm(a2[0], a2[1], 0x5410);
                     lo[k] = __byte_perm(c2[0], c2[1], 0x5410);
                 }
                 __syncwarp();
-                const float top = mine ? bc[lane] : kNegInf;   // head h0 + lane's
+                const float top = mine ? bc[lane] : kNothing;  // head h0 + lane's
                 // What O and the sums are relative to.
                 bool raise = false;
-                if (i == 0) {
-                    mx_s[sw * 32 + lane] = top;
+                if (opaque(i == 0)) {
+                    if (lane < kPer) mx_s[sw * kPer + lane] = top;
                     soft_sync();
                 } else {
-                    raise = half_sync_or(half, top - M > kRaise);
+                    raise = part_sync_or(part, top - M > kRaise);
                     if (raise) {
-                        mx_s[sw * 32 + lane] = top;
-                        half_sync_or(half, false);
+                        if (lane < kPer) mx_s[sw * kPer + lane] = top;
+                        part_sync_or(part, false);
                     }
                 }
-                if (i == 0 || raise) {
-                    const float* mx = mx_s + half * 128 + lane;
-                    const float to = fmaxf(fmaxf(mx[0], mx[32]), fmaxf(mx[64], mx[96]));
+                if (opaque(i == 0 || raise)) {
+                    const float* mx = mx_s + part * 4 * kPer + (lane & (kPer - 1));
+                    const float to = fmaxf(fmaxf(mx[0], mx[kPer]), fmaxf(mx[2 * kPer], mx[3 * kPer]));
                     if (i == 0) {
-                        M = to == kNegInf ? 0.f : to;
+                        M = to;
                     } else {
                         // Rare: some block grew too far; O and the sums follow.
                         float alpha = 1.f;
@@ -916,21 +1095,23 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                             alpha = exp2_fast(M - to);
                             M = to;
                         }
-                        if (mine) al_s[h0 + lane] = alpha; // the same from each of the half's four warps
+                        if (mine) al_s[h0 + lane] = alpha; // the same from each of the part's four warps
                         __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            if (k >= 4 * ng) break;
+                        for (int k = 0; k < kPer / 2; ++k) {
+                            if (2 * k >= hpp) break;
                             const float2 by = *reinterpret_cast<const float2*>(al_s + h0 + 2 * k);
                             l[k] = mul2(l[k], by);
                             lr[k] = mul2(lr[k], by);
                         }
-                        ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
+                        ok = opaque(ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1));
                         tc_fence_after();
-                        for (int blk = 0; ok && blk < p.nblk; ++blk)
-                            for (int k = 0; k < 2 * ng; ++k) {
+#pragma unroll 1
+                        for (int c = 0; ok && c < p.nblk * (kLow ? 2 : 1); ++c)
+#pragma unroll 1
+                            for (int k = 0; 4 * k < hpp; ++k) {
                                 uint32_t r[4];
-                                const uint32_t at = tl + blk * kHeads + h0 + 4 * k;
+                                const uint32_t at = tl + (kLow ? (c >> 1) * kHeads + (c & 1) * kLow : c * kHeads) + h0 + 4 * k;
                                 tmem_ld4(at, r);
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * al_s[h0 + 4 * k + j]);
@@ -939,42 +1120,45 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                         tmem_wait_st();
                     }
                 }
-                const int up = static_cast<int>(fmaxf(fminf((top == kNegInf ? M : top) - M, 127.f), -126.f));
-                bc[32 + lane] = __int_as_float((up + 127) << 23);
-                if (!__all_sync(0xffffffffu, pv_done)) ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
-                if (ok) {
+                const int up = static_cast<int>(fmaxf(fminf(top - M, 127.f), -126.f));
+                if (lane < kPer) bc[kPer + lane] = __int_as_float((up + 127) << 23);
+                if (!__all_sync(0xffffffffu, pv_done)) ok = opaque(ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1));
+                if (opaque(ok)) {
+                    // hi of the heads, then lo: in the same row of 64 bytes or in a
+                    // buffer of its own.  A quarter of the warp's lanes fill all
+                    // banks with 16 bytes each.
                     uint8_t* at = p_s + tok * 64;
-                    // A quarter of the warp's lanes fill all banks with 16 bytes each.
-                    const int swz = (tok >> 1) & 3;
-                    if (ng & 1) {
+                    const int swz = (tok >> 1) & 3, below = kPair ? kPBytes : 0, beside = kPair ? 0 : HP;
+                    if (hpp % 16 == 0) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (k >= ng) break;
-                            const int v = half * ng + k;   // eight heads: eight bytes
-                            const int off = (((v >> 1) ^ swz) << 4) + (v & 1) * 8;
-                            *reinterpret_cast<uint2*>(at + off) = make_uint2(hi[2 * k], hi[2 * k + 1]);
-                            *reinterpret_cast<uint2*>(at + kPBytes + off) = make_uint2(lo[2 * k], lo[2 * k + 1]);
+                        for (int k = 0; k < kPer / 16; ++k) {
+                            if (16 * k >= hpp) break;
+                            const int v = (h0 >> 4) + k, u = v + (beside >> 4);
+                            *reinterpret_cast<uint4*>(at + ((v ^ swz) << 4)) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                            *reinterpret_cast<uint4*>(at + below + ((u ^ swz) << 4)) =
+                                make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
                         }
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            if (2 * k >= ng) break;
-                            const int off = ((half * (ng >> 1) + k) ^ swz) << 4;
-                            *reinterpret_cast<uint4*>(at + off) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                            *reinterpret_cast<uint4*>(at + kPBytes + off) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                        for (int k = 0; k < kPer / 4; ++k) {
+                            if (4 * k >= hpp) break;
+                            const int v = h0 + 4 * k, u = v + beside;   // four heads: four bytes
+                            *reinterpret_cast<uint32_t*>(at + (((v >> 4) ^ swz) << 4) + (v & 12)) = hi[k];
+                            *reinterpret_cast<uint32_t*>(at + below + (((u >> 4) ^ swz) << 4) + (u & 12)) = lo[k];
                         }
                     }
                     if (mine) {
-                        const int h = h0 + lane;
-                        uint8_t* sf = sf_s + (h & 31) * 16 + (h >> 5) * 4 + quad;
-                        sf[0] = static_cast<uint8_t>(up + 127);
-                        sf[8] = static_cast<uint8_t>(max(up + 127 - 5, 0));
+                        const int h = h0 + lane, u = kPair ? h + 64 : h + HP;   // rows of the scales
+                        sf_s[(h & 31) * 16 + (h >> 5) * 4 + quad] = static_cast<uint8_t>(up + 127);
+                        sf_s[(u & 31) * 16 + (u >> 5) * 4 + quad] = static_cast<uint8_t>(max(up + 127 - 5, 0));
                     }
-                    if (valid < kTile) {
+                    if (opaque(valid < kTile)) {
                         // Rows past the length hold whatever the page or the
                         // buffer held: 0 * NaN would reach O, so their codes become 0.
                         // (S^T of this tile is done, so its chunks have landed.)
+#pragma unroll 1
                         for (int r = valid + (st >> 3); r < kTile; r += kSoftThreads / 8) {
+#pragma unroll 1
                             for (int j = 0; j < p.nblk; ++j) {
                                 int slot;
                                 uint32_t parity;
@@ -990,125 +1174,25 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 if (lane == 0) mbar_arrive(smem_u32(pfull));
                 // The sums, while the product runs.  Tokens whose values are far
                 // below their neighbours' count unrounded.
-                const bool tiny = lg < redux_max(in ? lg : -1.0e30f) - 8.f, any_tiny = __any_sync(0xffffffffu, tiny);
+                const bool tiny = lg < redux_max(in ? lg : -1.0e30f) - 8.f;
                 const float inv_s = exp2_fast(-lg);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (k >= 2 * ng) break;
-                    const float4 f = *reinterpret_cast<const float4*>(bc + 32 + 4 * k);
+                for (int k = 0; k < kPer / 4; ++k) {
+                    if (4 * k >= hpp) break;
+                    const float4 f = *reinterpret_cast<const float4*>(bc + kPer + 4 * k);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int e = 2 * k + j;
                         const float2 w = mul2(j ? make_float2(f.z, f.w) : make_float2(f.x, f.y), make_float2(inv_s, inv_s));
                         float2 r = __half22float2(sum[e]);
-                        if (any_tiny && tiny) r = z[e];
+                        r = make_float2(tiny ? z[e].x : r.x, tiny ? z[e].y : r.y);
                         l[e] = fma2(z[e], w, l[e]);
                         lr[e] = fma2(r, w, lr[e]);
                     }
                 }
                 __syncwarp();                              // bc is read
             }
-            // S^T of the last tile is done with q: the next job's takes its place
-            // while the last product runs.
             ++nq;
-            {
-                Run r = run;
-                r.advance();
-                if (seek(r) && ok) split_q(r, nq & 1);
-            }
-            // ---- output of the job (or of this worker's part of it)
-            // Sums over the tokens: lane k gets head h0 + k's.
-            float v[32], u[32];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                v[2 * k] = l[k].x; v[2 * k + 1] = l[k].y;
-                u[2 * k] = lr[k].x; u[2 * k + 1] = lr[k].y;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-                for (int k = 0; k < o; ++k) {
-                    const bool odd = lane & o;
-                    const float a = odd ? v[k] : v[k + o], c = odd ? u[k] : u[k + o];
-                    v[k] = (odd ? v[k + o] : v[k]) + __shfl_xor_sync(0xffffffffu, a, o);
-                    u[k] = (odd ? u[k + o] : u[k]) + __shfl_xor_sync(0xffffffffu, c, o);
-                }
-            bc[lane] = v[0];
-            bc[32 + lane] = u[0];
-            half_sync_or(half, false);                     // bc is next written after the next job's barrier
-            float ls = 0.f, lrs = 0.f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                ls += bc_s[(half * 4 + q) * 64 + lane];
-                lrs += bc_s[(half * 4 + q) * 64 + 32 + lane];
-            }
-            // A part's weights add up to its unrounded sum, which the join divides by.
-            if (mine) al_s[h0 + lane] = lrs > 0.f || lrs != lrs ? __fdividef(whole ? 1.0f : ls, lrs) : 0.f;
-            __syncwarp();                                  // the same from each of the half's four warps
-            ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
-            tc_fence_after();
-            if (!ok) continue;
-            if (whole) {
-                // 32 values x 32 heads at a time, through the warp's own 2 KB of
-                // p's buffers: stmatrix turns the fragments into rows of 32 values
-                // (16-byte chunks, chunk ^ (row / 2) % 4), which leave as 16-byte
-                // stores, 64 bytes of each of eight heads at once.
-                const uint32_t stage = smem_u32(p_s) + sw * 2048;
-                const int col0 = 2 * (lane & 3);
-                for (int blk = 0; blk < p.nblk; ++blk) {
-                    uint32_t x[2][16];
-                    const uint32_t src = tl + blk * kHeads + h0;
-                    tmem_ld_frag32(src, x[0]);
-                    tmem_ld_frag32(src + (16u << 16), x[1]);
-                    tmem_ld16_wait(x[0]);
-                    tmem_ld16_wait(x[1]);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {          // eight heads
-                        if (q >= ng) break;
-                        const float2 f = *reinterpret_cast<const float2*>(al_s + h0 + q * 8 + col0);
-                        uint32_t v[4];
-#pragma unroll
-                        for (int d = 0; d < 4; ++d)        // eight values
-                            v[d] = pack_bf16(__uint_as_float(x[d >> 1][q * 4 + (d & 1) * 2]) * f.x,
-                                             __uint_as_float(x[d >> 1][q * 4 + (d & 1) * 2 + 1]) * f.y);
-                        const int hl = q * 8 + (lane & 7), d = lane >> 3;
-                        stmatrix_x4_trans(stage + hl * 64 + ((d ^ ((hl >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
-                    }
-                    __syncwarp();
-                    __nv_bfloat16* o = p.out + b * p.ldo_b + blk * 128 + quad * 32 + (lane & 3) * 8;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j >= ng) break;
-                        const int hl = j * 8 + (lane >> 2), head = h0 + hl;
-                        uint4 v;
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                     : "r"(stage + hl * 64 + (((lane & 3) ^ ((hl >> 1) & 3)) << 4))
-                                     : "memory");
-                        if (head < run.count && bounds_ok(b >= 0 && b < p.B))
-                            *reinterpret_cast<uint4*>(o + static_cast<int64_t>(g * kHeads + head) * p.ldo_h) = v;
-                    }
-                    __syncwarp();
-                }
-            } else {
-                // A part, in the order the registers hold it: 512 bytes a store.
-                const int64_t slot = part_slot(p, w, run.j, run.j == j_first, g);
-                float4* o = reinterpret_cast<float4*>(p.part_o) + slot * p.nblk * 16 * 128 + quad * 32 + lane;
-                for (int k = 0; k < 2 * ng && h0 + 4 * k < run.count; ++k) {
-                    const float4 f = *reinterpret_cast<const float4*>(al_s + h0 + 4 * k);
-                    for (int blk = 0; blk < p.nblk; ++blk) {
-                        uint32_t x[4];
-                        tmem_ld4(tl + blk * kHeads + h0 + 4 * k, x);
-                        o[(blk * 16 + (h0 >> 2) + k) * 128] = make_float4(__uint_as_float(x[0]) * f.x, __uint_as_float(x[1]) * f.y,
-                                                                          __uint_as_float(x[2]) * f.z, __uint_as_float(x[3]) * f.w);
-                    }
-                }
-                if (quad == 0 && mine) p.part_ml[slot * kHeads + h0 + lane] = make_float2(M, ls);
-            }
-            const int head = g * kHeads + h0 + lane;
-            if (whole && p.lse && quad == 0 && mine && head < p.H)
-                p.lse[b * p.ldl_b + head] = ls == 0.f ? kNegInf : (M + log2f(ls)) * kLn2;
-            tc_fence_before();
         }
     }
 
@@ -1513,8 +1597,12 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
 
     CUtensorMap mc;
     if (!make_cache_map(&mc, t.cache, t.num_pages, z.page_size, cpt, t.ld_page, t.ld_row, p.box_rows)) return DSNQ_ERR_CUDA;
-    if (!set_smem_attr(reinterpret_cast<const void*>(latent_attention_fp8_kernel), smem)) return DSNQ_ERR_CUDA;
-    st = launch_result(launch_kernel(latent_attention_fp8_kernel, dim3(static_cast<unsigned>(p.W * p.G)), dim3(kThreads), smem, s, mc, p));
+    void (*kern)(CUtensorMap, Params) = p.q_rows <= 16   ? latent_attention_fp8_kernel<1>
+                                        : p.q_rows <= 32 ? latent_attention_fp8_kernel<2>
+                                        : p.q_rows <= 48 ? latent_attention_fp8_kernel<3>
+                                                         : latent_attention_fp8_kernel<4>;
+    if (!set_smem_attr(reinterpret_cast<const void*>(kern), smem)) return DSNQ_ERR_CUDA;
+    st = launch_result(launch_kernel(kern, dim3(static_cast<unsigned>(p.W * p.G)), dim3(kThreads), smem, s, mc, p));
     if (st != DSNQ_OK || (p.W == 1 && !z.prefix)) return st;
     // Few jobs: a request has many parts, so a CTA joins each item.  Many: a
     // warp does, and without a prefix no more requests can be split than there
