@@ -302,7 +302,7 @@ __device__ __forceinline__ float log2_fast(float x) {
 // Registers of a copying or issuing thread and of a softmax thread: together
 // those that the CTA is launched with.  What does not fit goes to local memory,
 // whose loads wait behind the products' reads of shared memory.
-constexpr int kRegsIssue = kPer == 16 ? 56 : 72, kRegsSoft = kPer == 16 ? 104 : 216;
+constexpr int kRegsIssue = kPer == 16 ? 56 : 88, kRegsSoft = kPer == 16 ? 104 : 208;
 static_assert(128 * kRegsIssue + kSoftThreads * kRegsSoft <= kThreads * (kPer == 16 ? 96 : 168), "registers of the CTA at its launch");
 
 // wait_bounded<true> in a few instructions: the clock is first read after 64
@@ -354,38 +354,32 @@ __device__ __forceinline__ bool part_sync_or(int part, bool v) {
 // slot or two: there (`twin`) a tile has four slots, and the last codes follow
 // the position columns, which S^T is done with early, in one slot.
 struct Chunks {
-    int i[2] = {0, 0};
-    uint32_t pass[2] = {0, 0}, n = 0;
-    __device__ __forceinline__ void at(const Params& p, int c, int& slot, uint32_t& parity) const {
-        if (opaque(p.twin)) {
-            const int pos = c == 4 ? 1 : c;
-            slot = static_cast<int>(n & 1) * 4 + pos;
-            parity = pos == 1 ? (c == 4) : (n >> 1) & 1;
+    int even = 0, odd = 0;            // places of the next even and odd chunk in their rings
+    uint32_t passes = 0;              // parities of the rings' passes: bit 0 even, bit 1 odd
+    int first_odd = 0;                // slot of the tile's first odd chunk
+    // Chunk c, the chunks of a tile being taken in order.
+    __device__ __forceinline__ void take(const Params& p, int c, int& slot, uint32_t& parity) {
+        const bool r = c & 1, twin = opaque(p.twin);
+        if (twin && c == 4) {
+            slot = first_odd;
+            parity = 1;
             return;
         }
-        const bool odd = c & 1;
-        const int size = odd ? p.odd_slots : p.slots - p.odd_slots;
-        slot = (odd ? i[1] : i[0]) + (c >> 1);
-        parity = odd ? pass[1] : pass[0];
-        if (slot >= size) {
-            slot -= size;
-            parity ^= 1;
-        }
-        if (odd) slot += p.slots - p.odd_slots;
+        const int at = r ? odd : even, evens = p.slots - p.odd_slots;
+        slot = twin ? 2 * at + r : at + (r ? evens : 0);
+        parity = twin && c == 1 ? 0 : passes >> r & 1;
+        if (c == 1) first_odd = slot;
+        const bool wrap = at + 1 == (r ? p.odd_slots : evens);
+        const int next = wrap ? 0 : at + 1;
+        odd = r ? next : odd;
+        even = r ? even : next;
+        passes ^= static_cast<uint32_t>(wrap) << r;
     }
-    __device__ __forceinline__ void next(const Params& p) {
-        ++n;
-        if (opaque(p.twin)) return;
-        const int cpt = p.cc + p.pe;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int size = r ? p.odd_slots : p.slots - p.odd_slots;
-            i[r] += (cpt + 1 - r) >> 1;
-            if (i[r] >= size && size > 0) {
-                i[r] -= size;
-                pass[r] ^= 1;
-            }
-        }
+    // Slot of chunk c of the n-th tile.
+    static __device__ __forceinline__ int slot_of(const Params& p, uint32_t n, int c) {
+        if (p.twin) return static_cast<int>(n & 1) * 4 + (c == 4 ? 1 : c);
+        const int r = c & 1, size = r ? p.odd_slots : p.slots - p.odd_slots, each = (p.cc + p.pe + 1 - r) >> 1;
+        return static_cast<int>((n % size * each + (c >> 1)) % size) + (r ? p.slots - p.odd_slots : 0);
     }
 };
 
@@ -610,7 +604,10 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         const int pieces = kTile / p.box_rows;             // copies of a chunk (1, 2, 4, 8 or 16)
         const int batch = 32 / pieces;                     // tiles whose table entries the lanes hold
         const int odd = warp == 3;
+        const int lines = p.twin ? 2 + odd : (cpt + 1 - odd) / 2;   // this warp's chunks of a tile
+        const uint32_t to = smem_u32(ring) + lane * p.box_rows * 128;
         Chunks ch;
+        uint32_t n = 0;
         bool ok = true, skip = !odd && (p.inject & kInjectSkipLoad) != 0;
 #pragma unroll 1
         for (; ok && run.next(p, g); run.advance()) {
@@ -621,7 +618,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             const uint64_t policy = prefix ? again : once;
             int ids = 0, offs = 0;
 #pragma unroll 1
-            for (int i = 0; ok && i < run.n; ++i, ch.next(p)) {
+            for (int i = 0; ok && i < run.n; ++i, ++n) {
                 const int tile = run.t0 + i;
                 if (i % batch == 0) {
                     const int64_t tok = static_cast<int64_t>(tile) * kTile + static_cast<int64_t>(lane) * p.box_rows;
@@ -640,22 +637,19 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 const int from = (i % batch) * pieces + (lane & (pieces - 1));
                 const int id = __shfl_sync(0xffffffffu, ids, from), in_page = __shfl_sync(0xffffffffu, offs, from);
 #pragma unroll 1
-                for (int k = 0; k < 3; ++k) {
-                    const int c = k == 2 && opaque(p.twin) ? (odd ? 4 : 5) : 2 * k + odd;
-                    if (c >= cpt) break;
+                for (int k = 0; k < lines; ++k) {
+                    const int c = odd && k == 2 ? 4 : 2 * k + odd;
                     const int chunk = c == 0 ? 0 : !p.pe ? c : c == 1 ? p.cc : c - 1;
                     int slot;
                     uint32_t parity;
-                    ch.at(p, c, slot, parity);
+                    ch.take(p, c, slot, parity);
                     ok = wait_uniform_asleep(smem_u32(&empty[slot]), parity ^ 1);
                     if (!ok) break;
                     const uint32_t fb = smem_u32(&full[slot]);
                     if (!skip) {                           // test hook: the first chunk never comes, the waits on it run out
                         if (lane == 0) mbar_arrive_expect_tx(fb, live * p.box_rows * 128);
                         __syncwarp();
-                        if (lane < live)
-                            tma_load_5d(smem_u32(ring) + slot * kChunkBytes + lane * p.box_rows * 128, &map_c, fb, chunk, in_page / 8, id,
-                                        policy);
+                        if (lane < live) tma_load_5d(to + slot * kChunkBytes, &map_c, fb, chunk, in_page / 8, id, policy);
                     }
                     skip = false;
                     if (c == 0) {
@@ -663,8 +657,8 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                         // has gone, since this chunk's slot is free.)
                         const int own = lane * 4 / p.box_rows;
                         const int page = __shfl_sync(0xffffffffu, id, own), first = __shfl_sync(0xffffffffu, in_page, own);
-                        float* sc = sc_s + (ch.n & (kScaleSlots - 1)) * kTile + lane * 4;
-                        const uint32_t sb = smem_u32(&scfull[ch.n & (kScaleSlots - 1)]);
+                        float* sc = sc_s + (n & (kScaleSlots - 1)) * kTile + lane * 4;
+                        const uint32_t sb = smem_u32(&scfull[n & (kScaleSlots - 1)]);
                         if (own < live && page < p.num_pages) {
                             copy16(smem_u32(sc), p.scales + static_cast<int64_t>(page) * p.ld_scale + first + lane * 4 - own * p.box_rows);
                             copies_arrive(sb);
@@ -683,7 +677,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         const uint32_t q_low = desc_low(smem_u32(q_s), 16), pe_low = desc_low(smem_u32(qpe_s), 16);
         const uint32_t d = tmem + kTmemS;
         Chunks ch;
-        uint32_t nq = 0;
+        uint32_t n = 0, nq = 0;
         bool ok = true;
 #pragma unroll 1
         for (; ok && run.next(p, g); run.advance()) {
@@ -691,14 +685,14 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             ok = wait_uniform(smem_u32(qfull), nq & 1);
             ++nq;
 #pragma unroll 1
-            for (int i = 0; ok && i < run.n; ++i, ch.next(p)) {
-                ok = wait_uniform(smem_u32(sempty), (ch.n & 1) ^ 1);
+            for (int i = 0; ok && i < run.n; ++i, ++n) {
+                ok = wait_uniform(smem_u32(sempty), (n & 1) ^ 1);
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; ok && c < cpt; ++c) {
                     int slot;
                     uint32_t parity;
-                    ch.at(p, c, slot, parity);
+                    ch.take(p, c, slot, parity);
                     const int code = c == 0 ? 0 : c - p.pe;
                     const bool pe = c == 1 && opaque(p.pe);
                     const uint32_t a = desc_low(smem_u32(ring) + slot * kChunkBytes, 16);
@@ -722,22 +716,25 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         const uint32_t p_low = desc_low(smem_u32(p_s), kPBytes);
         const uint64_t sf_desc = static_cast<uint64_t>(kHighRows16) << 32 | desc_low(smem_u32(sf_s), 0);
         Chunks ch;
+        uint32_t n = 0;
         bool ok = true;
 #pragma unroll 1
         for (; ok && run.next(p, g); run.advance()) {
             if (!run.live()) continue;
 #pragma unroll 1
-            for (int i = 0; i < run.n; ++i, ch.next(p)) {
-                ok = wait_uniform(smem_u32(pfull), ch.n & 1);
+            for (int i = 0; i < run.n; ++i, ++n) {
+                ok = wait_uniform(smem_u32(pfull), n & 1);
                 if (!ok) break;
                 tc_fence_after();
                 tc_copy_scales(tmem + kTmemSfb, sf_desc);
 #pragma unroll 1
-                for (int k = 0; k < p.nblk; ++k) {
+                for (int c = 0; c < cpt; ++c) {
                     int slot;
                     uint32_t parity;
-                    ch.at(p, k == 0 ? 0 : k + p.pe, slot, parity);
-                    tc_mma_scaled<kPair>(tmem + k * kHeads, desc_low(smem_u32(ring) + slot * kChunkBytes, kChunkBytes), p_low,
+                    ch.take(p, c, slot, parity);
+                    const int code = c == 0 ? 0 : c - p.pe;
+                    if ((c == 1 && p.pe) || code >= p.nblk) continue;
+                    tc_mma_scaled<kPair>(tmem + code * kHeads, desc_low(smem_u32(ring) + slot * kChunkBytes, kChunkBytes), p_low,
                                          idesc_o(kPair ? HP : 2 * HP), tmem + kTmemSfa, tmem + kTmemSfb, i > 0);
                     tc_commit(smem_u32(&empty[slot]));
                 }
@@ -760,7 +757,6 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         const int DV = p.nblk * 128;
         float* bc = bc_s + sw * 2 * kPer;
         uint32_t n = 0, nq = 0;
-        Chunks ch;
         bool ok = true;                                    // false: only the barriers are kept up
 
         // Splits the queries of the job r into shared memory, and leaves the
@@ -996,7 +992,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
 #pragma unroll
             for (int k = 0; k < kPer / 2; ++k) l[k] = lr[k] = make_float2(0.f, 0.f);
 #pragma unroll 1
-            for (int i = 0; i < run.n; ++i, ++n, ch.next(p)) {
+            for (int i = 0; i < run.n; ++i, ++n) {
                 const int valid = min(kTile, run.len - (run.t0 + i) * kTile);
                 const bool in = tok < valid;
                 const uint32_t sb = smem_u32(&scfull[n & (kScaleSlots - 1)]), sp = (n / kScaleSlots) & 1;
@@ -1157,14 +1153,12 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                         // buffer held: 0 * NaN would reach O, so their codes become 0.
                         // (S^T of this tile is done, so its chunks have landed.)
 #pragma unroll 1
-                        for (int r = valid + (st >> 3); r < kTile; r += kSoftThreads / 8) {
+                        for (int c = 0; c < cpt; ++c) {
+                            if ((c == 1 && p.pe) || c - (c > 0 ? p.pe : 0) >= p.nblk) continue;
+                            const int slot = Chunks::slot_of(p, n, c);
 #pragma unroll 1
-                            for (int j = 0; j < p.nblk; ++j) {
-                                int slot;
-                                uint32_t parity;
-                                ch.at(p, j == 0 ? 0 : j + p.pe, slot, parity);
+                            for (int r = valid + (st >> 3); r < kTile; r += kSoftThreads / 8)
                                 *reinterpret_cast<uint4*>(ring + slot * kChunkBytes + r * 128 + (st & 7) * 16) = make_uint4(0, 0, 0, 0);
-                            }
                         }
                     }
                 }
