@@ -255,6 +255,15 @@ __device__ __forceinline__ void tmem_ld8_wait(uint32_t (&r)[8]) {
                  :
                  : "memory");
 }
+__device__ __forceinline__ void tmem_ld4_issue(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld4_wait(uint32_t (&r)[4]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])::"memory");
+}
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
@@ -291,6 +300,13 @@ __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo, __h
     sum = __hfma2(half2_of(lo), __float2half2_rn(0.03125f), h);
 }
 __device__ __forceinline__ float2 unpack_bf16(uint32_t v) { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
+
+// The largest magnitude of eight bf16, as its bits (NaN above all others).
+__device__ __forceinline__ uint32_t largest8(const uint4& v) {
+    const uint32_t a = __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), b = __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
+    const uint32_t c = __vmaxu2(a, b);
+    return max(c & 0xffffu, c >> 16);
+}
 
 // lg2.approx: off by at most 2^-22 here, and its inverse is taken from itself.
 __device__ __forceinline__ float log2_fast(float x) {
@@ -517,7 +533,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         const int h = min(p.H, kHeads), joined = 5 * p.B * h / (16 * p.W_full);
         const int slack = max(1, p.W < kManyParts * p.B ? min(joined, 2 + h / 64) : joined);
         const bool uncut = !p.prefix_len && p.B <= p.W && most <= (tiles + p.W - 1) / p.W + slack;
-        const int lead = tiles >= p.W ? 1 : 0;
+        const int lead = tiles < p.W ? 0 : tiles < 2 * p.W ? 1 : 2;
         const int64_t front = static_cast<int64_t>(pjobs) * (lead + ptiles);   // units of the prefix
         const int64_t total = tiles + static_cast<int64_t>(lead) * (p.B + pjobs);
         before += front + static_cast<int64_t>(lead) * b0;
@@ -760,14 +776,16 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         bool ok = true;                                    // false: only the barriers are kept up
 
         // Splits the queries of the job r into shared memory, and leaves the
-        // factors of their scores.  Warp sw takes rows sw, sw + kSoftWarps, ...; a lane
-        // 16 codes, lanes 0..7 also eight position columns.
+        // factors of their scores.  Warp sw takes rows sw, sw + kSoftWarps, ..., four
+        // at once; a lane 16 codes, lanes 0..7 also eight position columns.  Rows
+        // that pad the job keep what they hold: nothing of their columns is used.
         auto split_q = [&](const Run& r, int buf) {
             const bool prefix = r.j < p.NP;
             const int row0 = prefix ? (r.j * p.G + g) * kHeads : g * kHeads;
-            constexpr int kAhead = 2;
+            constexpr int kAhead = 4;
+            const bool codes = lane * 16 < p.cc * 128, pos = p.pe && lane < 8;
 #pragma unroll 1
-            for (int i0 = sw; i0 < HP; i0 += kAhead * kSoftWarps) {
+            for (int i0 = sw; i0 < r.count; i0 += kAhead * kSoftWarps) {
                 uint4 x[kAhead][2], e[kAhead];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
@@ -780,30 +798,30 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     }
                     if (i >= r.count || h >= p.H || !bounds_ok(b >= 0 && b < p.B)) continue;
                     const __nv_bfloat16* src = p.q + b * p.ldq_b + h * p.ldq_h;
-                    if (lane * 16 < p.cc * 128) {
+                    if (codes) {
                         x[u][0] = *reinterpret_cast<const uint4*>(src + lane * 16);
                         x[u][1] = *reinterpret_cast<const uint4*>(src + lane * 16 + 8);
                     }
-                    if (p.pe && lane < 8) e[u] = *reinterpret_cast<const uint4*>(src + p.cc * 128 + lane * 8);
+                    if (pos) e[u] = *reinterpret_cast<const uint4*>(src + p.cc * 128 + lane * 8);
+                }
+                // The largest magnitudes, as the bits of a bf16 (NaN above all others).
+                uint32_t top[kAhead], etop[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    top[u] = largest8(x[u][0]);
+                    top[u] = __reduce_max_sync(0xffffffffu, max(top[u], largest8(x[u][1])));
+                    etop[u] = p.pe ? __reduce_max_sync(0xffffffffu, largest8(e[u])) : 0;
                 }
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int i = i0 + u * kSoftWarps;
-                    if (i >= HP) break;
-                    // The largest magnitude, as the bits of a bf16 (infinities and NaN above all others).
+                    if (i >= r.count) break;
                     const uint32_t* xw = reinterpret_cast<const uint32_t*>(x[u]);
                     const uint32_t* ew = reinterpret_cast<const uint32_t*>(&e[u]);
-                    uint32_t top = 0, etop = 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) top = max(top, max(xw[k] & 0x7fff, (xw[k] >> 16) & 0x7fff));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) etop = max(etop, max(ew[k] & 0x7fff, (ew[k] >> 16) & 0x7fff));
-                    top = __reduce_max_sync(0xffffffffu, top);
-                    if (p.pe) etop = __reduce_max_sync(0xffffffffu, etop);
                     // 2^ex > largest / 256, so that 32 (x - hi) <= 256; and the position columns divided by it stay finite.
-                    int ex = static_cast<int>(top >> 7) - 127 - 7;
-                    ex = max(max(ex, -100), static_cast<int>(etop >> 7) - 127 - 100);
-                    const bool finite = max(top, etop) < 0x7f80;
+                    int ex = static_cast<int>(top[u] >> 7) - 127 - 7;
+                    ex = max(max(ex, -100), static_cast<int>(etop[u] >> 7) - 127 - 100);
+                    const bool finite = max(top[u], etop[u]) < 0x7f80;
                     if (!finite) ex = 0;
                     const float inv = __int_as_float((127 - ex) << 23);
                     if (lane == 0)
@@ -813,22 +831,23 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     for (int k = 0; k < 4; ++k) {
                         uint32_t h0, h1, l0, l1;
                         __half2 s;
-                        const float2 a = unpack_bf16(xw[2 * k]), b = unpack_bf16(xw[2 * k + 1]);
-                        split2(make_float2(a.x * inv, a.y * inv), h0, l0, s);
-                        split2(make_float2(b.x * inv, b.y * inv), h1, l1, s);
-                        hi[k] = h0 | h1 << 16;
-                        lo[k] = l0 | l1 << 16;
+                        split2(mul2(unpack_bf16(xw[2 * k]), make_float2(inv, inv)), h0, l0, s);
+                        split2(mul2(unpack_bf16(xw[2 * k + 1]), make_float2(inv, inv)), h1, l1, s);
+                        hi[k] = __byte_perm(h0, h1, 0x5410);
+                        lo[k] = __byte_perm(l0, l1, 0x5410);
                     }
-                    if (lane * 16 < p.cc * 128) {
+                    if (codes) {
                         uint8_t* at = q_s + (lane >> 3) * q_chunk + (((lane & 7) ^ (i & 7)) << 4);
                         *reinterpret_cast<uint4*>(at + i * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4*>(at + (HP + i) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    if (p.pe && lane < 8) {
+                    if (pos) {
                         uint32_t v[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            v[k] = pack_bf16(__uint_as_float(ew[k] << 16) * inv, __uint_as_float(ew[k] & 0xffff0000u) * inv);
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = mul2(unpack_bf16(ew[k]), make_float2(inv, inv));
+                            v[k] = pack_bf16(f.x, f.y);
+                        }
                         *reinterpret_cast<uint4*>(qpe_s + i * 128 + ((lane ^ (i & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
@@ -866,7 +885,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             if (started) {
                 // ---- output of the job (or of this worker's part of it)
                 const int b = run.j - p.NP, h0 = part * hpp;
-                const bool whole = !p.prefix_len && run.t0 == 0 && run.n == run.tiles, mine = lane < hpp;
+                const bool whole = !p.prefix_len && run.t0 == 0 && run.n == run.tiles, mine = lane < hpp && h0 + lane < run.count;
                 // Sums over the tokens: lane k gets head h0 + k's.
                 float v[kPer], u[kPer];
 #pragma unroll
@@ -961,18 +980,25 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
 #pragma unroll 1
                     for (int k = 0; 4 * k < hpp && h0 + 4 * k < run.count; ++k) {
                         const float4 f = *reinterpret_cast<const float4*>(al_s + h0 + 4 * k);
-#pragma unroll 1
-                        for (int blk = 0; blk < p.nblk; ++blk) {
-                            uint32_t x[4];
-                            tmem_ld4(tl + blk * kHeads + h0 + 4 * k, x);
-                            if (kLow) {
-                                uint32_t y[4];
-                                tmem_ld4(tl + blk * kHeads + kLow + h0 + 4 * k, y);
+                        uint32_t x[4][4], y[4][4];
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) + __uint_as_float(y[u]));
+                        for (int blk = 0; blk < 4; ++blk) {
+                            if (blk >= p.nblk) break;
+                            tmem_ld4_issue(tl + blk * kHeads + h0 + 4 * k, x[blk]);
+                            if (kLow) tmem_ld4_issue(tl + blk * kHeads + kLow + h0 + 4 * k, y[blk]);
+                        }
+#pragma unroll
+                        for (int blk = 0; blk < 4; ++blk) {
+                            if (blk >= p.nblk) break;
+                            tmem_ld4_wait(x[blk]);
+                            if (kLow) {
+                                tmem_ld4_wait(y[blk]);
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) x[blk][u] = __float_as_uint(__uint_as_float(x[blk][u]) + __uint_as_float(y[blk][u]));
                             }
-                            o[(blk * 16 + (h0 >> 2) + k) * 128] = make_float4(__uint_as_float(x[0]) * f.x, __uint_as_float(x[1]) * f.y,
-                                                                              __uint_as_float(x[2]) * f.z, __uint_as_float(x[3]) * f.w);
+                            o[(blk * 16 + (h0 >> 2) + k) * 128] =
+                                make_float4(__uint_as_float(x[blk][0]) * f.x, __uint_as_float(x[blk][1]) * f.y, __uint_as_float(x[blk][2]) * f.z,
+                                            __uint_as_float(x[blk][3]) * f.w);
                         }
                     }
                     if (quad == 0 && mine) p.part_ml[slot * kHeads + h0 + lane] = make_float2(M, ls);
@@ -987,7 +1013,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             next.advance();
             started = true;
             const int h0 = part * hpp;                     // this warp's first head
-            const bool mine = lane < hpp;                  // this lane has a head: h0 + lane
+            const bool mine = lane < hpp && h0 + lane < run.count;   // this lane has a head: h0 + lane
             const float* cq = cq_s + (nq & 1) * kHeads + h0;
 #pragma unroll
             for (int k = 0; k < kPer / 2; ++k) l[k] = lr[k] = make_float2(0.f, 0.f);
