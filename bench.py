@@ -29,7 +29,7 @@ The JSON line also reports, measured in the same run:
   * cpu_baseline: the fp64 CPU oracle timed on the whole M=8192 workload.
 
 `--decode-ops` times the other operators of the decode step instead, case by
-case (perf/operators.py).
+case (perf/operators.py, perf/more_operators.py).
 
 `--impl reference` times the CPU oracle alone on the same metric (bounded
 samples of rows and output columns so the run ends within minutes).
@@ -920,7 +920,7 @@ DECODE_OPS = ["tables", "head_rope", "cache_write", "attention"]
 
 def run_decode_ops(args):
     """Times the library's call of every listed case of perf/operators.py and
-    of a few more and prints one JSON line: `graph_us` per call in a CUDA graph
+    perf/more_operators.py and of a few more and prints one JSON line: `graph_us` per call in a CUDA graph
     of DECODE_GRAPH_CALLS calls (a quarter of that from 64 MB a call on) over
     distinct inputs, L2 flushed before each replay; an input that a graph visits
     again has a gigabyte or more of others in between (so none is found in L2),
@@ -929,16 +929,21 @@ def run_decode_ops(args):
     import importlib.util
     import torch
     import gemm_dsnq_dual_gb300 as dsnq
-    spec = importlib.util.spec_from_file_location("decode_cases", os.path.join(ROOT, "perf", "operators.py"))
-    cases = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(cases)
-    cases.own = True
+
+    def load(name):
+        spec = importlib.util.spec_from_file_location("perf_" + name, os.path.join(ROOT, "perf", name + ".py"))
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.own = True
+        return module
+
+    first, second = load("operators"), load("more_operators")
     dev = torch.device("cuda", 0)
     torch.cuda.set_device(0)
     stream = torch.cuda.current_stream()
     flush = L2Flush(torch, dev)
     hbm_gbs, bf16, _, source = load_peaks()
-    by_name = {c["name"]: c for c in cases.listed()}
+    by_name = {c["name"]: c for c in first.listed()}
     more = [dict(by_name["rope prompt 4096"], name="rope prompt 4096, half pairs", layout="half"),
             dict(by_name["write prompt 8191"], name="write prompt 32768", M=32768, pad=0),
             dict(by_name["write prompt 8191"], name="write prompt 32768, half pairs", M=32768, pad=0, layout="half"),
@@ -946,12 +951,15 @@ def run_decode_ops(args):
             dict(by_name["attention 1 x 701"], name="attention 64 x 1000", B=64, maxlen=1000)]
     out = {}
     with ClockSampler(0) as clk:
-        for c in [*by_name.values(), *more]:
+        for cases, c in [*((first, c) for c in [*by_name.values(), *more]), *((second, c) for c in second.listed())]:
+            if args.only and not any(n in c["name"] for n in args.only.split(",")):
+                continue
             w = cases.work(c)
+            label = c["name"] + (" (8 bits)" if cases is second else "")
             sets = DECODE_GRAPH_CALLS if w["bytes"] < 16 << 20 else 25 if w["bytes"] < 64 << 20 else 5
             in_graph = DECODE_GRAPH_CALLS if w["bytes"] < 64 << 20 else DECODE_GRAPH_CALLS // 4
             states = [cases.prepare(c, 100 + i) for i in range(sets)]
-            calls = [lambda s=s: cases.run(s) for s in states]
+            calls = [lambda s=s, run=cases.run: run(s) for s in states]
             graph = timed_graph_calls(torch, stream, [calls[i % sets] for i in range(in_graph)], flush, reps=max(args.side_reps, 5))
             n = 2 * in_graph
             torch.cuda.synchronize()
@@ -961,8 +969,8 @@ def run_decode_ops(args):
             torch.cuda.synchronize()
             call = (time.perf_counter() - t0) / n * 1e6
             floor = max(w["bytes"] / hbm_gbs / 1e3, w["flops"] / bf16 / 1e6)
-            out[c["name"]] = {"floor_us": round(floor, 4), "graph_us": round(graph, 2), "call_us": round(call, 1), "sets": sets}
-            print(f"{c['name']:32s} floor {floor:9.4f}  graph {graph:8.2f}  call {call:8.1f} us", file=sys.stderr, flush=True)
+            out[label] = {"floor_us": round(floor, 4), "graph_us": round(graph, 2), "call_us": round(call, 1), "sets": sets}
+            print(f"{label:36s} floor {floor:9.4f}  graph {graph:8.2f}  call {call:8.1f} us", file=sys.stderr, flush=True)
             del states, calls
             torch.cuda.empty_cache()
         status = dsnq.debug_status()
@@ -1041,6 +1049,7 @@ def main():
     ap.add_argument("--no-long-context", dest="long_context", action="store_false",
                     help="skip the M=32768 long-context GEMM of the side measurements")
     ap.add_argument("--no-cpu-baseline", action="store_true")
+    ap.add_argument("--only", default="", help="with --decode-ops: only the cases whose names contain one of these texts (commas between)")
     ap.add_argument("--kernel-only", choices=["gemm", "norm_quant", "single_latent", "unfused", "fused_step", "bf16a", *DECODE_OPS],
                     default=None,
                     help="profiling aid: launch one kernel --launches times and exit")

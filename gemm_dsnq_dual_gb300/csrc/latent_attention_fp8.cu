@@ -131,7 +131,7 @@ __device__ __forceinline__ int tiles_of(int len) { return len > kTile ? (len + k
 // prefix every job leaves its parts: along the runs j + w grows from part to
 // part.  Otherwise only the first and the last job of a run can be cut.
 __device__ __forceinline__ int64_t part_slot(const Params& p, int w, int j, bool first, int g) {
-    return (p.prefix_len ? static_cast<int64_t>(j) + w : static_cast<int64_t>(w) * 2 + (first ? 0 : 1)) * p.G + g;
+    return static_cast<int64_t>(p.prefix_len ? j + w : 2 * w + (first ? 0 : 1)) * p.G + g;
 }
 
 // The same value, of which the compiler knows nothing: it would otherwise make
@@ -533,7 +533,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         const int h = min(p.H, kHeads), joined = 5 * p.B * h / (16 * p.W_full);
         const int slack = max(1, p.W < kManyParts * p.B ? min(joined, 2 + h / 64) : joined);
         const bool uncut = !p.prefix_len && p.B <= p.W && most <= (tiles + p.W - 1) / p.W + slack;
-        const int lead = tiles < p.W ? 0 : tiles < 2 * p.W ? 1 : 2;
+        const int lead = static_cast<int>(min(tiles / p.W, static_cast<int64_t>(3)));
         const int64_t front = static_cast<int64_t>(pjobs) * (lead + ptiles);   // units of the prefix
         const int64_t total = tiles + static_cast<int64_t>(lead) * (p.B + pjobs);
         before += front + static_cast<int64_t>(lead) * b0;
@@ -1240,7 +1240,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-template <int SHARE, int AHEAD, int CTAS>
+template <bool PREFIX, int SHARE, int AHEAD, int CTAS>
 __global__ void __launch_bounds__(kJoinThreads, CTAS)
 latent_attention_fp8_join_kernel(const Params p, const int by_cut) {
     grid_dependency_wait();
@@ -1271,15 +1271,14 @@ latent_attention_fp8_join_kernel(const Params p, const int by_cut) {
         w0 = before - 1;
         return upto - before + 1;
     };
-    int w1, w2 = 0, n1 = 0, n2;
+    int w1 = 0, w2, n1 = 0;
     const int sub = static_cast<int>(blockIdx.x) - what * per;
     const int item = SHARE == 1 ? sub * 8 + warp : sub;
     const int hq = min(item, items - 1) / p.nblk, blk = item - hq * p.nblk;
     int g1 = 0, hl1 = 0, j1 = 0;
     const int j2 = p.NP + b, g2 = hq * 4 / kHeads, hl2 = hq * 4 - g2 * kHeads;
-    n2 = parts_of(j2, w1);
-    if (p.prefix_len) {
-        w2 = w1;
+    int n2 = parts_of(j2, w2);
+    if (PREFIX) {
         if (clamp_len(p.cap, p.seq_lens[b]) == 0) n2 = 0;  // an empty request leaves none
         if (clamp_len(p.prefix_cap, *p.prefix_len) > 0) {
             // The rows of four heads lie in one group; a CTA's items may lie in two
@@ -1299,18 +1298,17 @@ latent_attention_fp8_join_kernel(const Params p, const int by_cut) {
             w1 = before - 1;
             n1 = upto - before + 1;
         }
-    } else {
-        w2 = w1;
-        if (n2 < 2) return;
+    } else if (n2 < 2) {
+        return;
     }
     if (item >= items) return;                             // SHARE = 8: the whole CTA
     const int np = n1 + n2;
     auto slot_of = [&](int k) -> int64_t {                 // part k's place in the workspace
+        if (!PREFIX) return part_slot(p, w2 + k, j2, k > 0 || meta_s[w2].x == j2, g2);
         const bool front = k < n1;
-        const int w = front ? w1 + k : w2 + k - n1, j = front ? j1 : j2;
-        return part_slot(p, w, j, meta_s[w].x == j, front ? g1 : g2);
+        return part_slot(p, front ? w1 + k : w2 + k - n1, front ? j1 : j2, false, front ? g1 : g2);
     };
-    auto row_of = [&](int k) { return k < n1 ? hl1 : hl2; };
+    auto row_of = [&](int k) { return PREFIX && k < n1 ? hl1 : hl2; };
     // Values 2 lane, + 1, 2 lane + 64, + 1 of the block.
     auto load = [&](int k, float4 (&o)[4]) {
         const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((slot_of(k) * p.nblk + blk) * 16 + row_of(k) / 4) * 128 + 2 * lane;
@@ -1634,9 +1632,16 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
     const bool share = p.W >= kManyParts * jobs;
     const int64_t grid = targets * (share ? items : (items + 7) / 8);
     void (*join)(Params, int);
-    if (share) join = p.W > 16 * jobs && grid <= sms ? latent_attention_fp8_join_kernel<8, 5, 1> : latent_attention_fp8_join_kernel<8, 2, 2>;
-    else if (!by_cut && grid <= 3 * sms) join = latent_attention_fp8_join_kernel<1, 4, 1>;
-    else join = grid <= 5 * sms ? latent_attention_fp8_join_kernel<1, 2, 2> : latent_attention_fp8_join_kernel<1, 2, 3>;
+    if (z.prefix) {
+        if (share) join = p.W > 16 * jobs && grid <= sms ? latent_attention_fp8_join_kernel<true, 8, 5, 1>
+                                                         : latent_attention_fp8_join_kernel<true, 8, 2, 2>;
+        else join = grid <= 3 * sms ? latent_attention_fp8_join_kernel<true, 1, 4, 1> : latent_attention_fp8_join_kernel<true, 1, 2, 2>;
+    } else {
+        if (share) join = p.W > 16 * jobs && grid <= sms ? latent_attention_fp8_join_kernel<false, 8, 5, 1>
+                                                         : latent_attention_fp8_join_kernel<false, 8, 2, 2>;
+        else if (!by_cut && grid <= 3 * sms) join = latent_attention_fp8_join_kernel<false, 1, 4, 1>;
+        else join = grid <= 5 * sms ? latent_attention_fp8_join_kernel<false, 1, 2, 2> : latent_attention_fp8_join_kernel<false, 1, 2, 3>;
+    }
     return launch_result(launch_kernel(join, dim3(static_cast<unsigned>(grid)), dim3(kJoinThreads), 0, s, p, by_cut));
 }
 
