@@ -757,6 +757,8 @@ def shared_prefix_latent_attention_fp8(q, cache, scales, prefix_table, prefix_le
     followed by seq_lens[b] tokens of its own row of block_table.  The prefix is
     read and multiplied once for every 64 (request, head) pairs of the batch.
     The workspace grows with the batch (about 8 v_dim bytes a pair)."""
+    if prefix_table is None:
+        raise TypeError("prefix_table must be a tensor; paged_latent_attention_fp8 takes requests without a common prefix")
     return _attention_fp8(q, cache, scales, prefix_table, prefix_len, block_table, seq_lens, v_dim, scale, out, lse, workspace, stream)
 
 
