@@ -452,8 +452,8 @@ def _workspace(size: int, dev, stream, handle: int):
 def release_workspaces() -> None:
     """Gives the workspaces that the attention calls keep for the calling thread
     (one for each of four streams of a device: up to 42 MB after
-    paged_latent_attention, more after shared_prefix_latent_attention_fp8) back
-    to torch's allocator.  Calls still running may go on using theirs: the memory goes to
+    paged_latent_attention, more by the batch's queries and partial results after
+    the calls over a cache in 8 bits) back to torch's allocator.  Calls still running may go on using theirs: the memory goes to
     later work of the same stream only."""
     _kept.__dict__.clear()
 
@@ -756,7 +756,8 @@ def shared_prefix_latent_attention_fp8(q, cache, scales, prefix_table, prefix_le
     prefix_len (int32 [1]) tokens of prefix_table [width] (int32 page ids), each
     followed by seq_lens[b] tokens of its own row of block_table.  The prefix is
     read and multiplied once for every 64 (request, head) pairs of the batch.
-    The workspace grows with the batch (about 8 v_dim bytes a pair)."""
+    The workspace grows with the batch (1200 bytes of split queries and 4 v_dim of
+    results a pair, twice)."""
     if prefix_table is None:
         raise TypeError("prefix_table must be a tensor; paged_latent_attention_fp8 takes requests without a common prefix")
     return _attention_fp8(q, cache, scales, prefix_table, prefix_len, block_table, seq_lens, v_dim, scale, out, lse, workspace, stream)

@@ -44,11 +44,11 @@
 // The prefix: its rows are the (request, head) pairs of the batch laid end to
 // end, so every tile of the prefix serves 64 rows whatever the number of heads.
 //
-// Warps: 0 and 3 copy tiles (TMA), 1 issues S^T, 2 issues O^T, the others do the softmax:
+// Warps: 0 and 3 copy tiles (TMA), 1 issues S^T, 2 issues O^T, 4..11 do the softmax:
 // warp w has tokens 32 (w % 4) .. of a tile (the TMEM lanes it can reach, and one
-// block of 32 of the scales) and one part of the heads.  They also split q,
-// for the next job while the last product of this one runs, and write the
-// output.
+// block of 32 of the scales) and one half of the heads; they also write the
+// output.  q is split beforehand, by a kernel of its own, and comes as one copy a
+// job.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -71,8 +71,7 @@ constexpr int kHeads = 64;                  // rows (heads) of a CTA
 constexpr int kTile = 128;                  // tokens of a tile
 constexpr int kChunkBytes = kTile * 128;    // 128 bytes of each row of a tile
 constexpr int kPer = 32;                    // heads of a softmax warp, at most
-constexpr int kParts = kHeads / kPer;
-constexpr int kSoftWarp0 = 4, kSoftWarps = 4 * kParts, kSoftThreads = kSoftWarps * 32;
+constexpr int kSoftWarp0 = 4, kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
 constexpr int kThreads = kSoftWarp0 * 32 + kSoftThreads;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSlots = 13;               // slots of the rings of chunks
@@ -90,8 +89,8 @@ constexpr int kPBytes = kTile * 64;         // hi (or lo) of p s of a tile: 64 b
 constexpr int kManyParts = 4;               // workers per job from which a CTA joins an item
 
 struct Params {
-    const __nv_bfloat16* q;
-    int64_t ldq_b, ldq_h;
+    const uint8_t* images;            // [B * G + NP * G] of a job's split queries (see split_queries_kernel)
+    int image;                        // bytes of one
     const float* scales;
     int64_t ld_scale;                 // of a page
     const int32_t* seq_lens;
@@ -143,6 +142,11 @@ __device__ __forceinline__ bool opaque(bool v) {
     return u != 0;
 }
 
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t chunk, int32_t group,
                                             int32_t page, uint64_t policy) {
     asm volatile(
@@ -150,6 +154,11 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%3, %3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(chunk), "r"(group), "r"(page), "l"(policy)
         : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
 }
 // 16 bytes into shared memory, and an arrival on the barrier when this thread's
 // copies so far are there.
@@ -316,10 +325,13 @@ __device__ __forceinline__ float log2_fast(float x) {
 }
 
 // Registers of a copying or issuing thread and of a softmax thread: together
-// those that the CTA is launched with.  What does not fit goes to local memory,
-// whose loads wait behind the products' reads of shared memory.
-constexpr int kRegsIssue = kPer == 16 ? 56 : 88, kRegsSoft = kPer == 16 ? 104 : 208;
-static_assert(128 * kRegsIssue + kSoftThreads * kRegsSoft <= kThreads * (kPer == 16 ? 96 : 168), "registers of the CTA at its launch");
+// those that the CTA is launched with (168 each).  What does not fit goes to
+// local memory, whose loads wait behind the products' reads of shared memory.
+// Measured, 88 and 208 against 72 and 216: 2.05 and 2.18 us a tile at 48 heads of
+// 512 columns; sixteen softmax warps of half as many heads each, 56 and 104
+// registers: 2.31.
+constexpr int kRegsIssue = 88, kRegsSoft = 208;
+static_assert(128 * kRegsIssue + kSoftThreads * kRegsSoft <= kThreads * 168, "registers of the CTA at its launch");
 
 // wait_bounded<true> in a few instructions: the clock is first read after 64
 // polls.  (The kernel's code has to stay small: the issuing warps run theirs
@@ -346,7 +358,7 @@ __device__ __forceinline__ bool wait_polled(uint32_t bar, uint32_t parity, volat
 // time limit, so every softmax warp reaches every one of them whether or not
 // its waits succeeded (the counts depend on the run alone).
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
-__device__ __forceinline__ bool part_sync_or(int part, bool v) {
+__device__ __forceinline__ bool half_sync_or(int half, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -354,7 +366,7 @@ __device__ __forceinline__ bool part_sync_or(int part, bool v) {
         "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(v)), "r"(2 + part)
+        : "r"(static_cast<uint32_t>(v)), "r"(2 + half)
         : "memory");
     return r != 0;
 }
@@ -426,13 +438,93 @@ struct Run {
     }
 };
 
+// ---------------------------------------------------------------------------
+// Splits the queries into images of what a job's CTA has in shared memory: codes
+// of hi and of lo, chunk by chunk of 128, rows 128-byte swizzled, then the bf16
+// position columns divided by the same power of two, then the factors of the
+// scores.  Image b G + g is that of heads 64 g .. of request b; behind those come
+// the prefix's, of 64 (request, head) pairs each.  A warp takes a row; rows that
+// pad an image keep what they hold (nothing of their columns is used).  In the
+// attention's own warps, between the jobs, this took 4.7 us a job of 64 heads:
+// 96 requests of mixed lengths at 128 heads 129 us.
+// ---------------------------------------------------------------------------
+struct SplitArgs {
+    const __nv_bfloat16* q;
+    int64_t ldq_b, ldq_h;
+    uint8_t* images;
+    int image, rows;                  // bytes of an image, rows of hi (and of lo) in it
+    int B, H, G, HR, cc, pe;
+    bool prefix;
+    float scale_log2;
+    uint32_t inject;
+};
+constexpr int kSplitThreads = 256;
+
+__global__ void __launch_bounds__(kSplitThreads)
+split_queries_kernel(const SplitArgs a) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    bounds_self_test(a.inject);
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kSplitThreads / 32) + (threadIdx.x >> 5);
+    if (row >= static_cast<int64_t>(a.B) * a.H) return;
+    const int b = static_cast<int>(row / a.H), h = static_cast<int>(row - static_cast<int64_t>(b) * a.H);
+    const bool codes = lane * 16 < a.cc * 128, pos = a.pe && lane < 8;
+    const __nv_bfloat16* src = a.q + b * a.ldq_b + h * a.ldq_h;
+    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, e = make_uint4(0, 0, 0, 0);
+    if (codes) {
+        x[0] = *reinterpret_cast<const uint4*>(src + lane * 16);
+        x[1] = *reinterpret_cast<const uint4*>(src + lane * 16 + 8);
+    }
+    if (pos) e = *reinterpret_cast<const uint4*>(src + a.cc * 128 + lane * 8);
+    // The largest magnitudes, as the bits of a bf16 (NaN above all others).
+    const uint32_t top = __reduce_max_sync(0xffffffffu, max(largest8(x[0]), largest8(x[1])));
+    const uint32_t etop = __reduce_max_sync(0xffffffffu, largest8(e));
+    // 2^ex > largest / 256, so that 32 (x - hi) <= 256; and the position columns divided by it stay finite.
+    int ex = static_cast<int>(top >> 7) - 127 - 7;
+    ex = max(max(ex, -100), static_cast<int>(etop >> 7) - 127 - 100);
+    const bool finite = max(top, etop) < 0x7f80;
+    if (!finite) ex = 0;
+    const float inv = __int_as_float((127 - ex) << 23);
+    const float factor = finite ? __int_as_float((127 + ex) << 23) * a.scale_log2 : __int_as_float(0x7fffffff);
+    const uint32_t* xw = reinterpret_cast<const uint32_t*>(x);
+    const uint32_t* ew = reinterpret_cast<const uint32_t*>(&e);
+    uint32_t hi[4], lo[4], v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t h0, h1, l0, l1;
+        __half2 s;
+        split2(mul2(unpack_bf16(xw[2 * k]), make_float2(inv, inv)), h0, l0, s);
+        split2(mul2(unpack_bf16(xw[2 * k + 1]), make_float2(inv, inv)), h1, l1, s);
+        hi[k] = __byte_perm(h0, h1, 0x5410);
+        lo[k] = __byte_perm(l0, l1, 0x5410);
+        const float2 f = mul2(unpack_bf16(ew[k]), make_float2(inv, inv));
+        v[k] = pack_bf16(f.x, f.y);
+    }
+    for (int to = 0; to < (a.prefix ? 2 : 1); ++to) {
+        const int64_t r = static_cast<int64_t>(b) * a.HR + h;
+        const int64_t image = to ? static_cast<int64_t>(a.B) * a.G + r / kHeads : static_cast<int64_t>(b) * a.G + h / kHeads;
+        const int i = to ? static_cast<int>(r % kHeads) : h % kHeads;
+        uint8_t* at = a.images + image * a.image;
+        if (!bounds_ok(i < a.rows)) continue;
+        if (codes) {
+            uint8_t* c = at + (lane >> 3) * 2 * a.rows * 128 + (((lane & 7) ^ (i & 7)) << 4);
+            *reinterpret_cast<uint4*>(c + i * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(c + (a.rows + i) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        if (pos)
+            *reinterpret_cast<uint4*>(at + a.cc * 2 * a.rows * 128 + i * 128 + ((lane ^ (i & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        if (lane == 0) *reinterpret_cast<float*>(at + a.image - kHeads * 4 + i * 4) = factor;
+    }
+}
+
 template <int NG>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Params p) {
     constexpr int HP = 16 * NG;                            // rows (heads) of a job, with those that pad it
     constexpr bool kPair = HP > kStacked;
     constexpr uint32_t kLow = kPair ? 0 : HP;              // columns from hi's part of O to lo's
-    constexpr int hpp = HP / kParts;                       // heads of a softmax warp, a multiple of four
+    constexpr int hpp = HP / 2;                            // heads of a softmax warp, a multiple of eight
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int q_chunk = 2 * p.q_rows * 128;                // bytes of a code chunk of q: hi, then lo
@@ -444,9 +536,9 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     uint8_t* misc = ring + p.slots * kChunkBytes;
     uint8_t* sf_s = misc;                                  // [32][16 B] block scales of p s
     float* sc_s = reinterpret_cast<float*>(sf_s + 512);    // [kScaleSlots][128] row scales
-    float* cq_s = sc_s + kScaleSlots * kTile;              // [2][64] factor of a head's scores
-    float* bc_s = cq_s + 2 * kHeads;                       // [kSoftWarps][kPer]{T, 2^(T - M)}; at a job's end {l, lr}
-    float* mx_s = bc_s + kSoftWarps * 2 * kPer;            // [kSoftWarps][kPer]
+    float* cq_s = sc_s + kScaleSlots * kTile;              // [64] factor of a head's scores
+    float* bc_s = cq_s + kHeads;                           // [8 warps][32]{T, 2^(T - M)}; at a job's end {l, lr}
+    float* mx_s = bc_s + kSoftWarps * 2 * kPer;            // [8 warps][32]
     float* al_s = mx_s + kSoftWarps * kPer;                // [64] factors of O
     uint64_t* full = reinterpret_cast<uint64_t*>(al_s + kHeads);   // [kMaxSlots]
     uint64_t* empty = full + kMaxSlots;                    // [kMaxSlots]
@@ -472,7 +564,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int s = 0; s < kScaleSlots; ++s) mbar_init(smem_u32(&scfull[s]), 32);
-        mbar_init(smem_u32(qfull), kSoftWarps);
+        mbar_init(smem_u32(qfull), 1);
         mbar_init(smem_u32(sfull), 1);
         mbar_init(smem_u32(sempty), kSoftWarps);
         mbar_init(smem_u32(pfull), kSoftWarps);
@@ -533,7 +625,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         const int h = min(p.H, kHeads), joined = 5 * p.B * h / (16 * p.W_full);
         const int slack = max(1, p.W < kManyParts * p.B ? min(joined, 2 + h / 64) : joined);
         const bool uncut = !p.prefix_len && p.B <= p.W && most <= (tiles + p.W - 1) / p.W + slack;
-        const int lead = static_cast<int>(min(tiles / p.W, static_cast<int64_t>(3)));
+        const int lead = static_cast<int>(min(tiles / p.W, static_cast<int64_t>(2)));
         const int64_t front = static_cast<int64_t>(pjobs) * (lead + ptiles);   // units of the prefix
         const int64_t total = tiles + static_cast<int64_t>(lead) * (p.B + pjobs);
         before += front + static_cast<int64_t>(lead) * b0;
@@ -698,6 +790,19 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
 #pragma unroll 1
         for (; ok && run.next(p, g); run.advance()) {
             if (!run.live()) continue;
+            // The job's queries, when the softmax has S^T of the job before: then
+            // neither its queries nor their factors are read any more.
+            ok = wait_uniform(smem_u32(sempty), (n & 1) ^ 1);
+            if (!ok) break;
+            if (elected()) {
+                const uint32_t bytes = p.image - kHeads * 4;
+                const int64_t at = run.j < p.NP ? static_cast<int64_t>(p.B + run.j) * p.G + g : static_cast<int64_t>(run.j - p.NP) * p.G + g;
+                const uint8_t* src = p.images + at * p.image;
+                mbar_arrive_expect_tx(smem_u32(qfull), p.image);
+                bulk_load(smem_u32(q_s), src, bytes, smem_u32(qfull));
+                bulk_load(smem_u32(cq_s), src + bytes, kHeads * 4, smem_u32(qfull));
+            }
+            __syncwarp();
             ok = wait_uniform(smem_u32(qfull), nq & 1);
             ++nq;
 #pragma unroll 1
@@ -765,9 +870,9 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     } else {
         // ------------------------------------- softmax, splitting q, output
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-        const int quad = warp & 3, sw = warp - kSoftWarp0, part = sw >> 2;
+        const int quad = warp & 3, sw = warp - kSoftWarp0, half = sw >> 2;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const int st = threadIdx.x - kSoftWarp0 * 32;      // 0 .. kSoftThreads - 1
+        const int st = threadIdx.x - kSoftWarp0 * 32;      // 0..255
         const float kNegInf = __int_as_float(0xff800000);
         const int tok = quad * 32 + lane;                  // this thread's token of a tile
         const int DV = p.nblk * 128;
@@ -775,89 +880,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
         uint32_t n = 0, nq = 0;
         bool ok = true;                                    // false: only the barriers are kept up
 
-        // Splits the queries of the job r into shared memory, and leaves the
-        // factors of their scores.  Warp sw takes rows sw, sw + kSoftWarps, ..., four
-        // at once; a lane 16 codes, lanes 0..7 also eight position columns.  Rows
-        // that pad the job keep what they hold: nothing of their columns is used.
-        auto split_q = [&](const Run& r, int buf) {
-            const bool prefix = r.j < p.NP;
-            const int row0 = prefix ? (r.j * p.G + g) * kHeads : g * kHeads;
-            constexpr int kAhead = 4;
-            const bool codes = lane * 16 < p.cc * 128, pos = p.pe && lane < 8;
-#pragma unroll 1
-            for (int i0 = sw; i0 < r.count; i0 += kAhead * kSoftWarps) {
-                uint4 x[kAhead][2], e[kAhead];
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int i = i0 + u * kSoftWarps;
-                    x[u][0] = x[u][1] = e[u] = make_uint4(0, 0, 0, 0);
-                    int b = r.j - p.NP, h = row0 + i;
-                    if (prefix) {
-                        b = (row0 + i) / p.HR;
-                        h = row0 + i - b * p.HR;
-                    }
-                    if (i >= r.count || h >= p.H || !bounds_ok(b >= 0 && b < p.B)) continue;
-                    const __nv_bfloat16* src = p.q + b * p.ldq_b + h * p.ldq_h;
-                    if (codes) {
-                        x[u][0] = *reinterpret_cast<const uint4*>(src + lane * 16);
-                        x[u][1] = *reinterpret_cast<const uint4*>(src + lane * 16 + 8);
-                    }
-                    if (pos) e[u] = *reinterpret_cast<const uint4*>(src + p.cc * 128 + lane * 8);
-                }
-                // The largest magnitudes, as the bits of a bf16 (NaN above all others).
-                uint32_t top[kAhead], etop[kAhead];
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    top[u] = largest8(x[u][0]);
-                    top[u] = __reduce_max_sync(0xffffffffu, max(top[u], largest8(x[u][1])));
-                    etop[u] = p.pe ? __reduce_max_sync(0xffffffffu, largest8(e[u])) : 0;
-                }
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int i = i0 + u * kSoftWarps;
-                    if (i >= r.count) break;
-                    const uint32_t* xw = reinterpret_cast<const uint32_t*>(x[u]);
-                    const uint32_t* ew = reinterpret_cast<const uint32_t*>(&e[u]);
-                    // 2^ex > largest / 256, so that 32 (x - hi) <= 256; and the position columns divided by it stay finite.
-                    int ex = static_cast<int>(top[u] >> 7) - 127 - 7;
-                    ex = max(max(ex, -100), static_cast<int>(etop[u] >> 7) - 127 - 100);
-                    const bool finite = max(top[u], etop[u]) < 0x7f80;
-                    if (!finite) ex = 0;
-                    const float inv = __int_as_float((127 - ex) << 23);
-                    if (lane == 0)
-                        cq_s[buf * kHeads + i] = finite ? __int_as_float((127 + ex) << 23) * p.scale_log2 : __int_as_float(0x7fffffff);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t h0, h1, l0, l1;
-                        __half2 s;
-                        split2(mul2(unpack_bf16(xw[2 * k]), make_float2(inv, inv)), h0, l0, s);
-                        split2(mul2(unpack_bf16(xw[2 * k + 1]), make_float2(inv, inv)), h1, l1, s);
-                        hi[k] = __byte_perm(h0, h1, 0x5410);
-                        lo[k] = __byte_perm(l0, l1, 0x5410);
-                    }
-                    if (codes) {
-                        uint8_t* at = q_s + (lane >> 3) * q_chunk + (((lane & 7) ^ (i & 7)) << 4);
-                        *reinterpret_cast<uint4*>(at + i * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(at + (HP + i) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                    if (pos) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = mul2(unpack_bf16(ew[k]), make_float2(inv, inv));
-                            v[k] = pack_bf16(f.x, f.y);
-                        }
-                        *reinterpret_cast<uint4*>(qpe_s + i * 128 + ((lane ^ (i & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(qfull));
-        };
-        // Job by job: the queries of the next one, while the last product of the
-        // one before runs; that one's output; the next one's tiles.
+        // Job by job: the output of the one before, the tiles of the next.
         Run next = run;
         bool started = false;
         float2 l[kPer / 2], lr[kPer / 2];                  // per head, this token's share of the sums of p: unrounded, rounded
@@ -881,10 +904,9 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 }
                 if (p.lse && st < kHeads && g * kHeads + st < p.H) p.lse[b * p.ldl_b + g * kHeads + st] = kNegInf;
             }
-            if (more && ok) split_q(next, nq & 1);
             if (started) {
                 // ---- output of the job (or of this worker's part of it)
-                const int b = run.j - p.NP, h0 = part * hpp;
+                const int b = run.j - p.NP, h0 = half * hpp;
                 const bool whole = !p.prefix_len && run.t0 == 0 && run.n == run.tiles, mine = lane < hpp && h0 + lane < run.count;
                 // Sums over the tokens: lane k gets head h0 + k's.
                 float v[kPer], u[kPer];
@@ -902,25 +924,18 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                         v[k] = (odd ? v[k + o] : v[k]) + __shfl_xor_sync(0xffffffffu, a, o);
                         u[k] = (odd ? u[k + o] : u[k]) + __shfl_xor_sync(0xffffffffu, c, o);
                     }
-#pragma unroll
-                for (int o = kPer; o < 32; o <<= 1) {
-                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-                    u[0] += __shfl_xor_sync(0xffffffffu, u[0], o);
-                }
-                if (lane < kPer) {
-                    bc[lane] = v[0];
-                    bc[kPer + lane] = u[0];
-                }
-                part_sync_or(part, false);                     // bc is next written after the next job's S^T
+                bc[lane] = v[0];
+                bc[kPer + lane] = u[0];
+                half_sync_or(half, false);                     // bc is next written after the next job's S^T
                 float ls = 0.f, lrs = 0.f;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    ls += bc_s[(part * 4 + q) * 2 * kPer + (lane & (kPer - 1))];
-                    lrs += bc_s[(part * 4 + q) * 2 * kPer + kPer + (lane & (kPer - 1))];
+                    ls += bc_s[(half * 4 + q) * 2 * kPer + lane];
+                    lrs += bc_s[(half * 4 + q) * 2 * kPer + kPer + lane];
                 }
                 // A part's weights add up to its unrounded sum, which the join divides by.
                 if (mine) al_s[h0 + lane] = lrs > 0.f || lrs != lrs ? __fdividef(whole ? 1.0f : ls, lrs) : 0.f;
-                __syncwarp();                                  // the same from each of the part's four warps
+                __syncwarp();                                  // the same from each of the half's four warps
                 ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
                 tc_fence_after();
                 if (ok && whole) {
@@ -948,7 +963,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                             for (int k = 0; k < 8; ++k) x[u][k] = __float_as_uint(__uint_as_float(x[u][k]) + __uint_as_float(y[k]));
                         }
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {          // eight heads; those past this part's are not stored
+                        for (int q = 0; q < 2; ++q) {          // eight heads; those past this half's are not stored
                             const float2 f = *reinterpret_cast<const float2*>(al_s + min(h0 + hb + q * 8 + col0, kHeads - 2));
                             uint32_t v[4];
 #pragma unroll
@@ -1012,9 +1027,9 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             run = next;
             next.advance();
             started = true;
-            const int h0 = part * hpp;                     // this warp's first head
+            const int h0 = half * hpp;                     // this warp's first head
             const bool mine = lane < hpp && h0 + lane < run.count;   // this lane has a head: h0 + lane
-            const float* cq = cq_s + (nq & 1) * kHeads + h0;
+            const float* cq = cq_s + h0;
 #pragma unroll
             for (int k = 0; k < kPer / 2; ++k) l[k] = lr[k] = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -1027,6 +1042,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 // possible lies between S^T and the product that waits for p s.
                 const bool landed = mbar_test(sb, sp);
                 ok = opaque(ok && wait_uniform(smem_u32(sfull), n & 1));
+                if (i == 0) ok = opaque(ok && wait_uniform(smem_u32(qfull), nq & 1));   // the factors of the scores
                 if (!__all_sync(0xffffffffu, landed)) ok = opaque(ok && wait_uniform(sb, sp));
                 tc_fence_after();
                 float2 z[kPer / 2];                        // log2 of p s, up to the reference; then x
@@ -1096,17 +1112,17 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 // What O and the sums are relative to.
                 bool raise = false;
                 if (opaque(i == 0)) {
-                    if (lane < kPer) mx_s[sw * kPer + lane] = top;
+                    mx_s[sw * kPer + lane] = top;
                     soft_sync();
                 } else {
-                    raise = part_sync_or(part, top - M > kRaise);
+                    raise = half_sync_or(half, top - M > kRaise);
                     if (raise) {
-                        if (lane < kPer) mx_s[sw * kPer + lane] = top;
-                        part_sync_or(part, false);
+                        mx_s[sw * kPer + lane] = top;
+                        half_sync_or(half, false);
                     }
                 }
                 if (opaque(i == 0 || raise)) {
-                    const float* mx = mx_s + part * 4 * kPer + (lane & (kPer - 1));
+                    const float* mx = mx_s + half * 4 * kPer + lane;
                     const float to = fmaxf(fmaxf(mx[0], mx[kPer]), fmaxf(mx[2 * kPer], mx[3 * kPer]));
                     if (i == 0) {
                         M = to;
@@ -1117,7 +1133,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                             alpha = exp2_fast(M - to);
                             M = to;
                         }
-                        if (mine) al_s[h0 + lane] = alpha; // the same from each of the part's four warps
+                        if (mine) al_s[h0 + lane] = alpha; // the same from each of the half's four warps
                         __syncwarp();
 #pragma unroll
                         for (int k = 0; k < kPer / 2; ++k) {
@@ -1143,7 +1159,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     }
                 }
                 const int up = static_cast<int>(fmaxf(fminf(top - M, 127.f), -126.f));
-                if (lane < kPer) bc[kPer + lane] = __int_as_float((up + 127) << 23);
+                bc[kPer + lane] = __int_as_float((up + 127) << 23);
                 if (!__all_sync(0xffffffffu, pv_done)) ok = opaque(ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1));
                 if (opaque(ok)) {
                     // hi of the heads, then lo: in the same row of 64 bytes or in a
@@ -1460,7 +1476,7 @@ struct Shape {
     int64_t prefix_width;
 };
 struct Plan {
-    int64_t G, HR, R, NP, W, parts;
+    int64_t G, HR, R, NP, W, parts, rows, images, image;
 };
 Plan plan_of(const Shape& s, int64_t ctas) {
     Plan x{};
@@ -1481,18 +1497,23 @@ Plan plan_of(const Shape& s, int64_t ctas) {
         if (tiles < x.W) x.W = tiles;
     }
     x.parts = (s.prefix ? x.NP + s.B + x.W : 2 * x.W) * x.G;
+    const int64_t most = x.NP ? x.R : s.H;                 // rows that a CTA can get
+    x.rows = most < kHeads ? (most + 15) / 16 * 16 : kHeads;
+    x.images = (s.B + x.NP) * x.G;
+    x.image = (2 * s.K / 128 + (s.P ? 1 : 0)) * x.rows * 128 + kHeads * 4;
     return x;
 }
 
 struct Layout {
-    int64_t meta, ml, o, total;                            // byte offsets of the workspace's parts
+    int64_t meta, ml, o, images, total;                    // byte offsets of the workspace's parts
 };
 Layout workspace_layout(const Plan& x, int64_t DV) {
     Layout L;
     L.meta = 0;
     L.ml = (x.W * 8 + 255) / 256 * 256;
     L.o = (L.ml + x.parts * kHeads * 8 + 255) / 256 * 256;
-    L.total = L.o + x.parts * kHeads * DV * 4;
+    L.images = L.o + x.parts * kHeads * DV * 4;
+    L.total = L.images + x.images * x.image;
     return L;
 }
 
@@ -1507,10 +1528,16 @@ dsnq_status check_sizes(const Shape& s) {
     return DSNQ_OK;
 }
 
+// What a call asks for: of the widest row, on the largest GPU.
+int64_t workspace_needed(Shape s) {
+    s.K = 512;
+    s.P = 64;
+    return workspace_layout(plan_of(s, kMaxCtas), s.DV).total;
+}
 dsnq_status workspace_bytes_of(const Shape& s, int64_t* bytes) {
     const dsnq_status st = check_sizes(s);
     if (st != DSNQ_OK) return st;
-    if (bytes) *bytes = s.B == 0 ? 0 : workspace_layout(plan_of(s, kMaxCtas), s.DV).total;
+    if (bytes) *bytes = s.B == 0 ? 0 : workspace_needed(s);
     return DSNQ_OK;
 }
 
@@ -1555,7 +1582,7 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
         !aligned(t.prefix_table, 4) || !aligned(t.prefix_len, 4) || !aligned(t.seq_lens, 4) || !aligned(t.lse, 4) ||
         !aligned(t.workspace, 16))
         return DSNQ_ERR_MISALIGNED;
-    if (t.workspace_bytes < workspace_layout(plan_of(z, kMaxCtas), z.DV).total) return DSNQ_ERR_INVALID_ARG;
+    if (t.workspace_bytes < workspace_needed(z)) return DSNQ_ERR_INVALID_ARG;
     const int sms = device_sm_count();
     if (sms <= 0) {
         cudaGetLastError();
@@ -1564,8 +1591,6 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
     const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
     const Plan x = plan_of(z, ctas);
     Params p{};
-    p.q = static_cast<const __nv_bfloat16*>(t.q);
-    p.ldq_b = t.ldq_tok; p.ldq_h = t.ldq_head;
     p.scales = t.scales; p.ld_scale = t.ld_scale;
     p.seq_lens = t.seq_lens;
     p.table = t.table; p.ld_table = t.ld_table;
@@ -1584,8 +1609,7 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
     p.cc = static_cast<int>(z.K / 128);
     p.pe = z.P ? 1 : 0;
     p.nblk = static_cast<int>(z.DV / 128);
-    const int64_t rows = x.NP ? x.R : z.H;                 // the most that a CTA can get
-    p.q_rows = static_cast<int>(rows < kHeads ? (rows + 15) / 16 * 16 : kHeads);
+    p.q_rows = static_cast<int>(x.rows);
     // Shared memory: q, p s, scales and barriers, and the rest for the rings, up
     // to the three tiles whose row scales have a place.
     const int64_t fixed = 1024 + static_cast<int64_t>(2 * p.cc + p.pe) * p.q_rows * 128 + 2 * kPBytes + kMiscBytes;
@@ -1609,10 +1633,14 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
     p.meta = reinterpret_cast<int2*>(ws + lay.meta);
     p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
     p.part_o = reinterpret_cast<float*>(ws + lay.o);
+    p.images = ws + lay.images;
+    p.image = static_cast<int>(x.image);
     const uint64_t limit = debug_wait_timeout_ns();
     p.timeout_ns = limit ? limit : kDefaultTimeoutNs;
     p.inject = debug_inject_flags();
 
+    SplitArgs sa{static_cast<const __nv_bfloat16*>(t.q), t.ldq_tok, t.ldq_head, ws + lay.images, p.image, p.q_rows, p.B, p.H, p.G, p.HR,
+                 p.cc, p.pe, x.NP > 0, p.scale_log2, p.inject};
     CUtensorMap mc;
     if (!make_cache_map(&mc, t.cache, t.num_pages, z.page_size, cpt, t.ld_page, t.ld_row, p.box_rows)) return DSNQ_ERR_CUDA;
     void (*kern)(CUtensorMap, Params) = p.q_rows <= 16   ? latent_attention_fp8_kernel<1>
@@ -1620,6 +1648,9 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
                                         : p.q_rows <= 48 ? latent_attention_fp8_kernel<3>
                                                          : latent_attention_fp8_kernel<4>;
     if (!set_smem_attr(reinterpret_cast<const void*>(kern), smem)) return DSNQ_ERR_CUDA;
+    const int64_t ctas_split = (z.B * z.H + kSplitThreads / 32 - 1) / (kSplitThreads / 32);
+    st = launch_result(launch_kernel(split_queries_kernel, dim3(static_cast<unsigned>(ctas_split)), dim3(kSplitThreads), 0, s, sa));
+    if (st != DSNQ_OK) return st;
     st = launch_result(launch_kernel(kern, dim3(static_cast<unsigned>(p.W * p.G)), dim3(kThreads), smem, s, mc, p));
     if (st != DSNQ_OK || (p.W == 1 && !z.prefix)) return st;
     // Few jobs: a request has many parts, so a CTA joins each item.  Many: a
@@ -1668,12 +1699,12 @@ using namespace dsnq;
 
 extern "C" dsnq_status dsnq_paged_latent_attention_fp8_workspace_bytes(int64_t B, int64_t H, int64_t DV, int64_t table_width,
                                                                        int64_t page_size, int64_t* bytes) {
-    return attn8::workspace_bytes_of({B, H, DV, 0, DV, table_width, page_size, false, 0}, bytes);
+    return attn8::workspace_bytes_of({B, H, 512, 64, DV, table_width, page_size, false, 0}, bytes);
 }
 
 extern "C" dsnq_status dsnq_shared_prefix_latent_attention_fp8_workspace_bytes(
     int64_t B, int64_t H, int64_t DV, int64_t prefix_width, int64_t table_width, int64_t page_size, int64_t* bytes) {
-    return attn8::workspace_bytes_of({B, H, DV, 0, DV, table_width, page_size, true, prefix_width}, bytes);
+    return attn8::workspace_bytes_of({B, H, 512, 64, DV, table_width, page_size, true, prefix_width}, bytes);
 }
 
 extern "C" dsnq_status dsnq_paged_latent_attention_fp8(

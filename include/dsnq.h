@@ -603,8 +603,10 @@ DSNQ_API dsnq_status dsnq_latent_cache_read_fp8(
     void* out, int64_t ldo,
     void* stream);
 
-/* Host-only queries: bytes of the workspaces of the two calls below.  Errors as
- * in those calls.  `bytes` may be NULL. */
+/* Host-only queries: bytes of the workspaces of the two calls below: the split
+ * queries (about as many bytes as q; for the widest row, K = 512 and P = 64) and
+ * the partial results (at most about 42 MB without a prefix).  Errors as in those
+ * calls.  `bytes` may be NULL. */
 DSNQ_API dsnq_status dsnq_paged_latent_attention_fp8_workspace_bytes(int64_t B, int64_t H, int64_t DV, int64_t table_width,
                                                                      int64_t page_size, int64_t* bytes);
 DSNQ_API dsnq_status dsnq_shared_prefix_latent_attention_fp8_workspace_bytes(int64_t B, int64_t H, int64_t DV, int64_t prefix_width,
@@ -629,8 +631,9 @@ DSNQ_API dsnq_status dsnq_shared_prefix_latent_attention_fp8_workspace_bytes(int
  *                 num_pages >= 1, page_size a multiple of 8, scales 16-byte
  *                 aligned, ld_scale a multiple of 4.  Scales are in [2^-60,
  *                 2^119], as the write leaves them (0 counts as a zero row).
- * Other arguments, page ids outside the cache, workspace and launches as in
- * dsnq_paged_latent_attention.
+ * Other arguments, page ids outside the cache and workspace as in
+ * dsnq_paged_latent_attention.  Three launches (two when a single worker takes
+ * all).
  */
 DSNQ_API dsnq_status dsnq_paged_latent_attention_fp8(
     int64_t B, int64_t H, int64_t K, int64_t P, int64_t DV,
@@ -654,9 +657,11 @@ DSNQ_API dsnq_status dsnq_paged_latent_attention_fp8(
  *                 * page_size]; 0: no prefix.
  *   seq_lens    : tokens behind the prefix; may be 0.
  *   workspace   : at least dsnq_shared_prefix_latent_attention_fp8_workspace_bytes:
- *                 the batch's partial results, 4 DV bytes for each (request,
- *                 head) pair, twice, and some for each worker.
- * Two launches.  Other arguments as in dsnq_paged_latent_attention_fp8.
+ *                 the batch's split queries and partial results, both twice
+ *                 (for the prefix and for the request's own tokens; 4 DV bytes of
+ *                 results for each of 64 heads of a request), and some for each
+ *                 worker.
+ * Three launches.  Other arguments as in dsnq_paged_latent_attention_fp8.
  */
 DSNQ_API dsnq_status dsnq_shared_prefix_latent_attention_fp8(
     int64_t B, int64_t H, int64_t K, int64_t P, int64_t DV,

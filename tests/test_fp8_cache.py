@@ -106,21 +106,25 @@ def test_attention_argument_checks(lib, shared):
 
 
 def test_workspace_queries(lib):
-    """Without a prefix at most what the whole GPU's workers leave; with one it
-    grows with the batch."""
+    """The split queries, and what the whole GPU's workers leave at most; with a
+    prefix the parts grow with the batch too."""
     def size(B, H, DV=512, width=16, ps=64):
         return dsnq.paged_latent_attention_fp8_workspace_bytes(B, H, DV, width, ps)
 
+    # Split queries: per 64 heads two e4m3 copies of 512 columns, 64 bf16 columns, a factor each.
+    image = lambda rows: (2 * 4 + 1) * rows * 128 + 64 * 4
     assert size(0, 128) == 0
-    assert size(1, 128, width=2) < size(1, 128) <= size(64, 128) == size(1000, 128)
-    assert size(1000, 128) < 43 << 20 and size(8192, 16, width=1000) < 43 << 20
+    assert size(1, 128, width=2) < size(1, 128) <= size(64, 128) - 63 * 2 * image(64)
+    assert size(1000, 128) - size(64, 128) == 936 * 2 * image(64)
+    assert size(1000, 128) < (43 << 20) + 2000 * image(64) and size(8192, 16, width=1000) < (43 << 20) + 8192 * image(16)
 
     def shared(B, H, pwidth=500, width=16):
         return dsnq.shared_prefix_latent_attention_fp8_workspace_bytes(B, H, 512, pwidth, width, 64)
 
     assert shared(0, 16) == 0 and shared(8, 16) < shared(64, 16) < shared(256, 16)
     # Two parts of DV floats for each pair of a request and a head (64 rows a part), and some for each worker.
-    assert shared(256, 16) < (256 * 16 // 64 + 256 + 160 + 2) * 64 * 516 * 4 + 4096
+    parts = 256 * 16 // 64 + 256 + 160
+    assert shared(256, 16) < (parts + 2) * 64 * 516 * 4 + (256 * 16 // 64 + 256) * image(64) + 4096
     assert shared(8192, 1024) > 1 << 35                       # in 64 bits
     n = C.c_int64()
     q = lib.dsnq_shared_prefix_latent_attention_fp8_workspace_bytes
