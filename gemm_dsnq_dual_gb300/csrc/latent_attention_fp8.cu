@@ -89,7 +89,7 @@ constexpr int kPBytes = kTile * 64;         // hi (or lo) of p s of a tile: 64 b
 constexpr int kManyParts = 4;               // workers per job from which a CTA joins an item
 
 struct Params {
-    const uint8_t* images;            // [B * G + NP * G] of a job's split queries (see split_queries_kernel)
+    uint8_t* images;                  // [B * G + NP * G] of a job's split queries (see prepare_kernel)
     int image;                        // bytes of one
     const float* scales;
     int64_t ld_scale;                 // of a page
@@ -113,7 +113,7 @@ struct Params {
     int64_t ldo_b, ldo_h;
     float* lse;                       // NULL: not written
     int64_t ldl_b;
-    int2* meta;                       // [W] first job of the worker and its first tile there
+    int2* meta;                       // [W + 1] first job of the worker and its first tile there; the end
     float2* part_ml;                  // [part][64] (reference in log2 units, sum)
     float* part_o;                    // [part][nblk][16][128][4]: value block, four heads, value, head
     uint64_t timeout_ns;
@@ -439,44 +439,123 @@ struct Run {
 };
 
 // ---------------------------------------------------------------------------
-// Splits the queries into images of what a job's CTA has in shared memory: codes
-// of hi and of lo, chunk by chunk of 128, rows 128-byte swizzled, then the bf16
-// position columns divided by the same power of two, then the factors of the
-// scores.  Image b G + g is that of heads 64 g .. of request b; behind those come
-// the prefix's, of 64 (request, head) pairs each.  A warp takes a row; rows that
-// pad an image keep what they hold (nothing of their columns is used).  In the
-// attention's own warps, between the jobs, this took 4.7 us a job of 64 heads:
-// 96 requests of mixed lengths at 128 heads 129 us.
+// What the attention's CTAs would each do again.
+//
+// The first CTA shares out the work.  Each job counts `lead` units (what it costs
+// beside its tiles: queries, pipeline fill, output), then one per tile; worker w
+// takes units [w U / workers, (w + 1) U / workers), and a cut among a job's
+// leading units is a cut before its first tile.  The jobs against the prefix come
+// first.
+//
+// The others split the queries into images of what a job's CTA has in shared
+// memory: codes of hi and of lo, chunk by chunk of 128, rows 128-byte swizzled,
+// then the bf16 position columns divided by the same power of two, then the
+// factors of the scores.  Image b G + g is that of heads 64 g .. of request b;
+// behind those come the prefix's, of 64 (request, head) pairs each.  A warp takes
+// a row; rows that pad an image keep what they hold (nothing of their columns is
+// used).  In the attention's own warps, between the jobs, the split took 4.7 us a
+// job of 64 heads.
 // ---------------------------------------------------------------------------
-struct SplitArgs {
-    const __nv_bfloat16* q;
-    int64_t ldq_b, ldq_h;
-    uint8_t* images;
-    int image, rows;                  // bytes of an image, rows of hi (and of lo) in it
-    int B, H, G, HR, cc, pe;
-    bool prefix;
-    float scale_log2;
-    uint32_t inject;
-};
-constexpr int kSplitThreads = 256;
+constexpr int kPrepareThreads = 256;
 
-__global__ void __launch_bounds__(kSplitThreads)
-split_queries_kernel(const SplitArgs a) {
+__device__ void share_out(const Params& p) {
+    constexpr int kWarps = kPrepareThreads / 32;
+    __shared__ int64_t sums[kWarps], before_s[kPrepareThreads];
+    __shared__ int longest[kWarps];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int plen = p.prefix_len ? clamp_len(p.prefix_cap, *p.prefix_len) : 0;
+    // Thread t sums requests [t * per, (t + 1) * per).
+    const int per = (p.B + kPrepareThreads - 1) / kPrepareThreads;
+    const int b0 = min(t * per, p.B), b1 = min(b0 + per, p.B);
+    int64_t mine = 0;
+    int most = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int n = tiles_of(clamp_len(p.cap, p.seq_lens[b]));
+        mine += n;
+        most = max(most, n);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) {
+        sums[warp] = inc;
+        longest[warp] = most;
+    }
+    __syncthreads();
+    int64_t before = inc - mine, tiles = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += sums[i];
+        tiles += sums[i];
+        most = max(most, longest[i]);
+    }
+    const int ptiles = plen > 0 ? tiles_of(plen) : 0, pjobs = plen > 0 ? p.NP : 0;
+    tiles += static_cast<int64_t>(pjobs) * ptiles;
+    // Requests a little longer than a worker's share go one to a worker, uncut.
+    const int h = min(p.H, kHeads), joined = 5 * p.B * h / (16 * p.W_full);
+    const int slack = max(1, p.W < kManyParts * p.B ? min(joined, 2 + h / 64) : joined);
+    const bool uncut = !p.prefix_len && p.B <= p.W && tiles > static_cast<int64_t>(most - slack - 1) * p.W;
+    const int lead = tiles < p.W ? 0 : tiles < 2 * p.W ? 1 : 2;
+    const int64_t front = static_cast<int64_t>(pjobs) * (lead + ptiles);   // units of the prefix
+    const int64_t total = tiles + static_cast<int64_t>(lead) * (p.B + pjobs);
+    before_s[t] = before + front + static_cast<int64_t>(lead) * b0;
+    __syncthreads();
+    const int workers = total < p.W ? static_cast<int>(total) : p.W;
+    for (int w = t; w <= p.W; w += kPrepareThreads) {
+        int2 cut = make_int2(p.NP + min(w, p.B), 0);       // uncut
+        if (!uncut) {
+            int64_t u = total;
+            if (w < workers)                               // (a 32-bit division is a fraction of the 64-bit one)
+                u = total < 1 << 24 ? static_cast<uint32_t>(w) * static_cast<uint32_t>(total) / static_cast<uint32_t>(workers)
+                                    : w * total / workers;
+            if (u == total) {
+                cut.x = p.NP + p.B;
+            } else if (u < front) {
+                cut.x = static_cast<int>(u / (lead + ptiles));
+                cut.y = max(static_cast<int>(u - static_cast<int64_t>(cut.x) * (lead + ptiles)) - lead, 0);
+            } else {
+                int k = 0;                                 // the last thread whose requests begin at or before u
+#pragma unroll
+                for (int o = kPrepareThreads / 2; o > 0; o >>= 1)
+                    if (before_s[k + o] <= u) k += o;
+                int64_t at = before_s[k];
+                int b = k * per, n = lead + tiles_of(clamp_len(p.cap, p.seq_lens[b]));
+                while (at + n <= u) {
+                    at += n;
+                    n = lead + tiles_of(clamp_len(p.cap, p.seq_lens[++b]));
+                }
+                cut = make_int2(p.NP + b, max(static_cast<int>(u - at) - lead, 0));
+            }
+        }
+        p.meta[w] = cut;
+    }
+}
+
+__global__ void __launch_bounds__(kPrepareThreads)
+prepare_kernel(const Params p, const __nv_bfloat16* q, int64_t ldq_b, int64_t ldq_h) {
     grid_dependency_wait();
     allow_dependent_launch();
-    bounds_self_test(a.inject);
+    bounds_self_test(p.inject);
+    if (blockIdx.x == 0) {
+        share_out(p);
+        return;
+    }
     const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kSplitThreads / 32) + (threadIdx.x >> 5);
-    if (row >= static_cast<int64_t>(a.B) * a.H) return;
-    const int b = static_cast<int>(row / a.H), h = static_cast<int>(row - static_cast<int64_t>(b) * a.H);
-    const bool codes = lane * 16 < a.cc * 128, pos = a.pe && lane < 8;
-    const __nv_bfloat16* src = a.q + b * a.ldq_b + h * a.ldq_h;
+    const int64_t row = static_cast<int64_t>(blockIdx.x - 1) * (kPrepareThreads / 32) + (threadIdx.x >> 5);
+    if (row >= static_cast<int64_t>(p.B) * p.H) return;
+    const int b = static_cast<int>(row / p.H), h = static_cast<int>(row - static_cast<int64_t>(b) * p.H);
+    const bool codes = lane * 16 < p.cc * 128, pos = p.pe && lane < 8;
+    const __nv_bfloat16* src = q + b * ldq_b + h * ldq_h;
     uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, e = make_uint4(0, 0, 0, 0);
     if (codes) {
         x[0] = *reinterpret_cast<const uint4*>(src + lane * 16);
         x[1] = *reinterpret_cast<const uint4*>(src + lane * 16 + 8);
     }
-    if (pos) e = *reinterpret_cast<const uint4*>(src + a.cc * 128 + lane * 8);
+    if (pos) e = *reinterpret_cast<const uint4*>(src + p.cc * 128 + lane * 8);
     // The largest magnitudes, as the bits of a bf16 (NaN above all others).
     const uint32_t top = __reduce_max_sync(0xffffffffu, max(largest8(x[0]), largest8(x[1])));
     const uint32_t etop = __reduce_max_sync(0xffffffffu, largest8(e));
@@ -486,7 +565,7 @@ split_queries_kernel(const SplitArgs a) {
     const bool finite = max(top, etop) < 0x7f80;
     if (!finite) ex = 0;
     const float inv = __int_as_float((127 - ex) << 23);
-    const float factor = finite ? __int_as_float((127 + ex) << 23) * a.scale_log2 : __int_as_float(0x7fffffff);
+    const float factor = finite ? __int_as_float((127 + ex) << 23) * p.scale_log2 : __int_as_float(0x7fffffff);
     const uint32_t* xw = reinterpret_cast<const uint32_t*>(x);
     const uint32_t* ew = reinterpret_cast<const uint32_t*>(&e);
     uint32_t hi[4], lo[4], v[4];
@@ -501,20 +580,20 @@ split_queries_kernel(const SplitArgs a) {
         const float2 f = mul2(unpack_bf16(ew[k]), make_float2(inv, inv));
         v[k] = pack_bf16(f.x, f.y);
     }
-    for (int to = 0; to < (a.prefix ? 2 : 1); ++to) {
-        const int64_t r = static_cast<int64_t>(b) * a.HR + h;
-        const int64_t image = to ? static_cast<int64_t>(a.B) * a.G + r / kHeads : static_cast<int64_t>(b) * a.G + h / kHeads;
+    for (int to = 0; to < (p.NP ? 2 : 1); ++to) {
+        const int64_t r = static_cast<int64_t>(b) * p.HR + h;
+        const int64_t image = to ? static_cast<int64_t>(p.B) * p.G + r / kHeads : static_cast<int64_t>(b) * p.G + h / kHeads;
         const int i = to ? static_cast<int>(r % kHeads) : h % kHeads;
-        uint8_t* at = a.images + image * a.image;
-        if (!bounds_ok(i < a.rows)) continue;
+        uint8_t* at = p.images + image * p.image;
+        if (!bounds_ok(i < p.q_rows)) continue;
         if (codes) {
-            uint8_t* c = at + (lane >> 3) * 2 * a.rows * 128 + (((lane & 7) ^ (i & 7)) << 4);
+            uint8_t* c = at + (lane >> 3) * 2 * p.q_rows * 128 + (((lane & 7) ^ (i & 7)) << 4);
             *reinterpret_cast<uint4*>(c + i * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(c + (a.rows + i) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(c + (p.q_rows + i) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         if (pos)
-            *reinterpret_cast<uint4*>(at + a.cc * 2 * a.rows * 128 + i * 128 + ((lane ^ (i & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-        if (lane == 0) *reinterpret_cast<float*>(at + a.image - kHeads * 4 + i * 4) = factor;
+            *reinterpret_cast<uint4*>(at + p.cc * 2 * p.q_rows * 128 + i * 128 + ((lane ^ (i & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        if (lane == 0) *reinterpret_cast<float*>(at + p.image - kHeads * 4 + i * 4) = factor;
     }
 }
 
@@ -525,6 +604,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     constexpr bool kPair = HP > kStacked;
     constexpr uint32_t kLow = kPair ? 0 : HP;              // columns from hi's part of O to lo's
     constexpr int hpp = HP / 2;                            // heads of a softmax warp, a multiple of eight
+    constexpr int kBands = (hpp + 15) / 16;                // sixteens of them
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int q_chunk = 2 * p.q_rows * 128;                // bytes of a code chunk of q: hi, then lo
@@ -549,11 +629,8 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
     uint64_t* pfull = sempty + 1;
     uint64_t* pempty = pfull + 1;
     uint64_t* drain = pempty + 1;                          // [2] abort: products already issued
-    int64_t* sums = reinterpret_cast<int64_t*>(drain + 2); // [kWarps]
-    int* longest = reinterpret_cast<int*>(sums + kWarps);  // [kWarps]
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(longest + kWarps);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-    int* run_s = reinterpret_cast<int*>(tmem_holder + 2);  // [4] first job and tile, end job and tile
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = blockIdx.x / p.G, g = blockIdx.x - w * p.G;
@@ -580,111 +657,33 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    grid_dependency_wait();
-    allow_dependent_launch();
-    bounds_self_test(p.inject);
-
-    // The worker's run.  Each job counts `lead` units (what it costs beside its
-    // tiles: queries, pipeline fill, output), then one per tile; worker w takes
-    // units [w U / workers, (w + 1) U / workers), and a cut among a job's
-    // leading units is a cut before its first tile.  Thread t sums requests
-    // [t * per, (t + 1) * per); the jobs against the prefix come first.
-    const int plen = p.prefix_len ? clamp_len(p.prefix_cap, *p.prefix_len) : 0;
-    {
-        const int per = (p.B + kThreads - 1) / kThreads;
-        const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
-        int64_t mine = 0;
-        int most = 0;
-#pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            const int t = tiles_of(clamp_len(p.cap, p.seq_lens[b]));
-            mine += t;
-            most = max(most, t);
-        }
-        most = __reduce_max_sync(0xffffffffu, most);
-        int64_t inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += u;
-        }
-        if (lane == 31) {
-            sums[warp] = inc;
-            longest[warp] = most;
-        }
-        __syncthreads();
-        int64_t before = inc - mine, tiles = 0;
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) before += sums[i];
-            tiles += sums[i];
-            most = max(most, longest[i]);
-        }
-        const int ptiles = plen > 0 ? tiles_of(plen) : 0, pjobs = plen > 0 ? p.NP : 0;
-        tiles += static_cast<int64_t>(pjobs) * ptiles;
-        // Requests a little longer than a worker's share go one to a worker, uncut.
-        const int h = min(p.H, kHeads), joined = 5 * p.B * h / (16 * p.W_full);
-        const int slack = max(1, p.W < kManyParts * p.B ? min(joined, 2 + h / 64) : joined);
-        const bool uncut = !p.prefix_len && p.B <= p.W && most <= (tiles + p.W - 1) / p.W + slack;
-        const int lead = static_cast<int>(min(tiles / p.W, static_cast<int64_t>(2)));
-        const int64_t front = static_cast<int64_t>(pjobs) * (lead + ptiles);   // units of the prefix
-        const int64_t total = tiles + static_cast<int64_t>(lead) * (p.B + pjobs);
-        before += front + static_cast<int64_t>(lead) * b0;
-        mine += static_cast<int64_t>(lead) * (b1 - b0);
-        const int64_t workers = total < p.W ? total : p.W;
-        if (uncut && threadIdx.x < 2) {
-            run_s[2 * threadIdx.x] = p.NP + min(w + static_cast<int>(threadIdx.x), p.B);
-            run_s[2 * threadIdx.x + 1] = 0;
-        }
-#pragma unroll
-        for (int e = 0; e < 2 && !uncut; ++e) {
-            const int64_t u = w + e < workers ? (w + e) * total / workers : total;
-            if (threadIdx.x == 0) {
-                if (u == total) {
-                    run_s[2 * e] = p.NP + p.B;
-                    run_s[2 * e + 1] = 0;
-                } else if (u < front) {
-                    const int j = static_cast<int>(u / (lead + ptiles));
-                    run_s[2 * e] = j;
-                    run_s[2 * e + 1] = max(static_cast<int>(u - static_cast<int64_t>(j) * (lead + ptiles)) - lead, 0);
-                }
-            }
-            if (u >= before && u < before + mine) {
-                int64_t at = before;
-                int b = b0, n = lead + tiles_of(clamp_len(p.cap, p.seq_lens[b]));
-                while (at + n <= u) {
-                    at += n;
-                    n = lead + tiles_of(clamp_len(p.cap, p.seq_lens[++b]));
-                }
-                run_s[2 * e] = p.NP + b;
-                run_s[2 * e + 1] = max(static_cast<int>(u - at) - lead, 0);
-            }
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    if (warp >= kSoftWarp0 && warp < kSoftWarp0 + 4) {     // the scales of C^T are ones
+    if (warp >= kSoftWarp0 && warp < kSoftWarp0 + 4) {     // the scales of C^T are ones (for the product after pfull)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                          tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmemSfa),
                      "r"(0x7f7f7f7f)
                      : "memory");
         tmem_wait_st();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint64_t tmo = p.timeout_ns;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    bounds_self_test(p.inject);
+
+    // The worker's run.
+    const int2 from = p.meta[w], to = p.meta[w + 1];
     Run run;
-    run.j = run_s[0];
-    run.t0 = run_s[1];
-    run.j_end = run_s[2];
-    run.t_end = run_s[3];
-    run.plen = plen;
+    run.j = from.x;
+    run.t0 = from.y;
+    run.j_end = to.x;
+    run.t_end = to.y;
+    run.plen = p.prefix_len ? clamp_len(p.prefix_cap, *p.prefix_len) : 0;
     run.ahead = 0;
     if (run.j >= p.NP && run.j < p.NP + p.B) run.ahead = p.seq_lens[run.j - p.NP];
     const int j_first = run.j;
-    if (threadIdx.x == 0 && g == 0) p.meta[w] = make_int2(run.j, run.t0);
+    const uint64_t tmo = p.timeout_ns;
 
     // A whole warp's wait: all of its lanes go on or none (warp-wide
     // instructions follow), and the compiler sees that it is so.
@@ -805,6 +804,9 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             __syncwarp();
             ok = wait_uniform(smem_u32(qfull), nq & 1);
             ++nq;
+            // The output of the job before waits for its last O^T, this job's
+            // softmax for the output: S^T comes second.
+            ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
 #pragma unroll 1
             for (int i = 0; ok && i < run.n; ++i, ++n) {
                 ok = wait_uniform(smem_u32(sempty), (n & 1) ^ 1);
@@ -939,53 +941,64 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 ok = ok && wait_uniform(smem_u32(pempty), (n & 1) ^ 1);
                 tc_fence_after();
                 if (ok && whole) {
-                    // 32 values x 16 heads at a time, through 1 KB of p's buffers
+                    // 32 values x 32 heads at a time, through 2 KB of p's buffers
                     // for each warp: stmatrix turns the fragments into rows of 32
                     // values (16-byte chunks, chunk ^ (row / 2) % 4), which leave as
                     // 16-byte stores, 64 bytes of each of eight heads at once.
-                    const uint32_t stage = smem_u32(p_s) + sw * 1024;
-                    const int col0 = 2 * (lane & 3);
+                    const uint32_t stage = smem_u32(p_s) + sw * 2048;
+                    const int col0 = 2 * (lane & 3), hl0 = lane >> 2, head0 = g * kHeads + h0;
+                    const int last = min(run.count - h0, hpp);
 #pragma unroll 1
-                    for (int c = 0; c < p.nblk * (kPer / 16); ++c) {
-                        const int blk = c / (kPer / 16), hb = c % (kPer / 16) * 16;   // value block, first head
-                        if (hb >= hpp) continue;
-                        uint32_t x[2][8];
-                        const uint32_t src = tl + blk * kHeads + h0 + hb;
+                    for (int blk = 0; blk < p.nblk; ++blk) {
+                        uint32_t x[kBands][2][8];
+                        const uint32_t src = tl + blk * kHeads + h0;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            tmem_ld_frag16(src + (u * 16u << 16), x[u]);
-                            tmem_ld8_wait(x[u]);
-                            if (!kLow) continue;
-                            uint32_t y[8];
-                            tmem_ld_frag16(src + kLow + (u * 16u << 16), y);
-                            tmem_ld8_wait(y);
+                        for (int k = 0; k < kBands; ++k)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) x[u][k] = __float_as_uint(__uint_as_float(x[u][k]) + __uint_as_float(y[k]));
+                            for (int u = 0; u < 2; ++u) tmem_ld_frag16(src + 16 * k + (u * 16u << 16), x[k][u]);
+                        if (kLow) {
+                            uint32_t y[2][8];              // (a single band)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) tmem_ld_frag16(src + kLow + (u * 16u << 16), y[u]);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                tmem_ld8_wait(x[0][u]);
+                                tmem_ld8_wait(y[u]);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) x[0][u][e] = __float_as_uint(__uint_as_float(x[0][u][e]) + __uint_as_float(y[u][e]));
+                            }
                         }
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {          // eight heads; those past this half's are not stored
-                            const float2 f = *reinterpret_cast<const float2*>(al_s + min(h0 + hb + q * 8 + col0, kHeads - 2));
-                            uint32_t v[4];
+                        for (int k = 0; k < kBands; ++k) {
+                            if (!kLow) {
+                                tmem_ld8_wait(x[k][0]);
+                                tmem_ld8_wait(x[k][1]);
+                            }
 #pragma unroll
-                            for (int d = 0; d < 4; ++d)        // eight values
-                                v[d] = pack_bf16(__uint_as_float(x[d >> 1][q * 4 + (d & 1) * 2]) * f.x,
-                                                 __uint_as_float(x[d >> 1][q * 4 + (d & 1) * 2 + 1]) * f.y);
-                            const int hl = q * 8 + (lane & 7), d = lane >> 3;
-                            stmatrix_x4_trans(stage + hl * 64 + ((d ^ ((hl >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
+                            for (int q = 0; q < 2; ++q) {  // eight heads; those past this half's are not stored
+                                const float2 f = *reinterpret_cast<const float2*>(al_s + min(h0 + k * 16 + q * 8 + col0, kHeads - 2));
+                                uint32_t v[4];
+#pragma unroll
+                                for (int d = 0; d < 4; ++d)    // eight values
+                                    v[d] = pack_bf16(__uint_as_float(x[k][d >> 1][q * 4 + (d & 1) * 2]) * f.x,
+                                                     __uint_as_float(x[k][d >> 1][q * 4 + (d & 1) * 2 + 1]) * f.y);
+                                const int hl = k * 16 + q * 8 + (lane & 7), d = lane >> 3;
+                                stmatrix_x4_trans(stage + hl * 64 + ((d ^ ((hl >> 1) & 3)) << 4), v[0], v[1], v[2], v[3]);
+                            }
                         }
                         __syncwarp();
                         __nv_bfloat16* o = p.out + b * p.ldo_b + blk * 128 + quad * 32 + (lane & 3) * 8;
+                        uint4 v[2 * kBands];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int hl = j * 8 + (lane >> 2), head = h0 + hb + hl;
-                            uint4 v;
+                        for (int j = 0; j < 2 * kBands; ++j)
                             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                         : "r"(stage + hl * 64 + (((lane & 3) ^ ((hl >> 1) & 3)) << 4))
+                                         : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w)
+                                         : "r"(stage + (j * 8 + hl0) * 64 + (((lane & 3) ^ ((hl0 >> 1) & 3)) << 4))
                                          : "memory");
-                            if (hb + hl < hpp && head < run.count && bounds_ok(b >= 0 && b < p.B))
-                                *reinterpret_cast<uint4*>(o + static_cast<int64_t>(g * kHeads + head) * p.ldo_h) = v;
-                        }
+#pragma unroll
+                        for (int j = 0; j < 2 * kBands; ++j)
+                            if (j * 8 + hl0 < last && bounds_ok(b >= 0 && b < p.B))
+                                *reinterpret_cast<uint4*>(o + static_cast<int64_t>(head0 + j * 8 + hl0) * p.ldo_h) = v[j];
                         __syncwarp();
                     }
                 } else if (ok) {
@@ -1510,7 +1523,7 @@ struct Layout {
 Layout workspace_layout(const Plan& x, int64_t DV) {
     Layout L;
     L.meta = 0;
-    L.ml = (x.W * 8 + 255) / 256 * 256;
+    L.ml = ((x.W + 1) * 8 + 255) / 256 * 256;
     L.o = (L.ml + x.parts * kHeads * 8 + 255) / 256 * 256;
     L.images = L.o + x.parts * kHeads * DV * 4;
     L.total = L.images + x.images * x.image;
@@ -1639,8 +1652,6 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
     p.timeout_ns = limit ? limit : kDefaultTimeoutNs;
     p.inject = debug_inject_flags();
 
-    SplitArgs sa{static_cast<const __nv_bfloat16*>(t.q), t.ldq_tok, t.ldq_head, ws + lay.images, p.image, p.q_rows, p.B, p.H, p.G, p.HR,
-                 p.cc, p.pe, x.NP > 0, p.scale_log2, p.inject};
     CUtensorMap mc;
     if (!make_cache_map(&mc, t.cache, t.num_pages, z.page_size, cpt, t.ld_page, t.ld_row, p.box_rows)) return DSNQ_ERR_CUDA;
     void (*kern)(CUtensorMap, Params) = p.q_rows <= 16   ? latent_attention_fp8_kernel<1>
@@ -1648,8 +1659,9 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
                                         : p.q_rows <= 48 ? latent_attention_fp8_kernel<3>
                                                          : latent_attention_fp8_kernel<4>;
     if (!set_smem_attr(reinterpret_cast<const void*>(kern), smem)) return DSNQ_ERR_CUDA;
-    const int64_t ctas_split = (z.B * z.H + kSplitThreads / 32 - 1) / (kSplitThreads / 32);
-    st = launch_result(launch_kernel(split_queries_kernel, dim3(static_cast<unsigned>(ctas_split)), dim3(kSplitThreads), 0, s, sa));
+    const int64_t rows = z.B * z.H, per = kPrepareThreads / 32;
+    st = launch_result(launch_kernel(prepare_kernel, dim3(static_cast<unsigned>(1 + (rows + per - 1) / per)), dim3(kPrepareThreads), 0, s,
+                                     p, static_cast<const __nv_bfloat16*>(t.q), t.ldq_tok, t.ldq_head));
     if (st != DSNQ_OK) return st;
     st = launch_result(launch_kernel(kern, dim3(static_cast<unsigned>(p.W * p.G)), dim3(kThreads), smem, s, mc, p));
     if (st != DSNQ_OK || (p.W == 1 && !z.prefix)) return st;
