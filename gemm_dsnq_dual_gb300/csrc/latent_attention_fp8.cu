@@ -67,7 +67,7 @@ namespace attn8 {
 
 using namespace attn;
 
-constexpr int kHeads = 64;                  // rows (heads) of a CTA
+constexpr int kHeads = 64;                  // rows (heads) of a CTA, at most
 constexpr int kTile = 128;                  // tokens of a tile
 constexpr int kChunkBytes = kTile * 128;    // 128 bytes of each row of a tile
 constexpr int kPer = 32;                    // heads of a softmax warp, at most
@@ -100,8 +100,9 @@ struct Params {
     const int32_t* prefix_len;        // NULL: no common prefix
     int B, H, G, W;                   // requests, heads, head groups, workers
     int W_full;                       // workers that the GPU has room for, whatever the tables hold
+    int hg;                           // log2 of the heads (rows) of a group
     int HR;                           // rows of a request against the prefix: heads, a multiple of 4
-    int R, NP;                        // rows against the prefix; jobs of them (G groups of 64 rows each)
+    int R, NP;                        // rows against the prefix; jobs of them (G groups each)
     int width, prefix_width, page_size, box_rows, num_pages;   // box_rows: tokens of one copy
     int64_t cap, prefix_cap;          // tokens the tables can hold
     int cc, pe, nblk;                 // 128-code chunks of a row, position chunk, 128-column blocks of the value
@@ -427,8 +428,8 @@ struct Run {
         if (j + 1 >= p.NP && j + 1 < p.NP + p.B) ahead = p.seq_lens[j + 1 - p.NP];
         tiles = tiles_of(len);
         n = (j == j_end ? t_end : tiles) - t0;
-        const int rows = prefix ? p.R - (j * p.G + g) * kHeads : p.H - g * kHeads;
-        count = max(0, min(kHeads, rows));
+        const int rows = prefix ? p.R - ((j * p.G + g) << p.hg) : p.H - (g << p.hg);
+        count = max(0, min(1 << p.hg, rows));
         return true;
     }
     __device__ __forceinline__ bool live() const { return len > 0 && count > 0; }
@@ -450,8 +451,8 @@ struct Run {
 // The others split the queries into images of what a job's CTA has in shared
 // memory: codes of hi and of lo, chunk by chunk of 128, rows 128-byte swizzled,
 // then the bf16 position columns divided by the same power of two, then the
-// factors of the scores.  Image b G + g is that of heads 64 g .. of request b;
-// behind those come the prefix's, of 64 (request, head) pairs each.  A warp takes
+// factors of the scores.  Image b G + g is that of group g's heads of request b;
+// behind those come the prefix's, of as many (request, head) pairs each.  A warp takes
 // a row; rows that pad an image keep what they hold (nothing of their columns is
 // used).  In the attention's own warps, between the jobs, the split took 4.7 us a
 // job of 64 heads.
@@ -496,7 +497,7 @@ __device__ void share_out(const Params& p) {
     const int ptiles = plen > 0 ? tiles_of(plen) : 0, pjobs = plen > 0 ? p.NP : 0;
     tiles += static_cast<int64_t>(pjobs) * ptiles;
     // Requests a little longer than a worker's share go one to a worker, uncut.
-    const int h = min(p.H, kHeads), joined = 5 * p.B * h / (16 * p.W_full);
+    const int h = min(p.H, 1 << p.hg), joined = 5 * p.B * h / (16 * p.W_full);
     const int slack = max(1, p.W < kManyParts * p.B ? min(joined, 2 + h / 64) : joined);
     const bool uncut = !p.prefix_len && p.B <= p.W && tiles > static_cast<int64_t>(most - slack - 1) * p.W;
     const int lead = tiles < p.W ? 0 : tiles < 2 * p.W ? 1 : 2;
@@ -582,8 +583,8 @@ prepare_kernel(const Params p, const __nv_bfloat16* q, int64_t ldq_b, int64_t ld
     }
     for (int to = 0; to < (p.NP ? 2 : 1); ++to) {
         const int64_t r = static_cast<int64_t>(b) * p.HR + h;
-        const int64_t image = to ? static_cast<int64_t>(p.B) * p.G + r / kHeads : static_cast<int64_t>(b) * p.G + h / kHeads;
-        const int i = to ? static_cast<int>(r % kHeads) : h % kHeads;
+        const int64_t image = to ? static_cast<int64_t>(p.B) * p.G + (r >> p.hg) : static_cast<int64_t>(b) * p.G + (h >> p.hg);
+        const int i = (to ? static_cast<int>(r) : h) & ((1 << p.hg) - 1);
         uint8_t* at = p.images + image * p.image;
         if (!bounds_ok(i < p.q_rows)) continue;
         if (codes) {
@@ -899,12 +900,12 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 // An empty request: zeros, and the logarithm of an empty sum.
                 const int b = next.j - p.NP;
 #pragma unroll 1
-                for (int e = st; e < kHeads * (DV / 8); e += kSoftThreads) {
-                    const int h = g * kHeads + e / (DV / 8), c = e % (DV / 8);
+                for (int e = st; e < (DV / 8) << p.hg; e += kSoftThreads) {
+                    const int h = (g << p.hg) + e / (DV / 8), c = e % (DV / 8);
                     if (h < p.H && bounds_ok(b >= 0 && b < p.B))
                         *reinterpret_cast<uint4*>(p.out + b * p.ldo_b + h * p.ldo_h + c * 8) = make_uint4(0, 0, 0, 0);
                 }
-                if (p.lse && st < kHeads && g * kHeads + st < p.H) p.lse[b * p.ldl_b + g * kHeads + st] = kNegInf;
+                if (p.lse && st < 1 << p.hg && (g << p.hg) + st < p.H) p.lse[b * p.ldl_b + (g << p.hg) + st] = kNegInf;
             }
             if (started) {
                 // ---- output of the job (or of this worker's part of it)
@@ -946,7 +947,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     // values (16-byte chunks, chunk ^ (row / 2) % 4), which leave as
                     // 16-byte stores, 64 bytes of each of eight heads at once.
                     const uint32_t stage = smem_u32(p_s) + sw * 2048;
-                    const int col0 = 2 * (lane & 3), hl0 = lane >> 2, head0 = g * kHeads + h0;
+                    const int col0 = 2 * (lane & 3), hl0 = lane >> 2, head0 = (g << p.hg) + h0;
                     const int last = min(run.count - h0, hpp);
 #pragma unroll 1
                     for (int blk = 0; blk < p.nblk; ++blk) {
@@ -1031,7 +1032,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     }
                     if (quad == 0 && mine) p.part_ml[slot * kHeads + h0 + lane] = make_float2(M, ls);
                 }
-                const int head = g * kHeads + h0 + lane;
+                const int head = (g << p.hg) + h0 + lane;
                 if (ok && whole && p.lse && quad == 0 && mine && head < p.H)
                     p.lse[b * p.ldl_b + head] = ls == 0.f ? kNegInf : (M + log2f(ls)) * kLn2;
                 tc_fence_before();
@@ -1305,17 +1306,17 @@ latent_attention_fp8_join_kernel(const Params p, const int by_cut) {
     const int item = SHARE == 1 ? sub * 8 + warp : sub;
     const int hq = min(item, items - 1) / p.nblk, blk = item - hq * p.nblk;
     int g1 = 0, hl1 = 0, j1 = 0;
-    const int j2 = p.NP + b, g2 = hq * 4 / kHeads, hl2 = hq * 4 - g2 * kHeads;
+    const int j2 = p.NP + b, g2 = hq * 4 >> p.hg, hl2 = hq * 4 - (g2 << p.hg);
     int n2 = parts_of(j2, w2);
     if (PREFIX) {
         if (clamp_len(p.cap, p.seq_lens[b]) == 0) n2 = 0;  // an empty request leaves none
         if (clamp_len(p.prefix_cap, *p.prefix_len) > 0) {
             // The rows of four heads lie in one group; a CTA's items may lie in two
             // jobs, so each warp finds its own.
-            const int r = b * p.HR + hq * 4, rg = r / kHeads;
+            const int r = b * p.HR + hq * 4, rg = r >> p.hg;
             j1 = rg / p.G;
             g1 = rg - j1 * p.G;
-            hl1 = r - rg * kHeads;
+            hl1 = r - (rg << p.hg);
             int before = 0, upto = 0;
             for (int k = lane; k < p.W; k += 32) {
                 const int2 m = meta_s[k];
@@ -1489,16 +1490,18 @@ struct Shape {
     int64_t prefix_width;
 };
 struct Plan {
-    int64_t G, HR, R, NP, W, parts, rows, images, image;
+    int64_t hg, G, HR, R, NP, W, parts, rows, images, image;
 };
-Plan plan_of(const Shape& s, int64_t ctas) {
+Plan plan_for(const Shape& s, int64_t ctas, int hg) {
     Plan x{};
-    x.G = (s.H + kHeads - 1) / kHeads;
+    const int64_t heads = 1 << hg;
+    x.hg = hg;
+    x.G = (s.H + heads - 1) / heads;
     x.HR = (s.H + 3) / 4 * 4;
     int64_t tiles = 0;
     if (s.prefix && s.prefix_width > 0) {
         x.R = s.B * x.HR;
-        x.NP = ((x.R + kHeads - 1) / kHeads + x.G - 1) / x.G;
+        x.NP = ((x.R + heads - 1) / heads + x.G - 1) / x.G;
         tiles = x.NP * tiles_for(s.prefix_width * s.page_size);
     }
     // Workers: bounded by the device and by the most tiles that the tables can hold.
@@ -1511,10 +1514,34 @@ Plan plan_of(const Shape& s, int64_t ctas) {
     }
     x.parts = (s.prefix ? x.NP + s.B + x.W : 2 * x.W) * x.G;
     const int64_t most = x.NP ? x.R : s.H;                 // rows that a CTA can get
-    x.rows = most < kHeads ? (most + 15) / 16 * 16 : kHeads;
+    x.rows = most < heads ? (most + 15) / 16 * 16 : heads;
     x.images = (s.B + x.NP) * x.G;
     x.image = (2 * s.K / 128 + (s.P ? 1 : 0)) * x.rows * 128 + kHeads * 4;
     return x;
+}
+
+// Heads of a group (rows of a CTA): 64, whose products cost the least a head, or
+// fewer while that gives every job a CTA of its own and few tiles: a tile of 16
+// heads takes two thirds of the time of one of 64, and its output or part a
+// quarter.  By what the tables can hold, which bounds the lengths.  Measured, us,
+// 16 / 32 / 64 heads (* the rule's choice) of
+//   1 request of 701 tokens, 128 heads      15.4* / 16.4 / 19.0
+//   1 x 4000, 128                           16.4* / 17.6 / 20.0
+//   4 x 2400, 128                           24.6 / 22.6* / 24.6
+//   16 x 2000, 128                          40.5 / 32.8* / 41.0
+//   32 x 500, 128                           32.3 / 20.5* / 24.1
+//   64 x 500, 128 (256 jobs of 32 heads)    51.3 / 36.4 / 27.2*
+//   1 x 64000, 128 (2000 tiles of 32)       62.0 / 41.4 / 36.9*
+//   4 behind a prefix of 900, 128           19.5* / 20.0 / 22.6
+//   8 behind a prefix of 2000, 128          30.7 / 24.8* / 30.0
+Plan plan_of(const Shape& s, int64_t ctas) {
+    for (int hg = 4; hg < 6; ++hg) {
+        const Plan x = plan_for(s, ctas, hg);
+        const int64_t jobs = (x.NP + s.B) * x.G;
+        const int64_t tiles = (x.NP * tiles_for(s.prefix_width * s.page_size) + s.B * tiles_for(s.width * s.page_size)) * x.G;
+        if (jobs <= ctas && tiles <= (hg == 4 ? 2 : 8) * ctas) return x;
+    }
+    return plan_for(s, ctas, 6);
 }
 
 struct Layout {
@@ -1541,11 +1568,17 @@ dsnq_status check_sizes(const Shape& s) {
     return DSNQ_OK;
 }
 
-// What a call asks for: of the widest row, on the largest GPU.
+// What a call asks for: of the widest row, on the largest GPU (a smaller one may
+// choose larger groups).
 int64_t workspace_needed(Shape s) {
     s.K = 512;
     s.P = 64;
-    return workspace_layout(plan_of(s, kMaxCtas), s.DV).total;
+    int64_t most = 0;
+    for (int hg = 4; hg <= 6; ++hg) {
+        const int64_t n = workspace_layout(plan_for(s, kMaxCtas, hg), s.DV).total;
+        if (hg >= plan_of(s, kMaxCtas).hg && n > most) most = n;
+    }
+    return most;
 }
 dsnq_status workspace_bytes_of(const Shape& s, int64_t* bytes) {
     const dsnq_status st = check_sizes(s);
@@ -1610,6 +1643,7 @@ dsnq_status attention(const Shape& z, const Tensors& t, cudaStream_t s) {
     p.prefix_table = t.prefix_table;
     p.prefix_len = z.prefix ? t.prefix_len : nullptr;
     p.B = static_cast<int>(z.B); p.H = static_cast<int>(z.H); p.G = static_cast<int>(x.G); p.W = static_cast<int>(x.W);
+    p.hg = static_cast<int>(x.hg);
     p.W_full = ctas > x.G ? static_cast<int>(ctas / x.G) : 1;
     p.HR = static_cast<int>(x.HR); p.R = static_cast<int>(x.R); p.NP = static_cast<int>(x.NP);
     p.width = static_cast<int>(z.width);

@@ -17,6 +17,7 @@ of |k| (what the split of q leaves), which moves every probability by 2 dz;
 sums and exponentials add 2^-18.  The output is rounded to bf16: 2^-8."""
 
 import math
+import sys
 
 import numpy as np
 import pytest
@@ -287,8 +288,22 @@ def check(q, cache, scales, tables, lens, v_dim, scale, got, prefix=None, page=N
             assert ((lse[b].double() - l).abs() <= dl).all(), f"request {b}: lse off by {float((lse[b].double() - l).abs().max()):.2e}"
 
 
+LONG = False                          # tables of many columns that no request uses
+
+
+@pytest.fixture(params=["short tables", "long tables"])
+def tables(request, monkeypatch):
+    """Heads go to CTAs by 16 or 32 where the tables hold few tokens, by 64 otherwise."""
+    monkeypatch.setattr(sys.modules[__name__], "LONG", request.param == "long tables")
+
+
+both = pytest.mark.usefixtures("tables")
+
+
 def paged(g, lens, page, spare=3, extra=2):
     held = [-(-n // page) for n in lens]
+    if LONG:
+        extra += 1300 * 128 // (max(len(lens), 1) * page)
     pages = sum(held) + spare
     ids = torch.randperm(pages, generator=g, device=DEV).to(I32)
     table = torch.full((len(lens), max(held, default=0) + extra), -1, dtype=I32, device=DEV)
@@ -323,16 +338,19 @@ def run(lens, H, K, P, DV, page, seed, spread=0.0, scale=None):
     return got
 
 
+@both
 @pytest.mark.parametrize("page", [8, 16, 24, 32, 48, 64, 128, 192, 256])
 def test_attention_page_sizes(page):
     run([1, 0, 127, 300, 1000], 16, 512, 64, 512, page, seed=page)
 
 
+@both
 @pytest.mark.parametrize("H", [1, 2, 7, 8, 16, 17, 32, 33, 48, 63, 64, 65, 100, 128, 130, 200])
 def test_attention_heads(H):
     run([5, 200, 129, 0], H, 512, 64, 512, 64, seed=H)
 
 
+@both
 @pytest.mark.parametrize("K,P,DV", [(128, 0, 128), (128, 64, 128), (256, 0, 128), (256, 64, 256), (384, 0, 384), (384, 64, 256), (512, 0, 512),
                                     (512, 64, 128), (512, 64, 512)])
 @pytest.mark.parametrize("H", [5, 48, 64])
@@ -340,16 +358,19 @@ def test_attention_widths(K, P, DV, H):
     run([1, 64, 700, 1500, 260], H, K, P, DV, 32, seed=K + P + DV)
 
 
+@both
 def test_attention_lengths_around_every_tile_border():
     run([n for t in (32, 64, 96, 128, 256, 384) for n in (t - 1, t, t + 1)], 8, 512, 64, 512, 64, seed=1)
 
 
+@both
 @pytest.mark.parametrize("lens,H", [([20000], 16), ([9000, 3], 128), ([0, 5000, 0, 1], 64), ([1] * 400, 8), ([128] * 160 + [0] * 30, 65),
                                     ([3000] * 152, 16), ([2000] * 80, 128), ([40000], 64), (list(range(0, 3000, 37)), 48), ([0] * 9, 3)])
 def test_attention_work_splits(lens, H):
     run(lens, H, 512, 64, 512, 64, seed=len(lens) + H)
 
 
+@both
 @pytest.mark.parametrize("K,P,H", [(512, 64, 16), (512, 64, 32), (512, 64, 48), (512, 64, 64), (512, 0, 48), (512, 0, 64), (384, 64, 64),
                                    (256, 64, 16), (128, 0, 64), (128, 64, 16)])
 def test_attention_long_runs_of_every_ring(K, P, H):
@@ -357,6 +378,7 @@ def test_attention_long_runs_of_every_ring(K, P, H):
     run([30000, 11111], H, K, P, K, 16, seed=K + P + H)
 
 
+@both
 @pytest.mark.parametrize("spread", [2.0, 6.0])
 def test_attention_scales_far_apart(spread):
     run([300, 90, 2000], 20, 256, 64, 256, 16, seed=5, spread=spread)
@@ -370,6 +392,7 @@ def test_attention_most_heads_requests_and_a_table_of_no_columns():
     assert (out == 0).all() and (lse == -math.inf).all() and dsnq.debug_status() == OK
 
 
+@both
 def test_attention_scores_that_grow_and_peak():
     """Scores that grow by hundreds from tile to tile (O and the sums follow),
     fall, and one token far above all others; a sink far above a long tail."""
@@ -391,6 +414,7 @@ def test_attention_scores_that_grow_and_peak():
         assert dsnq.debug_status() == OK
 
 
+@both
 @pytest.mark.parametrize("H", [16, 64])
 @pytest.mark.parametrize("n", [1, 2, 31, 500])
 def test_attention_of_equal_values_is_that_value(H, n):
@@ -408,6 +432,7 @@ def test_attention_of_equal_values_is_that_value(H, n):
     assert ((out[0].double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -18)).all()
 
 
+@both
 def test_attention_rows_of_no_scale():
     """A scale of 0 (a row never written): a zero row, with the weight of a zero score."""
     g = gen(8)
@@ -420,6 +445,7 @@ def test_attention_rows_of_no_scale():
     check(q, cache, scales, table, [40, 300], 128, 0.1, got)
 
 
+@both
 def test_attention_bad_pages_read_as_zero_rows_and_are_reported():
     g = gen(9)
     lens = [300, 70, 5]
@@ -447,6 +473,7 @@ def test_attention_lengths_outside_the_table():
     assert dsnq.debug_status() == OK
 
 
+@both
 def test_attention_strided_views():
     g = gen(11)
     lens, K, P, H = [200, 37, 130], 256, 64, 10
@@ -471,6 +498,7 @@ def test_attention_strided_views():
     assert (wide_out == 7).all() and (wide_lse == 7).all()
 
 
+@both
 def test_attention_non_finite_queries_stay_in_their_heads():
     g = gen(12)
     lens, K, P = [300, 4000], 512, 64
@@ -488,6 +516,7 @@ def test_attention_non_finite_queries_stay_in_their_heads():
         assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
 
 
+@both
 def test_attention_queries_of_any_size():
     """The split of q goes by each head's largest value: from 2^-90 to 2^90, and heads of zeros."""
     g = gen(13)
@@ -502,6 +531,7 @@ def test_attention_queries_of_any_size():
         check(q, cache, scales, table, lens, 256, float(np.float32(scale)), got)
 
 
+@both
 def test_attention_repeats_and_needs_no_clean_workspace():
     g = gen(14)
     lens = [5000, 3, 700, 128]
@@ -562,18 +592,21 @@ def run_shared(prefix, lens, H, K, P, DV, page, seed, stored=None):
     return got
 
 
+@both
 @pytest.mark.parametrize("prefix", [0, 1, 31, 127, 128, 129, 1000, 5000])
 @pytest.mark.parametrize("H", [1, 6, 16, 48, 64, 100, 128])
 def test_shared_prefix(prefix, H):
     run_shared(prefix, [1, 0, 200, 129, 33], H, 512, 64, 512, 64, seed=prefix + H)
 
 
+@both
 @pytest.mark.parametrize("lens,H,prefix", [([0] * 7, 16, 300), ([0], 3, 0), ([5000, 1, 0], 16, 60), ([7] * 300, 8, 2000), ([100] * 160, 65, 129),
                                            ([64], 16, 20000), ([0, 0, 9000], 128, 9000), ([3] * 33, 200, 40)])
 def test_shared_prefix_work_splits(lens, H, prefix):
     run_shared(prefix, lens, H, 512, 64, 512, 32, seed=len(lens))
 
 
+@both
 @pytest.mark.parametrize("K,P,DV,page", [(128, 0, 128, 8), (256, 64, 128, 48), (384, 64, 384, 128), (512, 0, 256, 16)])
 def test_shared_prefix_widths(K, P, DV, page):
     run_shared(777, [50, 0, 300, 1], 24, K, P, DV, page, seed=K + P)
@@ -598,6 +631,7 @@ def test_shared_prefix_of_no_pages_and_bad_pages():
     assert dsnq.debug_status() == BOUNDS and dsnq.debug_status() == OK
 
 
+@both
 def test_shared_prefix_agrees_with_separate_requests():
     """The same tokens as requests of their own whose tables begin with the prefix's pages."""
     g = gen(3)
@@ -613,6 +647,7 @@ def test_shared_prefix_agrees_with_separate_requests():
     assert ((a.float() - b.float()).abs() <= 4 * 2.0 ** -8 * top).all() and ((la - lb).abs() <= 2.0 ** -15).all()
 
 
+@both
 def test_shared_prefix_strides_repeats_and_workspaces():
     g = gen(4)
     lens, prefix, H = [70, 0, 300, 5], 700, 7
