@@ -884,7 +884,8 @@ def decode_ops(which, M, dev, tokens=1024, heads=128):
     requests, `head_rope` on the attention heads of wq_b's output (128 of 192
     columns, the last 64 rotated), `cache_write` of the kv latent and its
     position columns, `attention` of M requests of `tokens` tokens each with
-    `heads` heads over the 576-column cache."""
+    `heads` heads over the 576-column cache; the `_fp8` ones over the same cache
+    in 8 bits, `cache_read_fp8` of M requests' tokens."""
     import torch
     import gemm_dsnq_dual_gb300 as dsnq
     g = torch.Generator(device=dev).manual_seed(5)
@@ -903,19 +904,31 @@ def decode_ops(which, M, dev, tokens=1024, heads=128):
         x, pos = rnd(M, N_ATTN).view(M, 128, 192), ints(M, 1 << 17)
         out = torch.empty_like(x)
         return lambda: dsnq.head_rmsnorm_rope(x, pos, f, normalize=False, rope_scale=scale, out=out)
-    cache = rnd(pages, page, KKV + 64)
-    if which == "cache_write":
+    if which.endswith("_fp8"):                            # e4m3 codes, then bf16 position columns
+        codes, pe = rnd(pages, page, KKV).to(torch.float8_e4m3fn).view(torch.uint8), rnd(pages, page, 64).view(torch.uint8)
+        cache, scales = torch.cat([codes, pe], -1), torch.rand(pages, page, generator=g, device=dev)
+    else:
+        cache = rnd(pages, page, KKV + 64)
+    if which in ("cache_write", "cache_write_fp8"):
         row, pos = rnd(M, KQ + KKV + 64), ints(M, 1 << 17)
         slots = torch.randperm(pages * page, generator=g, device=dev)[:M]
         gamma = rnd(KKV)
+        if which == "cache_write_fp8":
+            return lambda: dsnq.latent_cache_write_fp8(row[:, KQ:KQ + KKV], row[:, KQ + KKV:], pos, slots, f, cache, scales,
+                                                       gamma=gamma, normalize=True, rope_scale=scale)
         return lambda: dsnq.latent_cache_write(row[:, KQ:KQ + KKV], row[:, KQ + KKV:], pos, slots, f, cache, gamma=gamma,
                                                normalize=True, rope_scale=scale)
     q, table = rnd(M, heads, KKV + 64), ids.view(M, -1)
     lens = torch.full((M,), tokens, dtype=torch.int32, device=dev)
+    if which == "cache_read_fp8":
+        starts = torch.arange(M + 1, dtype=torch.int32, device=dev) * tokens
+        return lambda: dsnq.latent_cache_read_fp8(cache, scales, KKV, table, starts, M * tokens)
+    if which == "attention_fp8":
+        return lambda: dsnq.paged_latent_attention_fp8(q, cache, scales, table, lens, KKV, 192 ** -0.5)
     return lambda: dsnq.paged_latent_attention(q, cache, table, lens, KKV, 192 ** -0.5)
 
 
-DECODE_OPS = ["tables", "head_rope", "cache_write", "attention"]
+DECODE_OPS = ["tables", "head_rope", "cache_write", "attention", "cache_write_fp8", "cache_read_fp8", "attention_fp8"]
 
 
 def run_decode_ops(args):

@@ -420,23 +420,23 @@ struct ReadArgs {
     uint32_t inject;
 };
 
-constexpr int kReadThreads = 256;
-constexpr int kReadRows = 32;            // rows of a CTA
+constexpr int kReadThreads = 128;
 
-// A CTA takes 32 rows of the output: each of its first threads finds one row's
+// A CTA takes ROWS rows of the output: each of its first threads finds one row's
 // request (the last that begins at or before it), page and scale, then all of
-// them take the rows' chunks of 8 columns one after the other, several on
-// their way at once.  Bound by HBM: 1.8 KB a row in and out.
+// them take the rows' chunks of 8 columns one after the other, U on their way at
+// once.  Bound by HBM: 1.8 KB a row in and out.
+template <int ROWS, int U>
 __global__ void __launch_bounds__(kReadThreads)
 latent_cache_read_fp8_kernel(const ReadArgs a) {
     grid_dependency_wait();
     allow_dependent_launch();
     bounds_self_test(a.inject);
-    __shared__ int64_t at_s[kReadRows];  // byte offset of the row in the cache, -1: zeros, -2: not written
-    __shared__ float scale_s[kReadRows];
+    __shared__ int64_t at_s[ROWS];  // byte offset of the row in the cache, -1: zeros, -2: not written
+    __shared__ float scale_s[ROWS];
     const int t = threadIdx.x;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kReadRows;
-    if (t < kReadRows) {
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * ROWS;
+    if (t < ROWS) {
         const int64_t r = r0 + t;
         int64_t at = -2;
         float scale = 0.f;
@@ -463,8 +463,7 @@ latent_cache_read_fp8_kernel(const ReadArgs a) {
         scale_s[t] = scale;
     }
     __syncthreads();
-    const int chunks = a.W / kChunk, items = kReadRows * chunks;
-    constexpr int U = 6;
+    const int chunks = a.W / kChunk, items = ROWS * chunks;
     for (int base = t; base < items; base += U * kReadThreads) {
         uint4 raw[U];
 #pragma unroll
@@ -864,8 +863,17 @@ extern "C" dsnq_status dsnq_latent_cache_read_fp8(
     const uint32_t chunks = static_cast<uint32_t>(W / kChunk);
     a.recip = static_cast<uint32_t>((0x100000000ull + chunks - 1) / chunks);   // exact for the few thousand items of a CTA
     a.inject = debug_inject_flags();
-    return launch_result(launch_kernel(latent_cache_read_fp8_kernel, dim3(static_cast<unsigned>((rows + kReadRows - 1) / kReadRows)),
-                                       dim3(kReadThreads), 0, static_cast<cudaStream_t>(stream), a));
+    // Few rows: small CTAs with all of their chunks on the way at once; many: fewer
+    // registers, so more CTAs on an SM.  Per call in a graph, 8 rows and 5 chunks
+    // against 16 and 3, us: 400 rows of 576 columns 3.6 and 4.6, 4000 4.1 and 5.1,
+    // 12000 both 5.7, 80000 28.6 and 27.1; 8000 of 192 4.1 and 3.6.  (32 rows a CTA
+    // of 256 threads with 6 chunks: 5.9 and, for 120003 rows, 34.4; now 4.3 and 30.8,
+    // 85% of the measured copy bandwidth.)
+    const bool few = rows <= 6144;
+    const int64_t per = few ? 8 : 16;
+    return launch_result(launch_kernel(few ? latent_cache_read_fp8_kernel<8, 5> : latent_cache_read_fp8_kernel<16, 3>,
+                                       dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kReadThreads), 0,
+                                       static_cast<cudaStream_t>(stream), a));
 }
 
 extern "C" dsnq_status dsnq_extend_block_tables(
