@@ -146,6 +146,20 @@ def test_write_codes_are_those_of_the_division():
     assert torch.equal(cache.view(-1, 512)[:4000], (x / s.double()[:, None]).float().to(E4).view(U8))
 
 
+def test_write_position_columns_are_those_of_the_division():
+    g = gen(21)
+    M, K, P = 5000, 16, 64
+    kv = randn(g, M, K) * torch.exp(torch.randn(M, 1, generator=g, device=DEV) * 8).to(BF)
+    pe = randn(g, M, P) * torch.exp(torch.randn(M, P, generator=g, device=DEV) * 8).to(BF)
+    cache, scales = torch.zeros(M // 8, 8, K + 2 * P, dtype=U8, device=DEV), torch.zeros(M // 8, 8, device=DEV)
+    at = torch.randperm(M, generator=g, device=DEV)
+    dsnq.latent_cache_write_fp8(kv, pe, torch.zeros(M, dtype=I64, device=DEV), at, torch.empty(0, dtype=F64, device=DEV), cache, scales)
+    s = scales.flatten()[at]
+    want = (pe.double() / s.double()[:, None]).float().to(BF)  # the 64-bit quotient rounds to 32 bits as the exact one does
+    got = cache.view(-1, K + 2 * P)[at, K:].contiguous().view(BF)
+    assert torch.equal(got, want) and dsnq.debug_status() == OK
+
+
 def test_write_zero_tiny_and_non_finite_rows():
     K, P = 256, 64
     kv = torch.zeros(7, K, dtype=BF, device=DEV)
