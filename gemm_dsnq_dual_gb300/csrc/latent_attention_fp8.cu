@@ -25,7 +25,7 @@
 // (those of tokens whose scale is below 2^-8 of their block's largest count
 // unrounded: they may have a large p and no value to speak of).
 //
-// One CTA, 64 heads, tiles of 128 tokens:
+// One CTA, 64 heads (or 32 or 16 where CTAs would idle), tiles of 128 tokens:
 //   S^T [128 tokens x (64 hi | 64 lo)]  = C Q^T        M = 128: a thread has a token
 //   O^T [DV x 64 heads]                += C^T (p s)^T   M = 128, block-scaled; C^T is the
 //                                                       same tile read column-major
@@ -34,15 +34,21 @@
 // one of O^T 52 (45): 2900 cycles a tile at 64 heads and 576 columns, where the
 // copy of a tile takes 3600 at this GPU's share of HBM per SM.
 //
-// Work split: jobs (a request, or 64 rows of the whole batch against the common
-// prefix) are laid end to end as tiles and cut into equal runs, one per worker
-// (one CTA per group of 64 heads), on the device, from the lengths.  A run that
+// Work split: jobs (a request, or as many rows of the whole batch against the
+// common prefix as a CTA has heads) are laid end to end as tiles and cut into
+// equal runs, one per worker (a CTA for each group of heads), on the device, from
+// the lengths (prepare_kernel).  A run that
 // covers a whole request writes its output; otherwise, and for all jobs of a
 // batch with a common prefix, (max, sum, output times that sum) go to the
 // workspace in fp32, and a second kernel joins them in the order of the tokens
 // (no atomics: results do not depend on timing).
 // The prefix: its rows are the (request, head) pairs of the batch laid end to
 // end, so every tile of the prefix serves 64 rows whatever the number of heads.
+//
+// Measured (152 CTAs, requests of 2048 and 8192 tokens, per tile): 1.90 us at 16
+// heads of 576 columns, where HBM needs 1.88; 2.05 at 48 of 512 (HBM 1.50), 2.87 at
+// 64 of 576 (2.75 where two groups share the tiles in L2).  There the softmax warps bound it, two on each quarter of the SM,
+// whose reads of shared memory and TMEM wait behind the products'.
 //
 // Warps: 0 and 3 copy tiles (TMA), 1 issues S^T, 2 issues O^T, 4..11 do the softmax:
 // warp w has tokens 32 (w % 4) .. of a tile (the TMEM lanes it can reach, and one
@@ -73,7 +79,6 @@ constexpr int kChunkBytes = kTile * 128;    // 128 bytes of each row of a tile
 constexpr int kPer = 32;                    // heads of a softmax warp, at most
 constexpr int kSoftWarp0 = 4, kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
 constexpr int kThreads = kSoftWarp0 * 32 + kSoftThreads;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSlots = 13;               // slots of the rings of chunks
 constexpr int kScaleSlots = 4;              // tiles whose row scales are kept; the rings hold at most three tiles
 constexpr int kMaxCtas = 160;               // bound of workers x head groups

@@ -531,6 +531,25 @@ def test_attention_non_finite_queries_stay_in_their_heads():
 
 
 @both
+@pytest.mark.parametrize("H", [3, 48, 64])
+def test_attention_of_a_row_that_is_not_finite(H):
+    """Its request is NaN in every head, the others are what they are without it."""
+    g = gen(31)
+    lens = [700, 90, 300]
+    table, pages = paged(g, lens, 16)
+    cache, scales = make_cache(g, pages, 16, 512, 64)
+    q = randn(g, 3, H, 576)
+    call = lambda: dsnq.paged_latent_attention_fp8(q, cache, scales, table, ints(lens), 512, 0.05)
+    want = call()
+    scales.view(-1)[slots_of(table[1], 16, 33, 34)] = math.nan
+    out, lse = call()
+    assert out[1].isnan().all() and lse[1].isnan().all()
+    for b in (0, 2):
+        assert torch.equal(out[b], want[0][b]) and torch.equal(lse[b], want[1][b])
+    assert dsnq.debug_status() == OK
+
+
+@both
 def test_attention_queries_of_any_size():
     """The split of q goes by each head's largest value: from 2^-90 to 2^90, and heads of zeros."""
     g = gen(13)
