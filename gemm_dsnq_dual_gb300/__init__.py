@@ -453,8 +453,9 @@ def release_workspaces() -> None:
     """Gives the workspaces that the attention calls keep for the calling thread
     (one for each of four streams of a device: up to 42 MB after
     paged_latent_attention, more by the batch's queries and partial results after
-    the calls over a cache in 8 bits) back to torch's allocator.  Calls still running may go on using theirs: the memory goes to
-    later work of the same stream only."""
+    the calls over a cache in 8 bits) back to torch's allocator.  Calls still
+    running may go on using theirs: the memory goes to later work of the same
+    stream only."""
     _kept.__dict__.clear()
 
 
@@ -755,7 +756,7 @@ def shared_prefix_latent_attention_fp8(q, cache, scales, prefix_table, prefix_le
     """paged_latent_attention_fp8 for requests that all begin with the first
     prefix_len (int32 [1]) tokens of prefix_table [width] (int32 page ids), each
     followed by seq_lens[b] tokens of its own row of block_table.  The prefix is
-    read and multiplied once for every 64 (request, head) pairs of the batch.
+    read and multiplied once for up to 64 (request, head) pairs of the batch.
     The workspace grows with the batch (1200 bytes of split queries and 4 v_dim of
     results a pair, twice)."""
     if prefix_table is None:

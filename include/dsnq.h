@@ -650,7 +650,7 @@ DSNQ_API dsnq_status dsnq_paged_latent_attention_fp8(
  * The same for a batch whose requests all begin with the same tokens: request
  * b's tokens are the first prefix_len[0] of prefix_table (int32
  * [prefix_width]), then the first seq_lens[b] of its own row of block_table.
- * The prefix is read and multiplied for all requests at once: 64 (request,
+ * The prefix is read and multiplied for all requests at once: up to 64 (request,
  * head) pairs share each pass over it, so with few heads it costs a fraction of
  * B separate passes.
  *   prefix_len  : int32 [1] in device memory, taken as within [0, prefix_width
