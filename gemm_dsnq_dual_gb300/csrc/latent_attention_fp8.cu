@@ -858,11 +858,17 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                 tc_copy_scales(tmem + kTmemSfb, sf_desc);
 #pragma unroll 1
                 for (int c = 0; c < cpt; ++c) {
-                    int slot;
+                    int slot, code = c == 0 ? 0 : c - p.pe;
                     uint32_t parity;
-                    ch.take(p, c, slot, parity);
-                    const int code = c == 0 ? 0 : c - p.pe;
-                    if ((c == 1 && p.pe) || code >= p.nblk) continue;
+                    if (opaque(p.twin)) {                  // the last codes first: their slot frees two loads one after the other
+                        if (c == 4) break;
+                        code = (c + 3) & 3;
+                        slot = static_cast<int>(n & 1) * 4 + (0x1320 >> 4 * code & 3);
+                    } else {
+                        ch.take(p, c, slot, parity);
+                        if (c == 1 && p.pe) continue;
+                    }
+                    if (code >= p.nblk) continue;
                     tc_mma_scaled<kPair>(tmem + code * kHeads, desc_low(smem_u32(ring) + slot * kChunkBytes, kChunkBytes), p_low,
                                          idesc_o(kPair ? HP : 2 * HP), tmem + kTmemSfa, tmem + kTmemSfb, i > 0);
                     tc_commit(smem_u32(&empty[slot]));
