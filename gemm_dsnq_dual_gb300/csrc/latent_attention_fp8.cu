@@ -46,9 +46,11 @@
 // end, so every tile of the prefix serves 64 rows whatever the number of heads.
 //
 // Measured (152 CTAs, requests of 2048 and 8192 tokens, per tile): 1.90 us at 16
-// heads of 576 columns, where HBM needs 1.88; 2.05 at 48 of 512 (HBM 1.50), 2.87 at
-// 64 of 576 (2.75 where two groups share the tiles in L2).  There the softmax warps bound it, two on each quarter of the SM,
-// whose reads of shared memory and TMEM wait behind the products'.
+// heads of 576 columns, where HBM needs 1.88; 2.1 at 48 of 512 (HBM 1.50), where the
+// softmax warps bound it, two on each quarter of the SM, whose reads of shared
+// memory and TMEM wait behind the products'; 2.69 at 64 of 576, where shared memory
+// holds two tiles: the way from O^T of a tile over its freed slots, the copies
+// into them, S^T and the softmax to the O^T two tiles on takes as long.
 //
 // Warps: 0 and 3 copy tiles (TMA), 1 issues S^T, 2 issues O^T, 4..11 do the softmax:
 // warp w has tokens 32 (w % 4) .. of a tile (the TMEM lanes it can reach, and one
@@ -160,6 +162,12 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
         " [%0], [%1, {%3, %3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(chunk), "r"(group), "r"(page), "l"(policy)
         : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_5d(const CUtensorMap* map, int32_t chunk, int32_t group, int32_t page, uint64_t policy) {
+    asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile.L2::cache_hint [%0, {%1, %1, %2, %3, %4}], %5;" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(0), "r"(chunk), "r"(group), "r"(page), "l"(policy)
+                 : "memory");
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
@@ -756,6 +764,11 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     int slot;
                     uint32_t parity;
                     ch.take(p, c, slot, parity);
+                    // Barely two tiles of room: while it waits for the slot, the
+                    // chunk comes as near as L2 (2.77 -> 2.69 us a tile at 64 heads
+                    // of 576 columns; a whole tile ahead 2.87; with more room
+                    // slower: 2.07 -> 2.26 at 48 of 512).
+                    if (opaque(p.twin) && lane < live) tma_prefetch_5d(&map_c, chunk, in_page / 8, id, policy);
                     ok = wait_uniform_asleep(smem_u32(&empty[slot]), parity ^ 1);
                     if (!ok) break;
                     const uint32_t fb = smem_u32(&full[slot]);
