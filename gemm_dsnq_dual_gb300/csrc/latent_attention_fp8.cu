@@ -768,7 +768,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     // chunk comes as near as L2 (2.77 -> 2.69 us a tile at 64 heads
                     // of 576 columns; a whole tile ahead 2.87; with more room
                     // slower: 128 x 8000 tokens, 48 heads of 512, 148 -> 157 us).
-                    if (opaque(p.twin) && lane < live) tma_prefetch_5d(&map_c, chunk, in_page / 8, id, policy);
+                    if (opaque(p.twin) && lane < live && id < p.num_pages) tma_prefetch_5d(&map_c, chunk, in_page / 8, id, policy);
                     ok = wait_uniform_asleep(smem_u32(&empty[slot]), parity ^ 1);
                     if (!ok) break;
                     const uint32_t fb = smem_u32(&full[slot]);

@@ -460,21 +460,22 @@ def test_attention_rows_of_no_scale():
 
 
 @both
-def test_attention_bad_pages_read_as_zero_rows_and_are_reported():
+@pytest.mark.parametrize("H,K", [(20, 256), (64, 512)])
+def test_attention_bad_pages_read_as_zero_rows_and_are_reported(H, K):
     g = gen(9)
     lens = [300, 70, 5]
     table, pages = paged(g, lens, 16)
-    cache, scales = make_cache(g, pages, 16, 256, 64)
-    q = randn(g, 3, 20, 320)
+    cache, scales = make_cache(g, pages, 16, K, 64)
+    q = randn(g, 3, H, K + 64)
     good = table.clone()
     table[0, 3], table[0, 18], table[1, 0], table[2, 0] = pages, -5, 2 ** 31 - 1, -2 ** 31
-    got = dsnq.paged_latent_attention_fp8(q, cache, scales, table, ints(lens), 256, 0.1)
+    got = dsnq.paged_latent_attention_fp8(q, cache, scales, table, ints(lens), K, 0.1)
     assert dsnq.debug_status() == BOUNDS and dsnq.debug_status() == OK
     zeros = torch.zeros(1, 16, cache.shape[-1], dtype=U8, device=DEV)
     more, more_s = torch.cat([cache, zeros]), torch.cat([scales, torch.zeros(1, 16, device=DEV)])
     table = torch.where((table < 0) | (table >= pages), pages, table)
     table = torch.where(good < 0, good, table)
-    check(q, more, more_s, table, lens, 256, 0.1, got)
+    check(q, more, more_s, table, lens, K, 0.1, got)
 
 
 def test_attention_lengths_outside_the_table():
