@@ -37,6 +37,20 @@ __device__ __forceinline__ void bounds_self_test(uint32_t inject) {
 #endif
 }
 
+// Test hook of the debug build (inject flag bit 2): the warps `who` come 50 us
+// late to their reads of shared memory that other warps wrote, so that a
+// missing barrier behind the reads shows in the results.
+__device__ __forceinline__ void late_self_test(uint32_t inject, bool who) {
+#ifdef DSNQ_DEBUG
+    if ((inject & kInjectLateReads) && who) {
+        for (int i = 0; i < 50; ++i) __nanosleep(1000);
+    }
+#else
+    (void)inject;
+    (void)who;
+#endif
+}
+
 // Reads and clears this unit's word (host; synchronizes `s`).
 static inline bool take_debug_word(cudaStream_t s, unsigned int* v) {
     const unsigned int zero = 0;

@@ -17,6 +17,7 @@ constexpr uint32_t kStatusBounds = 2u;    // a debug-build index check failed
 // Test-hook flags (dsnq_debug_set).
 constexpr uint32_t kInjectSkipLoad = 1u;          // the GEMM producer skips its first load
 constexpr uint32_t kInjectBoundsSelfTest = 2u;    // debug build: one deliberate failed index check
+constexpr uint32_t kInjectLateReads = 4u;         // debug build: some warps come late to reads of others' sums
 
 // Test hooks and the wait bound, set by dsnq_debug_set (dsnq_api.cu).
 uint32_t debug_inject_flags();

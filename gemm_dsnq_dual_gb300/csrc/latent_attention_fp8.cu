@@ -953,13 +953,17 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     }
                 bc[lane] = v[0];
                 bc[kPer + lane] = u[0];
-                half_sync_or(half, false);                     // bc is next written after the next job's S^T
+                half_sync_or(half, false);
+                late_self_test(p.inject, quad == 3);
                 float ls = 0.f, lrs = 0.f;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     ls += bc_s[(half * 4 + q) * 2 * kPer + lane];
                     lrs += bc_s[(half * 4 + q) * 2 * kPer + kPer + lane];
                 }
+                // The next job's first tile writes T into bc in front of its own
+                // barrier, and S^T of that tile waits for none of these reads.
+                half_sync_or(half, false);
                 // A part's weights add up to its unrounded sum, which the join divides by.
                 if (mine) al_s[h0 + lane] = lrs > 0.f || lrs != lrs ? __fdividef(whole ? 1.0f : ls, lrs) : 0.f;
                 __syncwarp();                                  // the same from each of the half's four warps

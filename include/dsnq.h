@@ -714,7 +714,9 @@ DSNQ_API void dsnq_set_launch_overlap(int32_t enable);
  * so the consumer's wait on it must run out: the kernel then records
  * DSNQ_ERR_TIMEOUT, releases its tensor memory and returns.  Bit 1 (debug
  * build only; ignored otherwise) makes every launch record one failed index
- * check that guards no access, to test the reporting path.
+ * check that guards no access, to test the reporting path.  Bit 2 (debug build
+ * only) makes some warps of the attention over an 8-bit cache 50 us late where
+ * they read what others wrote, to test the order of the accesses.
  */
 DSNQ_API void dsnq_debug_set(uint32_t inject_flags, uint64_t wait_timeout_ns);
 

@@ -93,3 +93,39 @@ def test_a_failed_check_is_reported_and_cleared(libs):
     codes, scale, _ = oracle.fused_dual_rmsnorm_group_quant(*[inputs.bits(t) for t in
                                                              (lat.q, lat.kv, lat.gamma_q, lat.gamma_kv)], lat.eps)
     assert np.array_equal(scale, got[1].cpu().numpy()) or np.allclose(scale, got[1].cpu().numpy(), rtol=1e-6)
+
+
+@pytest.mark.parametrize("prefix", [0, 300])
+@pytest.mark.parametrize("H", [16, 32, 48, 64])
+def test_sums_of_a_job_outlive_their_late_readers(libs, H, prefix):
+    """Attention over an 8-bit cache, several requests a worker: the warps of a
+    job read one another's sums at its end.  The hook lets a quarter of them
+    come late to that; the others may not have written over the sums by then."""
+    _, debug = libs
+    _native.use_library(debug)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(H + prefix)
+    B, page, K = 400, 64, 256
+    lens = torch.randint(1, 300, (B,), generator=g, device="cuda").to(torch.int32)
+    pages = 40
+    cache = (torch.randn(pages, page, K, generator=g, device="cuda") * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    scales = torch.rand(pages, page, generator=g, device="cuda") * 0.01
+    table = torch.randint(0, pages, (B, 5), generator=g, device="cuda").to(torch.int32)
+    q = torch.randn(B, H, K, generator=g, device="cuda").to(torch.bfloat16)
+    front, front_len = torch.arange(5, dtype=torch.int32, device="cuda"), torch.tensor([prefix], dtype=torch.int32, device="cuda")
+
+    def call():
+        if prefix:
+            return dsnq.shared_prefix_latent_attention_fp8(q, cache, scales, front, front_len, table, lens, K, 0.1)
+        return dsnq.paged_latent_attention_fp8(q, cache, scales, table, lens, K, 0.1)
+
+    want = call()
+    assert dsnq.debug_status() == OK
+    dsnq.debug_set(inject_flags=4)
+    try:
+        got = call()
+        assert dsnq.debug_status() == OK
+    finally:
+        dsnq.debug_set(0, 0)
+    for a, b in zip(got, want):
+        assert torch.equal(as_bits(a), as_bits(b))
