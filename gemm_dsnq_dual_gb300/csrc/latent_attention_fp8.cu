@@ -9,16 +9,16 @@
 // way in and in every read of it by a product.  What multiplies them is split
 // instead, into two e4m3 numbers, x = hi + lo / 32, hi = e4m3(x), lo =
 // e4m3(32 (x - hi)): eight significant bits, as many as bf16 has.
-//   q: divided by a power of two per head (exact) so that it is below 256; hi and
-//      lo then hold a bf16 exactly down to 2^-7 (hi's last bit is 2^-9 there, lo's
-//      2^-14), that is to 2^-15 of the head's largest; what is smaller is off by
-//      at most 2^-15, 2^-23 of the largest.  hi and lo are stacked along N, so a
-//      product reads a tile of the cache once.
+//   q: divided by a power of two per head (exact) so that its latent columns are
+//      in [128, 256) at most; hi and lo then hold a bf16 exactly down to 2^-7 (hi's
+//      last bit is 2^-9 there, lo's 2^-14), that is to 2^-14 of the head's largest;
+//      what is smaller is off by at most 2^-15, 2^-22 of the largest.  hi and lo
+//      are stacked along N, so a product reads a tile of the cache once.
 //   p s: x = p_j s_j 2^-T with T a power of two per head and block of 32 tokens
-//      such that the block's largest x lies in [64, 256]; the products put 2^T
+//      such that the block's largest x lies in [128, 256]; the products put 2^T
 //      back (block scales along K).  Rounded by at most 2^-8 of x (2^-4 of hi's
 //      remainder, which is at most 2^-4 of x) or 2^-15 (half of lo's last bit),
-//      at most 2^-21 of the block's largest.
+//      at most 2^-22 of the block's largest.
 // The position columns are a bf16 product into the same accumulators.  Scores,
 // softmax statistics and outputs are fp32.  The outputs are divided by the sum
 // of the p that the rounded x stand for, so that the weights add up to one
@@ -573,9 +573,14 @@ prepare_kernel(const Params p, const __nv_bfloat16* q, int64_t ldq_b, int64_t ld
     // The largest magnitudes, as the bits of a bf16 (NaN above all others).
     const uint32_t top = __reduce_max_sync(0xffffffffu, max(largest8(x[0]), largest8(x[1])));
     const uint32_t etop = __reduce_max_sync(0xffffffffu, largest8(e));
-    // 2^ex > largest / 256, so that 32 (x - hi) <= 256; and the position columns divided by it stay finite.
+    // 2^ex > largest / 256, so that 32 (x - hi) <= 256.  And the position columns
+    // divided by it are below 2^25: the cache's are divided by its scale (2^60 for
+    // a 1 behind a latent of zeros) and the sum of their 64 products has to stay
+    // finite, which leaves 2^96 for them.  (Latent columns that this rounds away
+    // are below 2^-39 of the position columns.)  The factor of the score times the
+    // scale may then be subnormal, off by 2^-150, which is 2^-22 of a score at most.
     int ex = static_cast<int>(top >> 7) - 127 - 7;
-    ex = max(max(ex, -100), static_cast<int>(etop >> 7) - 127 - 100);
+    ex = max(max(ex, -100), static_cast<int>(etop >> 7) - 127 - 24);
     const bool finite = max(top, etop) < 0x7f80;
     if (!finite) ex = 0;
     const float inv = __int_as_float((127 - ex) << 23);
@@ -1124,7 +1129,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                         if (!in) z[k] = make_float2(kNothing, kNothing);
                 }
                 // T of each head: x = 2^(z - T) <= 256, the block's largest at
-                // least 64.  (Rounded to a whole number by adding 1.5 2^23.)
+                // least 128.  (Rounded to a whole number by adding 1.5 2^23.)
                 uint32_t hi[kPer / 4], lo[kPer / 4];       // four heads each
                 __half2 sum[kPer / 2];                     // x as rounded
 #pragma unroll

@@ -616,8 +616,9 @@ DSNQ_API dsnq_status dsnq_shared_prefix_latent_attention_fp8_workspace_bytes(int
  * dsnq_paged_latent_attention over such a cache:
  *   z_j = scale * s_j * q[b,h] . (codes_j | pe_j),   j < seq_lens[b]
  *   out[b,h,:] = sum_j softmax(z)_j s_j codes_j[0:DV],   lse[b,h] = log sum_j exp z_j
- * q's latent columns are split into two e4m3 numbers each (exact down to 2^-15 of
- * the head's largest, off by at most 2^-23 of that below); the probabilities
+ * q's latent columns are split into two e4m3 numbers each (exact down to 2^-14 of
+ * the head's largest, off by at most 2^-22 of that below; 2^-39 of the largest
+ * position column where that is larger); the probabilities
  * times s_j are rounded to two e4m3 numbers (off by at most 2^-8 of themselves,
  * as bf16 would be, or 2^-22 of the largest among 32 neighbouring tokens), and
  * the outputs divided by the sum of the rounded ones; fp32 scores, sums and
@@ -631,6 +632,8 @@ DSNQ_API dsnq_status dsnq_shared_prefix_latent_attention_fp8_workspace_bytes(int
  *                 num_pages >= 1, page_size a multiple of 8, scales 16-byte
  *                 aligned, ld_scale a multiple of 4.  Scales are in [2^-60,
  *                 2^119], as the write leaves them (0 counts as a zero row).
+ *                 Position columns as stored (pe / s) are below 2^96 (1.0 behind
+ *                 an all-zero latent is stored as 2^60).
  * Other arguments, page ids outside the cache and workspace as in
  * dsnq_paged_latent_attention.  Three launches (two when a single worker takes
  * all).

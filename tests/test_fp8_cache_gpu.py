@@ -846,3 +846,30 @@ def test_no_requests():
                                 torch.empty(0, dtype=I64, device=DEV), torch.empty(0, dtype=I64, device=DEV),
                                 torch.empty(32, dtype=F64, device=DEV), cache, scales)
     assert dsnq.debug_status() == OK
+
+
+@both
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -90, 2.0 ** -20, 1.0])
+@pytest.mark.parametrize("H", [9, 64])
+def test_attention_of_queries_in_the_position_columns(H, size):
+    """Latent columns of q that are zero or far below its position columns, over
+    rows whose latent is zero or tiny, so that the cache holds position columns
+    of up to 2^61 (pe / s).  Scores and weights are those of ordinary numbers."""
+    K, P, page = 256, 64, 16
+    g = gen(H)
+    lens = [150, 700]
+    table, pages = paged(g, lens, page)
+    cache, scales = make_cache(g, pages, page, K, P)
+    for b, n in enumerate(lens):
+        at = slots_of(table[b], page, 0, n)
+        level = torch.tensor([0.0, 2.0 ** -33, 2.0 ** -13, 1.0], device=DEV)[torch.arange(n, device=DEV) % 4]
+        dsnq.latent_cache_write_fp8((torch.randn(n, K, generator=g, device=DEV) * level[:, None]).to(BF), randn(g, n, P),
+                                    torch.zeros(n, dtype=I64, device=DEV), at, torch.empty(0, dtype=F64, device=DEV), cache, scales)
+    assert scales.min() == 2.0 ** -60
+    q = torch.cat([(torch.randn(2, H, K, generator=g, device=DEV) * size).to(BF), randn(g, 2, H, P)], -1)
+    got = dsnq.paged_latent_attention_fp8(q, cache, scales, table, ints(lens), K, 0.1)
+    check(q, cache, scales, table, lens, K, float(np.float32(0.1)), got)
+    front = table[1, :-(-700 // page)].contiguous()
+    got = dsnq.shared_prefix_latent_attention_fp8(q[:1], cache, scales, front, ints([700]), table[:1], ints([150]), K, 0.1)
+    check(q[:1], cache, scales, table[:1], [150], K, float(np.float32(0.1)), got, prefix=(front, 700))
+    assert dsnq.debug_status() == OK
