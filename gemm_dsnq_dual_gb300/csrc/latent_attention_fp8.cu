@@ -90,7 +90,7 @@ constexpr int kTmemSfa = 384, kTmemSfb = 388;   // block scales of C^T (ones) an
 constexpr int kStacked = 32;                // heads up to which hi and lo of p s stand side by side too
 constexpr float kRaise = 32.0f;             // log2 by which a block may exceed the reference before O is rescaled
 constexpr float kLeastScale = 0x1p-60f;
-constexpr float kNothing = -1.0e30f;         // log2 of p s of a token past the length
+constexpr float kNothing = -3.402823466e38f; // log2 of p s of a token past the length: no finite one is lower
 constexpr int kMiscBytes = 7168;
 constexpr int kPBytes = kTile * 64;         // hi (or lo) of p s of a tile: 64 bytes a token
 constexpr int kManyParts = 4;               // workers per job from which a CTA joins an item

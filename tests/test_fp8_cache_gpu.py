@@ -873,3 +873,27 @@ def test_attention_of_queries_in_the_position_columns(H, size):
     got = dsnq.shared_prefix_latent_attention_fp8(q[:1], cache, scales, front, ints([700]), table[:1], ints([150]), K, 0.1)
     check(q[:1], cache, scales, table[:1], [150], K, float(np.float32(0.1)), got, prefix=(front, 700))
     assert dsnq.debug_status() == OK
+
+
+@both
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attention_of_scores_near_the_end_of_fp32(H, sign):
+    """Scores of 2^104 in magnitude, all tokens alike: masked tokens stay below
+    the lowest of them, and the output is the tokens' value."""
+    K, page = 256, 16
+    g = gen(H)
+    lens = [1, 33, 500]
+    table, pages = paged(g, lens, page)
+    cache, scales = make_cache(g, pages, page, K, 0)
+    cache[:] = cache[0, 0]
+    scales.fill_(0.0123)
+    code = cache[0, 0].view(E4).double()
+    q = (sign * code.sign() * 2.0 ** 100).to(BF).expand(3, H, K).contiguous()
+    out, lse = dsnq.paged_latent_attention_fp8(q, cache, scales, table, ints(lens), K, 0.05)
+    want = code * float(scales[0, 0])
+    assert ((out.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -18)).all()
+    score = sign * 2.0 ** 100 * code.abs().sum() * float(scales[0, 0]) * float(np.float32(0.05))
+    # Products of a power of two and few bits; what is left are the sum's truncations (dz) and six roundings.
+    assert ((lse.double() - score).abs() <= (K / 32 + 8) * 2.0 ** -23 * abs(score)).all()
+    assert dsnq.debug_status() == OK
