@@ -24,6 +24,9 @@
 // of the p that the rounded x stand for, so that the weights add up to one
 // (those of tokens whose scale is below 2^-8 of their block's largest count
 // unrounded: they may have a large p and no value to speak of).
+// The sums take p as x 2^T / s.  x below 2^-126 is lost and a block's 2^T is at
+// least 2^-126 of the largest: with scales within a factor of 2^80 a token's p is
+// then off by at most 2^-45 of the sum.
 //
 // One CTA, 64 heads (or 32 or 16 where CTAs would idle), tiles of 128 tokens:
 //   S^T [128 tokens x (64 hi | 64 lo)]  = C Q^T        M = 128: a thread has a token

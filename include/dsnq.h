@@ -632,6 +632,8 @@ DSNQ_API dsnq_status dsnq_shared_prefix_latent_attention_fp8_workspace_bytes(int
  *                 num_pages >= 1, page_size a multiple of 8, scales 16-byte
  *                 aligned, ld_scale a multiple of 4.  Scales are in [2^-60,
  *                 2^119], as the write leaves them (0 counts as a zero row).
+ *                 Those of a request's tokens are within a factor of 2^80 of one
+ *                 another (0 counts as 2^-60): probabilities are held times s.
  *                 Position columns as stored (pe / s) are below 2^96 (1.0 behind
  *                 an all-zero latent is stored as 2^60).
  * Other arguments, page ids outside the cache and workspace as in

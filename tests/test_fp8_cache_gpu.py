@@ -897,3 +897,24 @@ def test_attention_of_scores_near_the_end_of_fp32(H, sign):
     # Products of a power of two and few bits; what is left are the sum's truncations (dz) and six roundings.
     assert ((lse.double() - score).abs() <= (K / 32 + 8) * 2.0 ** -23 * abs(score)).all()
     assert dsnq.debug_status() == OK
+
+
+@both
+@pytest.mark.parametrize("H", [16, 64])
+def test_attention_scales_at_the_ends_of_their_range(H):
+    """Scales of one request 2^80 apart, from an all-zero row's on: rows of the
+    smallest scale count with their probability, whatever the others hold."""
+    K, page = 128, 16
+    g = gen(H)
+    lens = [300, 40, 1500]
+    table, pages = paged(g, lens, page)
+    cache, scales = make_cache(g, pages, page, K, 0)
+    for b, n in enumerate(lens):
+        at = slots_of(table[b], page, 0, n)
+        which = torch.randint(0, 3, (n,), generator=g, device=DEV)
+        which = torch.where(torch.arange(n, device=DEV) // 64 % 3 == 2, 0, which)       # whole blocks of the smallest too
+        scales.view(-1)[at] = torch.tensor([2.0 ** -60, 2.0 ** -8, 2.0 ** 20], device=DEV)[which]
+    q = (torch.randn(3, H, K, generator=g, device=DEV) * 2.0 ** -29).to(BF)
+    got = dsnq.paged_latent_attention_fp8(q, cache, scales, table, ints(lens), K, 0.1)
+    check(q, cache, scales, table, lens, K, float(np.float32(0.1)), got)
+    assert dsnq.debug_status() == OK
