@@ -757,8 +757,9 @@ def shared_prefix_latent_attention_fp8(q, cache, scales, prefix_table, prefix_le
     prefix_len (int32 [1]) tokens of prefix_table [width] (int32 page ids), each
     followed by seq_lens[b] tokens of its own row of block_table.  The prefix is
     read and multiplied once for up to 64 (request, head) pairs of the batch.
-    The workspace grows with the batch (1200 bytes of split queries and 4 v_dim of
-    results a pair, twice)."""
+    The workspace grows with the batch: about 74 KB + 256 v_dim bytes for each
+    request and 64 of its heads (or fewer), as much for each 64 pairs of the
+    batch, and at most 54 MB."""
     if prefix_table is None:
         raise TypeError("prefix_table must be a tensor; paged_latent_attention_fp8 takes requests without a common prefix")
     return _attention_fp8(q, cache, scales, prefix_table, prefix_len, block_table, seq_lens, v_dim, scale, out, lse, workspace, stream)

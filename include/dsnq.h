@@ -603,10 +603,17 @@ DSNQ_API dsnq_status dsnq_latent_cache_read_fp8(
     void* out, int64_t ldo,
     void* stream);
 
-/* Host-only queries: bytes of the workspaces of the two calls below: the split
- * queries (about as many bytes as q; for the widest row, K = 512 and P = 64) and
- * the partial results (at most about 42 MB without a prefix).  Errors as in those
- * calls.  `bytes` may be NULL. */
+/*
+ * Host-only queries: bytes of the workspaces of the two calls below, about
+ *   without a prefix: 1.2 KB of split queries for each head of a request, its heads
+ *     counted in 16s, and at most 42 MB of partial results;
+ *   with one: 74 KB + 256 DV bytes (queries and results of 64 rows) for each
+ *     request and 64 of its heads (or fewer: a request of one head costs as much
+ *     as one of 64), as much for each 64 (request, head) pairs of the batch
+ *     against the prefix, and at most 54 MB.
+ * For the widest row (K = 512 and P = 64).  Errors as in those calls.  `bytes` may
+ * be NULL.
+ */
 DSNQ_API dsnq_status dsnq_paged_latent_attention_fp8_workspace_bytes(int64_t B, int64_t H, int64_t DV, int64_t table_width,
                                                                      int64_t page_size, int64_t* bytes);
 DSNQ_API dsnq_status dsnq_shared_prefix_latent_attention_fp8_workspace_bytes(int64_t B, int64_t H, int64_t DV, int64_t prefix_width,
@@ -661,11 +668,8 @@ DSNQ_API dsnq_status dsnq_paged_latent_attention_fp8(
  *   prefix_len  : int32 [1] in device memory, taken as within [0, prefix_width
  *                 * page_size]; 0: no prefix.
  *   seq_lens    : tokens behind the prefix; may be 0.
- *   workspace   : at least dsnq_shared_prefix_latent_attention_fp8_workspace_bytes:
- *                 the batch's split queries and partial results, both twice
- *                 (for the prefix and for the request's own tokens; 4 DV bytes of
- *                 results for each of 64 heads of a request), and some for each
- *                 worker.
+ *   workspace   : at least dsnq_shared_prefix_latent_attention_fp8_workspace_bytes,
+ *                 which grows with the batch (above).
  * Three launches.  Other arguments as in dsnq_paged_latent_attention_fp8.
  */
 DSNQ_API dsnq_status dsnq_shared_prefix_latent_attention_fp8(

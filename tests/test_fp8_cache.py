@@ -314,3 +314,23 @@ def test_cpu_tensors_are_refused():
     for fn, args in OPS.values():
         with pytest.raises(ValueError, match="must be CUDA tensors"):
             fn(**args())
+
+
+def test_workspaces_are_as_large_as_stated():
+    """The header's and the binding's account of the workspaces, for few and many heads and requests."""
+    up = lambda a, b: -(-a // b)
+    for B in (1, 3, 64, 256, 1000, 8192):
+        for H in (1, 6, 16, 48, 64, 100, 128, 1024):
+            for DV in (128, 512):
+                for pwidth, width in ((20, 4), (500, 16), (40000, 2000)):
+                    groups = up(H, 64)
+                    for shared in (False, True):
+                        if shared:
+                            got = dsnq.shared_prefix_latent_attention_fp8_workspace_bytes(B, H, DV, pwidth, width, 64)
+                            sets = B * groups + up(B * up(H, 4) * 4, 64)
+                            least, most = sets * (73_000 + 256 * DV) if sets > 320 else 0, sets * (75_000 + 256 * DV + 512) + (54 << 20)
+                        else:
+                            got = dsnq.paged_latent_attention_fp8_workspace_bytes(B, H, DV, width, 64)
+                            rows = B * up(H, 16) * 16
+                            least, most = rows * 1152, B * H * 1300 + B * (groups * 256 + 16 * 1200) + (42 << 20) + (1 << 19)
+                        assert least <= got <= most, (B, H, DV, pwidth, width, shared, got, least, most)
