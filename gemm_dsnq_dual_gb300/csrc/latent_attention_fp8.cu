@@ -144,6 +144,14 @@ __device__ __forceinline__ int64_t part_slot(const Params& p, int w, int j, bool
     return static_cast<int64_t>(p.prefix_len ? j + w : 2 * w + (first ? 0 : 1)) * p.G + g;
 }
 
+// Whether a part or an image lies in the workspace (the debug build's checks).
+__device__ __forceinline__ bool part_ok(const Params& p, int64_t slot) {
+    return slot >= 0 && slot < static_cast<int64_t>(p.prefix_len ? p.NP + p.B + p.W : 2 * p.W) * p.G;
+}
+__device__ __forceinline__ bool image_ok(const Params& p, int64_t image) {
+    return image >= 0 && image < (static_cast<int64_t>(p.B) + p.NP) * p.G;
+}
+
 // The same value, of which the compiler knows nothing: it would otherwise make
 // copies of a loop for either outcome of a test in it (the softmax had four, and
 // the warps' code no room in the instruction cache).
@@ -548,7 +556,7 @@ __device__ void share_out(const Params& p) {
                 cut = make_int2(p.NP + b, max(static_cast<int>(u - at) - lead, 0));
             }
         }
-        p.meta[w] = cut;
+        if (bounds_ok(cut.x >= 0 && cut.x <= p.NP + p.B && cut.y >= 0)) p.meta[w] = cut;
     }
 }
 
@@ -607,7 +615,7 @@ prepare_kernel(const Params p, const __nv_bfloat16* q, int64_t ldq_b, int64_t ld
         const int64_t image = to ? static_cast<int64_t>(p.B) * p.G + (r >> p.hg) : static_cast<int64_t>(b) * p.G + (h >> p.hg);
         const int i = (to ? static_cast<int>(r) : h) & ((1 << p.hg) - 1);
         uint8_t* at = p.images + image * p.image;
-        if (!bounds_ok(i < p.q_rows)) continue;
+        if (!bounds_ok(i < p.q_rows && image_ok(p, image))) continue;
         if (codes) {
             uint8_t* c = at + (lane >> 3) * 2 * p.q_rows * 128 + (((lane & 7) ^ (i & 7)) << 4);
             *reinterpret_cast<uint4*>(c + i * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -772,6 +780,8 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     int slot;
                     uint32_t parity;
                     ch.take(p, c, slot, parity);
+                    ok = bounds_ok(slot >= 0 && slot < p.slots && chunk < cpt);
+                    if (!ok) break;
                     // Barely two tiles of room: while it waits for the slot, the
                     // chunk comes as near as L2 (2.77 -> 2.69 us a tile at 64 heads
                     // of 576 columns; a whole tile ahead 2.87; with more room
@@ -823,7 +833,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
             if (elected()) {
                 const uint32_t bytes = p.image - kHeads * 4;
                 const int64_t at = run.j < p.NP ? static_cast<int64_t>(p.B + run.j) * p.G + g : static_cast<int64_t>(run.j - p.NP) * p.G + g;
-                const uint8_t* src = p.images + at * p.image;
+                const uint8_t* src = p.images + (bounds_ok(image_ok(p, at)) ? at : 0) * p.image;
                 mbar_arrive_expect_tx(smem_u32(qfull), p.image);
                 bulk_load(smem_u32(q_s), src, bytes, smem_u32(qfull));
                 bulk_load(smem_u32(cq_s), src + bytes, kHeads * 4, smem_u32(qfull));
@@ -845,6 +855,8 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                     ch.take(p, c, slot, parity);
                     const int code = c == 0 ? 0 : c - p.pe;
                     const bool pe = c == 1 && opaque(p.pe);
+                    ok = bounds_ok(slot >= 0 && slot < p.slots && code < p.cc && kTmemS + 2 * HP <= kTmemSfa);
+                    if (!ok) break;
                     const uint32_t a = desc_low(smem_u32(ring) + slot * kChunkBytes, 16);
                     ok = wait_uniform(smem_u32(&full[slot]), parity);
                     if (!ok) break;
@@ -890,6 +902,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                         if (c == 1 && p.pe) continue;
                     }
                     if (code >= p.nblk) continue;
+                    if (!bounds_ok(slot >= 0 && slot < p.slots && code * kHeads + (kPair ? HP : 2 * HP) <= kTmemS)) continue;
                     tc_mma_scaled<kPair>(tmem + code * kHeads, desc_low(smem_u32(ring) + slot * kChunkBytes, kChunkBytes), p_low,
                                          idesc_o(kPair ? HP : 2 * HP), tmem + kTmemSfa, tmem + kTmemSfb, i > 0);
                     tc_commit(smem_u32(&empty[slot]));
@@ -1061,12 +1074,13 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) x[blk][u] = __float_as_uint(__uint_as_float(x[blk][u]) + __uint_as_float(y[blk][u]));
                             }
+                            if (!bounds_ok(part_ok(p, slot) && (h0 >> 2) + k < kHeads / 4)) continue;
                             o[(blk * 16 + (h0 >> 2) + k) * 128] =
                                 make_float4(__uint_as_float(x[blk][0]) * f.x, __uint_as_float(x[blk][1]) * f.y, __uint_as_float(x[blk][2]) * f.z,
                                             __uint_as_float(x[blk][3]) * f.w);
                         }
                     }
-                    if (quad == 0 && mine) p.part_ml[slot * kHeads + h0 + lane] = make_float2(M, ls);
+                    if (quad == 0 && mine && bounds_ok(part_ok(p, slot))) p.part_ml[slot * kHeads + h0 + lane] = make_float2(M, ls);
                 }
                 const int head = (g << p.hg) + h0 + lane;
                 if (ok && whole && p.lse && quad == 0 && mine && head < p.H)
@@ -1248,6 +1262,7 @@ latent_attention_fp8_kernel(const __grid_constant__ CUtensorMap map_c, const Par
                         for (int c = 0; c < cpt; ++c) {
                             if ((c == 1 && p.pe) || c - (c > 0 ? p.pe : 0) >= p.nblk) continue;
                             const int slot = Chunks::slot_of(p, n, c);
+                            if (!bounds_ok(slot >= 0 && slot < p.slots)) continue;
 #pragma unroll 1
                             for (int r = valid + (st >> 3); r < kTile; r += kSoftThreads / 8)
                                 *reinterpret_cast<uint4*>(ring + slot * kChunkBytes + r * 128 + (st & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -1377,6 +1392,7 @@ latent_attention_fp8_join_kernel(const Params p, const int by_cut) {
     auto row_of = [&](int k) { return PREFIX && k < n1 ? hl1 : hl2; };
     // Values 2 lane, + 1, 2 lane + 64, + 1 of the block.
     auto load = [&](int k, float4 (&o)[4]) {
+        if (!bounds_ok(part_ok(p, slot_of(k)) && row_of(k) < kHeads && blk < p.nblk)) return;
         const float4* src = reinterpret_cast<const float4*>(p.part_o) + ((slot_of(k) * p.nblk + blk) * 16 + row_of(k) / 4) * 128 + 2 * lane;
         o[0] = src[0];
         o[1] = src[1];
@@ -1398,7 +1414,7 @@ latent_attention_fp8_join_kernel(const Params p, const int by_cut) {
         for (int u = 0; u < AHEAD; ++u)                    // on their way while the factors are formed
             if (u < cnt) load(k0 + (c + u) * SHARE, o[u]);
         float f[4] = {kNegInf, kNegInf, kNegInf, kNegInf}, l[4] = {0.f, 0.f, 0.f, 0.f};
-        if (lane < cnt) {
+        if (lane < cnt && bounds_ok(part_ok(p, slot_of(k0 + (c + lane) * SHARE)) && row_of(k0 + (c + lane) * SHARE) + 4 <= kHeads)) {
             const int k = k0 + (c + lane) * SHARE;
             const float4* ml = reinterpret_cast<const float4*>(p.part_ml + slot_of(k) * kHeads + row_of(k));
             const float4 x = ml[0], y = ml[1];

@@ -129,3 +129,78 @@ def test_sums_of_a_job_outlive_their_late_readers(libs, H, prefix):
         dsnq.debug_set(0, 0)
     for a, b in zip(got, want):
         assert torch.equal(as_bits(a), as_bits(b))
+
+
+def run_decode_step_kernels():
+    """One small call of each kernel of the decode step's other operators;
+    returns every output tensor."""
+    outs = []
+    g = torch.Generator(device="cuda")
+    g.manual_seed(41)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    B, page, prefix = 9, 16, 200
+    freq, _ = dsnq.rope_frequencies(64, device="cuda")
+    for layout in ("interleaved", "half"):
+        outs.append(dsnq.head_rmsnorm_rope(randn(7, 5, 192), torch.arange(7, device="cuda") * 1000, freq, layout=layout))
+    # Requests of up to 1700 tokens and an empty one, before one more token each; odd pages, a table with room.
+    lens = ints([1699, 1, 127, 128, 300, 0, 40, 900, 15])
+    held = [-(-n // page) for n in lens.tolist()]
+    pages = sum(held) + B + 16
+    ids = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    table, at = torch.full((B, 120), -1, dtype=torch.int32, device="cuda"), 0
+    for b, n in enumerate(held):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    front, free = ids[at:at + 13].clone(), ids[at + 13:].clone()
+    lens, starts, positions, slots, counts = dsnq.extend_block_tables(lens, None, free, table, page, B + 3)
+    outs += [lens, starts, positions, slots, counts, table]
+    kv, pe = randn(B + 3, 512), randn(B + 3, 64)
+    wide = randn(pages, page, 576)
+    codes = torch.cat([(wide[..., :512].float() * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8),
+                       (wide[..., 512:].float() * 100).to(torch.bfloat16).view(torch.uint8)], -1)
+    scales = torch.rand(pages, page, generator=g, device="cuda") * 0.02
+    for layout in ("interleaved", "half"):
+        dsnq.latent_cache_write(kv, pe, positions, slots, freq, wide, normalize=True, layout=layout)
+        dsnq.latent_cache_write_fp8(kv, pe, positions, slots, freq, codes, scales, normalize=True, layout=layout)
+        outs += [wide.clone(), codes.clone(), scales.clone()]
+    total = int(lens.sum())
+    reads = torch.cat([ints([0]), lens.cumsum(0).to(torch.int32)])
+    outs.append(dsnq.latent_cache_read_fp8(codes, scales, 512, table, reads, total))                    # short: 8 rows a CTA
+    many = 5 * total
+    row_starts = torch.cat([ints([0])] + [reads[1:] + i * total for i in range(5)])
+    outs.append(dsnq.latent_cache_read_fp8(codes, scales, 512, table.repeat(5, 1), row_starts, many))   # 16 rows a CTA
+    # Attention: every count of heads that has a kernel, with and without position columns and a prefix, tables with
+    # and without room (CTAs of 16, 32 and 64 heads), many requests (several a worker).
+    narrow = codes[..., :512]
+    room = torch.cat([table, torch.full((B, 30000), -1, dtype=torch.int32, device="cuda")], 1)
+    for H in (7, 16, 32, 48, 64, 130):
+        q = randn(B, H, 576)
+        outs += dsnq.paged_latent_attention(q, wide, table, lens, 512, 0.05)
+        for t in (table, room):
+            outs += dsnq.paged_latent_attention_fp8(q, codes, scales, t, lens, 512, 0.05)
+            outs += dsnq.shared_prefix_latent_attention_fp8(q, codes, scales, front, ints([prefix]), t, lens, 512, 0.05)
+        outs += dsnq.paged_latent_attention_fp8(q[..., :512], narrow, scales, table, lens, 256, 0.05)
+        rows = torch.arange(400, device="cuda") % B
+        outs += dsnq.paged_latent_attention_fp8(q[rows], codes, scales, table[rows], lens[rows], 512, 0.05)
+        outs += dsnq.shared_prefix_latent_attention_fp8(q[rows], codes, scales, front, ints([prefix]), table[rows], lens[rows], 512, 0.05)
+    torch.cuda.synchronize()
+    return outs
+
+
+def test_decode_step_kernels_pass_their_index_checks_and_match_the_release_build(libs):
+    release, debug = libs
+    _native.use_library(release)
+    want = run_decode_step_kernels()
+    _native.use_library(debug)
+    assert dsnq.debug_status() == OK
+    got = run_decode_step_kernels()
+    assert dsnq.debug_status() == OK                          # no check failed
+    assert len(got) == len(want)
+    for g, w in zip(got, want):
+        assert g.dtype == w.dtype and torch.equal(g.contiguous().view(torch.uint8), w.contiguous().view(torch.uint8))
