@@ -131,6 +131,18 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// A place in a ring of shared-memory slots and the parity of its pass.
+struct Place {
+    int i = 0;
+    uint32_t pass = 0;
+    __device__ __forceinline__ void step(int slots) {
+        if (++i == slots) {
+            i = 0;
+            pass ^= 1;
+        }
+    }
+};
+
 // Four steps of D[tmem] (+)= A[smem] * B[smem]^T, bf16 x bf16 -> fp32, K = 16
 // each; A and B advance by ASTEP and BSTEP (16-byte units) a step, the first
 // overwrites D when !accumulate.  One elected lane issues all four: with an
@@ -162,12 +174,49 @@ __device__ __forceinline__ void tc_mma4_bf16(uint32_t d_tmem, uint64_t a_desc, u
 // swizzle: one copy then takes whole groups of a page, whatever its size.  Read
 // K-major (S = Q K^T), the next 8 tokens are a group (2 KB; odd chunk: 1 KB)
 // on.  Read column-major (V^T: M runs along the 64 columns of a chunk and on to
-// the next chunk, 1 KB on; K runs down the tokens), likewise.
+// the next chunk, 1 KB on; K runs down the tokens), likewise.  `lead` and
+// `stride` in bytes: to the next swizzle atom along the contiguous side, and to
+// the next eight rows.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lead, uint32_t stride) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFF);
+    d |= static_cast<uint64_t>((lead >> 4) & 0x3FFF) << 16;
+    d |= static_cast<uint64_t>((stride >> 4) & 0x3FFF) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
 
 // Instruction descriptor of kind::f16: D fp32, A and B bf16; a_mn: A column-major.
 constexpr uint32_t idesc_bf16(int m, int n, bool a_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+        ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+          "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+
+// 16 lanes x 8 N columns of TMEM in the layout of matrix fragments: of each
+// 8 columns, thread i gets columns 2 (i % 4), + 1 of lane i / 4 (r[0], r[1])
+// and of lane i / 4 + 8 (r[2], r[3]).
+__device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
 }
 
 // Barrier of the softmax warps; returns whether any thread passed true.  A

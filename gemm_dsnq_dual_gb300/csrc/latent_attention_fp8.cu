@@ -276,7 +276,8 @@ __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
         : "memory");
 }
 
-// 16 lanes x 16 columns of TMEM as matrix fragments (tmem_ld_frag32).
+// 16 lanes x 16 columns of TMEM as matrix fragments: of each 8 columns, thread i
+// gets columns 2 (i % 4), + 1 of lane i / 4 and of lane i / 4 + 8.
 __device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
