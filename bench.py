@@ -933,7 +933,8 @@ DECODE_OPS = ["tables", "head_rope", "cache_write", "attention", "cache_write_fp
 
 def run_decode_ops(args):
     """Times the library's call of every listed case of perf/operators.py and
-    perf/more_operators.py and of a few more and prints one JSON line: `graph_us` per call in a CUDA graph
+    perf/more_operators.py and of a few more and prints one JSON line
+    (`tile_us`: what a tile more costs a worker of the 8-bit attention): `graph_us` per call in a CUDA graph
     of DECODE_GRAPH_CALLS calls (a quarter of that from 64 MB a call on) over
     distinct inputs, L2 flushed before each replay; an input that a graph visits
     again has a gigabyte or more of others in between (so none is found in L2),
@@ -962,16 +963,35 @@ def run_decode_ops(args):
             dict(by_name["write prompt 8191"], name="write prompt 32768, half pairs", M=32768, pad=0, layout="half"),
             dict(by_name["attention 1 x 701"], name="attention 4 x 200", B=4, maxlen=200),
             dict(by_name["attention 1 x 701"], name="attention 64 x 1000", B=64, maxlen=1000)]
+    # Over the 8-bit cache also: half pairs, and short requests whose tables have room for `room` tokens.
+    by_name8 = {c["name"]: c for c in second.listed()}
+    more8 = [dict(by_name8["write prompt 8191"], name="write prompt 8191, half pairs", layout="half"),
+             dict(by_name8["write prompt 8191"], name="write prompt 32768", M=32768, pad=0)]
+    short = [by_name8["attention 1 x 701"], by_name8["shared 4 x 900 + 60"],
+             dict(by_name8["attention 1 x 701"], name="attention 16 x 2000", B=16, maxlen=2000),
+             dict(by_name8["attention 1 x 701"], name="attention 32 x 500", B=32, maxlen=500)]
+    more8 += short[2:] + [dict(c, name=f"{c['name']}, tables of 131072", room=131072) for c in short]
+    # One request a worker, short and long: the difference is the time of a tile of 128 tokens.
+    tiles = [dict(by_name8["attention 1 x 701"], name=f"tiles {n}, {H} heads of {512 + P}", B=152, H=H, P=P, maxlen=n)
+             for H, P in ((16, 64), (32, 64), (48, 0), (48, 64), (64, 0), (64, 64)) for n in (2048, 8192)]
     out = {}
+
+    def prepared(cases, c, seed):
+        state = cases.prepare(c, seed)
+        if c.get("room"):
+            table = state["table"]
+            state["table"] = torch.nn.functional.pad(table, (0, c["room"] // c["page"] - table.shape[1]), value=-1)
+        return state
+
     with ClockSampler(0) as clk:
-        for cases, c in [*((first, c) for c in [*by_name.values(), *more]), *((second, c) for c in second.listed())]:
+        for cases, c in [*((first, c) for c in [*by_name.values(), *more]), *((second, c) for c in [*by_name8.values(), *more8, *tiles])]:
             if args.only and not any(n in c["name"] for n in args.only.split(",")):
                 continue
             w = cases.work(c)
             label = c["name"] + (" (8 bits)" if cases is second else "")
             sets = DECODE_GRAPH_CALLS if w["bytes"] < 16 << 20 else 25 if w["bytes"] < 64 << 20 else 5
             in_graph = DECODE_GRAPH_CALLS if w["bytes"] < 64 << 20 else DECODE_GRAPH_CALLS // 4
-            states = [cases.prepare(c, 100 + i) for i in range(sets)]
+            states = [prepared(cases, c, 100 + i) for i in range(sets)]
             calls = [lambda s=s, run=cases.run: run(s) for s in states]
             graph = timed_graph_calls(torch, stream, [calls[i % sets] for i in range(in_graph)], flush, reps=max(args.side_reps, 5))
             n = 2 * in_graph
@@ -983,7 +1003,11 @@ def run_decode_ops(args):
             call = (time.perf_counter() - t0) / n * 1e6
             floor = max(w["bytes"] / hbm_gbs / 1e3, w["flops"] / bf16 / 1e6)
             out[label] = {"floor_us": round(floor, 4), "graph_us": round(graph, 2), "call_us": round(call, 1), "sets": sets}
-            print(f"{label:36s} floor {floor:9.4f}  graph {graph:8.2f}  call {call:8.1f} us", file=sys.stderr, flush=True)
+            print(f"{label:48s} floor {floor:9.4f}  graph {graph:8.2f}  call {call:8.1f} us", file=sys.stderr, flush=True)
+            if c in tiles and c["maxlen"] == 8192:
+                short_us = out[label.replace("8192", "2048")]["graph_us"]
+                out[label]["tile_us"] = round((graph - short_us) / 48, 3)
+                print(f"{'':48s} a tile of 128 tokens {out[label]['tile_us']:.3f} us", file=sys.stderr, flush=True)
             del states, calls
             torch.cuda.empty_cache()
         status = dsnq.debug_status()
