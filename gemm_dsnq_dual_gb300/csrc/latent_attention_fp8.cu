@@ -48,10 +48,10 @@
 // The prefix: its rows are the (request, head) pairs of the batch laid end to
 // end, so every tile of the prefix serves 64 rows whatever the number of heads.
 //
-// Measured (152 CTAs, requests of 2048 and 8192 tokens, per tile): 1.90 us at 16
-// heads of 576 columns, where HBM needs 1.88; 2.1 at 48 of 512 (HBM 1.50), where the
+// Measured (152 CTAs, requests of 2048 and 8192 tokens, per tile): 1.88 us at 16
+// heads of 576 columns, where HBM needs 1.88; 2.17 at 48 of 512 (HBM 1.50), where the
 // softmax warps bound it, two on each quarter of the SM, whose reads of shared
-// memory and TMEM wait behind the products'; 2.69 at 64 of 576, where shared memory
+// memory and TMEM wait behind the products'; 2.71 at 64 of 576, where shared memory
 // holds two tiles: the way from O^T of a tile over its freed slots, the copies
 // into them, S^T and the softmax to the O^T two tiles on takes as long.
 //
@@ -352,7 +352,8 @@ __device__ __forceinline__ float log2_fast(float x) {
 
 // Registers of a copying or issuing thread and of a softmax thread: together
 // those that the CTA is launched with (168 each).  What does not fit goes to
-// local memory, whose loads wait behind the products' reads of shared memory.
+// local memory, whose loads wait behind the products' reads of shared memory (16
+// bytes are spilled at 48 rows, 76 at 64, none below).
 // Measured, 88 and 208 against 72 and 216: 2.05 and 2.18 us a tile at 48 heads of
 // 512 columns; sixteen softmax warps of half as many heads each, 56 and 104
 // registers: 2.31.
@@ -1576,8 +1577,10 @@ Plan plan_for(const Shape& s, int64_t ctas, int hg) {
 // Heads of a group (rows of a CTA): 64, whose products cost the least a head, or
 // fewer while that gives every job a CTA of its own and few tiles: a tile of 16
 // heads takes two thirds of the time of one of 64, and its output or part a
-// quarter.  By what the tables can hold, which bounds the lengths.  Measured, us,
-// 16 / 32 / 64 heads (* the rule's choice) of
+// quarter.  By what the tables can hold, which bounds the lengths; where they hold
+// far more (131072 tokens each) the short requests below get 64 heads: 1 x 701
+// 17.0 us, 16 x 2000 40.5, 32 x 500 24.2, 4 behind 900 22.1.  Measured, us, with
+// tables as wide as the requests, 16 / 32 / 64 heads (* the rule's choice) of
 //   1 request of 701 tokens, 128 heads      15.4* / 16.4 / 19.0
 //   1 x 4000, 128                           16.4* / 17.6 / 20.0
 //   4 x 2400, 128                           24.6 / 22.6* / 24.6
